@@ -19,7 +19,8 @@ own = False
 
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 GROUP = 32          # channels that share (step, lo)
-F16_MAX = 65504.0
+LIMIT = 57344.0     # values beyond it saturate: every code's value is finite in fp16
+FIFTEENTH = 1.0 / 15.0
 SHIFTS = (0, 16, 4, 20, 8, 24, 12, 28)  # bit of channel e in its word
 DEVICE = "cuda"
 
@@ -201,11 +202,11 @@ def _prepare_logits(case, g):
 
 def _groups(x):
     """codes [..., D] int64 and (step, lo) [..., D / 32] fp16 of rows [..., D]."""
-    x = torch.nan_to_num(x.float(), nan=0.0, posinf=F16_MAX, neginf=-F16_MAX).clamp(-F16_MAX, F16_MAX)
+    x = torch.nan_to_num(x.float(), nan=0.0).clamp(-LIMIT, LIMIT)
     x = x.reshape(*x.shape[:-1], -1, GROUP)
     lo = x.amin(-1).half()
-    step = ((x.amax(-1) - x.amin(-1)) / 15.0).half()
-    at = (x - lo.float()[..., None]) / step.float()[..., None]
+    step = ((x.amax(-1) - x.amin(-1)) * FIFTEENTH).half()
+    at = (x - lo.float()[..., None]) * torch.reciprocal(step.float())[..., None]
     code = torch.where(step[..., None] > 0, at.round().clamp(0, 15), torch.zeros_like(at)).to(torch.int64)
     return code.flatten(-2), step, lo
 
@@ -388,10 +389,10 @@ def _exact_cache(case, s):
     for name in ("k", "v"):
         x = s[name].double().unflatten(-1, (-1, GROUP))
         lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
-        step = ((hi.float() - lo.float()) / 15.0).half().double()
+        step = ((hi.float() - lo.float()) * FIFTEENTH).half().double()
         lo = lo.half().double()
-        # the codes' quotient is a 32-bit one by definition
-        code = ((x.float() - lo.float()) / step.float()).round().clamp(0, 15).double()
+        # the codes are whole numbers of a 32-bit product by definition
+        code = ((x.float() - lo.float()) * (1.0 / step.float())).round().clamp(0, 15).double()
         found[name] = (lo + code * step).flatten(-2)
     return found
 
