@@ -78,6 +78,7 @@ typedef struct CUstream_st* spec_stream_t; /* same object as cudaStream_t */
 #define SPEC_MAX_POOL 16384       /* candidate-pool size P of spec_build_tree */
 #define SPEC_MAX_NODES 2048       /* tree nodes N per request */
 #define SPEC_MAX_VOCAB (1 << 22)  /* V of every logit row */
+#define SPEC_KV4_MAX_HEADS 256    /* KV heads of a 4-bit cache row */
 
 /* walk_info[b*3 + 2] values */
 #define SPEC_FINAL_ACCEPTED 0    /* the last committed token is an accepted draft */
@@ -454,6 +455,45 @@ int spec_verify_greedy_noalloc(int B, int N, int64_t V, int dtype, const void* t
 int spec_filter_logits(void* logits, int dtype, int64_t R, int64_t V, float T, int64_t top_k, float top_p,
                        int32_t* stats_or_null, spec_stream_t stream);
 
+/* Adjustment of the target logits before filtering and verification ([ZS]
+ * 5.1: the processed target probabilities): penalties for repeated tokens,
+ * biases and a grammar mask, on every row (b, n) of a tree.  The text of row
+ * (b, n) is the request's history (its root token included) and the tokens
+ * on the path from the root to n, the root excluded.  Per token v, in fp32
+ * with each operation rounded once, then rounded to dtype:
+ *   x1 = x / rep if x > 0, x * rep otherwise, for v in the text; x elsewhere
+ *   x2 = x1 - count * freq - pres where count > 0, count = occurrences of v
+ *        in the history from prompt_lens[b] on and on the path
+ *   x3 = x2 + bias, for v in the request's bias list
+ *   out = x3 where the row's mask allows v, -inf elsewhere
+ *   logits [B, N, V] (dtype); out [B, N, V]: other memory, or logits itself
+ *     (in place).  Rows n >= num_nodes[b] (NULL: N) are left as they were.
+ *   history [B, max_history] int32, the first history_lens[b] entries (NULL:
+ *     all) count; ids outside [0, V) are ignored.  NULL: no history.
+ *   rep / freq / pres [B] fp32; NULL: 1 / 0 / 0.  A rep that is not > 0 is
+ *     taken as 1 (SPEC_STAT_BAD_REQUEST).
+ *   draft_token [B, N], tree_mask [B, N, N] u8 as spec_build_tree writes
+ *     them.  No draft_token: no path counts; no tree_mask: a chain.
+ *   bias_ids, bias_vals [B, max_bias]: ids outside [0, V) are ignored; the
+ *     values of an id listed more than once are added in list order.
+ *   allowed [mask_rows, ceil(V / 32)] int32: bit v % 32 of word v / 32 set
+ *     iff v is allowed; allowed_row [B, N] names the row of each node (< 0:
+ *     none, the row is not masked; NULL: row b * N + n).  A row number >=
+ *     mask_rows is taken as none (SPEC_STAT_BAD_REQUEST).
+ * NaN logits stay NaN where allowed; a mask that allows nothing leaves a row
+ * of -inf, which the verify counts.  A history_lens[b] outside [0,
+ * max_history] is clamped (SPEC_STAT_BAD_REQUEST).  B <= 65535, max_history
+ * <= 2^28 (SPEC_ERR_UNSUPPORTED). */
+int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void* logits, void* out,
+                       const int32_t* num_nodes_or_null, const int32_t* history_or_null, int64_t max_history,
+                       const int32_t* history_lens_or_null, const int32_t* prompt_lens_or_null,
+                       const float* rep_penalty_or_null, const float* freq_penalty_or_null,
+                       const float* pres_penalty_or_null, const int32_t* draft_token_or_null,
+                       const uint8_t* tree_mask_or_null, const int32_t* bias_ids_or_null,
+                       const float* bias_vals_or_null, int max_bias, const int32_t* allowed_or_null,
+                       int64_t mask_rows, const int32_t* allowed_row_or_null, int32_t* stats_or_null,
+                       spec_stream_t stream);
+
 /* ------------------------------------------------------------- compaction */
 
 /* Capacity (entries) the freed list of spec_compact_slots needs. */
@@ -491,6 +531,78 @@ int spec_compact_slots(int B, int N, int page_size, const int32_t* seq_lens,
                        int64_t freed_capacity, int32_t* num_freed, int32_t* new_kv_len,
                        void* kv_pool_or_null, int64_t num_slots, int64_t bytes_per_slot,
                        int32_t* stats_or_null, spec_stream_t stream);
+
+/* ------------------------------------------------- 4-bit KV cache (target) */
+
+/* Bytes of one 4-bit cache row (slot): Hkv blocks of 5 D / 4 bytes, one per
+ * KV head (D = 64 or 128, 1 <= Hkv <= SPEC_KV4_MAX_HEADS; -1 otherwise):
+ *   [0, D/2) K codes, [D/2, D) V codes, [D, D + D/8) K's (step, lo) fp16
+ *   pairs, one per 32 channels, [D + D/8, 5 D / 4) V's.
+ * Eight channels share a little-endian 32-bit word, channel 2j in bits
+ * [4j, 4j + 4) and channel 2j + 1 16 bits higher; a code c stands for
+ * lo + c * step.  Rows are the kv_pool rows of spec_compact_slots, which
+ * moves them as they are; several layers may share a slot's bytes (the pool
+ * pointer then starts at the layer's block, slot_stride is the whole slot's). */
+int64_t spec_kv4_slot_bytes(int Hkv, int D);
+
+/* Quantises K and V of the step's tokens into the cache ([ZS] 5.2: the verify
+ * forward writes the KV of every tree node into slots allocated before
+ * drafting; with a long N, a prompt).  Token (b, n), n < num_nodes[b] (NULL:
+ * all N), lies at position seq_lens[b] + n, slot req_to_token[b * max_ctx +
+ * seq_lens[b] + n].  Per group of 32 channels, in fp32 with each operation
+ * rounded once:
+ *   lo = fp16(min x), step = fp16((max x - min x) * (1/15)),
+ *   code = clamp(rint((x - lo) * (1/step)), 0, 15), 0 where step is 0.
+ * NaN counts as 0 and values beyond +-57344 saturate (every code's value is
+ * then finite in fp16).
+ *   k, v [B, N, Hkv, D] (dtype); rows (b, n) lie k_stride / v_stride elements
+ *     apart (at least Hkv * D: parts of a fused projection need no copy).
+ *   pool: num_slots rows, slot_stride bytes apart.
+ * A token whose position or slot is out of range is skipped
+ * (SPEC_STAT_BAD_REQUEST, once per token).  Tokens of one call must have
+ * distinct slots.  k, v and pool 16-byte aligned, strides multiples of 16
+ * bytes, B N Hkv D / 16 < 2^31 (SPEC_ERR_UNSUPPORTED otherwise). */
+int spec_kv4_append(int B, int64_t N, int Hkv, int D, int dtype, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const int32_t* num_nodes_or_null, const int32_t* seq_lens,
+                    const int32_t* req_to_token, int64_t max_ctx, void* pool, int64_t num_slots, int64_t slot_stride,
+                    int32_t* stats_or_null, spec_stream_t stream);
+
+/* Reads tokens back: k, v [B, N, Hkv, D] (dtype, contiguous, 16-byte aligned)
+ * = lo + code * step of the rows that spec_kv4_append of the same B, N,
+ * num_nodes, seq_lens and req_to_token wrote (rounded once to dtype).  A
+ * token out of range reads as zeros (SPEC_STAT_BAD_REQUEST); rows n >=
+ * num_nodes[b] are left as they were. */
+int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* pool, int64_t num_slots,
+                    int64_t slot_stride, const int32_t* num_nodes_or_null, const int32_t* seq_lens,
+                    const int32_t* req_to_token, int64_t max_ctx, void* k, void* v, int32_t* stats_or_null,
+                    spec_stream_t stream);
+
+/* Attention of the tree's nodes over the cache ([HB] "Drafting, verification
+ * and slots": one target forward over all nodes under the tree mask; N = 1
+ * is single-token decoding).  Node n < num_nodes[b] (NULL: N) of request b
+ * attends to positions p < seq_lens[b] and to seq_lens[b] + m for every node
+ * m < num_nodes[b] with tree_mask[b][n][m] != 0 (NULL: m <= n, a chain):
+ *   out = sum_p w_p v_p / sum_p w_p, w_p = exp(scale q . k_p - max), k_p and
+ *   v_p the values of the row req_to_token[b * max_ctx + p].
+ *   q [B, N, Hq, D] bf16, rows (b, n) q_stride elements apart; query heads
+ *     [h Hq/Hkv, (h + 1) Hq/Hkv) share KV head h.
+ *   out [B, N, Hq, D] bf16 contiguous; lse_or_null [B, N, Hq] fp32: the
+ *     natural logarithm of sum_p exp(scale q . k_p).
+ * Every position that is attended has to have been appended.  Values enter
+ * the products in fp16 (relative 2^-11), sums are fp32.  A row that attends
+ * to nothing gives zeros and lse -inf.  Rows n >= num_nodes[b] are left as
+ * they were.  A position whose slot is out of range is not attended, and a
+ * request with seq_len < 0 or seq_len + num_nodes > max_ctx gives zeros
+ * (SPEC_STAT_BAD_REQUEST each).  q, pool and out 16-byte aligned, q_stride a
+ * multiple of 8, Hq <= 4096, B <= 65535 (SPEC_ERR_UNSUPPORTED otherwise).
+ *   ws: spec_kv4_attention_ws_size bytes (0 for sizes that are not
+ *   supported), 16-byte aligned; calls that may overlap need their own. */
+size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D);
+int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const void* pool,
+                       int64_t num_slots, int64_t slot_stride, const int32_t* num_nodes_or_null,
+                       const int32_t* seq_lens, const int32_t* req_to_token, int64_t max_ctx,
+                       const uint8_t* tree_mask_or_null, float scale, void* out, float* lse_or_null,
+                       int32_t* stats_or_null, void* ws, size_t ws_bytes, spec_stream_t stream);
 
 /* -------------------------------------------------------------------- TLI */
 

@@ -24,7 +24,8 @@ __all__ = [
     "spec_compact_slots", "tli_constrain_map", "tli_constrain_map_qlogits", "tli_plan_bytes", "tli_plan_build",
     "tli_map_ids",
     "tli_check_config", "tli_pruned_head", "spec_filter_logits", "spec_wait_probe", "spec_debug_bounds",
-    "new_stats", "new_pool",
+    "new_stats", "new_pool", "spec_kv4_slot_bytes", "spec_kv4_append", "spec_kv4_gather",
+    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_adjust_logits",
 ]
 
 F32 = 0
@@ -84,6 +85,14 @@ _SIGS = {
     "spec_debug_bounds": (_I, [_P, _I]),
     "tli_check_config": (_I, [_I, _I, _I]),
     "spec_filter_logits": (_I, [_P, _I, _I64, _I64, _F, _I64, _F, _P, _P]),
+    "spec_kv4_slot_bytes": (_I64, [_I, _I]),
+    "spec_kv4_append": (_I, [_I, _I64, _I, _I, _I, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _P, _P]),
+    "spec_kv4_gather": (_I, [_I, _I64, _I, _I, _I, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P, _P]),
+    "spec_kv4_attention_ws_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "spec_kv4_attention": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _F, _P, _P, _P, _P,
+                                _SZ, _P]),
+    "spec_adjust_logits": (_I, [_I, _I, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P,
+                                _I64, _P, _P, _P]),
     "tli_pruned_head_ws_size": (_SZ, [_I64, _I64]),
     "tli_pruned_head": (_I, [_I64, _I64, _I64, _P, _P, _P, _P, _I64, _F, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
@@ -463,6 +472,63 @@ def spec_filter_logits(logits, T, top_k=0, top_p=1.0, stats=None):
     return logits
 
 
+def _entries(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def spec_adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, rep_penalty=None, freq_penalty=None,
+                       pres_penalty=None, draft_token=None, tree_mask=None, bias_ids=None, bias_vals=None,
+                       allowed=None, allowed_row=None, num_nodes=None, out=None, stats=None):
+    """Penalties for repeated tokens, biases and grammar masks on the target
+    logits [B, N, V] of a tree's nodes (spec_adjust_logits): in place, or into
+    ``out``.  history [B, H] int32 with history_lens / prompt_lens [B];
+    penalties [B] f32; draft_token [B, N] and tree_mask [B, N, N] give each
+    row's path; bias_ids / bias_vals [B, M]; allowed [rows, ceil(V / 32)]
+    int32 bit masks with allowed_row [B, N].  Returns the adjusted tensor."""
+    _dev(logits, name="logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, N, V]")
+    B, N, V = logits.shape
+    out = logits if out is None else _dev(out, logits.dtype, "out")
+    _entries("out", out, logits.shape)
+    i32, f32 = torch.int32, torch.float32
+    for name, t, dtype, shape in (
+            ("history_lens", history_lens, i32, (B,)), ("prompt_lens", prompt_lens, i32, (B,)),
+            ("rep_penalty", rep_penalty, f32, (B,)), ("freq_penalty", freq_penalty, f32, (B,)),
+            ("pres_penalty", pres_penalty, f32, (B,)), ("draft_token", draft_token, i32, (B, N)),
+            ("tree_mask", tree_mask, torch.uint8, (B, N, N)), ("allowed_row", allowed_row, i32, (B, N)),
+            ("num_nodes", num_nodes, i32, (B,))):
+        if t is not None:
+            _dev(t, dtype, name)
+            _entries(name, t, shape)
+    H = M = rows = 0
+    if history is not None:
+        _dev(history, i32, "history")
+        H = history.shape[-1]
+        _entries("history", history, (B, H))
+    if bias_ids is not None:
+        _dev(bias_ids, i32, "bias_ids")
+        M = bias_ids.shape[-1]
+        _entries("bias_ids", bias_ids, (B, M))
+        if bias_vals is None:
+            raise ValueError("bias_ids needs bias_vals")
+        _dev(bias_vals, f32, "bias_vals")
+        _entries("bias_vals", bias_vals, (B, M))
+    if allowed is not None:
+        _dev(allowed, i32, "allowed")
+        rows = allowed.numel() // ((V + 31) // 32)
+        _entries("allowed", allowed.view(-1, allowed.shape[-1]), (rows, (V + 31) // 32))
+    _dev(stats, i32, "stats")
+    _same_device(logits, out, history, history_lens, prompt_lens, rep_penalty, freq_penalty, pres_penalty, draft_token,
+                 tree_mask, bias_ids, bias_vals, allowed, allowed_row, num_nodes, stats)
+    _call("spec_adjust_logits", B, N, V, _logit_code(logits), _ptr(logits), _ptr(out), _ptr(num_nodes), _ptr(history),
+          H, _ptr(history_lens), _ptr(prompt_lens), _ptr(rep_penalty), _ptr(freq_penalty), _ptr(pres_penalty),
+          _ptr(draft_token), _ptr(tree_mask), _ptr(bias_ids), _ptr(bias_vals), M, _ptr(allowed), rows,
+          _ptr(allowed_row), _ptr(stats), _stream())
+    return out
+
+
 # -------------------------------------------------------------- compaction
 
 def spec_compact_freed_capacity(B, N, page_size):
@@ -497,6 +563,139 @@ def spec_compact_slots(seq_lens, accept_path, accept_length, req_to_token, page_
           _ptr(req_to_token), max_ctx, _ptr(out["move_src"]), _ptr(out["move_dst"]), _ptr(out["num_moves"]),
           _ptr(out["freed"]), out["freed"].numel(), _ptr(out["num_freed"]), _ptr(out["new_kv_len"]), _ptr(kv_pool),
           slots, bps, _ptr(stats), _stream())
+    return out
+
+
+# ---------------------------------------------------------- 4-bit KV cache
+
+def spec_kv4_slot_bytes(Hkv, D) -> int:
+    """Bytes of one 4-bit cache row (the layout is in include/specdec.h)."""
+    n = lib().spec_kv4_slot_bytes(int(Hkv), int(D))
+    if n < 0:
+        raise SpecError("spec_kv4_slot_bytes", -2)
+    return n
+
+
+def _same_device(like, *tensors):
+    """The launch goes to the current device's current stream."""
+    if like.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {like.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != like.device:
+            raise ValueError(f"tensors are on {like.device} and {t.device}")
+
+
+def _rows(t, name):
+    """Row stride (elements) of t [B, N, H, D]: heads contiguous, rows (b, n)
+    evenly spaced (a slice of a fused projection qualifies)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, heads, D]")
+    B, N, H, D = t.shape
+    row = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else H * D)
+    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or (B > 1 and N > 1 and t.stride(0) != N * row):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
+    return row
+
+
+def _kv4_pool(pool, table, lens, num_nodes, B, name="kv_pool"):
+    """(num_slots, slot_stride) of a pool [slots, bytes] whose rows may be
+    part of wider ones (a layer's columns of a slot)."""
+    if not pool.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if pool.dtype != torch.uint8 or pool.dim() != 2 or pool.stride(1) != 1:
+        raise ValueError(f"{name} must be uint8 [slots, bytes] with contiguous rows")
+    _dev(table, torch.int32, "req_to_token")
+    _dev(lens, torch.int32, "seq_lens")
+    _dev(num_nodes, torch.int32, "num_nodes")
+    if table.dim() != 2 or table.shape[0] < B or lens.numel() < B or (num_nodes is not None and num_nodes.numel() < B):
+        raise ValueError("req_to_token [B, max_ctx], seq_lens [B] and num_nodes [B] need an entry per request")
+    return pool.shape[0], pool.stride(0) if pool.shape[0] > 1 else max(pool.stride(0), pool.shape[1])
+
+
+def spec_kv4_append(k, v, kv_pool, req_to_token, seq_lens, num_nodes=None, stats=None):
+    """Quantises k, v [B, N, Hkv, D] (bf16 or f32; rows may be strided) into
+    kv_pool [slots, bytes] uint8 at positions seq_lens[b] + n, n < num_nodes[b]
+    (None: all N).  Returns kv_pool."""
+    ks, vs = _rows(k, "k"), _rows(v, "v")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    B, N, H, D = k.shape
+    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
+    if kv_pool.shape[1] < spec_kv4_slot_bytes(H, D):
+        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
+    _dev(stats, torch.int32, "stats")
+    _same_device(k, v, kv_pool, req_to_token, seq_lens, num_nodes, stats)
+    _call("spec_kv4_append", B, N, H, D, _logit_code(k), _ptr(k), ks, _ptr(v), vs, _ptr(num_nodes), _ptr(seq_lens),
+          _ptr(req_to_token), req_to_token.shape[1], _ptr(kv_pool), slots, stride, _ptr(stats), _stream())
+    return kv_pool
+
+
+def spec_kv4_gather(kv_pool, req_to_token, seq_lens, N, Hkv, D, dtype=torch.bfloat16, num_nodes=None, k=None, v=None,
+                    stats=None):
+    """Reads positions seq_lens[b] + n, n < N, back as (k, v) [B, N, Hkv, D]
+    of dtype (bf16 or f32).  Rows n >= num_nodes[b] are left as they were."""
+    B = seq_lens.numel()
+    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
+    if kv_pool.shape[1] < spec_kv4_slot_bytes(Hkv, D):
+        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
+    k = _out(k, (B, N, Hkv, D), dtype, kv_pool, "k")
+    v = _out(v, (B, N, Hkv, D), dtype, kv_pool, "v")
+    if k.shape != (B, N, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, N, Hkv, D]")
+    _dev(stats, torch.int32, "stats")
+    _same_device(kv_pool, req_to_token, seq_lens, num_nodes, k, v, stats)
+    _call("spec_kv4_gather", B, int(N), int(Hkv), int(D), _logit_code(k), _ptr(kv_pool), slots, stride,
+          _ptr(num_nodes), _ptr(seq_lens), _ptr(req_to_token), req_to_token.shape[1], _ptr(k), _ptr(v), _ptr(stats),
+          _stream())
+    return k, v
+
+
+def spec_kv4_attention_ws_size(B, N, Hq, Hkv, D) -> int:
+    n = int(lib().spec_kv4_attention_ws_size(int(B), int(N), int(Hq), int(Hkv), int(D)))
+    if n == 0:
+        raise SpecError("spec_kv4_attention_ws_size", -2)
+    return n
+
+
+def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask=None, scale=None, num_nodes=None,
+                       out=None, lse=None, ws=None, stats=None):
+    """Attention of q [B, N, Hq, D] bf16 (rows may be strided) over the 4-bit
+    cache: positions below seq_lens[b], and node m at seq_lens[b] + m where
+    tree_mask [B, N, N] is set (None: a chain).  scale: None is D ** -0.5.
+    lse [B, N, Hq] f32 (optional) receives the log of the weights' sum.  ws:
+    a uint8 workspace of spec_kv4_attention_ws_size bytes to reuse between
+    calls that do not overlap.  Returns out [B, N, Hq, D] bf16."""
+    qs = _rows(q, "q")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bfloat16")
+    B, N, Hq, D = q.shape
+    Hkv = int(num_kv_heads)
+    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
+    if kv_pool.shape[1] < spec_kv4_slot_bytes(Hkv, D):
+        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
+    if Hq % Hkv:
+        raise ValueError("the number of query heads must be a multiple of num_kv_heads")
+    out = _out(out, q.shape, torch.bfloat16, q, "out")
+    _entries("out", out, q.shape)
+    if tree_mask is not None:
+        _dev(tree_mask, torch.uint8, "tree_mask")
+        _entries("tree_mask", tree_mask, (B, N, N))
+    if lse is not None:
+        _dev(lse, torch.float32, "lse")
+        _entries("lse", lse, (B, N, Hq))
+    if q.numel() == 0:
+        return out
+    if ws is None:
+        ws = torch.empty(spec_kv4_attention_ws_size(B, N, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
+    _dev(ws, torch.uint8, "ws")
+    _dev(stats, torch.int32, "stats")
+    _same_device(q, kv_pool, req_to_token, seq_lens, num_nodes, tree_mask, out, lse, ws, stats)
+    _call("spec_kv4_attention", B, N, Hq, Hkv, D, _ptr(q), qs, _ptr(kv_pool), slots, stride, _ptr(num_nodes),
+          _ptr(seq_lens), _ptr(req_to_token), req_to_token.shape[1], _ptr(tree_mask),
+          float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(stats), _ptr(ws), ws.numel(),
+          _stream())
     return out
 
 
