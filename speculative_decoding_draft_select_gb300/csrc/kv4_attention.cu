@@ -22,9 +22,7 @@
 // one line, each CTA takes an equal stretch of it, and a segment that is cut
 // between CTAs leaves partial (max, sum, weighted values) in the workspace,
 // which a second kernel merges in a fixed order.  The host knows no lengths.
-#include <cuda_fp16.h>
-
-#include "kv4.cuh"
+#include "kv4_attn.cuh"
 
 namespace specdec {
 namespace {
@@ -34,122 +32,6 @@ constexpr int kAttThreads = 128;
 constexpr int kAttWarps = kAttThreads / 32;
 constexpr int kMaxCtas = 608;    // CTAs of a launch at most (sizes the workspace): 4 on each of 152 SMs
 constexpr float kWeightExp = 15.0f;  // weights are held times 2^15
-
-struct AttnArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  int B, N, Hq, Hkv, G;
-  const uint8_t* pool;
-  int64_t num_slots, slot_stride;
-  const int32_t* table;
-  int64_t max_ctx;
-  const int32_t* seq_lens;
-  const int32_t* num_nodes;
-  const uint8_t* mask;
-  float scale_log2;
-  uint16_t* out;
-  float* lse;
-  float* ws;
-  int ctas;  // of the attention launch
-  int32_t* stats;
-};
-
-// Request b's share of the line: nodes, positions, tiles along the positions
-// and row tiles.  A request whose positions do not fit the table has no
-// positions (its rows get zeros) and one empty tile.
-struct Req {
-  int nodes, start, end, tiles, row_tiles;
-  bool bad;
-};
-
-template <int T>
-__device__ __forceinline__ Req attn_req(const AttnArgs& a, int b, int R) {
-  Req r;
-  r.nodes = kv4_nodes(a.num_nodes, b, a.N);
-  r.start = __ldg(a.seq_lens + b);
-  r.bad = r.start < 0 || static_cast<int64_t>(r.start) + r.nodes > a.max_ctx;
-  r.end = r.bad ? 0 : r.start + r.nodes;
-  if (r.bad) r.start = 0;
-  r.tiles = r.nodes == 0 ? 0 : (r.bad ? 1 : (r.end + T - 1) / T);
-  r.row_tiles = (r.nodes * a.G + R - 1) / R;
-  return r;
-}
-__device__ __forceinline__ int64_t attn_units(const Req& r, int Hkv) {
-  return static_cast<int64_t>(r.tiles) * r.row_tiles * Hkv;
-}
-
-// The line's length and, for CTA `cta` of `ctas` (or for request `want` when
-// want >= 0), where it begins: block-wide, every thread gets the result.
-struct Where {
-  int64_t total;   // units of all requests
-  int64_t ctas;    // CTAs that share them: no more than there are units
-  int64_t before;  // units of the requests before b
-  int b;
-};
-
-template <int T, int THREADS>
-__device__ __forceinline__ Where attn_where(const AttnArgs& a, int R, int cta, int want) {
-  __shared__ int64_t s_warp[THREADS / 32];
-  __shared__ int64_t s_before;
-  __shared__ int s_b;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (a.B + THREADS - 1) / THREADS;
-  const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += attn_units(attn_req<T>(a, b, R), a.Hkv);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (threadIdx.x == 0) s_b = a.B;
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int64_t pre = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) pre += s_warp[w];
-    total += s_warp[w];
-  }
-  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
-  const int64_t x = want >= 0 ? 0 : (cta < ctas ? cta * total / ctas : total);
-  if (want >= 0 ? (want >= b0 && want < b1) : (x >= pre && x < pre + mine)) {
-    int b = b0;
-    for (;; ++b) {
-      if (b == want) break;
-      const int64_t u = attn_units(attn_req<T>(a, b, R), a.Hkv);
-      if (want < 0 && x < pre + u) break;
-      pre += u;
-    }
-    s_before = pre;
-    s_b = b;
-  }
-  __syncthreads();
-  const Where w{total, ctas, s_before, s_b};
-  __syncthreads();
-  return w;
-}
-
-__device__ __forceinline__ uint32_t h2_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 u32_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-
-// Code pairs of one register to fp16 values: the four nibbles j = 0..3 of
-// both halves, out[j] = (lo + c * step) of nibble j.  A nibble ORed into the
-// fraction of 1024 (or, 4 bits higher, 16 c) is exact, and so is the
-// subtraction; the multiply-add rounds once.
-__device__ __forceinline__ void dequant4(uint32_t x, uint32_t step2, uint32_t lo2, uint32_t* out) {
-  const __half2 st = u32_h2(step2), lo = u32_h2(lo2);
-  const __half2 k1024 = u32_h2(0xe400e400u), k16 = u32_h2(0x2c002c00u), k64 = u32_h2(0xd400d400u);
-#pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    const uint32_t y = j ? x >> 8 : x;
-    const __half2 a = __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), k1024);        // - 1024
-    const __half2 b = __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), k16, k64);     // / 16 - 64
-    out[j] = h2_u32(__hfma2(a, st, lo));
-    out[j + 1] = h2_u32(__hfma2(b, st, lo));
-  }
-}
 
 // D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
 __device__ __forceinline__ void mma16816(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
@@ -252,12 +134,6 @@ struct AttShared {
 };
 
 __device__ __forceinline__ int padded(int ch) { return ch + (ch >> 5) * 4; }
-
-__device__ __forceinline__ uint16_t f_bf16(float x) {
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
-  return r;
-}
 
 // Query rows [r0, r0 + 16 MT) of (b, h) into shared memory: a warp per row.
 template <int D, int MT>
@@ -532,90 +408,18 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
           }
           continue;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // no position: zeros; NaN stays
+        const float inv = attn_inv(sum);
         const int rw = r0 + r, n = rw / a.G;
         const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
         uint2 v;
         v.x = f_bf16(acc.x * inv) | static_cast<uint32_t>(f_bf16(acc.y * inv)) << 16;
         v.y = f_bf16(acc.z * inv) | static_cast<uint32_t>(f_bf16(acc.w * inv)) << 16;
         *reinterpret_cast<uint2*>(a.out + at * D + ch) = v;
-        if (a.lse && ch == 0)
-          a.lse[at] = sum == 0.0f ? neg_inf() : (top + log2f(sum) - kWeightExp) * 0.6931471805599453f;
+        if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
       }
     }
     __syncthreads();
     u = s0 + t1;
-  }
-}
-
-// Merges the partials of the segments that were cut between CTAs: block
-// (row tile, KV head, request).  A warp takes a row; where there are fewer
-// rows than warps, the warps split the row's partials.
-constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
-
-template <int D, int T>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const AttnArgs a, int R) {
-  pdl_enter();
-  constexpr int per = D / 32;
-  const int b = blockIdx.z, h = blockIdx.y, rt = blockIdx.x;
-  const Req rq = attn_req<T>(a, b, R);
-  if (rt >= rq.row_tiles) return;
-  const Where w0 = attn_where<T, kMergeThreads>(a, R, 0, b);
-  const int64_t s0 = w0.before + (static_cast<int64_t>(h) * rq.row_tiles + rt) * rq.tiles, s1 = s0 + rq.tiles;
-  const int64_t i0 = ((s0 + 1) * w0.ctas - 1) / w0.total, i1 = (s1 * w0.ctas - 1) / w0.total;
-  if (i0 == i1) return;  // one CTA had the whole segment
-  const int pieces = static_cast<int>(i1 - i0) + 1;
-  auto part = [&](int i) {
-    return a.ws + ((i0 + i) * 2 + (i == 0 ? 1 : 0)) * static_cast<int64_t>(R * (D + 2));
-  };
-  const int rows = min(R, rq.nodes * a.G - rt * R);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool split = rows < kMergeWarps;  // all warps on one row
-  __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps];
-  for (int r = split ? 0 : warp; r < rows; r += split ? 1 : kMergeWarps) {
-    float top = neg_inf();
-    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, part(i)[R * D + 2 * r]);
-    top = warp_max(top);
-    float l = 0.0f, acc[per];
-#pragma unroll
-    for (int j = 0; j < per; ++j) acc[j] = 0.0f;
-    const int first = split ? warp : 0, step = split ? kMergeWarps : 1;
-#pragma unroll 4
-    for (int i = first; i < pieces; i += step) {
-      const float* p = part(i);
-      const float pm = p[R * D + 2 * r], pl = p[R * D + 2 * r + 1];
-      const float f = pm == neg_inf() ? 0.0f : fast_exp2(pm - top);
-      l += pl * f;
-#pragma unroll
-      for (int j = 0; j < per; ++j) acc[j] += p[r * D + lane * per + j] * f;
-    }
-    if (split) {
-#pragma unroll
-      for (int j = 0; j < per; ++j) s_o[warp][lane * per + j] = acc[j];
-      if (lane == 0) s_l[warp] = l;
-      __syncthreads();
-      l = 0.0f;
-#pragma unroll
-      for (int j = 0; j < per; ++j) acc[j] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        l += s_l[w];
-#pragma unroll
-        for (int j = 0; j < per; ++j) acc[j] += s_o[w][lane * per + j];
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    const int rw = rt * R + r, n = rw / a.G;
-    const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
-    uint32_t v[per / 2];
-#pragma unroll
-    for (int j = 0; j < per; j += 2)
-      v[j / 2] = f_bf16(acc[j] * inv) | static_cast<uint32_t>(f_bf16(acc[j + 1] * inv)) << 16;
-#pragma unroll
-    for (int j = 0; j < per / 2; ++j) reinterpret_cast<uint32_t*>(a.out + at * D + lane * per)[j] = v[j];
-    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? neg_inf() : (top + log2f(l) - kWeightExp) * 0.6931471805599453f;
   }
 }
 
@@ -634,12 +438,13 @@ int launch_attention(AttnArgs a, int sms, cudaStream_t s) {
   launch_k(kernel, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.N) * a.G + R - 1) / R), static_cast<unsigned>(a.Hkv),
                   static_cast<unsigned>(a.B));
-  launch_k(kv4_merge_kernel<D, kTile>, grid, kMergeThreads, 0, s, a, R);
+  launch_k(kv4_merge_kernel<D, kTile>, grid, kMergeThreads, 0, s, a, R, kWeightExp);
   return launch_status();
 }
 
-// Rows of a row tile: 16 where they suffice, else 32.
-int rows_of(int64_t rows) { return rows <= 16 ? 16 : 32; }
+// Rows of a row tile here: 16 where they suffice, else 32; 0: more rows than
+// that go to the tensor-memory kernel (kv4_tree.cu).
+int rows_of(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 0); }
 
 }  // namespace
 }  // namespace specdec
@@ -648,7 +453,9 @@ using namespace specdec;
 
 extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D) {
   if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || spec_kv4_slot_bytes(Hkv, D) < 0) return 0;
-  const int R = rows_of(static_cast<int64_t>(N) * (Hq / Hkv));
+  const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
+  const int R = rows_of(rows);
+  if (R == 0) return align256(tree_attention_ws(rows, D));
   return align256(static_cast<size_t>(kMaxCtas) * 2 * R * (D + 2) * sizeof(float));
 }
 
@@ -681,7 +488,9 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
              num_slots, slot_stride, req_to_token, max_ctx, seq_lens, num_nodes_or_null, tree_mask_or_null,
              scale * kLog2e, static_cast<uint16_t*>(out), lse_or_null, static_cast<float*>(ws), 0, stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool small = rows_of(static_cast<int64_t>(N) * a.G) == 16;
+  const int R = rows_of(static_cast<int64_t>(N) * a.G);
+  if (R == 0) return launch_tree_attention(a, D, sms, s);
+  const bool small = R == 16;
   if (D == 128) return small ? launch_attention<128, 1>(a, sms, s) : launch_attention<128, 2>(a, sms, s);
   return small ? launch_attention<64, 1>(a, sms, s) : launch_attention<64, 2>(a, sms, s);
 }
