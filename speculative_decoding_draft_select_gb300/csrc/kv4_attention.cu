@@ -28,9 +28,9 @@ namespace specdec {
 namespace {
 
 constexpr int kTile = 64;        // positions of a tile: 16 per warp
+constexpr int kEnds = 2;         // tiles that a segment's beginning and end cost
 constexpr int kAttThreads = 128;
 constexpr int kAttWarps = kAttThreads / 32;
-constexpr int kMaxCtas = 608;    // CTAs of a launch at most (sizes the workspace): 4 on each of 152 SMs
 constexpr float kWeightExp = 15.0f;  // weights are held times 2^15
 
 // D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
@@ -188,22 +188,14 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
   AttShared<D, MT>& sh = *reinterpret_cast<AttShared<D, MT>*>(att_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
-  const Where w0 = attn_where<kTile, kAttThreads>(a, R, blockIdx.x, -1);
-  if (blockIdx.x >= w0.ctas) return;
-  const int64_t lo = blockIdx.x * w0.total / w0.ctas, hi = (blockIdx.x + 1) * w0.total / w0.ctas;
-  int b = w0.b;
-  int64_t base = w0.before;  // first unit of request b
-  for (int64_t u = lo; u < hi;) {
-    Req rq = attn_req<kTile>(a, b, R);
-    while (u >= base + attn_units(rq, a.Hkv)) {
-      base += attn_units(rq, a.Hkv);
-      rq = attn_req<kTile>(a, ++b, R);
-    }
-    // the segment that unit u belongs to, and this CTA's part of it
-    const int seg = static_cast<int>((u - base) / rq.tiles);
-    const int h = seg / rq.row_tiles, rt = seg - h * rq.row_tiles;
-    const int64_t s0 = base + static_cast<int64_t>(seg) * rq.tiles, s1 = s0 + rq.tiles;
-    const int t0 = static_cast<int>(u - s0), t1 = static_cast<int>(min(hi, s1) - s0);
+  CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
+  if (threadIdx.x == 0) *cut = CutSegment{0, 0, 0, 0};
+  Line line;
+  Walk<kTile, kEnds, R> walk;
+  if (!attn_stretch<kTile, kEnds, R, kAttThreads>(a, line, walk)) return;
+  Part rq;
+  while (walk.next(a, rq)) {
+    const int b = rq.b, h = rq.h, rt = rq.rt, t0 = rq.t0, t1 = rq.t1;
     const int r0 = rt * R, rows = min(R, rq.nodes * a.G - r0);
     if (rq.bad && h == 0 && rt == 0 && threadIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
 
@@ -348,8 +340,10 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
     }
 
     // merge the warps
-    const bool complete = t0 == 0 && t1 == rq.tiles;
-    float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (s0 < lo ? 0 : 1)) * (R * (D + 2));
+    const bool complete = rq.complete();
+    float* part = attn_part(a, blockIdx.x, t0 > 0 ? 0 : 1, R, D);
+    if (t0 == 0 && t1 < rq.tiles && threadIdx.x == 0)
+      *cut = CutSegment{b, h, rt, line.pieces(static_cast<int>(blockIdx.x), rq.tiles, t1)};
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -419,7 +413,6 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
       }
     }
     __syncthreads();
-    u = s0 + t1;
   }
 }
 
@@ -436,9 +429,7 @@ int launch_attention(AttnArgs a, int sms, cudaStream_t s) {
   a.ctas = sms * (MT == 1 ? 3 : 2);
   a.ctas = a.ctas < kMaxCtas ? a.ctas : kMaxCtas;
   launch_k(kernel, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.N) * a.G + R - 1) / R), static_cast<unsigned>(a.Hkv),
-                  static_cast<unsigned>(a.B));
-  launch_k(kv4_merge_kernel<D, kTile>, grid, kMergeThreads, 0, s, a, R, kWeightExp);
+  launch_merge<D>(a, R, kWeightExp, s);
   return launch_status();
 }
 
@@ -455,8 +446,7 @@ extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int 
   if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || spec_kv4_slot_bytes(Hkv, D) < 0) return 0;
   const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
   const int R = rows_of(rows);
-  if (R == 0) return align256(tree_attention_ws(rows, D));
-  return align256(static_cast<size_t>(kMaxCtas) * 2 * R * (D + 2) * sizeof(float));
+  return align256(R == 0 ? attn_ws_bytes(kTreeMaxCtas, kTreeRows, D) : attn_ws_bytes(kMaxCtas, R, D));
 }
 
 extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,

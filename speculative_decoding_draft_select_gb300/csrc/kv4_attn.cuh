@@ -25,9 +25,9 @@ struct AttnArgs {
   int32_t* stats;
 };
 
-// Request b's share of the line: nodes, positions, tiles along the positions
-// and row tiles.  A request whose positions do not fit the table has no
-// positions (its rows get zeros) and one empty tile.
+// Request b: nodes, positions [0, end) of which [start, end) are nodes, tiles
+// of T positions and row tiles of R rows.  A request whose positions do not
+// fit the table has no positions (its rows get zeros) and one empty tile.
 struct Req {
   int nodes, start, end, tiles, row_tiles;
   bool bad;
@@ -45,61 +45,119 @@ __device__ __forceinline__ Req attn_req(const AttnArgs& a, int b, int R) {
   r.row_tiles = (r.nodes * a.G + R - 1) / R;
   return r;
 }
+
+// The line.  Each (request, KV head, row tile) with a row is a segment: E
+// units for its beginning and end (reading q, writing the result: about what
+// E tiles cost), then one per tile.  CTA i of the launch's n takes units
+// [i total / n, (i + 1) total / n).
+template <int E>
 __device__ __forceinline__ int64_t attn_units(const Req& r, int Hkv) {
-  return static_cast<int64_t>(r.tiles) * r.row_tiles * Hkv;
+  return r.tiles == 0 ? 0 : static_cast<int64_t>(r.tiles + E) * r.row_tiles * Hkv;
 }
 
-// The line's length and, for CTA `cta` of `ctas` (or for request `want` when
-// want >= 0), where it begins: block-wide, every thread gets the result.
-struct Where {
-  int64_t total;   // units of all requests
-  int64_t ctas;    // CTAs that share them: no more than there are units
-  int64_t before;  // units of the requests before b
-  int b;
+// A part of a segment: tiles [t0, t1) of its `tiles`.
+struct Part {
+  int b, h, rt, t0, t1;
+  int nodes, start, end, tiles;
+  bool bad;
+  __device__ __forceinline__ bool complete() const { return t0 == 0 && t1 == tiles; }
 };
 
-template <int T, int THREADS>
-__device__ __forceinline__ Where attn_where(const AttnArgs& a, int R, int cta, int want) {
+// A CTA's stretch of the line, walked segment by segment.
+template <int T, int E, int R>
+struct Walk {
+  int64_t left;  // units
+  int skip;      // units of the segment (b, h, rt) that an earlier CTA has
+  int b, h, rt, row_tiles;
+  int nodes, start, end, tiles;
+  bool bad;
+  __device__ __forceinline__ void request(const AttnArgs& a) {
+    const Req r = attn_req<T>(a, b, R);
+    nodes = r.nodes, start = r.start, end = r.end, tiles = r.tiles, row_tiles = r.row_tiles, bad = r.bad;
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a, Part& p) {
+    while (left > 0) {
+      if (h == a.Hkv) {
+        h = 0;
+        do {
+          ++b;
+          request(a);
+        } while (tiles == 0);
+      }
+      const int len = tiles + E - skip, take = left < len ? static_cast<int>(left) : len;
+      p.t0 = max(skip - E, 0);
+      p.t1 = skip + take - E;
+      p.b = b, p.h = h, p.rt = rt, p.nodes = nodes, p.start = start, p.end = end, p.tiles = tiles, p.bad = bad;
+      left -= take;
+      skip = 0;
+      if (++rt == row_tiles) rt = 0, ++h;
+      if (p.t1 > p.t0) return true;
+    }
+    return false;
+  }
+};
+
+// What a CTA needs to know of the whole line.
+struct Line {
+  int64_t total, ctas;  // units, CTAs that share them (no more than there are units)
+  // CTAs from this one on that hold a part of the segment whose tiles [0, t1)
+  // end this CTA's stretch
+  __device__ __forceinline__ int pieces(int cta, int tiles, int t1) const {
+    const int64_t end = (cta + 1) * total / ctas + tiles - t1;  // unit behind the segment's last
+    return static_cast<int>((end * ctas - 1) / total) - cta + 1;
+  }
+};
+
+// Finds this CTA's stretch (block-wide, every thread gets the result); false
+// when it has none.
+template <int T, int E, int R, int THREADS>
+__device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk<T, E, R>& w) {
   __shared__ int64_t s_warp[THREADS / 32];
-  __shared__ int64_t s_before;
+  __shared__ int64_t s_off;
   __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += attn_units(attn_req<T>(a, b, R), a.Hkv);
+  for (int b = b0; b < b1; ++b) mine += attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (threadIdx.x == 0) s_b = a.B;
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int64_t pre = incl - mine, total = 0;
+  int64_t pre = incl - mine;
+  line.total = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) pre += s_warp[w];
-    total += s_warp[w];
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i < warp) pre += s_warp[i];
+    line.total += s_warp[i];
   }
-  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
-  const int64_t x = want >= 0 ? 0 : (cta < ctas ? cta * total / ctas : total);
-  if (want >= 0 ? (want >= b0 && want < b1) : (x >= pre && x < pre + mine)) {
+  line.ctas = min(static_cast<int64_t>(a.ctas), line.total);
+  const int64_t cta = blockIdx.x;
+  if (cta >= line.ctas) return false;
+  const int64_t lo = cta * line.total / line.ctas;
+  if (lo >= pre && lo < pre + mine) {
     int b = b0;
     for (;; ++b) {
-      if (b == want) break;
-      const int64_t u = attn_units(attn_req<T>(a, b, R), a.Hkv);
-      if (want < 0 && x < pre + u) break;
+      const int64_t u = attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
+      if (lo < pre + u) break;
       pre += u;
     }
-    s_before = pre;
+    s_off = lo - pre;
     s_b = b;
   }
   __syncthreads();
-  const Where w{total, ctas, s_before, s_b};
-  __syncthreads();
-  return w;
+  w.left = (cta + 1) * line.total / line.ctas - lo;
+  w.b = s_b;
+  w.request(a);
+  const int64_t seg = s_off / (w.tiles + E);
+  w.skip = static_cast<int>(s_off - seg * (w.tiles + E));
+  w.h = static_cast<int>(seg / w.row_tiles);
+  w.rt = static_cast<int>(seg - static_cast<int64_t>(w.h) * w.row_tiles);
+  return true;
 }
 
 __device__ __forceinline__ uint32_t h2_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -136,81 +194,104 @@ __device__ __forceinline__ float attn_lse(float top, float sum, float held) {
   return sum == 0.0f ? neg_inf() : (top + log2f(sum) - held) * 0.6931471805599453f;
 }
 
-// Merges the partials of the segments that were cut between CTAs: block
-// (row tile, KV head, request).  A warp takes a row; where there are fewer
-// rows than warps, the warps split the row's partials.
-constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
+// The workspace: a header per CTA, then two partials per CTA of R rows, each
+// R D weighted values and R pairs (maximum, sum of weights).  A CTA's stretch
+// may begin within a segment (partial 0) and end within one that it began
+// (partial 1); the header names the latter, with the number of CTAs that hold
+// parts of it (0: none), this CTA's partial 1 and the next ones' partial 0.
+struct __align__(16) CutSegment {
+  int b, h, rt, pieces;
+};
+constexpr int kMaxCtas = 608;  // CTAs of a launch at most: 4 on each of 152 SMs
+constexpr size_t kHeaderBytes = (kMaxCtas * sizeof(CutSegment) + 255) / 256 * 256;
 
-template <int D, int T>
+__host__ __device__ __forceinline__ size_t attn_ws_bytes(int ctas, int R, int D) {
+  return kHeaderBytes + static_cast<size_t>(ctas) * 2 * R * (D + 2) * sizeof(float);
+}
+__device__ __forceinline__ float* attn_part(const AttnArgs& a, int64_t cta, int which, int R, int D) {
+  return reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + kHeaderBytes) + (cta * 2 + which) * (R * (D + 2));
+}
+
+// Merges a cut segment's partials in the order of the positions: block (CTA
+// that began the segment, eight rows).  A warp takes a row; with fewer than
+// eight rows, several warps split the row's partials.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const AttnArgs a, int R, float held) {
   pdl_enter();
   constexpr int per = D / 32;
-  const int b = blockIdx.z, h = blockIdx.y, rt = blockIdx.x;
-  const Req rq = attn_req<T>(a, b, R);
-  if (rt >= rq.row_tiles) return;
-  const Where w0 = attn_where<T, kMergeThreads>(a, R, 0, b);
-  const int64_t s0 = w0.before + (static_cast<int64_t>(h) * rq.row_tiles + rt) * rq.tiles, s1 = s0 + rq.tiles;
-  const int64_t i0 = ((s0 + 1) * w0.ctas - 1) / w0.total, i1 = (s1 * w0.ctas - 1) / w0.total;
-  if (i0 == i1) return;  // one CTA had the whole segment
-  const int pieces = static_cast<int>(i1 - i0) + 1;
-  auto part = [&](int i) {
-    return a.ws + ((i0 + i) * 2 + (i == 0 ? 1 : 0)) * static_cast<int64_t>(R * (D + 2));
-  };
-  const int rows = min(R, rq.nodes * a.G - rt * R);
+  const int4 hdr = __ldg(reinterpret_cast<const int4*>(a.ws) + blockIdx.x);
+  const int b = hdr.x, h = hdr.y, rt = hdr.z, pieces = hdr.w;
+  if (pieces == 0) return;
+  const int first = blockIdx.y * kMergeWarps;
+  const int rows = min(min(R, kv4_nodes(a.num_nodes, b, a.N) * a.G - rt * R) - first, kMergeWarps);
+  if (rows <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool split = rows < kMergeWarps;  // all warps on one row
+  int split = kMergeWarps;  // warps of a row
+  while (split * rows > kMergeWarps) split /= 2;
+  const int mine = warp / split, share = warp % split, r = first + mine;
   __shared__ float s_o[kMergeWarps][D], s_l[kMergeWarps];
-  for (int r = split ? 0 : warp; r < rows; r += split ? 1 : kMergeWarps) {
-    float top = neg_inf();
-    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, part(i)[R * D + 2 * r]);
+  float top = neg_inf(), l = 0.0f, acc[per];
+#pragma unroll
+  for (int j = 0; j < per; ++j) acc[j] = 0.0f;
+  auto part = [&](int i) { return attn_part(a, blockIdx.x + i, i == 0 ? 1 : 0, R, D); };
+  if (mine < rows) {
+    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, __ldg(part(i) + R * D + 2 * r));
     top = warp_max(top);
-    float l = 0.0f, acc[per];
-#pragma unroll
-    for (int j = 0; j < per; ++j) acc[j] = 0.0f;
-    const int first = split ? warp : 0, step = split ? kMergeWarps : 1;
 #pragma unroll 4
-    for (int i = first; i < pieces; i += step) {
+    for (int i = share; i < pieces; i += split) {
       const float* p = part(i);
-      const float pm = p[R * D + 2 * r], pl = p[R * D + 2 * r + 1];
-      const float f = pm == neg_inf() ? 0.0f : fast_exp2(pm - top);
-      l += pl * f;
-#pragma unroll
-      for (int j = 0; j < per; ++j) acc[j] += p[r * D + lane * per + j] * f;
-    }
-    if (split) {
-#pragma unroll
-      for (int j = 0; j < per; ++j) s_o[warp][lane * per + j] = acc[j];
-      if (lane == 0) s_l[warp] = l;
-      __syncthreads();
-      l = 0.0f;
-#pragma unroll
-      for (int j = 0; j < per; ++j) acc[j] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        l += s_l[w];
-#pragma unroll
-        for (int j = 0; j < per; ++j) acc[j] += s_o[w][lane * per + j];
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(p + R * D) + r);
+      float x[per];
+      if (per == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p + r * D) + lane);
+        x[0] = v.x, x[1] = v.y, x[per - 2] = v.z, x[per - 1] = v.w;
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p + r * D) + lane);
+        x[0] = v.x, x[1] = v.y;
       }
-      __syncthreads();
-      if (warp != 0) continue;
+      const float f = ml.x == neg_inf() ? 0.0f : fast_exp2(ml.x - top);
+      l += ml.y * f;
+#pragma unroll
+      for (int j = 0; j < per; ++j) acc[j] += x[j] * f;
     }
-    const float inv = attn_inv(l);
-    const int rw = rt * R + r, n = rw / a.G;
-    const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
-    uint32_t v[per / 2];
-#pragma unroll
-    for (int j = 0; j < per; j += 2)
-      v[j / 2] = f_bf16(acc[j] * inv) | static_cast<uint32_t>(f_bf16(acc[j + 1] * inv)) << 16;
-#pragma unroll
-    for (int j = 0; j < per / 2; ++j) reinterpret_cast<uint32_t*>(a.out + at * D + lane * per)[j] = v[j];
-    if (a.lse && lane == 0) a.lse[at] = attn_lse(top, l, held);
   }
+  if (split > 1) {
+#pragma unroll
+    for (int j = 0; j < per; ++j) s_o[warp][lane * per + j] = acc[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (share != 0) return;
+    for (int w = 1; w < split; ++w) {
+      l += s_l[warp + w];
+#pragma unroll
+      for (int j = 0; j < per; ++j) acc[j] += s_o[warp + w][lane * per + j];
+    }
+  }
+  if (mine >= rows) return;
+  const float inv = attn_inv(l);
+  const int rw = rt * R + r, n = rw / a.G;
+  const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
+  uint32_t v[per / 2];
+#pragma unroll
+  for (int j = 0; j < per; j += 2)
+    v[j / 2] = f_bf16(acc[j] * inv) | static_cast<uint32_t>(f_bf16(acc[j + 1] * inv)) << 16;
+#pragma unroll
+  for (int j = 0; j < per / 2; ++j) reinterpret_cast<uint32_t*>(a.out + at * D + lane * per)[j] = v[j];
+  if (a.lse && lane == 0) a.lse[at] = attn_lse(top, l, held);
+}
+
+template <int D>
+void launch_merge(const AttnArgs& a, int R, float held, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.N) * a.G < R ? static_cast<int64_t>(a.N) * a.G : R;
+  const dim3 grid(static_cast<unsigned>(a.ctas), static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  launch_k(kv4_merge_kernel<D>, grid, kMergeThreads, 0, s, a, R, held);
 }
 
 // Limits of the tensor-memory kernel's launches (kv4_tree.cu) and its entry.
 constexpr int kTreeRows = 128;     // rows of an accumulator
-constexpr int kTreeMaxCtas = 304;  // two on each of 152 SMs
+constexpr int kTreeMaxCtas = 304;  // two on each of 152 SMs (one with two accumulators)
 int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s);
-size_t tree_attention_ws(int64_t rows, int D);
 
 }  // namespace specdec
