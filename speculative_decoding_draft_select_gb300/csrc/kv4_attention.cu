@@ -145,7 +145,7 @@ __device__ void load_q(const AttnArgs& a, AttShared<D, MT>& sh, int b, int h, in
 #pragma unroll
     for (int j = 0; j < per; ++j) x[j] = 0.0f;
     if (r < rows) {
-      const int row = r0 + r, n = row / a.G;
+      const int row = r0 + r, n = attn_node(a, row);
       const uint16_t* src = a.q + (static_cast<int64_t>(b) * a.N + n) * a.q_stride +
                             static_cast<int64_t>(h * a.G + row - n * a.G) * D + lane * per;
       if (per == 4) {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
               const int at = 8 * j + 2 * t + (i & 1), node = p0 + at - rq.start;
               bool see = (there >> at) & 1u;
               if (see && node >= 0) {
-                const int r = mt * 16 + g + 8 * (i >> 1), n = (r0 + r) / a.G;
+                const int r = mt * 16 + g + 8 * (i >> 1), n = attn_node(a, r0 + r);
                 see = r < rows && (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0
                                           : node <= n);
               }
@@ -403,8 +403,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
           continue;
         }
         const float inv = attn_inv(sum);
-        const int rw = r0 + r, n = rw / a.G;
-        const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
+        const int64_t at = attn_row(a, b, h, r0 + r);
         uint2 v;
         v.x = f_bf16(acc.x * inv) | static_cast<uint32_t>(f_bf16(acc.y * inv)) << 16;
         v.y = f_bf16(acc.z * inv) | static_cast<uint32_t>(f_bf16(acc.w * inv)) << 16;
@@ -474,7 +473,8 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
-  AttnArgs a{static_cast<const uint16_t*>(q), q_stride, B, N, Hq, Hkv, Hq / Hkv, static_cast<const uint8_t*>(pool),
+  AttnArgs a{static_cast<const uint16_t*>(q), q_stride, B, N, Hq, Hkv, Hq / Hkv,
+             ((1ull << 40) + Hq / Hkv - 1) / (Hq / Hkv), static_cast<const uint8_t*>(pool),
              num_slots, slot_stride, req_to_token, max_ctx, seq_lens, num_nodes_or_null, tree_mask_or_null,
              scale * kLog2e, static_cast<uint16_t*>(out), lse_or_null, static_cast<float*>(ws), 0, stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -10,6 +10,7 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   int B, N, Hq, Hkv, G;
+  uint64_t g_inv;  // ceil(2^40 / G)
   const uint8_t* pool;
   int64_t num_slots, slot_stride;
   const int32_t* table;
@@ -24,6 +25,18 @@ struct AttnArgs {
   int ctas;  // of the attention launch
   int32_t* stats;
 };
+
+// Row r of a KV head is query head r % G of node r / G.  r < 2^23 and G <= 2^12
+// (both checked by the host), so r times the excess of g_inv G over 2^40 stays
+// below 2^40 / G and the quotient is exact.
+__device__ __forceinline__ int attn_node(const AttnArgs& a, int r) {
+  return static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+}
+// Index of row r of (b, h) in [B, N, Hq].
+__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int b, int h, int r) {
+  const int n = attn_node(a, r);
+  return (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + r - n * a.G;
+}
 
 // Request b: nodes, positions [0, end) of which [start, end) are nodes, tiles
 // of T positions and row tiles of R rows.  A request whose positions do not
@@ -76,9 +89,11 @@ struct Walk {
     nodes = r.nodes, start = r.start, end = r.end, tiles = r.tiles, row_tiles = r.row_tiles, bad = r.bad;
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, Part& p) {
+#pragma unroll 1
     while (left > 0) {
       if (h == a.Hkv) {
         h = 0;
+#pragma unroll 1
         do {
           ++b;
           request(a);
@@ -119,6 +134,7 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk
   const int per = (a.B + THREADS - 1) / THREADS;
   const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
   int64_t incl = mine;
 #pragma unroll
@@ -141,6 +157,7 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk
   const int64_t lo = cta * line.total / line.ctas;
   if (lo >= pre && lo < pre + mine) {
     int b = b0;
+#pragma unroll 1
     for (;; ++b) {
       const int64_t u = attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
       if (lo < pre + u) break;
@@ -271,8 +288,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const AttnArgs
   }
   if (mine >= rows) return;
   const float inv = attn_inv(l);
-  const int rw = rt * R + r, n = rw / a.G;
-  const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + rw - n * a.G;
+  const int64_t at = attn_row(a, b, h, rt * R + r);
   uint32_t v[per / 2];
 #pragma unroll
   for (int j = 0; j < per; j += 2)

@@ -7,11 +7,15 @@
 //   O += P V    128 x D x 128, P from tensor memory, V in shared memory
 // all operands fp16 with fp32 accumulation.  Roles of a CTA:
 //   warps 0 .. 4 MT - 1   softmax: a thread owns one row of an accumulator, so
-//       maximum and sum need no exchange; it also writes the results.
+//       maximum and sum need no exchange; it also writes the results.  The
+//       first warp of an accumulator issues its matrix instructions: its next
+//       step waits for them in any case.
 //   the next 4 MT warps   unpack the cache: codes go from memory through
 //       registers (one tile ahead, whichever segment it belongs to) to swizzled
 //       fp16 slabs; Q likewise.
-//   the last warp         one thread issues the matrix instructions.
+// 16 warps an SM leave each thread 128 registers: with a warp more for the
+// issue (96 registers) the codes read ahead spilled, and a spill waits for
+// its load (64-node trees, B=128: 323 us).
 // With MT = 2 the exponentials of one accumulator run under the products of
 // the other, on one CTA per SM with two stages of K and V; with MT = 1 two
 // CTAs share an SM to the same end.
@@ -44,11 +48,13 @@ struct TreeCfg {
   static constexpr int kStages = MT == 2 ? 2 : 1;
   static constexpr int kSoftThreads = 128 * MT;
   static constexpr int kUnpackThreads = 128 * MT;
-  static constexpr int kThreads = kSoftThreads + kUnpackThreads + 32;
+  static constexpr int kThreads = kSoftThreads + kUnpackThreads;
   static constexpr int kSlabs = D / 64;
   static constexpr int kSlab = kTT * 128;          // bytes: 128 rows of 64 elements
   static constexpr int kOperand = kSlabs * kSlab;  // K, V or one accumulator's Q
-  static constexpr size_t kSmem = static_cast<size_t>(kOperand) * (MT + 2 * kStages) + 1024;
+  // a warp's 32 rows of 64 bytes of results, 16 bytes of padding each
+  static constexpr int kStageRow = 80, kStageWarp = 32 * kStageRow;
+  static constexpr size_t kSmem = static_cast<size_t>(kOperand) * (MT + 2 * kStages) + 4 * MT * kStageWarp + 1024;
   // columns: S of each accumulator, then O of each
   static constexpr uint32_t kCols = MT * 256;
 };
@@ -70,67 +76,108 @@ struct Chunk {
   uint32_t m;
 };
 
-// A thread's row of S, 16 columns at a time with the next 16 on their way:
-// the largest element that `see` shows, and the weights 2^(S c - base) as fp16
-// over S's first columns (column i of P holds positions 2 i and 2 i + 1; it
-// never reaches columns that are still to be read), with their fp32 sum.
-// Rolled to a word of `see` an iteration: unrolled further, the roles' code
-// together falls out of the instruction cache.
-__device__ __forceinline__ uint32_t pick(const uint32_t* v, int i) {
-  return i < 2 ? (i == 0 ? v[0] : v[1]) : (i == 2 ? v[2] : v[3]);
-}
-template <bool MASKED>
-__device__ __forceinline__ float row_max(uint32_t col, const uint32_t* see) {
-  uint32_t x[2][16];
-  float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-  tc::ld16(col, x[0]);
+// Which of the nodes [first, first + 128) this thread's node sees, a bit each
+// (nodes below 0 are context: set; nodes past the request's: clear).  A lane
+// loads the mask bytes of its place in each word for four of the warp's nodes
+// at a time, ballots give the words.  All loads come first and none is behind
+// a condition of its own (a load that is tested where it was issued is a wait
+// each).
+__device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int node, int first, uint32_t* words) {
+  const int lane = threadIdx.x & 31;
+  const int n_lo = __shfl_sync(0xffffffffu, node, 0), n_hi = __shfl_sync(0xffffffffu, node, 31);
+  const uint8_t* mask = a.mask + static_cast<int64_t>(p.b) * a.N * a.N;
+  int nd[4], at[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    nd[w] = first + 32 * w + lane;
+    at[w] = min(max(nd[w], 0), p.nodes - 1);
+  }
 #pragma unroll 1
-  for (int w = 0; w < kTT / 32; ++w) {
-    const uint32_t sw = MASKED ? pick(see, w) : 0;
+  for (int nb = n_lo; nb <= n_hi; nb += 4) {
+    uint8_t on[4][4];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      tc::wait_ld(x[hf]);
-      // the load behind the last one rereads S's first columns
-      tc::ld16(col + ((32 * w + 16 * (hf + 1)) & (kTT - 1)), x[hf ^ 1]);
+    for (int q = 0; q < 4; ++q) {
+      const int n = min(nb + q, n_hi);
+      const uint8_t* row = mask + n * a.N;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float y = __uint_as_float(x[hf][i]);
-        if (MASKED) y = (sw >> (16 * hf + i)) & 1u ? y : neg_inf();
-        m[i & 3] = fmaxf(m[i & 3], y);
+      for (int w = 0; w < 4; ++w) on[q][w] = a.mask ? __ldg(row + at[w]) : static_cast<uint8_t>(at[w] <= n);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, nd[w] < 0 || (nd[w] < p.nodes && on[q][w] != 0));
+        if (nb + q == node) words[w] = bits;
       }
+  }
+}
+
+// A thread's row of S, 32 columns (a word of `see`) at a time with the next 32
+// on their way: the largest element that `see` shows, and the weights
+// 2^(S c - base) as fp16 over S's first columns (column i of P holds positions
+// 2 i and 2 i + 1; it never reaches columns that are still to be read), with
+// their fp32 sum.  Words that every lane sees whole skip the mask.  One form,
+// two words an iteration: the code of all roles has to stay small (at 106 KB
+// instruction fetches were what a tile waited for).
+__device__ __forceinline__ float row_max(uint32_t col, const uint32_t* see) {
+  uint32_t x[2][32];
+  float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+  tc::ld32(col, x[0]);
+#pragma unroll 1
+  for (int w = 0; w < kTT / 32; w += 2) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t sw = w == 0 ? see[q] : see[2 + q];
+      tc::wait_ld32(x[q]);
+      // the load behind the last one rereads S's first columns
+      tc::ld32(col + ((32 * (w + q + 1)) & (kTT - 1)), x[q ^ 1]);
+      if (__any_sync(0xffffffffu, sw != ~0u)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!((sw >> i) & 1u)) x[q][i] = 0xff800000u;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(x[q][i]));
     }
   }
-  tc::wait_ld(x[0]);
+  tc::wait_ld32(x[0]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-template <bool MASKED>
 __device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, float c, float base) {
-  uint32_t x[2][16], y[8];
+  uint32_t x[2][32], y[16];
   const float2 c2 = splat(c), nb2 = splat(-base);
   float2 acc[2] = {splat(0.0f), splat(0.0f)};
-  tc::ld16(col, x[0]);
+  tc::ld32(col, x[0]);
 #pragma unroll 1
-  for (int w = 0; w < kTT / 32; ++w) {
-    const uint32_t sw = MASKED ? pick(see, w) : 0;
+  for (int w = 0; w < kTT / 32; w += 2) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      tc::wait_ld(x[hf]);
-      // behind the last: columns that no P of this loop reaches (16 w + 8 .. < 64)
-      tc::ld16(col + (w == kTT / 32 - 1 && hf == 1 ? kTT - 16 : 32 * w + 16 * (hf + 1)), x[hf ^ 1]);
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t sw = w == 0 ? see[q] : see[2 + q];
+      tc::wait_ld32(x[q]);
+      // behind the last: columns that P does not reach (it ends at 64)
+      tc::ld32(col + min(32 * (w + q + 1), kTT - 32), x[q ^ 1]);
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float2 e = exp2_2(fma2(make_float2(__uint_as_float(x[hf][i]), __uint_as_float(x[hf][i + 1])), c2, nb2));
-        if (MASKED) {
-          e.x = (sw >> (16 * hf + i)) & 1u ? e.x : 0.0f;
-          e.y = (sw >> (16 * hf + i + 1)) & 1u ? e.y : 0.0f;
-        }
+      for (int i = 0; i < 32; i += 2) {
+        const float2 e =
+            exp2_2(fma2(make_float2(__uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1])), c2, nb2));
+        x[q][i] = __float_as_uint(e.x);
+        x[q][i + 1] = __float_as_uint(e.y);
+      }
+      if (__any_sync(0xffffffffu, sw != ~0u)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!((sw >> i) & 1u)) x[q][i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 e = make_float2(__uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
         acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], e);
         y[i / 2] = h2_u32(__floats2half2_rn(e.x, e.y));
       }
-      tc::st8(col + 16 * w + 8 * hf, y);
+      tc::st16(col + 16 * (w + q), y);
     }
   }
-  tc::wait_ld(x[0]);
+  tc::wait_ld32(x[0]);
   const float2 t = add2(acc[0], acc[1]);
   return t.x + t.y;
 }
@@ -146,14 +193,16 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
   uint8_t* sm_q = smem;                       // [MT] operands
   uint8_t* sm_k = sm_q + MT * C::kOperand;    // [S]
   uint8_t* sm_v = sm_k + S * C::kOperand;     // [S]
+  uint8_t* sm_o = sm_v + S * C::kOperand;     // [4 MT] warps' staging
   __shared__ __align__(8) uint64_t q_full[2], k_full[4], v_full[2], k_empty[2], v_empty[2], s_full[MT], p_full[MT],
       o_full[MT], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ uint32_t s_there[4][4];      // positions of the tile that have a slot
   __shared__ float s_c[2][R];             // factor of a row's scores
+  __shared__ uint32_t s_seen[4 * MT][6][32];  // nodes that a thread's node sees
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMmaWarp = C::kThreads / 32 - 1, kUnpackWarp = C::kSoftThreads / 32;
+  constexpr int kUnpackWarp = C::kSoftThreads / 32;
 
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
   if (tid == 0) *cut = CutSegment{0, 0, 0, 0};
@@ -164,8 +213,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&q_full[i], C::kUnpackThreads / 32);
       tc::bar_init(&v_full[i], C::kUnpackThreads / 32);
-      tc::bar_init(&k_empty[i], 1);
-      tc::bar_init(&v_empty[i], 1);
+      tc::bar_init(&k_empty[i], MT);
+      tc::bar_init(&v_empty[i], MT);
     }
     for (int i = 0; i < 4; ++i) tc::bar_init(&k_full[i], C::kUnpackThreads / 32);
     for (int i = 0; i < MT; ++i) {
@@ -173,76 +222,17 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
       tc::bar_init(&p_full[i], 4);
       tc::bar_init(&o_full[i], 1);
     }
-    tc::bar_init(&drain, 1);
+    tc::bar_init(&drain, MT);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) tc::alloc<C::kCols>(&s_tmem);
+  if (warp == 0) tc::alloc<C::kCols>(&s_tmem);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      // the line of tiles: S of tile j + 1 is issued behind O of tile j
-      constexpr uint32_t kIdS = tc::idesc_f16(kTT, false), kIdO = tc::idesc_f16(D, true);
-      Part p;
-      // S of tile j, accumulator m; `fresh`: the tile begins segment `seg`
-      auto issue_s = [&](int64_t j, int m, bool fresh, int seg) {
-        const int st = static_cast<int>(j % S);
-        if (m == 0 && !tc::bar_wait(&k_full[j & 3], (j >> 2) & 1, &s_abort)) return false;
-        if (m == 0 && fresh && !tc::bar_wait(&q_full[seg & 1], (seg >> 1) & 1, &s_abort)) return false;
-        tc::fence_after();
-        const uint32_t qa = tc::smem_addr(sm_q + m * C::kOperand), ka = tc::smem_addr(sm_k + st * C::kOperand);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * C::kSlab + (kk % 4) * 32;
-          tc::mma_ss(tmem + m * kTT, tc::desc(qa + off, 0), tc::desc(ka + off, 0), kIdS, kk != 0 ? 1u : 0u);
-        }
-        tc::commit(&s_full[m]);
-        if (m == MT - 1) tc::commit(&k_empty[st]);
-        return true;
-      };
-      bool ok = walk.next(a, p), begins = true;
-      int seg = 0, tiles = p.t1 - p.t0;
-      for (int m = 0; m < MT && ok; ++m) ok = issue_s(0, m, true, 0);
-      for (int64_t j = 0; ok; ++j) {
-        // tile j + 1, if there is one, is of this segment or begins the next
-        const bool last = --tiles == 0, next = !last || walk.next(a, p);
-        if (last && next) {
-          tiles = p.t1 - p.t0;
-          ++seg;
-        }
-        const int st = static_cast<int>(j % S);
-        for (int m = 0; m < MT && ok; ++m) {
-          ok = tc::bar_wait(&p_full[m], j & 1, &s_abort);
-          if (m == 0) ok = ok && tc::bar_wait(&v_full[j & 1], (j >> 1) & 1, &s_abort);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t va = tc::smem_addr(sm_v + st * C::kOperand);
-#pragma unroll
-          for (int kk = 0; kk < kTT / 16; ++kk)  // a segment's first tile starts O afresh
-            tc::mma_ts(tmem + MT * kTT + m * D, tmem + m * kTT + kk * 8, tc::desc(va + kk * 16 * 128, C::kSlab), kIdO,
-                       (begins && kk == 0) ? 0u : 1u);
-          tc::commit(&o_full[m]);
-          if (m == MT - 1) tc::commit(&v_empty[st]);
-          if (next) {
-            // P lies over S: O has to be done before S is written again
-            ok = tc::bar_wait(&o_full[m], j & 1, &s_abort) && issue_s(j + 1, m, last, seg);
-          }
-        }
-        if (!next) break;
-        begins = last;
-      }
-      // nothing in flight when tensor memory is freed
-      tc::commit(&drain);
-      const long long t0 = clock64();
-      while (!tc::bar_test(&drain, 0) && clock64() - t0 < tc::kWaitCycles) {
-      }
-    }
-    __syncwarp();
-  } else if (warp >= kUnpackWarp) {
+  if (warp >= kUnpackWarp) {
     // ------------------------------------------------------------- unpack
     const int ut = tid - C::kSoftThreads, uw = warp - kUnpackWarp;
     constexpr int UT = C::kUnpackThreads, kStep = UT / CH, kPer = kTT / kStep;  // positions of a thread: kStep apart
@@ -315,13 +305,14 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
     bool ok = true;
     int64_t j = 0;
     int seg = 0;
+#pragma unroll 1
     while (ok && walk.next(a, p)) {
       if (p.bad && p.h == 0 && p.rt == 0 && ut == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
       // Q of the segment: read, then stored once the S of the segment before
       // are done (the wait for a K stage below covers one stage only).  Eight
-      // lanes a row, D / 8 channels a lane, four rows of a lane in flight
+      // lanes a row, D / 8 channels a lane, two rows of a lane in flight
       const int r0 = p.rt * R, rows = min(R, p.nodes * a.G - r0);
-      constexpr int per = D / 8, kBatch = 2 * MT;
+      constexpr int per = D / 8, kBatch = 2;
       const int sub = lane & 7;
 #pragma unroll 1
       for (int rb = uw * 4 + (lane >> 3); rb < R; rb += UT / 8 * kBatch) {
@@ -332,7 +323,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll
           for (int i = 0; i < per / 8; ++i) raw[q][i] = make_uint4(0, 0, 0, 0);
           if (r < rows) {
-            const int rw = r0 + r, n = rw / a.G;
+            const int rw = r0 + r, n = attn_node(a, rw);
             const uint16_t* src = a.q + (static_cast<int64_t>(p.b) * a.N + n) * a.q_stride +
                                   static_cast<int64_t>(p.h * a.G + rw - n * a.G) * D + sub * per;
 #pragma unroll
@@ -372,6 +363,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&q_full[seg & 1]);
 
+#pragma unroll 1
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
         const int st = static_cast<int>(j % S);
         // K: the stage is free once S of tile j - S has been computed
@@ -414,59 +406,79 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
     const int m = warp >> 2;                                     // accumulator
     const int r = m * kTreeRows + (warp & 3) * 32 + lane;        // row of the row tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool issuer = (warp & 3) == 0;
+    constexpr uint32_t kIdS = tc::idesc_f16(kTT, false), kIdO = tc::idesc_f16(D, true);
     const uint32_t s_col = tmem + lanes + m * kTT, o_col = tmem + lanes + MT * kTT + m * D;
+    int seen_b = -1, seen_rt = -1;  // whose words s_seen holds (a thread reads its own only)
     Part p;
     bool ok = true;
     int64_t j = 0;
     int seg = 0;
+#pragma unroll 1
     while (ok && walk.next(a, p)) {
       const int r0 = p.rt * R, rows = min(R, p.nodes * a.G - r0);
       const bool active = r - lane < rows;  // the warp has a row
-      const int node = (r0 + min(r, rows - 1)) / a.G;
+      const int node = attn_node(a, r0 + min(r, rows - 1));
       if (p.t0 == 0 && p.t1 < p.tiles && tid == 0)
         *cut = CutSegment{p.b, p.h, p.rt, line.pieces(static_cast<int>(blockIdx.x), p.tiles, p.t1)};
       ok = wait_warp(&q_full[seg & 1], (seg >> 1) & 1, &s_abort);
       if (!ok) break;
       const float c = s_c[seg & 1][r];
       float top = neg_inf(), sum = 0.0f;  // maximum in use (units of log2), sum of weights
+#pragma unroll 1
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
+        ok = wait_warp(&k_full[j & 3], (j >> 2) & 1, &s_abort);
+        if (issuer) {
+          // S, once K is there and O of the tile before is done: P lies over S
+          if (j > 0) ok = ok && wait_warp(&o_full[m], static_cast<uint32_t>(j - 1) & 1u, &s_abort);
+          if (ok && lane == 0) {
+            tc::fence_after();
+            const uint64_t qd = tc::desc(tc::smem_addr(sm_q + m * C::kOperand), 0);
+            const uint64_t kd = tc::desc(tc::smem_addr(sm_k + static_cast<int>(j % S) * C::kOperand), 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4;  // addresses stay below 2^18
+              tc::mma_ss(tmem + m * kTT, qd + off, kd + off, kIdS, kk != 0 ? 1u : 0u);
+            }
+            tc::commit(&s_full[m]);
+            tc::commit(&k_empty[j % S]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
         const int p0 = tile * kTT;
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        bool masked = false;
         if (active && p0 + kTT > p.start) {
-          // positions of nodes: bit i of word w is position p0 + 32 w + i, the
-          // node that less start.  A lane loads the mask byte of its position
-          // for four of the warp's nodes at a time, ballots give their words
-          masked = true;
-          const int n_lo = __shfl_sync(0xffffffffu, node, 0), n_hi = __shfl_sync(0xffffffffu, node, 31);
-          for (int nb = n_lo; nb <= n_hi; nb += 4) {
-            bool on[4][4];
+          const int shift = p0 - p.start;  // node of the tile's first position
+          const bool keep = a.N <= kTT;    // then the words of all nodes serve every head of the request
+          if (!keep || p.b != seen_b || p.rt != seen_rt) {
+            node_words(a, p, node, keep ? 0 : shift, see);
+            seen_b = p.b;
+            seen_rt = p.rt;
+            if (keep) {
+              // a word of context before the nodes' four, one of nothing behind
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+              for (int w = 0; w < 4; ++w) s_seen[warp][w + 1][lane] = see[w];
+              s_seen[warp][0][lane] = ~0u;
+              s_seen[warp][5][lane] = 0u;
+            }
+          }
+          if (keep) {
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const int nd = p0 + 32 * w + lane - p.start, n = min(nb + q, n_hi);
-                on[q][w] = nd < 0;
-                if (nd >= 0 && nd < p.nodes)
-                  on[q][w] = a.mask ? __ldg(a.mask + (static_cast<int64_t>(p.b) * a.N + n) * a.N + nd) != 0 : nd <= n;
-              }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const uint32_t bits = __ballot_sync(0xffffffffu, on[q][w]);
-                if (nb + q == node) see[w] = bits;
-              }
+            for (int w = 0; w < 4; ++w) {
+              const int i = (shift >> 5) + w + 1;
+              see[w] = __funnelshift_r(s_seen[warp][min(max(i, 0), 5)][lane], s_seen[warp][min(max(i + 1, 0), 5)][lane],
+                                       shift & 31);
+            }
           }
         }
-        ok = wait_warp(&k_full[j & 3], (j >> 2) & 1, &s_abort) && wait_warp(&s_full[m], j & 1, &s_abort);
+        ok = wait_warp(&s_full[m], j & 1, &s_abort);
         if (!ok) break;
         tc::fence_after();
         if (active) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) see[i] &= s_there[j & 3][i];
-          masked = masked || (see[0] & see[1] & see[2] & see[3]) != ~0u;  // missing slots are the same in every lane
-          float mx = masked ? row_max<true>(s_col, see) : row_max<false>(s_col, see);
+          float mx = row_max(s_col, see);
           mx = mx == neg_inf() ? mx : mx * c;
           const bool grow = mx > top + kLagExp || (top == neg_inf() && mx > top);
           if (__any_sync(0xffffffffu, grow)) {
@@ -486,12 +498,27 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
             }
           }
           const float base = (top == neg_inf() ? 0.0f : top) - kHeldExp;
-          sum += masked ? row_weights<true>(s_col, see, c, base) : row_weights<false>(s_col, see, c, base);
+          sum += row_weights(s_col, see, c, base);
           tc::wait_st();
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&p_full[m]);
+        if (issuer) {
+          ok = wait_warp(&p_full[m], j & 1, &s_abort) && wait_warp(&v_full[j & 1], (j >> 1) & 1, &s_abort);
+          if (!ok) break;
+          if (lane == 0) {
+            tc::fence_after();
+            const uint64_t vd = tc::desc(tc::smem_addr(sm_v + static_cast<int>(j % S) * C::kOperand), C::kSlab);
+#pragma unroll
+            for (int kk = 0; kk < kTT / 16; ++kk)  // a part's first tile starts O afresh
+              tc::mma_ts(tmem + MT * kTT + m * D, tmem + m * kTT + kk * 8, vd + (kk * 16 * 128 >> 4), kIdO,
+                         (tile == p.t0 && kk == 0) ? 0u : 1u);
+            tc::commit(&o_full[m]);
+            tc::commit(&v_empty[j % S]);
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
       // the segment's part is done: its last O
@@ -499,48 +526,73 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
       if (!ok) break;
       tc::fence_after();
       if (active) {
-        const int rw = r0 + r, n = rw / a.G;
-        const int64_t at = (static_cast<int64_t>(p.b) * a.N + n) * a.Hq + p.h * a.G + rw - n * a.G;
         float* part = attn_part(a, blockIdx.x, p.t0 > 0 ? 0 : 1, R, D);
         const float inv = attn_inv(sum);
+        // 64 bytes of every row at a time through shared memory, so that four
+        // lanes store them together: a lane that stores its own row touches 32
+        // lines an instruction (8.5k cycles a segment instead of 2k)
+        uint8_t* stage = sm_o + warp * C::kStageWarp;
+        const int cols = p.complete() ? 32 : 16;
+        char* base = reinterpret_cast<char*>(p.complete() ? static_cast<void*>(a.out) : static_cast<void*>(part));
+        int64_t to[4];  // where this lane's 16 bytes of the rows 8 i + lane / 4 go
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = r - lane + 8 * i + (lane >> 2);
+          to[i] = (p.complete() ? attn_row(a, p.b, p.h, r0 + rr) * (D * 2) : static_cast<int64_t>(rr) * (D * 4)) + 16 * (lane & 3);
+        }
 #pragma unroll 1
-        for (int w = 0; w < D / 16; ++w) {
+        for (int w = 0; w < D / cols; ++w) {
           uint32_t x[16];
-          tc::ld16(o_col + 16 * w, x);
-          tc::wait_ld(x);
-          if (r < rows && p.complete()) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 16 * w);
+          if (p.complete()) {
+            uint32_t y[32];
+            tc::ld32(o_col + 32 * w, y);
+            tc::wait_ld32(y);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t y[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                y[q] = f_bf16(__uint_as_float(x[8 * i + 2 * q]) * inv) |
-                       static_cast<uint32_t>(f_bf16(__uint_as_float(x[8 * i + 2 * q + 1]) * inv)) << 16;
-              dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          } else if (r < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(part + r * D + 16 * w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 16; ++i)
+              x[i] = f_bf16(__uint_as_float(y[2 * i]) * inv) |
+                     static_cast<uint32_t>(f_bf16(__uint_as_float(y[2 * i + 1]) * inv)) << 16;
+          } else {
+            tc::ld16(o_col + 16 * w, x);
+            tc::wait_ld(x);
           }
-          __syncwarp();  // the next load is warp-wide
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stage + lane * C::kStageRow + 16 * i) =
+                make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int lr = 8 * i + (lane >> 2);  // row of the warp
+            if (r - lane + lr < rows) {
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + lr * C::kStageRow + 16 * (lane & 3));
+              *reinterpret_cast<uint4*>(base + (i == 0 ? to[0] : i == 1 ? to[1] : i == 2 ? to[2] : to[3]) + 64 * w) = v;
+            }
+          }
+          __syncwarp();
         }
         if (r < rows) {
           if (!p.complete()) {
             part[R * D + 2 * r] = top;
             part[R * D + 2 * r + 1] = sum;
           } else if (a.lse) {
-            a.lse[at] = attn_lse(top, sum, kHeldExp);
+            a.lse[attn_row(a, p.b, p.h, r0 + r)] = attn_lse(top, sum, kHeldExp);
           }
         }
       }
       ++seg;
     }
+    if (issuer && lane == 0) {
+      // nothing in flight when tensor memory is freed
+      tc::commit(&drain);
+      const long long t0 = clock64();
+      while (!tc::bar_test(&drain, 0) && clock64() - t0 < tc::kWaitCycles) {
+      }
+    }
+    __syncwarp();
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     tc::fence_after();
     tc::dealloc<C::kCols>(tmem);
   }
