@@ -38,6 +38,12 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int b, int h, int
   return (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + r - n * a.G;
 }
 
+// Element of q where row r of (b, h) begins.
+__device__ __forceinline__ int64_t attn_q(const AttnArgs& a, int b, int h, int r, int D) {
+  const int n = attn_node(a, r);
+  return (static_cast<int64_t>(b) * a.N + n) * a.q_stride + static_cast<int64_t>(h * a.G + r - n * a.G) * D;
+}
+
 // Request b: nodes, positions [0, end) of which [start, end) are nodes, tiles
 // of T positions and row tiles of R rows.  A request whose positions do not
 // fit the table has no positions (its rows get zeros) and one empty tile.

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
   uint8_t* sm_v = sm_k + S * C::kOperand;     // [S]
   uint8_t* sm_o = sm_v + S * C::kOperand;     // [4 MT] warps' staging
   __shared__ __align__(8) uint64_t q_full[2], k_full[4], v_full[2], k_empty[2], v_empty[2], s_full[MT], p_full[MT],
-      o_full[MT], drain;
+      o_full[MT], turn[MT], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ uint32_t s_there[4][4];      // positions of the tile that have a slot
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
       tc::bar_init(&s_full[i], 1);
       tc::bar_init(&p_full[i], 4);
       tc::bar_init(&o_full[i], 1);
+      tc::bar_init(&turn[i], 4);
     }
     tc::bar_init(&drain, MT);
     s_abort = 0;
@@ -473,6 +474,10 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
           }
         }
         ok = wait_warp(&s_full[m], j & 1, &s_abort);
+        // the accumulators take turns: in step with one another both would
+        // wait for the exponentials and then both for the products
+        if (MT == 2 && (m == 1 || j > 0))
+          ok = ok && wait_warp(&turn[m], static_cast<uint32_t>(m == 1 ? j : j - 1) & 1u, &s_abort);
         if (!ok) break;
         tc::fence_after();
         if (active) {
@@ -503,7 +508,10 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(&p_full[m]);
+        if (lane == 0) {
+          tc::bar_arrive(&p_full[m]);
+          if (MT == 2) tc::bar_arrive(&turn[(m + 1) % MT]);
+        }
         if (issuer) {
           ok = wait_warp(&p_full[m], j & 1, &s_abort) && wait_warp(&v_full[j & 1], (j >> 1) & 1, &s_abort);
           if (!ok) break;
