@@ -70,6 +70,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* a
   return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, abort));
 }
 
+__device__ __forceinline__ uint32_t word_of4(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 // A group of 32 channels: codes and their (step, lo).
 struct Chunk {
   uint4 c;
@@ -309,60 +313,67 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll 1
     while (ok && walk.next(a, p)) {
       if (p.bad && p.h == 0 && p.rt == 0 && ut == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-      // Q of the segment: read, then stored once the S of the segment before
-      // are done (the wait for a K stage below covers one stage only).  Eight
-      // lanes a row, D / 8 channels a lane, two rows of a lane in flight
+      // Q of the segment, behind its first K and once the S of the segment
+      // before are done: all rows are copied as they are to where they belong,
+      // then each lane turns its own bytes into fp16 in place (eight lanes a
+      // row, D / 8 channels a lane).  The rows are on their way to the L2 cache
+      // before
       const int r0 = p.rt * R, rows = min(R, p.nodes * a.G - r0);
-      constexpr int per = D / 8, kBatch = 2;
-      const int sub = lane & 7;
+      constexpr int per = D / 8;
+      const int sub = lane & 7, q_row = uw * 4 + (lane >> 3);
+      if ((sub & 3) == 0)
 #pragma unroll 1
-      for (int rb = uw * 4 + (lane >> 3); rb < R; rb += UT / 8 * kBatch) {
-        uint4 raw[kBatch][per / 8];
+        for (int r = q_row; r < rows; r += UT / 8)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + attn_q(a, p.b, p.h, r0 + r, D) + sub * per));
+      auto q_unit = [&](int r, int i) {
+        const int ch = sub * per + 8 * i, rr = r % kTreeRows;
+        return reinterpret_cast<uint4*>(sm_q + (r / kTreeRows) * C::kOperand + (ch / 64) * C::kSlab + rr * 128 +
+                                        (((ch % 64 / 8) ^ (rr & 7)) << 4));
+      };
+      auto store_q = [&]() {
+#pragma unroll 2
+        for (int r = q_row; r < R; r += UT / 8) {
+          const uint16_t* src = a.q + attn_q(a, p.b, p.h, r0 + min(r, rows - 1), D) + sub * per;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int r = rb + q * (UT / 8);
-#pragma unroll
-          for (int i = 0; i < per / 8; ++i) raw[q][i] = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int rw = r0 + r, n = attn_node(a, rw);
-            const uint16_t* src = a.q + (static_cast<int64_t>(p.b) * a.N + n) * a.q_stride +
-                                  static_cast<int64_t>(p.h * a.G + rw - n * a.G) * D + sub * per;
-#pragma unroll
-            for (int i = 0; i < per / 8; ++i) raw[q][i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-          }
+          for (int i = 0; i < per / 8; ++i) cp_async16(q_unit(r, i), src + 8 * i, r < rows ? 16 : 0);
         }
-        if (rb < UT / 8 && j > 0)
-          for (int m = 0; m < MT && ok; ++m) ok = wait_warp(&s_full[m], (j - 1) & 1, &s_abort);
-        if (!ok) break;
+        cp_async_commit();
+        cp_async_wait<0>();
+#pragma unroll 2
+        for (int r = q_row; r < R; r += UT / 8) {
+          // the largest magnitude: bf16 bits without the sign compare as integers
+          uint32_t big = 0;
+          uint4 raw[per / 8];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int r = rb + q * (UT / 8);
-          float x[per], mx = 0.0f;
+          for (int i = 0; i < per / 8; ++i) {
+            raw[i] = *q_unit(r, i);
 #pragma unroll
-          for (int i = 0; i < per / 8; ++i) unpack<SPEC_BF16>(raw[q][i], x + 8 * i);
+            for (int z = 0; z < 4; ++z) big = __vmaxu2(big, word_of4(raw[i], z) & 0x7fff7fffu);
+          }
 #pragma unroll
-          for (int i = 0; i < per; ++i) mx = fmaxf(mx, fabsf(x[i]));
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = max(mx > 0.0f && isfinite(mx) ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0, -126);
+          for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+          const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
+          // 2^e <= max < 2^(e + 1); zeros, and rows with an infinity or NaN, are
+          // taken as they are
+          const int e = bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -126);
           // the sign of the scale goes into q, so that a larger S is a larger score
           const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), a.scale_log2);
           if (sub == 0) s_c[seg & 1][r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-          uint8_t* op = sm_q + (r / kTreeRows) * C::kOperand;
 #pragma unroll
-          for (int i = 0; i < per; i += 8) {
-            const int ch = sub * per + i;
+          for (int i = 0; i < per / 8; ++i) {
             uint32_t y[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) y[z] = h2_u32(__floats2half2_rn(x[i + 2 * z] * down, x[i + 2 * z + 1] * down));
-            put_unit(op + (ch / 64) * C::kSlab, r % kTreeRows, (ch % 64) / 8, y);
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t w = word_of4(raw[i], z);
+              y[z] = h2_u32(__floats2half2_rn(bf16_lo(w) * down, bf16_hi(w) * down));
+            }
+            *q_unit(r, i) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
-      }
-      if (!ok) break;
-      tc::fence_smem();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&q_full[seg & 1]);
+        tc::fence_smem();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&q_full[seg & 1]);
+      };
 
 #pragma unroll 1
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
@@ -374,21 +385,31 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         for (int i = 0; i < kPer; ++i) unpack_to(sm_k + st * C::kOperand, k[i], p_of + i * kStep);
         // which of this warp's positions have a slot: 32 / CH in a row from
         // uw 32 / CH + i kStep on, CH lanes each
+        const bool all = __all_sync(0xffffffffu, have == (1u << kPer) - 1u);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const unsigned bal = __ballot_sync(0xffffffffu, (have >> i) & 1u);
-          if (lane == 0) {
-            uint32_t bits = 0;
-#pragma unroll
+          uint32_t bits = (1u << (32 / CH)) - 1u;
+          if (!all) {
+            const unsigned bal = __ballot_sync(0xffffffffu, (have >> i) & 1u);
+            bits = 0;
+#pragma unroll 1
             for (int q = 0; q < 32 / CH; ++q) bits |= ((bal >> (q * CH)) & 1u) << q;
+          }
+          if (lane == 0) {
             uint8_t* to = reinterpret_cast<uint8_t*>(s_there[j & 3]) + (uw * (32 / CH) + i * kStep) / 8;
-            to[0] = static_cast<uint8_t>(bits);
-            if (CH == 2) to[1] = static_cast<uint8_t>(bits >> 8);
+            if (CH == 4) *to = static_cast<uint8_t>(bits);
+            else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(bits);
           }
         }
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&k_full[j & 3]);
+        if (tile == p.t0) {
+          if (j > 0)
+            for (int m = 0; m < MT && ok; ++m) ok = wait_warp(&s_full[m], (j - 1) & 1, &s_abort);
+          if (!ok) break;
+          store_q();
+        }
         // V: free once O of tile j - S has been computed
         if (j >= S) ok = wait_warp(&v_empty[st], static_cast<uint32_t>(j / S - 1) & 1u, &s_abort);
         if (!ok) break;
