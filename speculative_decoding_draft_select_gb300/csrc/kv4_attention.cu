@@ -56,81 +56,52 @@ struct Vec<4> {
   using type = uint32_t;
 };
 
-template <class T>
-__device__ __forceinline__ T ld_code(const uint8_t* p) {
-  return __ldg(reinterpret_cast<const T*>(p));
-}
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 __device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
 __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
-__device__ __forceinline__ void zero(uint4& v) { v = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void zero(uint2& v) { v = make_uint2(0, 0); }
-__device__ __forceinline__ void zero(uint32_t& v) { v = 0; }
 
-// The codes a lane holds of its warp's 16 positions.  With t = lane % 4 and
-// g = lane / 4: of positions g and g + 8 the D/4 channels of K from t D/4 on
-// (the lane's share of the B fragments of q k^T, whose order of channels is
-// free); of positions 2t, 2t + 1, 2t + 8, 2t + 9 the D/8 channels of V from
-// g D/8 on (its share of the B fragments of w v: channel g D/8 + i is column
-// g of block i).  So every code goes from memory to its lane's registers
-// and no shared memory is needed; quads (K) and octets (V) of lanes read the
-// 64 contiguous bytes of a head row.
+// A warp's 16 positions of a tile in shared memory: a stage of a ring that
+// only this warp fills (asynchronous copies of 16 bytes, a position's bytes by
+// neighbouring lanes) and reads.  With t = lane % 4 and g = lane / 4 a lane
+// reads, of positions g and g + 8, the D/4 channels of K from t D/4 on (its
+// share of the B fragments of q k^T, whose order of channels is free), and of
+// positions 2t, 2t + 1, 2t + 8, 2t + 9 the D/8 channels of V from g D/8 on (its
+// share of the B fragments of w v: channel g D/8 + i is column g of block i).
+// K's codes lie 16 words a position apart and V's with their (step, lo) 20
+// (D = 64: 8 and 12), which makes every read free of bank conflicts.
 template <int D>
-struct Raw {
-  typename Vec<D / 8>::type k[2];
-  typename Vec<D / 16>::type v[4];
-  uint32_t km[2], vm[4];
+struct Stage {
+  static constexpr int kChunks = kv4_head_bytes(D) / 16;        // of a position
+  static constexpr int kVRow = D == 128 ? 80 : 48;              // D = 64: with K's (step, lo) too
+  static constexpr int kKMeta = D == 128 ? 16 * 64 : 16 * 32 + 32;
+  static constexpr int kV = D == 128 ? 16 * 80 : 16 * 32;       // V's first byte
+  static constexpr int kBytes = 16 * kv4_head_bytes(D);
+  // where chunk c of position pos goes
+  __device__ __forceinline__ static int place(int pos, int c) {
+    constexpr int kk = D / 32;  // chunks of K's codes, and of V's
+    if (c < kk) return pos * (D / 2) + c * 16;
+    if (c < 2 * kk) return kV + pos * kVRow + (c - kk) * 16;
+    if (D == 128 && c == 2 * kk) return kKMeta + pos * 16;
+    return kV + pos * kVRow + D / 2;
+  }
 };
+constexpr int kRing = 4;  // stages of a warp
 
-// The slot of position p (lanes 0..15 of a warp), -1 when there is none.
-__device__ __forceinline__ int attn_slot(const AttnArgs& a, const int32_t* row, int p, int end, bool count) {
-  if (p >= end) return -1;
-  const int32_t s = __ldg(row + p);
-  if (s >= 0 && s < a.num_slots) return s;
-  if (count) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-  return -1;
-}
-
-template <int D>
-__device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* head, int64_t slot_stride, int slot, int lane) {
-  const int t = lane & 3, g = lane >> 2;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int s = __shfl_sync(0xffffffffu, slot, g + 8 * j);
-    zero(r.k[j]);
-    r.km[j] = 0;
-    if (s >= 0) {
-      const uint8_t* p = head + s * slot_stride;
-      r.k[j] = ld_code<typename Vec<D / 8>::type>(p + t * (D / 8));
-      r.km[j] = __ldg(reinterpret_cast<const uint32_t*>(p + D + (t * (D / 4) / kKv4Group) * 4));
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int s = __shfl_sync(0xffffffffu, slot, 2 * t + (j & 1) + 8 * (j >> 1));
-    zero(r.v[j]);
-    r.vm[j] = 0;
-    if (s >= 0) {
-      const uint8_t* p = head + s * slot_stride;
-      r.v[j] = ld_code<typename Vec<D / 16>::type>(p + D / 2 + g * (D / 16));
-      r.vm[j] = __ldg(reinterpret_cast<const uint32_t*>(p + D + D / 8 + (g * (D / 8) / kKv4Group) * 4));
-    }
-  }
-}
-
-// Shared memory of a CTA: q in the order of the A fragments, the warps' row
-// statistics, and the warps' weighted values of 16 rows at a time (rows 16
-// floats longer than D and 4 floats of padding per 32 channels, so the
-// fragment's stores spread over the banks).
+// Shared memory of a CTA: the warps' rings, q in the order of the A fragments,
+// the warps' row statistics, and the weighted values of two warps' 16 rows at
+// a time (rows 16 floats longer than D and 4 floats of padding per 32
+// channels, so the fragment's stores spread over the banks).
 template <int D, int MT>
 struct AttShared {
   static constexpr int kRow = D + 16;
+  uint8_t ring[kAttWarps][kRing][Stage<D>::kBytes];
   uint4 q[MT][D / 16][32];
   float c[16 * MT];  // factor of a row's scores
   float m[kAttWarps][16 * MT], l[kAttWarps][16 * MT];
-  float o[kAttWarps][16][kRow];
+  unsigned there[kAttWarps][kRing];  // positions of a stage that have a slot
+  float o[2][16][kRow];
 };
 
 __device__ __forceinline__ int padded(int ch) { return ch + (ch >> 5) * 4; }
@@ -180,10 +151,12 @@ __device__ void load_q(const AttnArgs& a, AttShared<D, MT>& sh, int b, int h, in
   }
 }
 
-template <int D, int MT>
+// EIGHT: no row past the eighth; the upper half of the fragments is not worked.
+template <int D, int MT, bool EIGHT>
 __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_kernel(const AttnArgs a) {
   pdl_enter();
-  constexpr int R = 16 * MT;
+  constexpr int R = 16 * MT, H = EIGHT ? 1 : 2;  // halves of a fragment's rows
+  using St = Stage<D>;
   extern __shared__ __align__(16) unsigned char att_sm[];
   AttShared<D, MT>& sh = *reinterpret_cast<AttShared<D, MT>*>(att_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
@@ -193,7 +166,68 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
   Line line;
   Walk<kTile, kEnds, R> walk;
   if (!attn_stretch<kTile, kEnds, R, kAttThreads>(a, line, walk)) return;
+
+  // the cursor that reads ahead, across segments: slots kRing + 1 tiles before
+  // their use, codes kRing
+  auto ahead = walk;
+  Part ap;
+  bool more = ahead.next(a, ap);
+  int next_tile = ap.t0;
+  int32_t slot = -2;  // of position warp * 16 + lane % 16; -2: no position
+  const uint8_t* head = nullptr;
+  bool count = false, loaded = false;
+  auto load_slot = [&]() {
+    loaded = more;
+    if (!more) return;
+    const int pos = next_tile * kTile + warp * 16 + (lane & 15);
+    head = a.pool + static_cast<int64_t>(ap.h) * kv4_head_bytes(D);
+    count = ap.h == 0 && ap.rt == 0 && lane < 16;
+    slot = pos < ap.end ? __ldg(a.table + static_cast<int64_t>(ap.b) * a.max_ctx + pos) : -2;
+    if (++next_tile == ap.t1) {
+      more = ahead.next(a, ap);
+      next_tile = ap.t0;
+    }
+  };
+  constexpr int kCopies = (16 * St::kChunks + 31) / 32;
+  uint32_t plan[kCopies];  // of a copy: position, chunk, place in the stage
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int id = min(lane + 32 * i, 16 * St::kChunks - 1), pos = id / St::kChunks, c = id - pos * St::kChunks;
+    plan[i] = pos | c << 8 | St::place(pos, c) << 16;
+  }
+  const unsigned ring = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp][0]));
+  auto copy_codes = [&](int st) {  // one commit group, empty behind the line's end
+    if (loaded) {
+      const bool ok = slot >= 0 && slot < a.num_slots;
+      if (!ok && slot != -2 && count) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      const unsigned there = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      if (lane == 0) sh.there[warp][st] = there;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int pos = plan[i] & 255;
+        const int32_t sl = __shfl_sync(0xffffffffu, slot, pos);
+        const bool have = (there >> pos) & 1u;
+        if (32 * (i + 1) <= 16 * St::kChunks || lane + 32 * i < 16 * St::kChunks) {
+          // a position without a slot is zeroed: its weights are zero, its values must not be NaN
+          const uint8_t* src = head + (have ? sl : 0) * a.slot_stride + ((plan[i] >> 8) & 255) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + st * St::kBytes + (plan[i] >> 16)),
+                       "l"(src), "r"(have ? 16 : 0)
+                       : "memory");
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  load_slot();
+#pragma unroll 1
+  for (int i = 0; i < kRing - 1; ++i) {
+    copy_codes(i);
+    load_slot();
+  }
+  int st = 0;  // stage of the tile at hand
+
   Part rq;
+#pragma unroll 1
   while (walk.next(a, rq)) {
     const int b = rq.b, h = rq.h, rt = rq.rt, t0 = rq.t0, t1 = rq.t1;
     const int r0 = rt * R, rows = min(R, rq.nodes * a.G - r0);
@@ -201,11 +235,11 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
 
     load_q<D, MT>(a, sh, b, h, r0, rows);
     __syncthreads();
-    float cr[MT][2], m[MT][2], l[MT][2], o[MT][D / 8][4];
+    float cr[MT][H], m[MT][H], l[MT][H], o[MT][D / 8][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < H; ++i) {
         cr[mt][i] = sh.c[mt * 16 + g + 8 * i];
         m[mt][i] = neg_inf();
         l[mt][i] = 0.0f;
@@ -217,24 +251,18 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[mt][i][j] = 0.0f;
 
-    const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_ctx;
-    const uint8_t* head = a.pool + static_cast<int64_t>(h) * kv4_head_bytes(D);
-    const bool count = h == 0 && rt == 0 && lane < 16;
-    // positions of this warp: [tile * 64 + warp * 16, + 16); slots are read
-    // two tiles ahead of their use, codes one tile ahead
-    auto slot_at = [&](int tile) {
-      return tile < t1 ? attn_slot(a, row, tile * kTile + warp * 16 + (lane & 15), rq.end, count) : -1;
-    };
-    int slot = slot_at(t0), slot_next = slot_at(t0 + 1);
-    Raw<D> raw;
-    load_raw<D>(raw, head, a.slot_stride, slot, lane);
+#pragma unroll 1
     for (int tile = t0; tile < t1; ++tile) {
-      const unsigned there = __ballot_sync(0xffffffffu, slot >= 0);  // bit i: position i of the 16
-      const Raw<D> cur = raw;
-      load_raw<D>(raw, head, a.slot_stride, slot_next, lane);
-      slot = slot_next;
-      slot_next = slot_at(tile + 2);
-      if ((there & 0xffffu) == 0) continue;
+      // the stage that the tile before used is free: every lane has read it
+      __syncwarp();
+      copy_codes((st + kRing - 1) % kRing);
+      load_slot();
+      cp_async_wait<kRing - 1>();
+      __syncwarp();  // every lane's copies of this tile have landed
+      const uint8_t* s8 = sh.ring[warp][st];
+      const unsigned there = sh.there[warp][st];
+      st = (st + 1) % kRing;
+      if (there == 0) continue;
       float s[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -242,12 +270,21 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[mt][j][i] = 0.0f;
+      typename Vec<D / 8>::type kc[2];
+      uint32_t km[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pos = g + 8 * j;
+        kc[j] = *reinterpret_cast<const typename Vec<D / 8>::type*>(s8 + pos * (D / 2) + t * (D / 8));
+        km[j] = *reinterpret_cast<const uint32_t*>(
+            s8 + (D == 128 ? St::kKMeta + pos * 16 + t * 4 : St::kV + pos * St::kVRow + D / 2 + (t >> 1) * 4));
+      }
 #pragma unroll
       for (int wd = 0; wd < D / 32; ++wd) {  // words of 8 channels: two steps of 16 (4 channels a lane)
         uint32_t kv[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          dequant4(word_of(cur.k[j], wd), __byte_perm(cur.km[j], 0, 0x1010), __byte_perm(cur.km[j], 0, 0x3232), kv[j]);
+          dequant4(word_of(kc[j], wd), __byte_perm(km[j], 0, 0x1010), __byte_perm(km[j], 0, 0x3232), kv[j]);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -260,15 +297,20 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
       // scores in units of log2, masked; s[..][j][i]: row g + 8 (i / 2),
       // position 8 j + 2 t + i % 2
       const int p0 = tile * kTile + warp * 16;
-      const bool whole = (there & 0xffffu) == 0xffffu && p0 + 16 <= rq.start;
+      const bool whole = there == 0xffffu && p0 + 16 <= rq.start;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[mt][j][i] *= cr[mt][i >> 1];
-            if (!whole) {
+          for (int i = 0; i < 2 * H; ++i) s[mt][j][i] *= cr[mt][i >> 1];
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2 * H; ++i) {
               const int at = 8 * j + 2 * t + (i & 1), node = p0 + at - rq.start;
               bool see = (there >> at) & 1u;
               if (see && node >= 0) {
@@ -278,14 +320,14 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
               }
               if (!see) s[mt][j][i] = neg_inf();
             }
-          }
+      }
       uint4 pa[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float mn[2], al[2];
+        float mn[H], al[H];
         bool up = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < H; ++i) {
           float x = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -298,29 +340,36 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
         }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[mt][i][0] *= al[0];
-            o[mt][i][1] *= al[0];
-            o[mt][i][2] *= al[1];
-            o[mt][i][3] *= al[1];
-          }
-          l[mt][0] *= al[0];
-          l[mt][1] *= al[1];
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * H; ++e) o[mt][i][e] *= al[e >> 1];
+#pragma unroll
+          for (int i = 0; i < H; ++i) l[mt][i] *= al[i];
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2 * H; ++i) {
             s[mt][j][i] = fast_exp2(s[mt][j][i] - mn[i >> 1]);
             l[mt][i >> 1] += s[mt][j][i];
           }
-        pa[mt] = make_uint4(h2_u32(__floats2half2_rn(s[mt][0][0], s[mt][0][1])),
-                            h2_u32(__floats2half2_rn(s[mt][0][2], s[mt][0][3])),
-                            h2_u32(__floats2half2_rn(s[mt][1][0], s[mt][1][1])),
-                            h2_u32(__floats2half2_rn(s[mt][1][2], s[mt][1][3])));
+        pa[mt] = make_uint4(h2_u32(__floats2half2_rn(s[mt][0][0], s[mt][0][1])), 0u,
+                            h2_u32(__floats2half2_rn(s[mt][1][0], s[mt][1][1])), 0u);
+        if (!EIGHT) {
+          pa[mt].y = h2_u32(__floats2half2_rn(s[mt][0][2], s[mt][0][3]));
+          pa[mt].w = h2_u32(__floats2half2_rn(s[mt][1][2], s[mt][1][3]));
+        }
       }
-      const uint32_t st0 = __byte_perm(cur.vm[0], cur.vm[1], 0x5410), lo0 = __byte_perm(cur.vm[0], cur.vm[1], 0x7632);
-      const uint32_t st1 = __byte_perm(cur.vm[2], cur.vm[3], 0x5410), lo1 = __byte_perm(cur.vm[2], cur.vm[3], 0x7632);
+      typename Vec<D / 16>::type vc[4];
+      uint32_t vm[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* row = s8 + St::kV + (2 * t + (j & 1) + 8 * (j >> 1)) * St::kVRow;
+        vc[j] = *reinterpret_cast<const typename Vec<D / 16>::type*>(row + g * (D / 16));
+        vm[j] = *reinterpret_cast<const uint32_t*>(row + (D == 128 ? 64 + (g >> 1) * 4 : 40 + (g >> 2) * 4));
+      }
+      const uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
+      const uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
 #pragma unroll
       for (int wd = 0; wd < D / 64; ++wd) {
         // even channels of a word lie in its low half, odd ones in its high
@@ -329,8 +378,8 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
         for (int odd = 0; odd < 2; ++odd) {
           const uint32_t sel = odd ? 0x7632u : 0x5410u;
           uint32_t v0[4], v1[4];
-          dequant4(__byte_perm(word_of(cur.v[0], wd), word_of(cur.v[1], wd), sel), st0, lo0, v0);
-          dequant4(__byte_perm(word_of(cur.v[2], wd), word_of(cur.v[3], wd), sel), st1, lo1, v1);
+          dequant4(__byte_perm(word_of(vc[0], wd), word_of(vc[1], wd), sel), st0, lo0, v0);
+          dequant4(__byte_perm(word_of(vc[2], wd), word_of(vc[3], wd), sel), st1, lo1, v1);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -339,7 +388,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
       }
     }
 
-    // merge the warps
+    // merge the warps: 2 and 3 hand their values to 0 and 1, then 1 to 0's place
     const bool complete = rq.complete();
     float* part = attn_part(a, blockIdx.x, t0 > 0 ? 0 : 1, R, D);
     if (t0 == 0 && t1 < rq.tiles && threadIdx.x == 0)
@@ -347,7 +396,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < H; ++i) {
         float x = l[mt][i];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
@@ -359,41 +408,50 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
     __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      if (mt > 0) __syncthreads();
+      float f[H];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < H; ++i) {
         const int r = mt * 16 + g + 8 * i;
         float top = sh.m[0][r];
 #pragma unroll
         for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-        const float f = m[mt][i] == neg_inf() ? 0.0f : fast_exp2(m[mt][i] - top);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int c = 0; c < D / 8; c += 4) {
-            const int ch = (2 * t + e) * (D / 8) + c;
-            *reinterpret_cast<float4*>(&sh.o[warp][g + 8 * i][padded(ch)]) =
-                make_float4(o[mt][c][2 * i + e] * f, o[mt][c + 1][2 * i + e] * f, o[mt][c + 2][2 * i + e] * f,
-                            o[mt][c + 3][2 * i + e] * f);
-          }
+        f[i] = m[mt][i] == neg_inf() ? 0.0f : fast_exp2(m[mt][i] - top);
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (D / 4); i += kAttThreads) {
+#pragma unroll
+      for (int stage = 0; stage < 2; ++stage) {
+        // stage 0: warps 2 and 3 store; stage 1: warps 0 and 1 add
+        if ((stage == 0) == (warp >= 2)) {
+#pragma unroll
+          for (int i = 0; i < H; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int c = 0; c < D / 8; c += 4) {
+                const int ch = (2 * t + e) * (D / 8) + c;
+                float4* at = reinterpret_cast<float4*>(&sh.o[warp & 1][g + 8 * i][padded(ch)]);
+                float4 x = make_float4(o[mt][c][2 * i + e] * f[i], o[mt][c + 1][2 * i + e] * f[i],
+                                       o[mt][c + 2][2 * i + e] * f[i], o[mt][c + 3][2 * i + e] * f[i]);
+                if (stage == 1) {
+                  const float4 y = *at;
+                  x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                }
+                *at = x;
+              }
+        }
+        __syncthreads();
+      }
+      for (int i = threadIdx.x; i < 8 * H * (D / 4); i += kAttThreads) {
         const int rr = i / (D / 4), ch = (i - rr * (D / 4)) * 4, r = mt * 16 + rr;
         if (r >= rows) continue;
+        const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][rr][padded(ch)]);
+        const float4 y = *reinterpret_cast<const float4*>(&sh.o[1][rr][padded(ch)]);
+        const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         float top = sh.m[0][r], sum = 0.0f;
 #pragma unroll
         for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][rr][padded(ch)]);
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
+        for (int w = 0; w < kAttWarps; ++w)
           if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
-        }
         if (!complete) {
           *reinterpret_cast<float4*>(part + r * D + ch) = acc;
           if (ch == 0) {
@@ -410,16 +468,17 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
         *reinterpret_cast<uint2*>(a.out + at * D + ch) = v;
         if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
+  cp_async_wait<0>();
 }
 
-template <int D, int MT>
+template <int D, int MT, bool EIGHT>
 int launch_attention(AttnArgs a, int sms, cudaStream_t s) {
   constexpr int R = 16 * MT;
   const size_t smem = sizeof(AttShared<D, MT>);
-  auto kernel = kv4_attention_kernel<D, MT>;
+  auto kernel = kv4_attention_kernel<D, MT, EIGHT>;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
@@ -480,7 +539,12 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int R = rows_of(static_cast<int64_t>(N) * a.G);
   if (R == 0) return launch_tree_attention(a, D, sms, s);
-  const bool small = R == 16;
-  if (D == 128) return small ? launch_attention<128, 1>(a, sms, s) : launch_attention<128, 2>(a, sms, s);
-  return small ? launch_attention<64, 1>(a, sms, s) : launch_attention<64, 2>(a, sms, s);
+  const bool eight = static_cast<int64_t>(N) * a.G <= 8;
+  if (D == 128)
+    return eight     ? launch_attention<128, 1, true>(a, sms, s)
+           : R == 16 ? launch_attention<128, 1, false>(a, sms, s)
+                     : launch_attention<128, 2, false>(a, sms, s);
+  return eight     ? launch_attention<64, 1, true>(a, sms, s)
+         : R == 16 ? launch_attention<64, 1, false>(a, sms, s)
+                   : launch_attention<64, 2, false>(a, sms, s);
 }
