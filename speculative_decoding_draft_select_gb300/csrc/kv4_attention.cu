@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kTile = 64;        // positions of a tile: 16 per warp
 constexpr int kEnds = 2;         // tiles that a segment's beginning and end cost
+constexpr int kEnds8 = 1;        // of four times 32 positions
 constexpr int kAttThreads = 128;
 constexpr int kAttWarps = kAttThreads / 32;
 constexpr float kWeightExp = 15.0f;  // weights are held times 2^15
@@ -62,7 +63,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 __device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
 __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
 
-// A warp's 16 positions of a tile in shared memory: a stage of a ring that
+// A warp's P positions of a tile in shared memory: a stage of a ring that
 // only this warp fills (asynchronous copies of 16 bytes, a position's bytes by
 // neighbouring lanes) and reads.  With t = lane % 4 and g = lane / 4 a lane
 // reads, of positions g and g + 8, the D/4 channels of K from t D/4 on (its
@@ -71,13 +72,13 @@ __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
 // share of the B fragments of w v: channel g D/8 + i is column g of block i).
 // K's codes lie 16 words a position apart and V's with their (step, lo) 20
 // (D = 64: 8 and 12), which makes every read free of bank conflicts.
-template <int D>
+template <int D, int P>
 struct Stage {
   static constexpr int kChunks = kv4_head_bytes(D) / 16;        // of a position
   static constexpr int kVRow = D == 128 ? 80 : 48;              // D = 64: with K's (step, lo) too
-  static constexpr int kKMeta = D == 128 ? 16 * 64 : 16 * 32 + 32;
-  static constexpr int kV = D == 128 ? 16 * 80 : 16 * 32;       // V's first byte
-  static constexpr int kBytes = 16 * kv4_head_bytes(D);
+  static constexpr int kKMeta = P * 64;                         // D = 128 only
+  static constexpr int kV = D == 128 ? P * 80 : P * 32;         // V's first byte
+  static constexpr int kBytes = P * kv4_head_bytes(D);
   // where chunk c of position pos goes
   __device__ __forceinline__ static int place(int pos, int c) {
     constexpr int kk = D / 32;  // chunks of K's codes, and of V's
@@ -86,8 +87,105 @@ struct Stage {
     if (D == 128 && c == 2 * kk) return kKMeta + pos * 16;
     return kV + pos * kVRow + D / 2;
   }
+  // A lane's share of one position: K's codes and (step, lo), V's.
+  __device__ __forceinline__ static void k(const uint8_t* s, int pos, int t, typename Vec<D / 8>::type& c, uint32_t& m) {
+    c = *reinterpret_cast<const typename Vec<D / 8>::type*>(s + pos * (D / 2) + t * (D / 8));
+    m = *reinterpret_cast<const uint32_t*>(
+        s + (D == 128 ? kKMeta + pos * 16 + t * 4 : kV + pos * kVRow + D / 2 + (t >> 1) * 4));
+  }
+  __device__ __forceinline__ static void v(const uint8_t* s, int pos, int g, typename Vec<D / 16>::type& c, uint32_t& m) {
+    const uint8_t* row = s + kV + pos * kVRow;
+    c = *reinterpret_cast<const typename Vec<D / 16>::type*>(row + g * (D / 16));
+    m = *reinterpret_cast<const uint32_t*>(row + (D == 128 ? 64 + (g >> 1) * 4 : 40 + (g >> 2) * 4));
+  }
 };
-constexpr int kRing = 4;  // stages of a warp
+
+// A warp's ring of RING stages and the cursor that fills it, across segments:
+// slots RING + 1 tiles before their use, codes RING.  A tile is 4 P positions,
+// P for each of four warps.
+template <int D, int P, int RING, int E, int R>
+struct Filler {
+  using St = Stage<D, P>;
+  static constexpr int kTile = 4 * P, kCopies = (P * St::kChunks + 31) / 32;
+  Walk<kTile, E, R> ahead;
+  Part ap;
+  bool more, loaded, count;
+  int next_tile;
+  int32_t slot;  // of position lane % P of the warp's; -2: no position
+  const uint8_t* head;
+  unsigned ring;
+  unsigned* there;          // [RING]: positions of a stage that have a slot
+  uint32_t plan[kCopies];   // of a copy: position, chunk, place in the stage
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R>& walk, uint8_t* stages, unsigned* t) {
+    ahead = walk;
+    more = ahead.next(a, ap);
+    next_tile = ap.t0;
+    ring = static_cast<unsigned>(__cvta_generic_to_shared(stages));
+    there = t;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int id = min(lane + 32 * i, P * St::kChunks - 1), pos = id / St::kChunks, c = id - pos * St::kChunks;
+      plan[i] = pos | c << 8 | St::place(pos, c) << 16;
+    }
+    load_slot(a);
+#pragma unroll 1
+    for (int i = 0; i < RING - 1; ++i) {
+      copy(a, i);
+      load_slot(a);
+    }
+  }
+  __device__ __forceinline__ void load_slot(const AttnArgs& a) {
+    loaded = more;
+    if (!more) return;
+    const int lane = threadIdx.x & 31;
+    const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + (lane & (P - 1));
+    head = a.pool + static_cast<int64_t>(ap.h) * kv4_head_bytes(D);
+    count = ap.h == 0 && ap.rt == 0 && lane < P;
+    slot = pos < ap.end ? __ldg(a.table + static_cast<int64_t>(ap.b) * a.max_ctx + pos) : -2;
+    if (++next_tile == ap.t1) {
+      more = ahead.next(a, ap);
+      next_tile = ap.t0;
+    }
+  }
+  __device__ __forceinline__ void copy(const AttnArgs& a, int st) {  // one commit group, empty behind the line's end
+    if (loaded) {
+      const int lane = threadIdx.x & 31;
+      const bool ok = slot >= 0 && slot < a.num_slots;
+      if (!ok && slot != -2 && count) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      const unsigned have = __ballot_sync(0xffffffffu, ok) & (0xffffffffu >> (32 - P));
+      if (lane == 0) there[st] = have;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int pos = plan[i] & 255;
+        const int32_t sl = __shfl_sync(0xffffffffu, slot, pos);
+        const bool in = (have >> pos) & 1u;
+        if (32 * (i + 1) <= P * St::kChunks || lane + 32 * i < P * St::kChunks) {
+          // a position without a slot is zeroed: its weights are zero, its values must not be NaN
+          const uint8_t* src = head + (in ? sl : 0) * a.slot_stride + ((plan[i] >> 8) & 255) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + st * St::kBytes + (plan[i] >> 16)),
+                       "l"(src), "r"(in ? 16 : 0)
+                       : "memory");
+        }
+      }
+    }
+    cp_async_commit();
+  }
+  // The next tile into the stage that was read last, then the wait for stage
+  // `st`; returns its positions.
+  __device__ __forceinline__ unsigned turn(const AttnArgs& a, int st) {
+    __syncwarp();  // every lane has read the stage before
+    copy(a, (st + RING - 1) % RING);
+    load_slot(a);
+    cp_async_wait<RING - 1>();
+    __syncwarp();  // every lane's copies of this tile have landed
+    return there[st];
+  }
+};
+
+constexpr int kRing = 4;     // stages of a warp, of 16 positions
+constexpr int kRing8 = 2;    // and of 32, with up to eight rows
 
 // Shared memory of a CTA: the warps' rings, q in the order of the A fragments,
 // the warps' row statistics, and the weighted values of two warps' 16 rows at
@@ -96,7 +194,7 @@ constexpr int kRing = 4;  // stages of a warp
 template <int D, int MT>
 struct AttShared {
   static constexpr int kRow = D + 16;
-  uint8_t ring[kAttWarps][kRing][Stage<D>::kBytes];
+  uint8_t ring[kAttWarps][kRing][Stage<D, 16>::kBytes];
   uint4 q[MT][D / 16][32];
   float c[16 * MT];  // factor of a row's scores
   float m[kAttWarps][16 * MT], l[kAttWarps][16 * MT];
@@ -106,57 +204,89 @@ struct AttShared {
 
 __device__ __forceinline__ int padded(int ch) { return ch + (ch >> 5) * 4; }
 
+// Row r of (b, h) of q (zeros when !in), D / 32 channels a lane from lane D/32
+// on, and its largest magnitude.
+template <int D>
+__device__ __forceinline__ void q_row(const AttnArgs& a, int b, int h, int r, bool in, float* x, float& mx) {
+  constexpr int per = D / 32;
+  const int lane = threadIdx.x & 31;
+  uint32_t w[per / 2];
+#pragma unroll
+  for (int j = 0; j < per / 2; ++j) w[j] = 0;
+  if (in) {
+    const uint16_t* src = a.q + attn_q(a, b, h, r, D) + lane * per;
+    if (per == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+      w[0] = v.x;
+      w[per / 2 - 1] = v.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    }
+  }
+  mx = 0.0f;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    x[j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+    mx = fmaxf(mx, fabsf(x[j]));
+  }
+  mx = warp_max(mx);
+}
+// The power of two that brings mx into [1, 2) (1 for zeros, infinities and NaN;
+// 2^126 at most); the row's scores are multiplied by *factor.
+__device__ __forceinline__ float q_scale(float mx, float scale_log2, float* factor) {
+  const int e = max(mx > 0.0f && isfinite(mx) ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0, -126);
+  if ((threadIdx.x & 31) == 0) *factor = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
 // Query rows [r0, r0 + 16 MT) of (b, h) into shared memory: a warp per row.
 template <int D, int MT>
 __device__ void load_q(const AttnArgs& a, AttShared<D, MT>& sh, int b, int h, int r0, int rows) {
-  constexpr int per = D / 32;  // channels of a lane: [lane per, + per)
+  constexpr int per = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 4
   for (int r = warp; r < 16 * MT; r += kAttWarps) {
-    float x[per];
-#pragma unroll
-    for (int j = 0; j < per; ++j) x[j] = 0.0f;
-    if (r < rows) {
-      const int row = r0 + r, n = attn_node(a, row);
-      const uint16_t* src = a.q + (static_cast<int64_t>(b) * a.N + n) * a.q_stride +
-                            static_cast<int64_t>(h * a.G + row - n * a.G) * D + lane * per;
-      if (per == 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-        x[0] = bf16_lo(w.x);
-        x[1] = bf16_hi(w.x);
-        x[per - 2] = bf16_lo(w.y);
-        x[per - 1] = bf16_hi(w.y);
-      } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
-        x[0] = bf16_lo(w);
-        x[1] = bf16_hi(w);
-      }
-    }
-    float mx = 0.0f;
-#pragma unroll
-    for (int j = 0; j < per; ++j) mx = fmaxf(mx, fabsf(x[j]));
-    mx = warp_max(mx);
-    // 2^e <= mx < 2^(e+1) for a normal mx; rows of zeros or subnormals are
-    // taken times 2^126
-    const int e = mx > 0.0f && isfinite(mx) ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0;
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - max(e, -126)) << 23);
-    if (lane == 0) sh.c[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + max(e, -126)) << 23);
+    float x[per], mx;
+    q_row<D>(a, b, h, r0 + r, r < rows, x, mx);
+    const float down = q_scale(mx, a.scale_log2, sh.c + r);
     // channel ch = t D/4 + 4 kk + 2 i + odd: A register 2 i + (row half) of
     // lane 4 (row % 8) + t at step kk
 #pragma unroll
     for (int j = 0; j < per; j += 2) {
       const int ch = lane * per + j, t = ch / (D / 4), kk = ch % (D / 4) / 4, i = ch % 4 / 2;
-      const __half2 v = __floats2half2_rn(x[j] * down, x[j + 1] * down);
-      reinterpret_cast<uint32_t*>(&sh.q[r / 16][kk][(r % 8) * 4 + t])[2 * i + (r % 16) / 8] = h2_u32(v);
+      reinterpret_cast<uint32_t*>(&sh.q[r / 16][kk][(r % 8) * 4 + t])[2 * i + (r % 16) / 8] =
+          h2_u32(__floats2half2_rn(x[j] * down, x[j + 1] * down));
     }
   }
 }
 
-// EIGHT: no row past the eighth; the upper half of the fragments is not worked.
-template <int D, int MT, bool EIGHT>
+// Four channels of a row's weighted values: the result, or this CTA's partial.
+template <int D>
+__device__ __forceinline__ void attn_store(const AttnArgs& a, const Part& p, int r, int R, int ch, const float4& acc,
+                                           float top, float sum, float* part) {
+  if (!p.complete()) {
+    const int rr = r - p.rt * R;
+    *reinterpret_cast<float4*>(part + rr * D + ch) = acc;
+    if (ch == 0) {
+      part[R * D + 2 * rr] = top;
+      part[R * D + 2 * rr + 1] = sum;
+    }
+    return;
+  }
+  const float inv = attn_inv(sum);
+  const int64_t at = attn_row(a, p.b, p.h, r);
+  uint2 v;
+  v.x = f_bf16(acc.x * inv) | static_cast<uint32_t>(f_bf16(acc.y * inv)) << 16;
+  v.y = f_bf16(acc.z * inv) | static_cast<uint32_t>(f_bf16(acc.w * inv)) << 16;
+  *reinterpret_cast<uint2*>(a.out + at * D + ch) = v;
+  if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
+}
+
+template <int D, int MT>
 __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_kernel(const AttnArgs a) {
   pdl_enter();
-  constexpr int R = 16 * MT, H = EIGHT ? 1 : 2;  // halves of a fragment's rows
-  using St = Stage<D>;
+  constexpr int R = 16 * MT, H = 2;  // halves of a fragment's rows
+  using St = Stage<D, 16>;
   extern __shared__ __align__(16) unsigned char att_sm[];
   AttShared<D, MT>& sh = *reinterpret_cast<AttShared<D, MT>*>(att_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
@@ -167,63 +297,8 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
   Walk<kTile, kEnds, R> walk;
   if (!attn_stretch<kTile, kEnds, R, kAttThreads>(a, line, walk)) return;
 
-  // the cursor that reads ahead, across segments: slots kRing + 1 tiles before
-  // their use, codes kRing
-  auto ahead = walk;
-  Part ap;
-  bool more = ahead.next(a, ap);
-  int next_tile = ap.t0;
-  int32_t slot = -2;  // of position warp * 16 + lane % 16; -2: no position
-  const uint8_t* head = nullptr;
-  bool count = false, loaded = false;
-  auto load_slot = [&]() {
-    loaded = more;
-    if (!more) return;
-    const int pos = next_tile * kTile + warp * 16 + (lane & 15);
-    head = a.pool + static_cast<int64_t>(ap.h) * kv4_head_bytes(D);
-    count = ap.h == 0 && ap.rt == 0 && lane < 16;
-    slot = pos < ap.end ? __ldg(a.table + static_cast<int64_t>(ap.b) * a.max_ctx + pos) : -2;
-    if (++next_tile == ap.t1) {
-      more = ahead.next(a, ap);
-      next_tile = ap.t0;
-    }
-  };
-  constexpr int kCopies = (16 * St::kChunks + 31) / 32;
-  uint32_t plan[kCopies];  // of a copy: position, chunk, place in the stage
-#pragma unroll
-  for (int i = 0; i < kCopies; ++i) {
-    const int id = min(lane + 32 * i, 16 * St::kChunks - 1), pos = id / St::kChunks, c = id - pos * St::kChunks;
-    plan[i] = pos | c << 8 | St::place(pos, c) << 16;
-  }
-  const unsigned ring = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp][0]));
-  auto copy_codes = [&](int st) {  // one commit group, empty behind the line's end
-    if (loaded) {
-      const bool ok = slot >= 0 && slot < a.num_slots;
-      if (!ok && slot != -2 && count) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-      const unsigned there = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      if (lane == 0) sh.there[warp][st] = there;
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int pos = plan[i] & 255;
-        const int32_t sl = __shfl_sync(0xffffffffu, slot, pos);
-        const bool have = (there >> pos) & 1u;
-        if (32 * (i + 1) <= 16 * St::kChunks || lane + 32 * i < 16 * St::kChunks) {
-          // a position without a slot is zeroed: its weights are zero, its values must not be NaN
-          const uint8_t* src = head + (have ? sl : 0) * a.slot_stride + ((plan[i] >> 8) & 255) * 16;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + st * St::kBytes + (plan[i] >> 16)),
-                       "l"(src), "r"(have ? 16 : 0)
-                       : "memory");
-        }
-      }
-    }
-    cp_async_commit();
-  };
-  load_slot();
-#pragma unroll 1
-  for (int i = 0; i < kRing - 1; ++i) {
-    copy_codes(i);
-    load_slot();
-  }
+  Filler<D, 16, kRing, kEnds, R> fill;
+  fill.begin(a, walk, sh.ring[warp][0], sh.there[warp]);
   int st = 0;  // stage of the tile at hand
 
   Part rq;
@@ -253,14 +328,8 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
 
 #pragma unroll 1
     for (int tile = t0; tile < t1; ++tile) {
-      // the stage that the tile before used is free: every lane has read it
-      __syncwarp();
-      copy_codes((st + kRing - 1) % kRing);
-      load_slot();
-      cp_async_wait<kRing - 1>();
-      __syncwarp();  // every lane's copies of this tile have landed
+      const unsigned there = fill.turn(a, st);
       const uint8_t* s8 = sh.ring[warp][st];
-      const unsigned there = sh.there[warp][st];
       st = (st + 1) % kRing;
       if (there == 0) continue;
       float s[MT][2][4];
@@ -273,12 +342,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
       typename Vec<D / 8>::type kc[2];
       uint32_t km[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int pos = g + 8 * j;
-        kc[j] = *reinterpret_cast<const typename Vec<D / 8>::type*>(s8 + pos * (D / 2) + t * (D / 8));
-        km[j] = *reinterpret_cast<const uint32_t*>(
-            s8 + (D == 128 ? St::kKMeta + pos * 16 + t * 4 : St::kV + pos * St::kVRow + D / 2 + (t >> 1) * 4));
-      }
+      for (int j = 0; j < 2; ++j) St::k(s8, g + 8 * j, t, kc[j], km[j]);
 #pragma unroll
       for (int wd = 0; wd < D / 32; ++wd) {  // words of 8 channels: two steps of 16 (4 channels a lane)
         uint32_t kv[2][4];
@@ -353,21 +417,15 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
             s[mt][j][i] = fast_exp2(s[mt][j][i] - mn[i >> 1]);
             l[mt][i >> 1] += s[mt][j][i];
           }
-        pa[mt] = make_uint4(h2_u32(__floats2half2_rn(s[mt][0][0], s[mt][0][1])), 0u,
-                            h2_u32(__floats2half2_rn(s[mt][1][0], s[mt][1][1])), 0u);
-        if (!EIGHT) {
-          pa[mt].y = h2_u32(__floats2half2_rn(s[mt][0][2], s[mt][0][3]));
-          pa[mt].w = h2_u32(__floats2half2_rn(s[mt][1][2], s[mt][1][3]));
-        }
+        pa[mt] = make_uint4(h2_u32(__floats2half2_rn(s[mt][0][0], s[mt][0][1])),
+                            h2_u32(__floats2half2_rn(s[mt][0][2], s[mt][0][3])),
+                            h2_u32(__floats2half2_rn(s[mt][1][0], s[mt][1][1])),
+                            h2_u32(__floats2half2_rn(s[mt][1][2], s[mt][1][3])));
       }
       typename Vec<D / 16>::type vc[4];
       uint32_t vm[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* row = s8 + St::kV + (2 * t + (j & 1) + 8 * (j >> 1)) * St::kVRow;
-        vc[j] = *reinterpret_cast<const typename Vec<D / 16>::type*>(row + g * (D / 16));
-        vm[j] = *reinterpret_cast<const uint32_t*>(row + (D == 128 ? 64 + (g >> 1) * 4 : 40 + (g >> 2) * 4));
-      }
+      for (int j = 0; j < 4; ++j) St::v(s8, 2 * t + (j & 1) + 8 * (j >> 1), g, vc[j], vm[j]);
       const uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
       const uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
 #pragma unroll
@@ -389,7 +447,6 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
     }
 
     // merge the warps: 2 and 3 hand their values to 0 and 1, then 1 to 0's place
-    const bool complete = rq.complete();
     float* part = attn_part(a, blockIdx.x, t0 > 0 ? 0 : 1, R, D);
     if (t0 == 0 && t1 < rq.tiles && threadIdx.x == 0)
       *cut = CutSegment{b, h, rt, line.pieces(static_cast<int>(blockIdx.x), rq.tiles, t1)};
@@ -452,21 +509,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w)
           if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
-        if (!complete) {
-          *reinterpret_cast<float4*>(part + r * D + ch) = acc;
-          if (ch == 0) {
-            part[R * D + 2 * r] = top;
-            part[R * D + 2 * r + 1] = sum;
-          }
-          continue;
-        }
-        const float inv = attn_inv(sum);
-        const int64_t at = attn_row(a, b, h, r0 + r);
-        uint2 v;
-        v.x = f_bf16(acc.x * inv) | static_cast<uint32_t>(f_bf16(acc.y * inv)) << 16;
-        v.y = f_bf16(acc.z * inv) | static_cast<uint32_t>(f_bf16(acc.w * inv)) << 16;
-        *reinterpret_cast<uint2*>(a.out + at * D + ch) = v;
-        if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
+        attn_store<D>(a, rq, r0 + r, R, ch, acc, top, sum, part);
       }
       __syncthreads();
     }
@@ -474,26 +517,273 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
   cp_async_wait<0>();
 }
 
-template <int D, int MT, bool EIGHT>
-int launch_attention(AttnArgs a, int sms, cudaStream_t s) {
-  constexpr int R = 16 * MT;
-  const size_t smem = sizeof(AttShared<D, MT>);
-  auto kernel = kv4_attention_kernel<D, MT, EIGHT>;
+// Up to eight rows (single tokens of up to eight query heads a KV head).  The
+// products are taken transposed: S^T = K Q^T and O^T = V^T P^T with positions
+// and channels as the 16 rows of a fragment and the eight query rows as its
+// columns, half the matrix instructions and half the registers of O.  The same
+// lanes' registers serve: K's B fragments of two position blocks are the A
+// fragment of 16 positions, V's of two channel blocks that of 16 channels.  The
+// weights (position g, rows 2t, 2t + 1) become the B fragment (positions 2t,
+// 2t + 1, row g) by one 8 x 8 transposition a block (movmatrix).  A warp takes
+// 32 positions at a time: what a tile costs beside the unpacking (the slots,
+// the copies' addresses, the maximum) is shared by more positions.  Bound by
+// the instructions that unpack the codes: 26 a position and lane of 128
+// channels.
+template <int D>
+struct AttShared8 {
+  static constexpr int kRow = D + 4;
+  uint8_t ring[kAttWarps][kRing8][Stage<D, 32>::kBytes];
+  uint2 q[D / 16][32];
+  float c[8];
+  float m[kAttWarps][8], l[kAttWarps][8];
+  unsigned there[kAttWarps][kRing8];
+  float o[2][8][kRow];
+};
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAttThreads, 4) kv4_attention8_kernel(const AttnArgs a) {
+  pdl_enter();
+  constexpr int R = 8, T = 4 * 32;
+  using St = Stage<D, 32>;
+  extern __shared__ __align__(16) unsigned char att_sm[];
+  AttShared8<D>& sh = *reinterpret_cast<AttShared8<D>*>(att_sm);
+  if (!spec_smem_ok(sizeof(sh), a.stats)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
+  CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
+  if (threadIdx.x == 0) *cut = CutSegment{0, 0, 0, 0};
+  Line line;
+  Walk<T, kEnds8, R> walk;
+  if (!attn_stretch<T, kEnds8, R, kAttThreads>(a, line, walk)) return;
+  Filler<D, 32, kRing8, kEnds8, R> fill;
+  fill.begin(a, walk, sh.ring[warp][0], sh.there[warp]);
+  int st = 0;  // stage of the tile at hand
+
+  Part rq;
+#pragma unroll 1
+  while (walk.next(a, rq)) {
+    const int b = rq.b, h = rq.h, t0 = rq.t0, t1 = rq.t1;
+    const int rows = min(R, rq.nodes * a.G);
+    if (rq.bad && h == 0 && threadIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    // a warp's two rows of q: channel ch = t D/4 + 4 kk + 2 i + odd is B
+    // register i of lane 4 row + t at step kk
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      const int r = warp * 2 + rr;
+      float mx;
+      constexpr int per = D / 32;
+      float x[per];
+      q_row<D>(a, b, h, r, r < rows, x, mx);
+      const float down = q_scale(mx, a.scale_log2, sh.c + r);
+#pragma unroll
+      for (int j = 0; j < per; j += 2) {
+        const int ch = lane * per + j, tt = ch / (D / 4), kk = ch % (D / 4) / 4, i = ch % 4 / 2;
+        reinterpret_cast<uint32_t*>(&sh.q[kk][r * 4 + tt])[i] = h2_u32(__floats2half2_rn(x[j] * down, x[j + 1] * down));
+      }
+    }
+    __syncthreads();
+    float cr[2], m[2], l[2], o[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      cr[e] = sh.c[2 * t + e];
+      m[e] = neg_inf();
+      l[e] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+
+#pragma unroll 1
+    for (int tile = t0; tile < t1; ++tile) {
+      const unsigned there = fill.turn(a, st);
+      const uint8_t* s8 = sh.ring[warp][st];
+      st = (st + 1) % kRing8;
+      if (there == 0) continue;
+      // s[u][2 i + e]: position 16 u + g + 8 i, row 2 t + e
+      float s[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        typename Vec<D / 8>::type kc[2];
+        uint32_t km[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          St::k(s8, 16 * u + g + 8 * j, t, kc[j], km[j]);
+          s[u][2 * j] = s[u][2 * j + 1] = 0.0f;
+        }
+#pragma unroll
+        for (int wd = 0; wd < D / 32; ++wd) {
+          uint32_t kv[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            dequant4(word_of(kc[j], wd), __byte_perm(km[j], 0, 0x1010), __byte_perm(km[j], 0, 0x3232), kv[j]);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint2 q = sh.q[wd * 2 + half][lane];
+            mma16816(s[u], make_uint4(kv[0][2 * half], kv[1][2 * half], kv[0][2 * half + 1], kv[1][2 * half + 1]), q.x, q.y);
+          }
+        }
+      }
+      const int p0 = tile * T + warp * 32;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] *= cr[i & 1];
+      if (there != 0xffffffffu || p0 + 32 > rq.start) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = 16 * u + g + 8 * (i >> 1), node = p0 + at - rq.start, r = 2 * t + (i & 1);
+            bool see = (there >> at) & 1u;
+            if (see && node >= 0) {
+              const int n = attn_node(a, r);
+              see = r < rows && (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0
+                                        : node <= n);
+            }
+            if (!see) s[u][i] = neg_inf();
+          }
+      }
+      float mn[2], al[2];
+      bool up = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+        mn[e] = fmaxf(m[e], x);
+        up = up || mn[e] != m[e];
+        const float base_m = mn[e] == neg_inf() ? 0.0f : mn[e];
+        al[e] = fast_exp2(m[e] - base_m);
+        m[e] = mn[e];
+        mn[e] = base_m - kWeightExp;
+      }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] *= al[j & 1];
+        l[0] *= al[0];
+        l[1] *= al[1];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[u][i] = fast_exp2(s[u][i] - mn[i & 1]);
+          l[i & 1] += s[u][i];
+        }
+        const uint32_t p_lo = transpose8(h2_u32(__floats2half2_rn(s[u][0], s[u][1])));
+        const uint32_t p_hi = transpose8(h2_u32(__floats2half2_rn(s[u][2], s[u][3])));
+        typename Vec<D / 16>::type vc[4];
+        uint32_t vm[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) St::v(s8, 16 * u + 2 * t + (j & 1) + 8 * (j >> 1), g, vc[j], vm[j]);
+        const uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
+        const uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
+#pragma unroll
+        for (int wd = 0; wd < D / 64; ++wd) {
+          uint32_t v[2][2][4];  // odd channel, upper positions, pair of channels
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const uint32_t sel = odd ? 0x7632u : 0x5410u;
+            dequant4(__byte_perm(word_of(vc[0], wd), word_of(vc[1], wd), sel), st0, lo0, v[odd][0]);
+            dequant4(__byte_perm(word_of(vc[2], wd), word_of(vc[3], wd), sel), st1, lo1, v[odd][1]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // channels g D/8 + 8 wd + 2 j (o[..][0, 1]) and the next (o[..][2, 3])
+            mma16816(o[wd * 4 + j], make_uint4(v[0][0][j], v[1][0][j], v[0][1][j], v[1][1][j]), p_lo, p_hi);
+        }
+      }
+    }
+
+    // merge the warps: 2 and 3 store, 0 and 1 add, then all sum the two
+    float* part = attn_part(a, blockIdx.x, t0 > 0 ? 0 : 1, R, D);
+    if (t0 == 0 && t1 < rq.tiles && threadIdx.x == 0)
+      *cut = CutSegment{b, h, 0, line.pieces(static_cast<int>(blockIdx.x), rq.tiles, t1)};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = l[e];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (g == 0) {
+        sh.m[warp][2 * t + e] = m[e];
+        sh.l[warp][2 * t + e] = x;
+      }
+    }
+    __syncthreads();
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = sh.m[0][2 * t + e];
+#pragma unroll
+      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][2 * t + e]);
+      f[e] = m[e] == neg_inf() ? 0.0f : fast_exp2(m[e] - top);
+    }
+#pragma unroll
+    for (int stage = 0; stage < 2; ++stage) {
+      if ((stage == 0) == (warp >= 2)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2) {
+            float4* at = reinterpret_cast<float4*>(&sh.o[warp & 1][2 * t + e][g * (D / 8) + 2 * i]);
+            float4 x = make_float4(o[i][e] * f[e], o[i][2 + e] * f[e], o[i + 1][e] * f[e], o[i + 1][2 + e] * f[e]);
+            if (stage == 1) {
+              const float4 y = *at;
+              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            *at = x;
+          }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kAttThreads) {
+      const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
+      const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][ch]), y = *reinterpret_cast<const float4*>(&sh.o[1][r][ch]);
+      const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      float top = sh.m[0][r], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w)
+        if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
+      attn_store<D>(a, rq, r, R, ch, acc, top, sum, part);
+    }
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+}
+
+template <class K>
+int launch_rows(K kernel, AttnArgs& a, int D, int R, size_t smem, int ctas, cudaStream_t s) {
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
-  a.ctas = sms * (MT == 1 ? 3 : 2);
-  a.ctas = a.ctas < kMaxCtas ? a.ctas : kMaxCtas;
+  a.ctas = ctas < kMaxCtas ? ctas : kMaxCtas;
   launch_k(kernel, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
-  launch_merge<D>(a, R, kWeightExp, s);
+  if (D == 128) launch_merge<128>(a, R, kWeightExp, s);
+  else launch_merge<64>(a, R, kWeightExp, s);
   return launch_status();
 }
 
-// Rows of a row tile here: 16 where they suffice, else 32; 0: more rows than
-// that go to the tensor-memory kernel (kv4_tree.cu).
-int rows_of(int64_t rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 0); }
+template <int D>
+int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
+  if (R == 8) return launch_rows(kv4_attention8_kernel<D>, a, D, R, sizeof(AttShared8<D>), sms * 4, s);
+  if (R == 16) return launch_rows(kv4_attention_kernel<D, 1>, a, D, R, sizeof(AttShared<D, 1>), sms * 3, s);
+  return launch_rows(kv4_attention_kernel<D, 2>, a, D, R, sizeof(AttShared<D, 2>), sms * 2, s);
+}
+
+// Rows of a row tile here: 8 or 16 where they suffice, else 32; 0: more rows
+// than that go to the tensor-memory kernel (kv4_tree.cu).
+int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 0)); }
 
 }  // namespace
 }  // namespace specdec
@@ -539,12 +829,5 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int R = rows_of(static_cast<int64_t>(N) * a.G);
   if (R == 0) return launch_tree_attention(a, D, sms, s);
-  const bool eight = static_cast<int64_t>(N) * a.G <= 8;
-  if (D == 128)
-    return eight     ? launch_attention<128, 1, true>(a, sms, s)
-           : R == 16 ? launch_attention<128, 1, false>(a, sms, s)
-                     : launch_attention<128, 2, false>(a, sms, s);
-  return eight     ? launch_attention<64, 1, true>(a, sms, s)
-         : R == 16 ? launch_attention<64, 1, false>(a, sms, s)
-                   : launch_attention<64, 2, false>(a, sms, s);
+  return D == 128 ? launch_few<128>(a, R, sms, s) : launch_few<64>(a, R, sms, s);
 }
