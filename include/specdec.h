@@ -594,7 +594,8 @@ int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* poo
  * they were.  A position whose slot is out of range is not attended, and a
  * request with seq_len < 0 or seq_len + num_nodes > max_ctx gives zeros
  * (SPEC_STAT_BAD_REQUEST each).  q, pool and out 16-byte aligned, q_stride a
- * multiple of 8, Hq <= 4096, B <= 65535 (SPEC_ERR_UNSUPPORTED otherwise).
+ * multiple of 8, slot_stride a multiple of 16 below 2^31, Hq <= 4096, B <=
+ * 65535 (SPEC_ERR_UNSUPPORTED otherwise).
  *   ws: spec_kv4_attention_ws_size bytes (0 for sizes that are not
  *   supported), 16-byte aligned; calls that may overlap need their own. */
 size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D);

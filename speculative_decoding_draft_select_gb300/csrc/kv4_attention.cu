@@ -74,19 +74,10 @@ __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
 // (D = 64: 8 and 12), which makes every read free of bank conflicts.
 template <int D, int P>
 struct Stage {
-  static constexpr int kChunks = kv4_head_bytes(D) / 16;        // of a position
   static constexpr int kVRow = D == 128 ? 80 : 48;              // D = 64: with K's (step, lo) too
   static constexpr int kKMeta = P * 64;                         // D = 128 only
   static constexpr int kV = D == 128 ? P * 80 : P * 32;         // V's first byte
   static constexpr int kBytes = P * kv4_head_bytes(D);
-  // where chunk c of position pos goes
-  __device__ __forceinline__ static int place(int pos, int c) {
-    constexpr int kk = D / 32;  // chunks of K's codes, and of V's
-    if (c < kk) return pos * (D / 2) + c * 16;
-    if (c < 2 * kk) return kV + pos * kVRow + (c - kk) * 16;
-    if (D == 128 && c == 2 * kk) return kKMeta + pos * 16;
-    return kV + pos * kVRow + D / 2;
-  }
   // A lane's share of one position: K's codes and (step, lo), V's.
   __device__ __forceinline__ static void k(const uint8_t* s, int pos, int t, typename Vec<D / 8>::type& c, uint32_t& m) {
     c = *reinterpret_cast<const typename Vec<D / 8>::type*>(s + pos * (D / 2) + t * (D / 8));
@@ -102,82 +93,91 @@ struct Stage {
 
 // A warp's ring of RING stages and the cursor that fills it, across segments:
 // slots RING + 1 tiles before their use, codes RING.  A tile is 4 P positions,
-// P for each of four warps.
+// P for each of four warps.  A pair of lanes copies a position's 32-byte
+// sectors (one instruction: 16 positions), so the addresses are two shuffles a
+// 16 positions and constants.
 template <int D, int P, int RING, int E, int R>
 struct Filler {
   using St = Stage<D, P>;
-  static constexpr int kTile = 4 * P, kCopies = (P * St::kChunks + 31) / 32;
+  static constexpr int kTile = 4 * P;
   Walk<kTile, E, R> ahead;
   Part ap;
-  bool more, loaded, count;
+  bool more, loaded;
   int next_tile;
   int32_t slot;  // of position lane % P of the warp's; -2: no position
   const uint8_t* head;
+  const int32_t* row;  // the request's slots from this lane's position of tile 0 on
   unsigned ring;
-  unsigned* there;          // [RING]: positions of a stage that have a slot
-  uint32_t plan[kCopies];   // of a copy: position, chunk, place in the stage
+  unsigned* there;  // [RING]: positions of a stage that have a slot
 
+  __device__ __forceinline__ void segment(const AttnArgs& a) {
+    next_tile = ap.t0;
+    head = a.pool + ap.h * kv4_head_bytes(D);
+    row = a.table + static_cast<int64_t>(ap.b) * a.max_ctx + (threadIdx.x >> 5) * P + (threadIdx.x & (P - 1));
+  }
   __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R>& walk, uint8_t* stages, unsigned* t) {
     ahead = walk;
     more = ahead.next(a, ap);
-    next_tile = ap.t0;
+    segment(a);
     ring = static_cast<unsigned>(__cvta_generic_to_shared(stages));
     there = t;
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int id = min(lane + 32 * i, P * St::kChunks - 1), pos = id / St::kChunks, c = id - pos * St::kChunks;
-      plan[i] = pos | c << 8 | St::place(pos, c) << 16;
-    }
-    load_slot(a);
+    load_slot();
 #pragma unroll 1
     for (int i = 0; i < RING - 1; ++i) {
       copy(a, i);
-      load_slot(a);
+      load_slot();
     }
   }
-  __device__ __forceinline__ void load_slot(const AttnArgs& a) {
+  __device__ __forceinline__ void load_slot() {
     loaded = more;
     if (!more) return;
-    const int lane = threadIdx.x & 31;
-    const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + (lane & (P - 1));
-    head = a.pool + static_cast<int64_t>(ap.h) * kv4_head_bytes(D);
-    count = ap.h == 0 && ap.rt == 0 && lane < P;
-    slot = pos < ap.end ? __ldg(a.table + static_cast<int64_t>(ap.b) * a.max_ctx + pos) : -2;
-    if (++next_tile == ap.t1) {
-      more = ahead.next(a, ap);
-      next_tile = ap.t0;
-    }
+    const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + static_cast<int>(threadIdx.x & (P - 1));
+    slot = pos < ap.end ? __ldg(row + next_tile * kTile) : -2;
+    ++next_tile;
   }
-  __device__ __forceinline__ void copy(const AttnArgs& a, int st) {  // one commit group, empty behind the line's end
+  // Copies the tile whose slots were loaded last; one commit group, empty
+  // behind the line's end.
+  __device__ __forceinline__ void copy(const AttnArgs& a, int st) {
     if (loaded) {
-      const int lane = threadIdx.x & 31;
+      const int lane = threadIdx.x & 31, b = lane & 1;
       const bool ok = slot >= 0 && slot < a.num_slots;
-      if (!ok && slot != -2 && count) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      if (!ok && slot != -2 && ap.h == 0 && ap.rt == 0 && lane < P) bump(a.stats, SPEC_STAT_BAD_REQUEST);
       const unsigned have = __ballot_sync(0xffffffffu, ok) & (0xffffffffu >> (32 - P));
       if (lane == 0) there[st] = have;
+      const uint64_t mine = reinterpret_cast<uint64_t>(head) +
+                            static_cast<uint64_t>(ok ? slot : 0) * static_cast<uint32_t>(a.slot_stride);
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int pos = plan[i] & 255;
-        const int32_t sl = __shfl_sync(0xffffffffu, slot, pos);
-        const bool in = (have >> pos) & 1u;
-        if (32 * (i + 1) <= P * St::kChunks || lane + 32 * i < P * St::kChunks) {
-          // a position without a slot is zeroed: its weights are zero, its values must not be NaN
-          const uint8_t* src = head + (in ? sl : 0) * a.slot_stride + ((plan[i] >> 8) & 255) * 16;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + st * St::kBytes + (plan[i] >> 16)),
-                       "l"(src), "r"(in ? 16 : 0)
-                       : "memory");
+      for (int u = 0; u < P / 16; ++u) {
+        const int pos = u * 16 + (lane >> 1);
+        const uint64_t src = __shfl_sync(0xffffffffu, mine, pos) + b * 16;
+        // a position without a slot is zeroed: its weights are zero, its values must not be NaN
+        const unsigned size = (have >> pos) & 1u ? 16u : 0u;
+        const unsigned k = ring + st * St::kBytes + pos * (D / 2) + b * 16, v = ring + st * St::kBytes + St::kV + pos * St::kVRow + b * 16;
+        constexpr int kk = D / 64;  // sectors of K's codes, and of V's
+#pragma unroll
+        for (int i = 0; i < kk; ++i) {
+          put(k + 32 * i, src + 32 * i, size);
+          put(v + 32 * i, src + D / 2 + 32 * i, size);
         }
+        if (D == 128) put(b ? v - 16 + 64 : ring + st * St::kBytes + St::kKMeta + pos * 16, src + 128, size);
+        else if (b == 0) put(v + 32, src + 64, size);
       }
     }
+    if (more && next_tile == ap.t1) {
+      more = ahead.next(a, ap);
+      segment(a);
+    }
     cp_async_commit();
+  }
+  __device__ __forceinline__ static void put(unsigned dst, uint64_t src, unsigned size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
   }
   // The next tile into the stage that was read last, then the wait for stage
   // `st`; returns its positions.
   __device__ __forceinline__ unsigned turn(const AttnArgs& a, int st) {
     __syncwarp();  // every lane has read the stage before
     copy(a, (st + RING - 1) % RING);
-    load_slot(a);
+    load_slot();
     cp_async_wait<RING - 1>();
     __syncwarp();  // every lane's copies of this tile have landed
     return there[st];
@@ -808,7 +808,8 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
   const int64_t row = spec_kv4_slot_bytes(Hkv, D);
   if (row < 0 || N > SPEC_MAX_NODES || Hq > SPEC_KV4_MAX_HEADS * 16 || B > 65535) return SPEC_ERR_UNSUPPORTED;
   if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
-  if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kTile)
+  if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kTile ||
+      slot_stride > INT32_MAX)
     return SPEC_ERR_UNSUPPORTED;
   if (B == 0 || N == 0) return SPEC_OK;
   if (!q || !pool || !seq_lens || !req_to_token || !out || !ws) return SPEC_ERR_INVALID_ARG;
