@@ -185,7 +185,7 @@ struct Filler {
 };
 
 constexpr int kRing = 4;     // stages of a warp, of 16 positions
-constexpr int kRing8 = 2;    // and of 32, with up to eight rows
+constexpr int kRing8 = 3;    // and of 32, with up to eight rows
 
 // Shared memory of a CTA: the warps' rings, q in the order of the A fragments,
 // the warps' row statistics, and the weighted values of two warps' 16 rows at
@@ -547,7 +547,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAttThreads, 4) kv4_attention8_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const AttnArgs a) {
   pdl_enter();
   constexpr int R = 8, T = 4 * 32;
   using St = Stage<D, 32>;
@@ -607,26 +607,26 @@ __global__ void __launch_bounds__(kAttThreads, 4) kv4_attention8_kernel(const At
       if (there == 0) continue;
       // s[u][2 i + e]: position 16 u + g + 8 i, row 2 t + e
       float s[2][4];
+      typename Vec<D / 8>::type kc[2][2];
+      uint32_t km[2][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        typename Vec<D / 8>::type kc[2];
-        uint32_t km[2];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          St::k(s8, 16 * u + g + 8 * j, t, kc[j], km[j]);
+          St::k(s8, 16 * u + g + 8 * j, t, kc[u][j], km[u][j]);
           s[u][2 * j] = s[u][2 * j + 1] = 0.0f;
         }
 #pragma unroll
-        for (int wd = 0; wd < D / 32; ++wd) {
+      for (int wd = 0; wd < D / 32; ++wd) {
+        const uint2 q0 = sh.q[wd * 2][lane], q1 = sh.q[wd * 2 + 1][lane];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           uint32_t kv[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            dequant4(word_of(kc[j], wd), __byte_perm(km[j], 0, 0x1010), __byte_perm(km[j], 0, 0x3232), kv[j]);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint2 q = sh.q[wd * 2 + half][lane];
-            mma16816(s[u], make_uint4(kv[0][2 * half], kv[1][2 * half], kv[0][2 * half + 1], kv[1][2 * half + 1]), q.x, q.y);
-          }
+            dequant4(word_of(kc[u][j], wd), __byte_perm(km[u][j], 0, 0x1010), __byte_perm(km[u][j], 0, 0x3232), kv[j]);
+          mma16816(s[u], make_uint4(kv[0][0], kv[1][0], kv[0][1], kv[1][1]), q0.x, q0.y);
+          mma16816(s[u], make_uint4(kv[0][2], kv[1][2], kv[0][3], kv[1][3]), q1.x, q1.y);
         }
       }
       const int p0 = tile * T + warp * 32;
@@ -776,7 +776,7 @@ int launch_rows(K kernel, AttnArgs& a, int D, int R, size_t smem, int ctas, cuda
 
 template <int D>
 int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
-  if (R == 8) return launch_rows(kv4_attention8_kernel<D>, a, D, R, sizeof(AttShared8<D>), sms * 4, s);
+  if (R == 8) return launch_rows(kv4_attention8_kernel<D>, a, D, R, sizeof(AttShared8<D>), sms * 3, s);
   if (R == 16) return launch_rows(kv4_attention_kernel<D, 1>, a, D, R, sizeof(AttShared<D, 1>), sms * 3, s);
   return launch_rows(kv4_attention_kernel<D, 2>, a, D, R, sizeof(AttShared<D, 2>), sms * 2, s);
 }
