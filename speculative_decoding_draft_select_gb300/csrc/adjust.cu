@@ -18,12 +18,15 @@
 // scanned once per chunk and its counts serve N rows from shared memory:
 //   info[t]  count (low 29 bits), kSeen, kBias; a token that some node of
 //            the tree carries holds kPath and the number of its slot instead
-//   bits     one bit per token with a non-zero info
-// Most tokens have none: a 16-byte vector of logits whose bits are clear is
-// copied (or masked), 8 table entries are never looked at.  Tokens on paths
-// differ by row: the pass leaves them as they are and the same warp then
-// fixes the row's few path tokens from the slot's list of nodes, so each
-// element is computed once even in place.
+//   list     the tokens of the chunk that have any of these (few)
+// The pass itself copies vectors of 16 bytes and writes -inf where the mask
+// says so (vectors without an allowed token are not read); the same warp then
+// computes the row's listed tokens from the values at hand.  A masked token is
+// -inf whatever else holds of it, so the pass leaves every value that is still
+// needed, in place too; in place without a mask only the listed tokens are
+// touched at all.  (Looking the bits of every vector up in the pass instead
+// took 128 instructions a vector where histories crowd: 890 us against 764 at
+// 64-node trees, B=128, V=128256.)
 #include <climits>
 
 #include "common.cuh"
@@ -36,6 +39,8 @@ constexpr int kAdjWarps = kAdjThreads / 32;
 constexpr int kAdjMaxChunk = 4096;  // tokens of a chunk: 16 KB of info, 16 KB of biases
 constexpr int kAdjMinChunk = 512;
 constexpr int kAdjUnroll = 4;       // 16-byte vectors in flight per lane
+constexpr int kAdjFirst = 2;        // listed tokens in flight per lane beside the pass
+constexpr int kAdjBatch = 4;        // and behind it
 
 constexpr uint32_t kPath = 1u << 31, kSeen = 1u << 30, kBias = 1u << 29, kCount = kBias - 1;
 
@@ -73,7 +78,7 @@ __device__ __forceinline__ uint4 ld_plain(const void* p) {
   return v;
 }
 __device__ __forceinline__ void st_vec(void* p, const uint4& v) {
-  asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 template <int DT>
@@ -93,6 +98,16 @@ __device__ __forceinline__ void adj_store(void* p, int64_t i, float x) {
   else static_cast<float*>(p)[i] = x;
 }
 
+// Listed tokens of a lane: from the chunk's start (-1: none), their mask words,
+// their values.
+template <int Q>
+struct Listed {
+  static constexpr int size = Q;
+  int tok[Q];
+  uint32_t word[Q];
+  float val[Q];
+};
+
 struct Penalty {
   float rep, freq, pres;
 };
@@ -105,68 +120,88 @@ __device__ __forceinline__ float adj_value(float x, uint32_t info, float bias, c
   return x;
 }
 
-// The n (<= 8) bits [t, t + n) of a bit array; words past the last that these
-// bits touch are not read.
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int t, int n) {
+// The kv (4 or 8) bits of a mask from token t on.  whole: t is a multiple of
+// kv, so they lie in one byte; otherwise words past the last that the bits
+// touch are not read.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int t, int kv, bool whole) {
+  if (whole) {
+    const uint32_t b = __ldg(reinterpret_cast<const uint8_t*>(w) + (t >> 3));
+    return kv == 8 ? b : (b >> (t & 4)) & 15u;
+  }
   const int i = t >> 5, s = t & 31;
-  uint32_t v = w[i] >> s;
-  if (s + n > 32) v |= w[i + 1] << (32 - s);
-  return v & ((1u << n) - 1u);
+  uint32_t v = __ldg(w + i) >> s;
+  if (s + kv > 32) v |= __ldg(w + i + 1) << (32 - s);
+  return v & ((1u << kv) - 1u);
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a, int chunk) {
   pdl_enter();
   constexpr int esz = DT == SPEC_BF16 ? 2 : 4, kv = Logit<DT>::kVec;
+  constexpr uint32_t kAll = (1u << kv) - 1u;
   extern __shared__ __align__(16) uint32_t adj_sm[];
-  const int b = blockIdx.y, N = a.N;
+  const int b = blockIdx.x, N = a.N;
   uint32_t* info = adj_sm;                                          // [chunk]
   float* bias = reinterpret_cast<float*>(info + chunk);             // [chunk]
-  uint32_t* bits = reinterpret_cast<uint32_t*>(bias + (a.M > 0 ? chunk : 0));  // [chunk / 32]
-  int32_t* slot_tok = reinterpret_cast<int32_t*>(bits + chunk / 32);  // [N] token of a slot, from the chunk's start
+  uint16_t* list = reinterpret_cast<uint16_t*>(bias + (a.M > 0 ? chunk : 0));  // [chunk] tokens with info, from the chunk's start
+  int32_t* slot_tok = reinterpret_cast<int32_t*>(list + chunk);     // [N] token of a slot, likewise
   int32_t* slot_head = slot_tok + N;                                // [N] last node that carries it
   uint32_t* slot_info = reinterpret_cast<uint32_t*>(slot_head + N); // [N] its info without the path
   int32_t* next = reinterpret_cast<int32_t*>(slot_info + N);        // [N] node before it in the slot's list
-  if (!spec_smem_ok(reinterpret_cast<char*>(next + (a.draft_token ? N : 0)) - reinterpret_cast<char*>(adj_sm), a.stats))
+  if (!spec_smem_ok(reinterpret_cast<char*>(a.draft_token ? next + N : slot_tok) - reinterpret_cast<char*>(adj_sm),
+                    a.stats))
     return;
-  __shared__ int s_slots;
+  __shared__ int s_slots, s_list;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int nodes = N;
   if (a.num_nodes) nodes = min(max(__ldg(a.num_nodes + b), 0), N);
   if (nodes == 0) return;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * chunk;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * chunk;
   const int len = static_cast<int>(min(static_cast<int64_t>(chunk), a.V - c0));  // tokens [c0, c0 + len)
 
   // the chunk's table
   for (int i = tid; i < chunk / 4; i += kAdjThreads) reinterpret_cast<uint4*>(info)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = tid; i < chunk / 32; i += kAdjThreads) bits[i] = 0;
-  if (tid == 0) s_slots = 0;
+  if (tid == 0) s_slots = s_list = 0;
   Penalty pen{1.0f, 0.0f, 0.0f};
   if (a.rep) {
     const float r = __ldg(a.rep + b);
     if (r > 0.0f) pen.rep = r;
-    else if (blockIdx.x == 0 && tid == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    else if (blockIdx.y == 0 && tid == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
   }
   if (a.freq) pen.freq = __ldg(a.freq + b);
   if (a.pres) pen.pres = __ldg(a.pres + b);
   __syncthreads();
-  auto mark = [&](int t) { atomicOr(bits + (t >> 5), 1u << (t & 31)); };
+  // adds `bits` to token t's info; the first to do so lists it
+  auto mark = [&](int t, uint32_t bits) {
+    const uint32_t old = atomicOr(info + t, bits);
+    if ((old & ~kCount) == 0) list[atomicAdd(&s_list, 1)] = static_cast<uint16_t>(t);
+    return old;
+  };
   if (a.history) {
     int64_t hl = a.hist_len ? __ldg(a.hist_len + b) : a.max_hist;
     if (hl < 0 || hl > a.max_hist) {
-      if (blockIdx.x == 0 && tid == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      if (blockIdx.y == 0 && tid == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
       hl = hl < 0 ? 0 : a.max_hist;
     }
     const int64_t pl = a.prompt_len ? __ldg(a.prompt_len + b) : 0;
     const int32_t* h = a.history + b * a.max_hist;
-    for (int64_t i = tid; i < hl; i += kAdjThreads) {
-      const int64_t t = __ldg(h + i) - c0;
+    auto entry = [&](int32_t id, int64_t i) {
+      const int64_t t = id - c0;
       if (t >= 0 && t < len) {
+        mark(static_cast<int>(t), kSeen);
         if (i >= pl) atomicAdd(info + t, 1u);
-        atomicOr(info + t, kSeen);
-        mark(static_cast<int>(t));
       }
+    };
+    const int64_t quads = (reinterpret_cast<uintptr_t>(h) & 15) == 0 ? hl / 4 : 0;
+#pragma unroll 2
+    for (int64_t i = tid; i < quads; i += kAdjThreads) {
+      const int4 v = __ldg(reinterpret_cast<const int4*>(h) + i);
+      entry(v.x, 4 * i);
+      entry(v.y, 4 * i + 1);
+      entry(v.z, 4 * i + 2);
+      entry(v.w, 4 * i + 3);
     }
+    for (int64_t i = 4 * quads + tid; i < hl; i += kAdjThreads) entry(__ldg(h + i), i);
   }
   if (a.M > 0) {
     const int32_t* ids = a.bias_ids + static_cast<int64_t>(b) * a.M;
@@ -183,8 +218,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
       for (int j = i + 1; j < a.M; ++j)
         if (__ldg(ids + j) == id) s = __fadd_rn(s, __ldg(vals + j));
       bias[t] = s;
-      atomicOr(info + t, kBias);
-      mark(static_cast<int>(t));
+      mark(static_cast<int>(t), kBias);
     }
   }
   __syncthreads();
@@ -195,7 +229,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
     for (int m = 1 + tid; m < nodes; m += kAdjThreads) {
       const int64_t t = __ldg(tok + m) - c0;
       if (t < 0 || t >= len) continue;
-      const uint32_t old = atomicOr(info + t, kPath);
+      const uint32_t old = mark(static_cast<int>(t), kPath);
       if (!(old & kPath)) {
         const int j = atomicAdd(&s_slots, 1);
         if (spec_in(j, N, a.stats)) {
@@ -203,7 +237,6 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
           slot_info[j] = old;
           slot_head[j] = -1;
         }
-        mark(static_cast<int>(t));
       }
     }
     __syncthreads();
@@ -217,10 +250,12 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
     }
     __syncthreads();
   }
-  const int slots = a.draft_token ? s_slots : 0;
+  const int listed = s_list;
+  const bool in_place = a.in == a.out;
 
-  // rows: a warp takes a part of a row at a time (a whole chunk when there
-  // are rows enough for the warps)
+  // rows: a warp takes a part of a row at a time (a whole chunk when there are
+  // rows enough for the warps; smaller parts to even five rows out over eight
+  // warps cost more than they gave: 67 us against 60)
   int parts = 1;
   while (parts * nodes < kAdjWarps && chunk / (parts * 2) >= 32 * kv) parts *= 2;
   const int psize = chunk / parts;
@@ -235,112 +270,114 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
     if (a.allowed) {
       const int64_t r = a.allowed_row ? __ldg(a.allowed_row + row) : row;
       if (r >= a.mask_rows) {
-        if (blockIdx.x == 0 && p0 == 0 && lane == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+        if (blockIdx.y == 0 && p0 == 0 && lane == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
       } else if (r >= 0) {
         ok = reinterpret_cast<const uint32_t*>(a.allowed) + r * words + c0 / 32;
       }
     }
-    auto one = [&](int t) {  // element t of the chunk, unless it is a path token
-      const uint32_t e = info[t];
-      float x = adj_load<DT>(in, t);
-      if (!(e & kPath)) {
-        x = adj_value(x, e, (e & kBias) ? bias[t] : 0.0f, pen);
-        if (ok && !((__ldg(ok + (t >> 5)) >> (t & 31)) & 1u)) x = neg_inf();
+    // The row's listed tokens, several a lane at a time: begin loads their
+    // values and mask words, finish computes and stores them.  The first ones
+    // are loaded before the pass, whose stores leave these values as they are
+    auto begin = [&](auto& x, int first) {
+#pragma unroll
+      for (int q = 0; q < x.size; ++q) {
+        const int i = first + 32 * q;
+        x.tok[q] = i < listed ? list[i] : -1;
+        if (x.tok[q] < p0 || x.tok[q] >= p1) x.tok[q] = -1;
+        const int at = x.tok[q] < 0 ? p0 : x.tok[q];
+        x.word[q] = ok ? __ldg(ok + (at >> 5)) : ~0u;
+        if (x.tok[q] >= 0) x.val[q] = adj_load<DT>(in, at);
       }
-      adj_store<DT>(out, t, x);
     };
-    // aligned span of the part; rows whose input and output are aligned
-    // differently go element by element
-    const int ha = static_cast<int>(((16 - ((reinterpret_cast<uintptr_t>(in) + p0 * esz) & 15)) & 15) / esz);
-    const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    const int head = same ? min(ha, p1 - p0) : p1 - p0;
-    const int nvec = (p1 - p0 - head) / kv;
-    const int v0 = p0 + head;
-    for (int t = p0 + lane; t < v0; t += 32) one(t);
-    for (int i0 = 0; i0 < nvec; i0 += 32 * kAdjUnroll) {
-      uint4 raw[kAdjUnroll];
-      uint32_t al[kAdjUnroll];
+    auto finish = [&](auto& x) {
 #pragma unroll
-      for (int q = 0; q < kAdjUnroll; ++q) {
-        const int i = i0 + q * 32 + lane;
-        if (i < nvec) raw[q] = ld_plain(in + (v0 + i * kv) * esz);
+      for (int q = 0; q < x.size; ++q) {
+        const int t = x.tok[q];
+        if (t < 0 || !((x.word[q] >> (t & 31)) & 1u)) continue;  // masked: -inf already
+        uint32_t e = info[t];
+        if (e & kPath) {
+          const int j = static_cast<int>(e & ~kPath);
+          if (!spec_in(j, N, a.stats)) continue;
+          e = slot_info[j];
+          uint32_t extra = 0;
+          for (int m = slot_head[j]; m >= 0; m = next[m]) {
+            if (!spec_in(m, N, a.stats)) break;
+            extra += a.tree_mask ? (__ldg(a.tree_mask + row * N + m) != 0 ? 1u : 0u) : (m <= n ? 1u : 0u);
+          }
+          if (extra) e = (e | kSeen) + extra;
+        }
+        adj_store<DT>(out, t, adj_value(x.val[q], e, (e & kBias) ? bias[t] : 0.0f, pen));
       }
+    };
+    Listed<kAdjFirst> early;
+    begin(early, lane);
+    auto masked = [&](int t) { return ok && !((__ldg(ok + (t >> 5)) >> (t & 31)) & 1u); };
+    if (!in_place || ok) {
+      auto one = [&](int t) {
+        if (masked(t)) adj_store<DT>(out, t, neg_inf());
+        else if (DT == SPEC_BF16) reinterpret_cast<uint16_t*>(out)[t] = reinterpret_cast<const uint16_t*>(in)[t];
+        else reinterpret_cast<uint32_t*>(out)[t] = reinterpret_cast<const uint32_t*>(in)[t];
+      };
+      // aligned span of the part; rows whose input and output are aligned
+      // differently go element by element
+      const int ha = static_cast<int>(((16 - ((reinterpret_cast<uintptr_t>(in) + p0 * esz) & 15)) & 15) / esz);
+      const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+      const int head = same ? min(ha, p1 - p0) : p1 - p0;
+      const int nvec = (p1 - p0 - head) / kv;
+      const int v0 = p0 + head;
+      const bool whole = (v0 & (kv - 1)) == 0;
+      for (int t = p0 + lane; t < v0; t += 32) one(t);
+      uint32_t keep[kAdjUnroll], later[kAdjUnroll];  // mask bits of these vectors, of the next ones
+      auto load_bits = [&](int i0, uint32_t* k) {
 #pragma unroll
-      for (int q = 0; q < kAdjUnroll; ++q) {
-        const int i = i0 + q * 32 + lane;
-        al[q] = ok && i < nvec ? bits_at(ok, v0 + i * kv, kv) : (1u << kv) - 1u;
-      }
+        for (int q = 0; q < kAdjUnroll; ++q) {
+          const int i = i0 + q * 32;
+          k[q] = ok && i < nvec ? bits_at(ok, v0 + i * kv, kv, whole) : kAll;
+        }
+      };
+      load_bits(lane, later);
+      for (int i0 = lane; i0 < nvec; i0 += 32 * kAdjUnroll) {
+        uint4 raw[kAdjUnroll];
 #pragma unroll
-      for (int q = 0; q < kAdjUnroll; ++q) {
-        const int i = i0 + q * 32 + lane;
-        if (i >= nvec) continue;
-        const int t = v0 + i * kv;
-        const uint32_t special = bits_at(bits, t, kv);
-        uint32_t keep = al[q];
-        uint32_t* w = reinterpret_cast<uint32_t*>(&raw[q]);
-        if (special) {
-          for (uint32_t left = special; left; left &= left - 1) {
-            const int j = __ffs(left) - 1;
-            const uint32_t e = info[t + j];
-            if (e & kPath) {
-              keep |= 1u << j;  // as it is: fixed below
-              continue;
-            }
-            const float bv = (e & kBias) ? bias[t + j] : 0.0f;
+        for (int q = 0; q < kAdjUnroll; ++q) {
+          const int i = i0 + q * 32;
+          keep[q] = later[q];
+          if (i < nvec && keep[q] != 0) raw[q] = ld_plain(in + (v0 + i * kv) * esz);
+        }
+        load_bits(i0 + 32 * kAdjUnroll, later);
+#pragma unroll
+        for (int q = 0; q < kAdjUnroll; ++q) {
+          const int i = i0 + q * 32;
+          if (i >= nvec || (in_place && keep[q] == kAll)) continue;
+          uint4 v = raw[q];
+          if (keep[q] != kAll) {
+            if (keep[q] == 0) v = neg_inf_vec<DT>();
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
             if (DT == SPEC_BF16) {
-              const uint32_t word = j < 4 ? (j < 2 ? raw[q].x : raw[q].y) : (j < 6 ? raw[q].z : raw[q].w);
-              const float y = adj_value((j & 1) ? bf16_hi(word) : bf16_lo(word), e, bv, pen);
-              const uint32_t h = to_bf16(y);
-              const uint32_t nw = (j & 1) ? (word & 0xffffu) | (h << 16) : (word & 0xffff0000u) | h;
-              if (j < 2) raw[q].x = nw;
-              else if (j < 4) raw[q].y = nw;
-              else if (j < 6) raw[q].z = nw;
-              else raw[q].w = nw;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {  // bytes of the value, or of two -inf
+                const uint32_t k2 = keep[q] >> (2 * j);
+                w[j] = __byte_perm(w[j], 0xff80ff80u, 0x7654u - (k2 & 1u) * 0x44u - ((k2 >> 1) & 1u) * 0x4400u);
+              }
             } else {
-              const uint32_t word = j < 2 ? (j < 1 ? raw[q].x : raw[q].y) : (j < 3 ? raw[q].z : raw[q].w);
-              const uint32_t nw = __float_as_uint(adj_value(__uint_as_float(word), e, bv, pen));
-              if (j == 0) raw[q].x = nw;
-              else if (j == 1) raw[q].y = nw;
-              else if (j == 2) raw[q].z = nw;
-              else raw[q].w = nw;
-            }
-          }
-        }
-        if (keep != (1u << kv) - 1u) {
-          if (DT == SPEC_BF16) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (!(keep & (1u << (2 * j)))) w[j] = (w[j] & 0xffff0000u) | 0xff80u;
-              if (!(keep & (2u << (2 * j)))) w[j] = (w[j] & 0xffffu) | 0xff800000u;
+              for (int j = 0; j < 4; ++j)
+                if (!(keep[q] & (1u << j))) w[j] = 0xff800000u;
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!(keep & (1u << j))) w[j] = 0xff800000u;
+            v = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          st_vec(out + static_cast<int64_t>(v0 + i * kv) * esz, v);
         }
-        st_vec(out + static_cast<int64_t>(t) * esz, raw[q]);
       }
+      for (int t = v0 + nvec * kv + lane; t < p1; t += 32) one(t);
+      __syncwarp();
     }
-    for (int t = v0 + nvec * kv + lane; t < p1; t += 32) one(t);
-    // the row's path tokens; in place, the value read is the one that the
-    // pass above wrote back unchanged
-    __syncwarp();
-    for (int j = lane; j < slots; j += 32) {
-      const int t = slot_tok[j];
-      if (t < p0 || t >= p1) continue;
-      uint32_t e = slot_info[j];
-      uint32_t extra = 0;
-      for (int m = slot_head[j]; m >= 0; m = next[m]) {
-        if (!spec_in(m, N, a.stats)) break;
-        extra += a.tree_mask ? (__ldg(a.tree_mask + row * N + m) != 0 ? 1u : 0u) : (m <= n ? 1u : 0u);
-      }
-      if (extra) e = (e | kSeen) + extra;
-      float x = adj_value(adj_load<DT>(in, t), e, (e & kBias) ? bias[t] : 0.0f, pen);
-      if (ok && !((__ldg(ok + (t >> 5)) >> (t & 31)) & 1u)) x = neg_inf();
-      adj_store<DT>(out, t, x);
+    finish(early);
+    for (int first = lane + 32 * kAdjFirst; first < listed; first += 32 * kAdjBatch) {
+      Listed<kAdjBatch> more;
+      begin(more, first);
+      finish(more);
     }
-    __syncwarp();
   }
 }
 
@@ -377,9 +414,13 @@ extern "C" int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void
             history_lens_or_null, prompt_lens_or_null, rep_penalty_or_null, freq_penalty_or_null,
             pres_penalty_or_null, draft_token_or_null, tree_mask_or_null, bias_ids_or_null, bias_vals_or_null,
             max_bias, allowed_or_null, mask_rows, allowed_row_or_null, stats_or_null};
+  // the largest chunk that gives 1000 CTAs (608 are resident): a chunk scans
+  // the history once, but the one that holds the frequent ids has to be short
+  // beside the whole (V=32000, 16 rows: 69 us at 2048 tokens, 121 at 4096;
+  // V=128256, 64 rows: 819 and 782)
   int chunk = kAdjMaxChunk;
-  while (chunk > kAdjMinChunk && static_cast<int64_t>(B) * ((V + chunk - 1) / chunk) < 2 * 152) chunk /= 2;
-  const size_t smem = sizeof(uint32_t) * (static_cast<size_t>(chunk) * (max_bias > 0 ? 2 : 1) + chunk / 32 +
+  while (chunk > kAdjMinChunk && static_cast<int64_t>(B) * ((V + chunk - 1) / chunk) < 1000) chunk /= 2;
+  const size_t smem = sizeof(uint32_t) * (static_cast<size_t>(chunk) * (max_bias > 0 ? 2 : 1) + chunk / 2 +
                                           (draft_token_or_null ? 4 * static_cast<size_t>(N) : 0));
   auto kernel = dtype == SPEC_BF16 ? adjust_kernel<SPEC_BF16> : adjust_kernel<SPEC_F32>;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -387,7 +428,9 @@ extern "C" int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
-  const dim3 grid(static_cast<unsigned>((V + chunk - 1) / chunk), static_cast<unsigned>(B));
+  // chunks in order, each for all requests: frequent ids crowd at the front of a
+  // vocabulary, and the CTAs with the most to do should not come last
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((V + chunk - 1) / chunk));
   launch_k(kernel, grid, kAdjThreads, smem, reinterpret_cast<cudaStream_t>(stream), a, chunk);
   return launch_status();
 }
