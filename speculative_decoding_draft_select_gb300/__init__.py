@@ -12,6 +12,7 @@ build(debug=True)); spec_debug_bounds reads its count.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -144,7 +145,8 @@ def _call(name, *args):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a Stream object around it (3 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t):
@@ -472,9 +474,26 @@ def spec_filter_logits(logits, T, top_k=0, top_p=1.0, stats=None):
     return logits
 
 
-def _entries(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _device(t, name):
+    """t's device index, which has to be the current device: the launch goes
+    to its current stream."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of this type, shape and device (None of
+    None).  One test in the common case: these calls are a few microseconds."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def spec_adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, rep_penalty=None, freq_penalty=None,
@@ -486,46 +505,33 @@ def spec_adjust_logits(logits, history=None, history_lens=None, prompt_lens=None
     penalties [B] f32; draft_token [B, N] and tree_mask [B, N, N] give each
     row's path; bias_ids / bias_vals [B, M]; allowed [rows, ceil(V / 32)]
     int32 bit masks with allowed_row [B, N].  Returns the adjusted tensor."""
-    _dev(logits, name="logits")
+    dev = _device(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits must be [B, N, V]")
-    B, N, V = logits.shape
-    out = logits if out is None else _dev(out, logits.dtype, "out")
-    _entries("out", out, logits.shape)
-    i32, f32 = torch.int32, torch.float32
-    for name, t, dtype, shape in (
-            ("history_lens", history_lens, i32, (B,)), ("prompt_lens", prompt_lens, i32, (B,)),
-            ("rep_penalty", rep_penalty, f32, (B,)), ("freq_penalty", freq_penalty, f32, (B,)),
-            ("pres_penalty", pres_penalty, f32, (B,)), ("draft_token", draft_token, i32, (B, N)),
-            ("tree_mask", tree_mask, torch.uint8, (B, N, N)), ("allowed_row", allowed_row, i32, (B, N)),
-            ("num_nodes", num_nodes, i32, (B,))):
-        if t is not None:
-            _dev(t, dtype, name)
-            _entries(name, t, shape)
-    H = M = rows = 0
-    if history is not None:
-        _dev(history, i32, "history")
-        H = history.shape[-1]
-        _entries("history", history, (B, H))
-    if bias_ids is not None:
-        _dev(bias_ids, i32, "bias_ids")
-        M = bias_ids.shape[-1]
-        _entries("bias_ids", bias_ids, (B, M))
-        if bias_vals is None:
-            raise ValueError("bias_ids needs bias_vals")
-        _dev(bias_vals, f32, "bias_vals")
-        _entries("bias_vals", bias_vals, (B, M))
-    if allowed is not None:
-        _dev(allowed, i32, "allowed")
-        rows = allowed.numel() // ((V + 31) // 32)
-        _entries("allowed", allowed.view(-1, allowed.shape[-1]), (rows, (V + 31) // 32))
-    _dev(stats, i32, "stats")
-    _same_device(logits, out, history, history_lens, prompt_lens, rep_penalty, freq_penalty, pres_penalty, draft_token,
-                 tree_mask, bias_ids, bias_vals, allowed, allowed_row, num_nodes, stats)
-    _call("spec_adjust_logits", B, N, V, _logit_code(logits), _ptr(logits), _ptr(out), _ptr(num_nodes), _ptr(history),
-          H, _ptr(history_lens), _ptr(prompt_lens), _ptr(rep_penalty), _ptr(freq_penalty), _ptr(pres_penalty),
-          _ptr(draft_token), _ptr(tree_mask), _ptr(bias_ids), _ptr(bias_vals), M, _ptr(allowed), rows,
-          _ptr(allowed_row), _ptr(stats), _stream())
+    shape = logits.shape
+    B, N, V = shape
+    code = _logit_code(logits)
+    src = _arg(logits, logits.dtype, shape, dev, "logits")
+    out = logits if out is None else out
+    dst = _arg(out, logits.dtype, shape, dev, "out")
+    i32, f32, one, two = torch.int32, torch.float32, (B,), (B, N)
+    H = history.shape[-1] if history is not None else 0
+    M = bias_ids.shape[-1] if bias_ids is not None else 0
+    if (bias_ids is None) != (bias_vals is None):
+        raise ValueError("bias_ids and bias_vals go together")
+    words = (V + 31) // 32
+    rows = allowed.numel() // words if allowed is not None else 0
+    rc = lib().spec_adjust_logits(
+        B, N, V, code, src, dst, _arg(num_nodes, i32, one, dev, "num_nodes"),
+        _arg(history, i32, (B, H), dev, "history"), H, _arg(history_lens, i32, one, dev, "history_lens"),
+        _arg(prompt_lens, i32, one, dev, "prompt_lens"), _arg(rep_penalty, f32, one, dev, "rep_penalty"),
+        _arg(freq_penalty, f32, one, dev, "freq_penalty"), _arg(pres_penalty, f32, one, dev, "pres_penalty"),
+        _arg(draft_token, i32, two, dev, "draft_token"), _arg(tree_mask, torch.uint8, (B, N, N), dev, "tree_mask"),
+        _arg(bias_ids, i32, (B, M), dev, "bias_ids"), _arg(bias_vals, f32, (B, M), dev, "bias_vals"), M,
+        _arg(allowed, i32, (rows, words), dev, "allowed"), rows, _arg(allowed_row, i32, two, dev, "allowed_row"),
+        _arg(stats, i32, (NUM_STATS,), dev, "stats"), _stream())
+    if rc:
+        raise SpecError("spec_adjust_logits", rc)
     return out
 
 
@@ -576,59 +582,51 @@ def spec_kv4_slot_bytes(Hkv, D) -> int:
     return n
 
 
-def _same_device(like, *tensors):
-    """The launch goes to the current device's current stream."""
-    if like.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {like.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != like.device:
-            raise ValueError(f"tensors are on {like.device} and {t.device}")
-
-
 def _rows(t, name):
     """Row stride (elements) of t [B, N, H, D]: heads contiguous, rows (b, n)
     evenly spaced (a slice of a fused projection qualifies)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, N, heads, D]")
     B, N, H, D = t.shape
-    row = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else H * D)
-    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or (B > 1 and N > 1 and t.stride(0) != N * row):
+    sb, sn, sh, sd = t.stride()
+    row = sn if N > 1 else (sb if B > 1 else H * D)
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or (sb != N * row and B > 1 and N > 1):
         raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
     return row
 
 
-def _kv4_pool(pool, table, lens, num_nodes, B, name="kv_pool"):
-    """(num_slots, slot_stride) of a pool [slots, bytes] whose rows may be
-    part of wider ones (a layer's columns of a slot)."""
-    if not pool.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if pool.dtype != torch.uint8 or pool.dim() != 2 or pool.stride(1) != 1:
-        raise ValueError(f"{name} must be uint8 [slots, bytes] with contiguous rows")
-    _dev(table, torch.int32, "req_to_token")
-    _dev(lens, torch.int32, "seq_lens")
-    _dev(num_nodes, torch.int32, "num_nodes")
-    if table.dim() != 2 or table.shape[0] < B or lens.numel() < B or (num_nodes is not None and num_nodes.numel() < B):
-        raise ValueError("req_to_token [B, max_ctx], seq_lens [B] and num_nodes [B] need an entry per request")
-    return pool.shape[0], pool.stride(0) if pool.shape[0] > 1 else max(pool.stride(0), pool.shape[1])
+def _kv4_pool(pool, table, B, H, D, dev):
+    """(pool, slots, slot stride, table, max_ctx) of a pool [slots, bytes]
+    whose rows may be part of wider ones (a layer's columns of a slot)."""
+    if pool.dtype is not torch.uint8 or pool.dim() != 2 or pool.get_device() != dev or pool.stride(1) != 1:
+        raise ValueError(f"kv_pool must be uint8 [slots, bytes] with contiguous rows on cuda:{dev}")
+    slots, width = pool.shape
+    if D not in (64, 128) or not 0 < H <= 256:
+        raise SpecError("4-bit cache of these heads", -2)
+    if width < H * (D + D // 4):
+        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
+    if table.dim() != 2 or table.shape[0] < B:
+        raise ValueError("req_to_token must be [B, max_ctx]")
+    return (pool.data_ptr(), slots, pool.stride(0) if slots > 1 else max(pool.stride(0), width),
+            _arg(table, torch.int32, table.shape, dev, "req_to_token"), table.shape[1])
 
 
 def spec_kv4_append(k, v, kv_pool, req_to_token, seq_lens, num_nodes=None, stats=None):
     """Quantises k, v [B, N, Hkv, D] (bf16 or f32; rows may be strided) into
     kv_pool [slots, bytes] uint8 at positions seq_lens[b] + n, n < num_nodes[b]
     (None: all N).  Returns kv_pool."""
+    dev = _device(k, "k")
     ks, vs = _rows(k, "k"), _rows(v, "v")
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must have the same shape and dtype")
+    if v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != dev:
+        raise ValueError("k and v must have the same shape, dtype and device")
     B, N, H, D = k.shape
-    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
-    if kv_pool.shape[1] < spec_kv4_slot_bytes(H, D):
-        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
-    _dev(stats, torch.int32, "stats")
-    _same_device(k, v, kv_pool, req_to_token, seq_lens, num_nodes, stats)
-    _call("spec_kv4_append", B, N, H, D, _logit_code(k), _ptr(k), ks, _ptr(v), vs, _ptr(num_nodes), _ptr(seq_lens),
-          _ptr(req_to_token), req_to_token.shape[1], _ptr(kv_pool), slots, stride, _ptr(stats), _stream())
+    pool, slots, stride, table, ctx = _kv4_pool(kv_pool, req_to_token, B, H, D, dev)
+    i32 = torch.int32
+    rc = lib().spec_kv4_append(B, N, H, D, _logit_code(k), k.data_ptr(), ks, v.data_ptr(), vs,
+                               _arg(num_nodes, i32, (B,), dev, "num_nodes"), _arg(seq_lens, i32, (B,), dev, "seq_lens"),
+                               table, ctx, pool, slots, stride, _arg(stats, i32, (NUM_STATS,), dev, "stats"), _stream())
+    if rc:
+        raise SpecError("spec_kv4_append", rc)
     return kv_pool
 
 
@@ -636,22 +634,23 @@ def spec_kv4_gather(kv_pool, req_to_token, seq_lens, N, Hkv, D, dtype=torch.bflo
                     stats=None):
     """Reads positions seq_lens[b] + n, n < N, back as (k, v) [B, N, Hkv, D]
     of dtype (bf16 or f32).  Rows n >= num_nodes[b] are left as they were."""
+    dev = _device(kv_pool, "kv_pool")
     B = seq_lens.numel()
-    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
-    if kv_pool.shape[1] < spec_kv4_slot_bytes(Hkv, D):
-        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
-    k = _out(k, (B, N, Hkv, D), dtype, kv_pool, "k")
-    v = _out(v, (B, N, Hkv, D), dtype, kv_pool, "v")
-    if k.shape != (B, N, Hkv, D) or v.shape != k.shape:
-        raise ValueError("k and v must be [B, N, Hkv, D]")
-    _dev(stats, torch.int32, "stats")
-    _same_device(kv_pool, req_to_token, seq_lens, num_nodes, k, v, stats)
-    _call("spec_kv4_gather", B, int(N), int(Hkv), int(D), _logit_code(k), _ptr(kv_pool), slots, stride,
-          _ptr(num_nodes), _ptr(seq_lens), _ptr(req_to_token), req_to_token.shape[1], _ptr(k), _ptr(v), _ptr(stats),
-          _stream())
+    shape = (B, N, Hkv, D)
+    pool, slots, stride, table, ctx = _kv4_pool(kv_pool, req_to_token, B, Hkv, D, dev)
+    k = torch.empty(shape, dtype=dtype, device=kv_pool.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=kv_pool.device) if v is None else v
+    i32 = torch.int32
+    rc = lib().spec_kv4_gather(B, N, Hkv, D, _logit_code(k), pool, slots, stride,
+                               _arg(num_nodes, i32, (B,), dev, "num_nodes"), _arg(seq_lens, i32, (B,), dev, "seq_lens"),
+                               table, ctx, _arg(k, dtype, shape, dev, "k"), _arg(v, dtype, shape, dev, "v"),
+                               _arg(stats, i32, (NUM_STATS,), dev, "stats"), _stream())
+    if rc:
+        raise SpecError("spec_kv4_gather", rc)
     return k, v
 
 
+@functools.lru_cache(maxsize=256)  # of the sizes alone
 def spec_kv4_attention_ws_size(B, N, Hq, Hkv, D) -> int:
     n = int(lib().spec_kv4_attention_ws_size(int(B), int(N), int(Hq), int(Hkv), int(D)))
     if n == 0:
@@ -667,35 +666,32 @@ def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_ma
     lse [B, N, Hq] f32 (optional) receives the log of the weights' sum.  ws:
     a uint8 workspace of spec_kv4_attention_ws_size bytes to reuse between
     calls that do not overlap.  Returns out [B, N, Hq, D] bf16."""
+    dev = _device(q, "q")
     qs = _rows(q, "q")
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise ValueError("q must be bfloat16")
-    B, N, Hq, D = q.shape
-    Hkv = int(num_kv_heads)
-    slots, stride = _kv4_pool(kv_pool, req_to_token, seq_lens, num_nodes, B)
-    if kv_pool.shape[1] < spec_kv4_slot_bytes(Hkv, D):
-        raise ValueError("kv_pool rows are shorter than spec_kv4_slot_bytes")
-    if Hq % Hkv:
+    shape = q.shape
+    B, N, Hq, D = shape
+    pool, slots, stride, table, ctx = _kv4_pool(kv_pool, req_to_token, B, num_kv_heads, D, dev)
+    if Hq % num_kv_heads:
         raise ValueError("the number of query heads must be a multiple of num_kv_heads")
-    out = _out(out, q.shape, torch.bfloat16, q, "out")
-    _entries("out", out, q.shape)
-    if tree_mask is not None:
-        _dev(tree_mask, torch.uint8, "tree_mask")
-        _entries("tree_mask", tree_mask, (B, N, N))
-    if lse is not None:
-        _dev(lse, torch.float32, "lse")
-        _entries("lse", lse, (B, N, Hq))
+    out = torch.empty(shape, dtype=torch.bfloat16, device=q.device) if out is None else out
+    i32 = torch.int32
+    dst = _arg(out, torch.bfloat16, shape, dev, "out")
+    lse_at = _arg(lse, torch.float32, (B, N, Hq), dev, "lse")
+    mask = _arg(tree_mask, torch.uint8, (B, N, N), dev, "tree_mask")
     if q.numel() == 0:
         return out
     if ws is None:
-        ws = torch.empty(spec_kv4_attention_ws_size(B, N, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
-    _dev(ws, torch.uint8, "ws")
-    _dev(stats, torch.int32, "stats")
-    _same_device(q, kv_pool, req_to_token, seq_lens, num_nodes, tree_mask, out, lse, ws, stats)
-    _call("spec_kv4_attention", B, N, Hq, Hkv, D, _ptr(q), qs, _ptr(kv_pool), slots, stride, _ptr(num_nodes),
-          _ptr(seq_lens), _ptr(req_to_token), req_to_token.shape[1], _ptr(tree_mask),
-          float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(stats), _ptr(ws), ws.numel(),
-          _stream())
+        ws = torch.empty(spec_kv4_attention_ws_size(B, N, Hq, num_kv_heads, D), dtype=torch.uint8, device=q.device)
+    rc = lib().spec_kv4_attention(B, N, Hq, num_kv_heads, D, q.data_ptr(), qs, pool, slots, stride,
+                                  _arg(num_nodes, i32, (B,), dev, "num_nodes"),
+                                  _arg(seq_lens, i32, (B,), dev, "seq_lens"), table, ctx, mask,
+                                  D ** -0.5 if scale is None else scale, dst, lse_at,
+                                  _arg(stats, i32, (NUM_STATS,), dev, "stats"),
+                                  _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel(), _stream())
+    if rc:
+        raise SpecError("spec_kv4_attention", rc)
     return out
 
 
