@@ -132,7 +132,7 @@ struct Filler {
     loaded = more;
     if (!more) return;
     const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + static_cast<int>(threadIdx.x & (P - 1));
-    slot = pos < ap.end ? __ldg(row + next_tile * kTile) : -2;
+    slot = pos < ap.end && spec_in(pos, ap.end, nullptr) ? __ldg(row + next_tile * kTile) : -2;
     ++next_tile;
   }
   // Copies the tile whose slots were loaded last; one commit group, empty
@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
               bool see = (there >> at) & 1u;
               if (see && node >= 0) {
                 const int r = mt * 16 + g + 8 * (i >> 1), n = attn_node(a, r0 + r);
-                see = r < rows && (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0
-                                          : node <= n);
+                see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
+                      (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
               }
               if (!see) s[mt][j][i] = neg_inf();
             }
@@ -643,8 +643,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
             bool see = (there >> at) & 1u;
             if (see && node >= 0) {
               const int n = attn_node(a, r);
-              see = r < rows && (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0
-                                        : node <= n);
+              see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
+                    (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
             }
             if (!see) s[u][i] = neg_inf();
           }
@@ -760,25 +760,23 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
   cp_async_wait<0>();
 }
 
-template <class K>
-int launch_rows(K kernel, AttnArgs& a, int D, int R, size_t smem, int ctas, cudaStream_t s) {
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess) {
+template <auto KERNEL, int D, int R>
+int launch_rows(AttnArgs& a, int dev, size_t smem, int ctas, cudaStream_t s) {
+  if (!attn_smem<KERNEL>(dev, smem)) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
   a.ctas = ctas < kMaxCtas ? ctas : kMaxCtas;
-  launch_k(kernel, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
-  if (D == 128) launch_merge<128>(a, R, kWeightExp, s);
-  else launch_merge<64>(a, R, kWeightExp, s);
+  launch_k(KERNEL, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
+  launch_merge<D>(a, R, kWeightExp, s);
   return launch_status();
 }
 
 template <int D>
-int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
-  if (R == 8) return launch_rows(kv4_attention8_kernel<D>, a, D, R, sizeof(AttShared8<D>), sms * 3, s);
-  if (R == 16) return launch_rows(kv4_attention_kernel<D, 1>, a, D, R, sizeof(AttShared<D, 1>), sms * 3, s);
-  return launch_rows(kv4_attention_kernel<D, 2>, a, D, R, sizeof(AttShared<D, 2>), sms * 2, s);
+int launch_few(AttnArgs& a, int R, int dev, int sms, cudaStream_t s) {
+  if (R == 8) return launch_rows<kv4_attention8_kernel<D>, D, 8>(a, dev, sizeof(AttShared8<D>), sms * 3, s);
+  if (R == 16) return launch_rows<kv4_attention_kernel<D, 1>, D, 16>(a, dev, sizeof(AttShared<D, 1>), sms * 3, s);
+  return launch_rows<kv4_attention_kernel<D, 2>, D, 32>(a, dev, sizeof(AttShared<D, 2>), sms * 2, s);
 }
 
 // Rows of a row tile here: 8 or 16 where they suffice, else 32; 0: more rows
@@ -817,9 +815,9 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
     if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return SPEC_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return SPEC_ERR_INVALID_ARG;
   if (ws_bytes < spec_kv4_attention_ws_size(B, N, Hq, Hkv, D)) return SPEC_ERR_WORKSPACE;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  int dev = 0;
+  const int sms = attn_sms(dev);
+  if (sms == 0) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
@@ -829,6 +827,6 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
              scale * kLog2e, static_cast<uint16_t*>(out), lse_or_null, static_cast<float*>(ws), 0, stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int R = rows_of(static_cast<int64_t>(N) * a.G);
-  if (R == 0) return launch_tree_attention(a, D, sms, s);
-  return D == 128 ? launch_few<128>(a, R, sms, s) : launch_few<64>(a, R, sms, s);
+  if (R == 0) return launch_tree_attention(a, D, dev, sms, s);
+  return D == 128 ? launch_few<128>(a, R, dev, sms, s) : launch_few<64>(a, R, dev, sms, s);
 }

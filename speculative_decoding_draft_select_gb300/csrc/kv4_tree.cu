@@ -102,7 +102,7 @@ __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int n = min(nb + q, n_hi);
-      const uint8_t* row = mask + n * a.N;
+      const uint8_t* row = mask + (spec_in(n, a.N, a.stats) ? n : 0) * a.N;
 #pragma unroll
       for (int w = 0; w < 4; ++w) on[q][w] = a.mask ? __ldg(row + at[w]) : static_cast<uint8_t>(at[w] <= n);
     }
@@ -629,12 +629,11 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 }
 
 template <int D, int MT>
-int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
+int launch_tree(AttnArgs a, int dev, int sms, cudaStream_t s) {
   using C = TreeCfg<D, MT>;
   constexpr int R = kTreeRows * MT;
-  auto kernel = kv4_tree_kernel<D, MT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem)) !=
-      cudaSuccess) {
+  constexpr auto kernel = kv4_tree_kernel<D, MT>;
+  if (!attn_smem<kernel>(dev, C::kSmem)) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
@@ -647,10 +646,10 @@ int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s) {
+int launch_tree_attention(AttnArgs a, int D, int dev, int sms, cudaStream_t s) {
   const bool two = static_cast<int64_t>(a.N) * a.G > kTreeRows;
-  if (D == 128) return two ? launch_tree<128, 2>(a, sms, s) : launch_tree<128, 1>(a, sms, s);
-  return two ? launch_tree<64, 2>(a, sms, s) : launch_tree<64, 1>(a, sms, s);
+  if (D == 128) return two ? launch_tree<128, 2>(a, dev, sms, s) : launch_tree<128, 1>(a, dev, sms, s);
+  return two ? launch_tree<64, 2>(a, dev, sms, s) : launch_tree<64, 1>(a, dev, sms, s);
 }
 
 }  // namespace specdec

@@ -22,6 +22,13 @@ spec_verify_sample_qlogits on the draft logits plus the per-row (max,
 normaliser) the draft kernel records (q_mode "logits": no q is written; the
 q values are bit-identical).  Compaction: spec_compact_slots.
 
+Between draft and verify lies the target's forward over the tree's nodes,
+which is the caller's model; what depends on the tree and on the cache's
+addressing is here: run_kv4_append writes the nodes' K and V into a 4-bit
+kv_pool, run_attention attends over it under the tree mask, and run_adjust
+applies penalties, biases and grammar masks to the target logits of every
+node, its own path counted.  run_compact moves the same kv_pool's rows.
+
 All buffers are allocated once in ``StepBuffers``; a step only enqueues
 kernels on the current stream, so a whole step can be captured once in a
 CUDA graph (``capture_step``) and replayed: the same kernels, without the
@@ -31,7 +38,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (new_pool, new_stats, spec_build_tree, spec_compact_freed_capacity, spec_compact_slots,
+from . import (new_pool, new_stats, spec_adjust_logits, spec_build_tree, spec_compact_freed_capacity,
+               spec_compact_slots, spec_kv4_append, spec_kv4_attention, spec_kv4_attention_ws_size,
                spec_softmax_sample, spec_softmax_topk, spec_verify_greedy, spec_verify_sample,
                spec_verify_sample_qlogits, spec_verify_ws_size, tli_constrain_map, tli_constrain_map_qlogits,
                tli_plan_build, tli_plan_bytes)
@@ -93,6 +101,7 @@ class StepBuffers:
         self.ws = torch.empty(max(spec_verify_ws_size(B, N), 256), dtype=torch.uint8, device=dev)
         self.verify_out = None
         self.stats = new_stats(dev)
+        self.attention_ws = None  # run_attention's, kept from its first call
         self.compact_out = None
         if page_size:
             cap = spec_compact_freed_capacity(B, N, page_size)
@@ -165,6 +174,32 @@ def run_draft(buf: StepBuffers, draft_table, T, root_token, seq_lens, draft_u=No
             timer.end(s)
     spec_build_tree(buf.pool, buf.N, root_token, seq_lens, out=buf.tree)
     return buf.tree
+
+
+def run_kv4_append(buf: StepBuffers, k, v, seq_lens, req_to_token, kv_pool, num_nodes=None):
+    """K and V [B, N, Hkv, D] of buf.tree's nodes into the 4-bit kv_pool."""
+    return spec_kv4_append(k, v, kv_pool, req_to_token, seq_lens, num_nodes=num_nodes, stats=buf.stats)
+
+
+def run_attention(buf: StepBuffers, q, seq_lens, req_to_token, kv_pool, num_kv_heads, scale=None, num_nodes=None,
+                  out=None, lse=None):
+    """Attention of q [B, N, Hq, D] of buf.tree's nodes over context and tree
+    (their K and V appended before).  The workspace is allocated by the first
+    call and kept, so that a captured step has one of its own."""
+    B, N, Hq, D = q.shape
+    need = spec_kv4_attention_ws_size(B, N, Hq, int(num_kv_heads), D)
+    if buf.attention_ws is None or buf.attention_ws.numel() < need:
+        buf.attention_ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask=buf.tree["tree_mask"],
+                              scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=buf.attention_ws, stats=buf.stats)
+
+
+def run_adjust(buf: StepBuffers, target, out=None, **penalties):
+    """spec_adjust_logits of target [B, N, V] with buf.tree's paths (in place
+    without ``out``); penalties: its history, penalty, bias and mask
+    arguments.  Comes before spec_filter_logits and run_verify."""
+    return spec_adjust_logits(target, draft_token=buf.tree["draft_token"], tree_mask=buf.tree["tree_mask"], out=out,
+                              stats=buf.stats, **penalties)
 
 
 def run_verify(buf: StepBuffers, target, mode, T=1.0, coins=None, u_final=None, budget=None, eos_id=-1,
