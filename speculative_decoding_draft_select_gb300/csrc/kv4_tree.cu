@@ -116,72 +116,62 @@ __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int
   }
 }
 
-// A thread's row of S, 32 columns (a word of `see`) at a time with the next 32
-// on their way: the largest element that `see` shows, and the weights
-// 2^(S c - base) as fp16 over S's first columns (column i of P holds positions
-// 2 i and 2 i + 1; it never reaches columns that are still to be read), with
-// their fp32 sum.  Words that every lane sees whole skip the mask.  One form,
-// two words an iteration: the code of all roles has to stay small (at 106 KB
-// instruction fetches were what a tile waited for).
+// A thread's row of S, 32 columns (a word of `see`) at a time: the largest
+// element that `see` shows, and the weights 2^(S c - base) as fp16 over S's
+// first columns (column i of P holds positions 2 i and 2 i + 1; it never
+// reaches columns that are still to be read), with their fp32 sum.  Words that
+// every lane sees whole skip the mask.  A word an iteration and none ahead: a
+// load from tensor memory takes some 30 cycles, and the code of all roles has
+// to stay small, since instruction fetches are what a tile waits for.
+__device__ __forceinline__ uint32_t pick(const uint32_t* v, int i) {
+  return i < 2 ? (i == 0 ? v[0] : v[1]) : (i == 2 ? v[2] : v[3]);
+}
 __device__ __forceinline__ float row_max(uint32_t col, const uint32_t* see) {
-  uint32_t x[2][32];
+  uint32_t x[32];
   float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-  tc::ld32(col, x[0]);
 #pragma unroll 1
-  for (int w = 0; w < kTT / 32; w += 2) {
+  for (int w = 0; w < kTT / 32; ++w) {
+    const uint32_t sw = pick(see, w);
+    tc::ld32(col + 32 * w, x);
+    tc::wait_ld32(x);
+    if (__any_sync(0xffffffffu, sw != ~0u)) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t sw = w == 0 ? see[q] : see[2 + q];
-      tc::wait_ld32(x[q]);
-      // the load behind the last one rereads S's first columns
-      tc::ld32(col + ((32 * (w + q + 1)) & (kTT - 1)), x[q ^ 1]);
-      if (__any_sync(0xffffffffu, sw != ~0u)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!((sw >> i) & 1u)) x[q][i] = 0xff800000u;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(x[q][i]));
+      for (int i = 0; i < 32; ++i)
+        if (!((sw >> i) & 1u)) x[i] = 0xff800000u;
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(x[i]));
   }
-  tc::wait_ld32(x[0]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 __device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, float c, float base) {
-  uint32_t x[2][32], y[16];
+  uint32_t x[32], y[16];
   const float2 c2 = splat(c), nb2 = splat(-base);
   float2 acc[2] = {splat(0.0f), splat(0.0f)};
-  tc::ld32(col, x[0]);
 #pragma unroll 1
-  for (int w = 0; w < kTT / 32; w += 2) {
+  for (int w = 0; w < kTT / 32; ++w) {
+    const uint32_t sw = pick(see, w);
+    tc::ld32(col + 32 * w, x);
+    tc::wait_ld32(x);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t sw = w == 0 ? see[q] : see[2 + q];
-      tc::wait_ld32(x[q]);
-      // behind the last: columns that P does not reach (it ends at 64)
-      tc::ld32(col + min(32 * (w + q + 1), kTT - 32), x[q ^ 1]);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 e =
-            exp2_2(fma2(make_float2(__uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1])), c2, nb2));
-        x[q][i] = __float_as_uint(e.x);
-        x[q][i + 1] = __float_as_uint(e.y);
-      }
-      if (__any_sync(0xffffffffu, sw != ~0u)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!((sw >> i) & 1u)) x[q][i] = 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 e = make_float2(__uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
-        acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], e);
-        y[i / 2] = h2_u32(__floats2half2_rn(e.x, e.y));
-      }
-      tc::st16(col + 16 * (w + q), y);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 e = exp2_2(fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, nb2));
+      x[i] = __float_as_uint(e.x);
+      x[i + 1] = __float_as_uint(e.y);
     }
+    if (__any_sync(0xffffffffu, sw != ~0u)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!((sw >> i) & 1u)) x[i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 e = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], e);
+      y[i / 2] = h2_u32(__floats2half2_rn(e.x, e.y));
+    }
+    tc::st16(col + 16 * w, y);
   }
-  tc::wait_ld32(x[0]);
   const float2 t = add2(acc[0], acc[1]);
   return t.x + t.y;
 }
@@ -331,7 +321,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
                                         (((ch % 64 / 8) ^ (rr & 7)) << 4));
       };
       auto store_q = [&]() {
-#pragma unroll 2
+#pragma unroll 1
         for (int r = q_row; r < R; r += UT / 8) {
           const uint16_t* src = a.q + attn_q(a, p.b, p.h, r0 + min(r, rows - 1), D) + sub * per;
 #pragma unroll
@@ -339,7 +329,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         }
         cp_async_commit();
         cp_async_wait<0>();
-#pragma unroll 2
+#pragma unroll 1
         for (int r = q_row; r < R; r += UT / 8) {
           // the largest magnitude: bf16 bits without the sign compare as integers
           uint32_t big = 0;
