@@ -41,6 +41,7 @@ constexpr int kAdjMinChunk = 512;
 constexpr int kAdjUnroll = 4;       // 16-byte vectors in flight per lane
 constexpr int kAdjFirst = 2;        // listed tokens in flight per lane beside the pass
 constexpr int kAdjBatch = 4;        // and behind it
+constexpr int kAdjSort = 128;       // more listed tokens than this are put in order
 
 constexpr uint32_t kPath = 1u << 31, kSeen = 1u << 30, kBias = 1u << 29, kCount = kBias - 1;
 
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
   if (!spec_smem_ok(reinterpret_cast<char*>(a.draft_token ? next + N : slot_tok) - reinterpret_cast<char*>(adj_sm),
                     a.stats))
     return;
-  __shared__ int s_slots, s_list;
+  __shared__ int s_slots, s_list, s_sorted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int nodes = N;
   if (a.num_nodes) nodes = min(max(__ldg(a.num_nodes + b), 0), N);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
 
   // the chunk's table
   for (int i = tid; i < chunk / 4; i += kAdjThreads) reinterpret_cast<uint4*>(info)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) s_slots = s_list = 0;
+  if (tid == 0) s_slots = s_list = s_sorted = 0;
   Penalty pen{1.0f, 0.0f, 0.0f};
   if (a.rep) {
     const float r = __ldg(a.rep + b);
@@ -251,6 +252,19 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
     __syncthreads();
   }
   const int listed = s_list;
+  if (listed > kAdjSort) {
+    // where histories crowd, the list in the order of the tokens (by 32): its
+    // accesses then share sectors
+    for (int t = tid; t < chunk; t += kAdjThreads) {
+      const bool has = info[t] != 0;
+      const uint32_t votes = __ballot_sync(0xffffffffu, has);
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_sorted, __popc(votes));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
+      if (has && spec_in(at, chunk, a.stats)) list[at] = static_cast<uint16_t>(t);
+    }
+    __syncthreads();
+  }
   const bool in_place = a.in == a.out;
 
   // rows: a warp takes a part of a row at a time (a whole chunk when there are
