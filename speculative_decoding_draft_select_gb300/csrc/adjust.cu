@@ -25,8 +25,9 @@
 // -inf whatever else holds of it, so the pass leaves every value that is still
 // needed, in place too; in place without a mask only the listed tokens are
 // touched at all.  (Looking the bits of every vector up in the pass instead
-// took 128 instructions a vector where histories crowd: 890 us against 764 at
-// 64-node trees, B=128, V=128256.)
+// took 128 instructions a vector where histories crowd: 64-node trees, B=128,
+// V=128256, bf16: 890 us.)  Measured there: 757 us for 4.26 GB, 5.6 TB/s; the
+// listed tokens take 40 of them, the masks' bits 64, histories 30.
 #include <climits>
 
 #include "common.cuh"
@@ -39,7 +40,7 @@ constexpr int kAdjWarps = kAdjThreads / 32;
 constexpr int kAdjMaxChunk = 4096;  // tokens of a chunk: 16 KB of info, 16 KB of biases
 constexpr int kAdjMinChunk = 512;
 constexpr int kAdjUnroll = 4;       // 16-byte vectors in flight per lane
-constexpr int kAdjFirst = 2;        // listed tokens in flight per lane beside the pass
+constexpr int kAdjFirst = 1;        // listed tokens in flight per lane beside the pass
 constexpr int kAdjBatch = 4;        // and behind it
 constexpr int kAdjSort = 128;       // more listed tokens than this are put in order
 
@@ -254,7 +255,8 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
   const int listed = s_list;
   if (listed > kAdjSort) {
     // where histories crowd, the list in the order of the tokens (by 32): its
-    // accesses then share sectors
+    // accesses then share sectors (V=32000, 16 rows, 8000 ids of history: 69 us
+    // without, 62 with)
     for (int t = tid; t < chunk; t += kAdjThreads) {
       const bool has = info[t] != 0;
       const uint32_t votes = __ballot_sync(0xffffffffu, has);
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
 
   // rows: a warp takes a part of a row at a time (a whole chunk when there are
   // rows enough for the warps; smaller parts to even five rows out over eight
-  // warps cost more than they gave: 67 us against 60)
+  // warps cost more than they gave: 63 us against 59)
   int parts = 1;
   while (parts * nodes < kAdjWarps && chunk / (parts * 2) >= 32 * kv) parts *= 2;
   const int psize = chunk / parts;
@@ -340,7 +342,21 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
       const int nvec = (p1 - p0 - head) / kv;
       const int v0 = p0 + head;
       const bool whole = (v0 & (kv - 1)) == 0;
-      for (int t = p0 + lane; t < v0; t += 32) one(t);
+      // elements before and behind the vectors: fewer than kv each, loaded
+      // ahead of the pass (after it, each of the two cost its own latencies)
+      int edge = -1;
+      uint32_t edge_word = ~0u, edge_bits = 0;
+      if (same) {
+        if (lane < 8) edge = p0 + lane < v0 ? p0 + lane : -1;
+        else if (lane < 16) edge = v0 + nvec * kv + lane - 8 < p1 ? v0 + nvec * kv + lane - 8 : -1;
+        if (edge >= 0) {
+          if (ok) edge_word = __ldg(ok + (edge >> 5));
+          edge_bits = DT == SPEC_BF16 ? reinterpret_cast<const volatile uint16_t*>(in)[edge]
+                                      : reinterpret_cast<const volatile uint32_t*>(in)[edge];
+        }
+      } else {
+        for (int t = p0 + lane; t < p1; t += 32) one(t);
+      }
       uint32_t keep[kAdjUnroll], later[kAdjUnroll];  // mask bits of these vectors, of the next ones
       auto load_bits = [&](int i0, uint32_t* k) {
 #pragma unroll
@@ -383,7 +399,11 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
           st_vec(out + static_cast<int64_t>(v0 + i * kv) * esz, v);
         }
       }
-      for (int t = v0 + nvec * kv + lane; t < p1; t += 32) one(t);
+      if (edge >= 0) {
+        const bool drop = !((edge_word >> (edge & 31)) & 1u);
+        if (DT == SPEC_BF16) reinterpret_cast<uint16_t*>(out)[edge] = drop ? 0xff80u : edge_bits;
+        else reinterpret_cast<uint32_t*>(out)[edge] = drop ? 0xff800000u : edge_bits;
+      }
       __syncwarp();
     }
     finish(early);
@@ -430,8 +450,8 @@ extern "C" int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void
             max_bias, allowed_or_null, mask_rows, allowed_row_or_null, stats_or_null};
   // the largest chunk that gives 1000 CTAs (608 are resident): a chunk scans
   // the history once, but the one that holds the frequent ids has to be short
-  // beside the whole (V=32000, 16 rows: 69 us at 2048 tokens, 121 at 4096;
-  // V=128256, 64 rows: 819 and 782)
+  // beside the whole (B=64, V=32000, 16 rows: 62 us at 2048 tokens, 87 at 4096
+  // and 73 at 1024; B=128, V=128256, 64 rows: 757 at 4096, 795 at 2048)
   int chunk = kAdjMaxChunk;
   while (chunk > kAdjMinChunk && static_cast<int64_t>(B) * ((V + chunk - 1) / chunk) < 1000) chunk /= 2;
   const size_t smem = sizeof(uint32_t) * (static_cast<size_t>(chunk) * (max_bias > 0 ? 2 : 1) + chunk / 2 +
