@@ -801,10 +801,13 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
                                   const int32_t* req_to_token, int64_t max_ctx, const uint8_t* tree_mask_or_null,
                                   float scale, void* out, float* lse_or_null, int32_t* stats_or_null, void* ws,
                                   size_t ws_bytes, spec_stream_t stream) {
-  if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !isfinite(scale))
+  if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !(scale > 0.0f) ||
+      !isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   const int64_t row = spec_kv4_slot_bytes(Hkv, D);
   if (row < 0 || N > SPEC_MAX_NODES || Hq > SPEC_KV4_MAX_HEADS * 16 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  // a row's factor, scale log2(e) times a power of two down to 2^-126, must not vanish
+  if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
   if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
   if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kTile ||
       slot_stride > INT32_MAX)
@@ -815,6 +818,10 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
     if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return SPEC_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return SPEC_ERR_INVALID_ARG;
   if (ws_bytes < spec_kv4_attention_ws_size(B, N, Hq, Hkv, D)) return SPEC_ERR_WORKSPACE;
+  // results are written while other CTAs still read q
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const int64_t tokens = static_cast<int64_t>(B) * N, wide = static_cast<int64_t>(Hq) * D;
+  if (q0 < o0 + 2 * tokens * wide && o0 < q0 + 2 * ((tokens - 1) * q_stride + wide)) return SPEC_ERR_INVALID_ARG;
   int dev = 0;
   const int sms = attn_sms(dev);
   if (sms == 0) {

@@ -339,3 +339,33 @@ def test_binding_checks(gpu):
             sd.spec_kv4_attention(**{**ok, **bad})
     empty = sd.spec_kv4_attention(**{**ok, "q": q[:, :0]})
     assert empty.shape == (2, 0, 4, 64)
+
+
+def test_refused_scales_and_overlaps():
+    build()
+    lib, null = sd.lib(), None
+
+    def call(scale=1.0, q=null, out=null, ptr=null, N=2, qs=128):
+        return lib.spec_kv4_attention(1, N, 2, 1, 64, q, qs, ptr, 8, 80, null, ptr, ptr, 8, null, scale, out, null, null,
+                                      ptr, 1 << 40, null)
+    assert call(0.0) == -1 and call(-0.125) == -1 and call(-math.inf) == -1
+    assert call(2.0 ** -21) == -2 and call(2.0 ** 21) == -2
+    if not torch.cuda.is_available():  # made-up addresses: only where nothing could run
+        a = dict(ptr=ctypes.c_void_p(4096))
+        at = lambda x: ctypes.c_void_p(4096 * 16 + x)  # noqa: E731
+        assert call(q=at(0), out=at(0), **a) == -1            # in place
+        assert call(q=at(0), out=at(2 * 256 - 16), **a) == -1  # q's last 16 bytes
+        assert call(q=at(2 * 256 - 16), out=at(0), **a) == -1  # out's last 16 bytes
+        assert call(q=at(0), out=at(256), qs=256, **a) == -1   # between q's rows and into the last
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 12, 24, 48])
+@pytest.mark.parametrize("scale", [2.0 ** -20, 1.0, 2.0 ** 20])
+def test_smallest_and_largest_scales(gpu, N, scale):
+    # the largest with q as much smaller, so that scores stay where softmax is not a choice
+    c = make_case(77 + N, 2, N, 4, 2, 64, [5, 130], page=5)
+    c["scale"] = scale
+    c["q"] = (c["q"].float() * (2.0 ** -23 if scale > 1 else 2.0 ** -3)).to(torch.bfloat16)
+    out, lse = run(c)
+    check(out, lse, expected(c))
