@@ -519,7 +519,7 @@ def spec_adjust_logits(logits, history=None, history_lens=None, prompt_lens=None
     M = bias_ids.shape[-1] if bias_ids is not None else 0
     if (bias_ids is None) != (bias_vals is None):
         raise ValueError("bias_ids and bias_vals go together")
-    words = (V + 31) // 32
+    words = max(1, (V + 31) // 32)
     rows = allowed.numel() // words if allowed is not None else 0
     rc = lib().spec_adjust_logits(
         B, N, V, code, src, dst, _arg(num_nodes, i32, one, dev, "num_nodes"),

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
   if (!spec_smem_ok(reinterpret_cast<char*>(a.draft_token ? next + N : slot_tok) - reinterpret_cast<char*>(adj_sm),
                     a.stats))
     return;
-  __shared__ int s_slots, s_list, s_sorted;
+  __shared__ int s_slots, s_list, s_sorted, s_twice;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int nodes = N;
   if (a.num_nodes) nodes = min(max(__ldg(a.num_nodes + b), 0), N);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
 
   // the chunk's table
   for (int i = tid; i < chunk / 4; i += kAdjThreads) reinterpret_cast<uint4*>(info)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) s_slots = s_list = s_sorted = 0;
+  if (tid == 0) s_slots = s_list = s_sorted = s_twice = 0;
   Penalty pen{1.0f, 0.0f, 0.0f};
   if (a.rep) {
     const float r = __ldg(a.rep + b);
@@ -209,10 +209,17 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
     const int32_t* ids = a.bias_ids + static_cast<int64_t>(b) * a.M;
     const float* vals = a.bias_vals + static_cast<int64_t>(b) * a.M;
     for (int i = tid; i < a.M; i += kAdjThreads) {
+      const int64_t t = __ldg(ids + i) - c0;
+      if (t < 0 || t >= len) continue;
+      if (mark(static_cast<int>(t), kBias) & kBias) s_twice = 1;
+      bias[t] = __ldg(vals + i);
+    }
+    __syncthreads();
+    // an id listed more than once: its first entry adds them in list order
+    for (int i = s_twice ? tid : a.M; i < a.M; i += kAdjThreads) {
       const int32_t id = __ldg(ids + i);
       const int64_t t = id - c0;
       if (t < 0 || t >= len) continue;
-      // an id listed more than once: its first entry adds them in list order
       bool first = true;
       for (int j = 0; j < i && first; ++j) first = __ldg(ids + j) != id;
       if (!first) continue;
@@ -220,7 +227,6 @@ __global__ void __launch_bounds__(kAdjThreads, 4) adjust_kernel(const AdjArgs a,
       for (int j = i + 1; j < a.M; ++j)
         if (__ldg(ids + j) == id) s = __fadd_rn(s, __ldg(vals + j));
       bias[t] = s;
-      mark(static_cast<int>(t), kBias);
     }
   }
   __syncthreads();
@@ -432,10 +438,10 @@ extern "C" int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void
   if (B < 0 || N < 1 || V < 1 || max_history < 0 || max_bias < 0) return SPEC_ERR_INVALID_ARG;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
   if (V > SPEC_MAX_VOCAB || N > SPEC_MAX_NODES || B > 65535 || max_history > (1 << 28)) return SPEC_ERR_UNSUPPORTED;
+  if (B == 0) return SPEC_OK;
   if (allowed_or_null && (mask_rows < 1 || (!allowed_row_or_null && mask_rows < static_cast<int64_t>(B) * N)))
     return SPEC_ERR_INVALID_ARG;
   if (max_bias > 0 && (!bias_ids_or_null || !bias_vals_or_null)) return SPEC_ERR_INVALID_ARG;
-  if (B == 0) return SPEC_OK;
   if (!logits || !out) return SPEC_ERR_INVALID_ARG;
   const unsigned esz = dtype == SPEC_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(logits) % esz || reinterpret_cast<uintptr_t>(out) % esz) return SPEC_ERR_INVALID_ARG;

@@ -242,3 +242,35 @@ def test_binding_checks(gpu):
         sd.spec_adjust_logits(x.half())
     with pytest.raises(ValueError):
         sd.spec_adjust_logits(x.transpose(0, 1))
+
+
+def test_empty_batch():
+    build()
+    p = ctypes.c_void_p(4096)  # not read: there is nothing to do
+    for M, rows in ((3, 0), (0, 0), (3, 2)):
+        assert sd.lib().spec_adjust_logits(0, 2, 8, 1, None, None, None, None, 0, None, None, None, None, None, None, None,
+                                           None, None, M, p, rows, None, None, None) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("twice", [False, True])
+def test_bias_of_every_token(gpu, twice):
+    B, N, V = 2, 3, 9001
+    c = make_case(21, B, N, V, torch.float32)
+    rng = np.random.default_rng(22)
+    ids = np.stack([rng.permutation(V) for _ in range(B)]).astype(np.int32)
+    if twice:  # in one chunk of the vocabulary and far apart, and side by side
+        ids[0, -1], ids[1, 7] = ids[0, 0], ids[1, 6]
+    c["bias_ids"], c["bias_vals"] = ids, rng.normal(0, 3, ids.shape).astype(np.float32)
+    x = c["x"].cuda()
+    same(sd.spec_adjust_logits(x, **on_gpu(c)), expected(c))
+
+
+@pytest.mark.gpu
+def test_empty_shapes_through_the_binding(gpu):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.zeros((0, 3, 64), device="cuda")
+    assert sd.spec_adjust_logits(x, history=i(0, 4), bias_ids=i(0, 2), bias_vals=i(0, 2).float(), draft_token=i(0, 3),
+                                 allowed=i(1, 2)).shape == (0, 3, 64)
+    with pytest.raises(sd.SpecError):
+        sd.spec_adjust_logits(torch.zeros((2, 3, 0), device="cuda"), allowed=i(2, 1))
