@@ -101,7 +101,7 @@ class StepBuffers:
         self.ws = torch.empty(max(spec_verify_ws_size(B, N), 256), dtype=torch.uint8, device=dev)
         self.verify_out = None
         self.stats = new_stats(dev)
-        self.attention_ws = None  # run_attention's, kept from its first call
+        self.attention_ws = {}  # run_attention's, by their size, kept from the first call on
         self.compact_out = None
         if page_size:
             cap = spec_compact_freed_capacity(B, N, page_size)
@@ -184,14 +184,16 @@ def run_kv4_append(buf: StepBuffers, k, v, seq_lens, req_to_token, kv_pool, num_
 def run_attention(buf: StepBuffers, q, seq_lens, req_to_token, kv_pool, num_kv_heads, scale=None, num_nodes=None,
                   out=None, lse=None):
     """Attention of q [B, N, Hq, D] of buf.tree's nodes over context and tree
-    (their K and V appended before).  The workspace is allocated by the first
-    call and kept, so that a captured step has one of its own."""
+    (their K and V appended before).  The workspace of a size is allocated by
+    the first call that needs it and kept as long as buf, so that a captured
+    step's stays its own."""
     B, N, Hq, D = q.shape
     need = spec_kv4_attention_ws_size(B, N, Hq, int(num_kv_heads), D)
-    if buf.attention_ws is None or buf.attention_ws.numel() < need:
-        buf.attention_ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws = buf.attention_ws.get(need)
+    if ws is None:
+        ws = buf.attention_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
     return spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask=buf.tree["tree_mask"],
-                              scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=buf.attention_ws, stats=buf.stats)
+                              scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=ws, stats=buf.stats)
 
 
 def run_adjust(buf: StepBuffers, target, out=None, **penalties):

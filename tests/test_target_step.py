@@ -144,6 +144,32 @@ def test_captured_step(gpu):
 
 
 @pytest.mark.gpu
+def test_captured_steps_of_two_head_layouts(gpu):
+    """One buf serves layers of different heads: the larger workspace does not
+    replace the one that a captured call holds."""
+    page = 16
+    x = {k: v.cuda() for k, v in inputs(8, page).items()}
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=page)
+    pl.run_draft(buf, x["draft"], 1.0, x["root"], x["lens"])
+    fill(x)
+    pl.run_kv4_append(buf, x["k"], x["v"], x["lens"], x["table"], x["pool"])
+    narrow = x["q"][:, :, :HKV].contiguous()  # one query head a KV head
+    few, many = torch.empty_like(narrow), torch.empty_like(x["q"])
+    graph = pl.capture_step(lambda: pl.run_attention(buf, narrow, x["lens"], x["table"], x["pool"], HKV, out=few))
+    held = {n: w.data_ptr() for n, w in buf.attention_ws.items()}
+    pl.run_attention(buf, x["q"], x["lens"], x["table"], x["pool"], HKV, out=many)
+    assert len(held) == 1 and len(buf.attention_ws) == 2
+    assert all(buf.attention_ws[n].data_ptr() == at for n, at in held.items())
+    few.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    mask = buf.tree["tree_mask"].cpu().numpy()
+    for q, out in ((narrow, few), (x["q"], many)):
+        check(out, None, ref.kv4_attention(q.float().cpu().numpy(), x["pool"].cpu().numpy(), x["table"].cpu().numpy(),
+                                           x["lens"].cpu().numpy(), HKV, D ** -0.5, tree_mask=mask))
+
+
+@pytest.mark.gpu
 @pytest.mark.timeout(1200)
 def test_under_the_bounds_checking_build():
     """The new calls' tests against libspecdec_debug.so: no index that depends
