@@ -26,7 +26,7 @@
 // needed, in place too; in place without a mask only the listed tokens are
 // touched at all.  (Looking the bits of every vector up in the pass instead
 // took 128 instructions a vector where histories crowd: 64-node trees, B=128,
-// V=128256, bf16: 890 us.)  Measured there: 757 us for 4.26 GB, 5.6 TB/s; the
+// V=128256, bf16: 890 us.)  Measured there: 750 us for 4.27 GB, 5.7 TB/s; the
 // listed tokens take 40 of them, the masks' bits 64, histories 30.
 #include <climits>
 

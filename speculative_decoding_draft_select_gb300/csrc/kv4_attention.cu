@@ -16,12 +16,21 @@
 // its bits down to 2^-29 of the largest; the sum that divides uses the
 // unrounded weights.
 //
-// The rows of a KV head (N nodes times G query heads) are cut into row tiles
-// and the positions into tiles of 64.  Work is dealt out evenly whatever the
+// The rows of a KV head (N nodes times G query heads) are cut into row tiles.
+// Three kernels, by the rows: here up to 8 (positions in tiles of 128) and up
+// to 16 (tiles of 64) with matrix instructions from registers, each warp with
+// its own positions and a ring of asynchronous copies; more rows in
+// kv4_tree.cu.  Work is dealt out evenly whatever the
 // lengths are: the tiles of all (request, KV head, row tile) segments form
 // one line, each CTA takes an equal stretch of it, and a segment that is cut
 // between CTAs leaves partial (max, sum, weighted values) in the workspace,
 // which a second kernel merges in a fixed order.  The host knows no lengths.
+//
+// Bound by the instructions that unpack the codes, not by the bytes: 960 a
+// warp and 32 positions of 8 rows, 536 of them unpacking, at 12 warps an SM
+// (164 registers hold O and the codes at hand).  Measured at D = 128, 8 KV
+// heads: B=128, 32 heads, contexts 16..2048: 80 us for 172 MB; B=4, 64 heads,
+// contexts 60001..131001: 153 us for 491 MB.
 #include "kv4_attn.cuh"
 
 namespace specdec {
@@ -191,13 +200,13 @@ constexpr int kRing8 = 3;    // and of 32, with up to eight rows
 // the warps' row statistics, and the weighted values of two warps' 16 rows at
 // a time (rows 16 floats longer than D and 4 floats of padding per 32
 // channels, so the fragment's stores spread over the banks).
-template <int D, int MT>
+template <int D>
 struct AttShared {
   static constexpr int kRow = D + 16;
   uint8_t ring[kAttWarps][kRing][Stage<D, 16>::kBytes];
-  uint4 q[MT][D / 16][32];
-  float c[16 * MT];  // factor of a row's scores
-  float m[kAttWarps][16 * MT], l[kAttWarps][16 * MT];
+  uint4 q[D / 16][32];
+  float c[16];  // factor of a row's scores
+  float m[kAttWarps][16], l[kAttWarps][16];
   unsigned there[kAttWarps][kRing];  // positions of a stage that have a slot
   float o[2][16][kRow];
 };
@@ -239,13 +248,13 @@ __device__ __forceinline__ float q_scale(float mx, float scale_log2, float* fact
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-// Query rows [r0, r0 + 16 MT) of (b, h) into shared memory: a warp per row.
-template <int D, int MT>
-__device__ void load_q(const AttnArgs& a, AttShared<D, MT>& sh, int b, int h, int r0, int rows) {
+// Query rows [r0, r0 + 16) of (b, h) into shared memory: a warp per row.
+template <int D>
+__device__ void load_q(const AttnArgs& a, AttShared<D>& sh, int b, int h, int r0, int rows) {
   constexpr int per = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 4
-  for (int r = warp; r < 16 * MT; r += kAttWarps) {
+  for (int r = warp; r < 16; r += kAttWarps) {
     float x[per], mx;
     q_row<D>(a, b, h, r0 + r, r < rows, x, mx);
     const float down = q_scale(mx, a.scale_log2, sh.c + r);
@@ -254,7 +263,7 @@ __device__ void load_q(const AttnArgs& a, AttShared<D, MT>& sh, int b, int h, in
 #pragma unroll
     for (int j = 0; j < per; j += 2) {
       const int ch = lane * per + j, t = ch / (D / 4), kk = ch % (D / 4) / 4, i = ch % 4 / 2;
-      reinterpret_cast<uint32_t*>(&sh.q[r / 16][kk][(r % 8) * 4 + t])[2 * i + (r % 16) / 8] =
+      reinterpret_cast<uint32_t*>(&sh.q[kk][(r % 8) * 4 + t])[2 * i + (r % 16) / 8] =
           h2_u32(__floats2half2_rn(x[j] * down, x[j + 1] * down));
     }
   }
@@ -282,13 +291,13 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, const Part& p, int
   if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_kernel(const AttnArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const AttnArgs a) {
   pdl_enter();
-  constexpr int R = 16 * MT, H = 2;  // halves of a fragment's rows
+  constexpr int R = 16, H = 2;  // halves of a fragment's rows
   using St = Stage<D, 16>;
   extern __shared__ __align__(16) unsigned char att_sm[];
-  AttShared<D, MT>& sh = *reinterpret_cast<AttShared<D, MT>*>(att_sm);
+  AttShared<D>& sh = *reinterpret_cast<AttShared<D>*>(att_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
@@ -308,23 +317,19 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
     const int r0 = rt * R, rows = min(R, rq.nodes * a.G - r0);
     if (rq.bad && h == 0 && rt == 0 && threadIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
 
-    load_q<D, MT>(a, sh, b, h, r0, rows);
+    load_q<D>(a, sh, b, h, r0, rows);
     __syncthreads();
-    float cr[MT][H], m[MT][H], l[MT][H], o[MT][D / 8][4];
+    float cr[H], m[H], l[H], o[D / 8][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < H; ++i) {
+      cr[i] = sh.c[g + 8 * i];
+      m[i] = neg_inf();
+      l[i] = 0.0f;
+    }
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
-        cr[mt][i] = sh.c[mt * 16 + g + 8 * i];
-        m[mt][i] = neg_inf();
-        l[mt][i] = 0.0f;
-      }
+    for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[mt][i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
 
 #pragma unroll 1
     for (int tile = t0; tile < t1; ++tile) {
@@ -332,13 +337,11 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
       const uint8_t* s8 = sh.ring[warp][st];
       st = (st + 1) % kRing;
       if (there == 0) continue;
-      float s[MT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][j][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) s[j][i] = 0.0f;
       typename Vec<D / 8>::type kc[2];
       uint32_t km[2];
 #pragma unroll
@@ -350,78 +353,67 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
         for (int j = 0; j < 2; ++j)
           dequant4(word_of(kc[j], wd), __byte_perm(km[j], 0, 0x1010), __byte_perm(km[j], 0, 0x3232), kv[j]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half) {
+          const uint4 qa = sh.q[wd * 2 + half][lane];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint4 qa = sh.q[mt][wd * 2 + half][lane];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma16816(s[mt][j], qa, kv[j][2 * half], kv[j][2 * half + 1]);
-          }
+          for (int j = 0; j < 2; ++j) mma16816(s[j], qa, kv[j][2 * half], kv[j][2 * half + 1]);
+        }
       }
-      // scores in units of log2, masked; s[..][j][i]: row g + 8 (i / 2),
+      // scores in units of log2, masked; s[j][i]: row g + 8 (i / 2),
       // position 8 j + 2 t + i % 2
       const int p0 = tile * kTile + warp * 16;
       const bool whole = there == 0xffffu && p0 + 16 <= rq.start;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 2 * H; ++i) s[mt][j][i] *= cr[mt][i >> 1];
+        for (int i = 0; i < 2 * H; ++i) s[j][i] *= cr[i >> 1];
       if (!whole) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 2 * H; ++i) {
-              const int at = 8 * j + 2 * t + (i & 1), node = p0 + at - rq.start;
-              bool see = (there >> at) & 1u;
-              if (see && node >= 0) {
-                const int r = mt * 16 + g + 8 * (i >> 1), n = attn_node(a, r0 + r);
-                see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
-                      (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
-              }
-              if (!see) s[mt][j][i] = neg_inf();
-            }
-      }
-      uint4 pa[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float mn[H], al[H];
-        bool up = false;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-          float x = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mn[i] = fmaxf(m[mt][i], x);
-          up = up || mn[i] != m[mt][i];
-          const float base_m = mn[i] == neg_inf() ? 0.0f : mn[i];
-          al[i] = fast_exp2(m[mt][i] - base_m);
-          m[mt][i] = mn[i];
-          mn[i] = base_m - kWeightExp;
-        }
-        if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * H; ++e) o[mt][i][e] *= al[e >> 1];
-#pragma unroll
-          for (int i = 0; i < H; ++i) l[mt][i] *= al[i];
-        }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 2 * H; ++i) {
-            s[mt][j][i] = fast_exp2(s[mt][j][i] - mn[i >> 1]);
-            l[mt][i >> 1] += s[mt][j][i];
+            const int at = 8 * j + 2 * t + (i & 1), node = p0 + at - rq.start;
+            bool see = (there >> at) & 1u;
+            if (see && node >= 0) {
+              const int r = g + 8 * (i >> 1), n = attn_node(a, r0 + r);
+              see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
+                    (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
+            }
+            if (!see) s[j][i] = neg_inf();
           }
-        pa[mt] = make_uint4(h2_u32(__floats2half2_rn(s[mt][0][0], s[mt][0][1])),
-                            h2_u32(__floats2half2_rn(s[mt][0][2], s[mt][0][3])),
-                            h2_u32(__floats2half2_rn(s[mt][1][0], s[mt][1][1])),
-                            h2_u32(__floats2half2_rn(s[mt][1][2], s[mt][1][3])));
       }
+      float mn[H], al[H];
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        float x = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        mn[i] = fmaxf(m[i], x);
+        up = up || mn[i] != m[i];
+        const float base_m = mn[i] == neg_inf() ? 0.0f : mn[i];
+        al[i] = fast_exp2(m[i] - base_m);
+        m[i] = mn[i];
+        mn[i] = base_m - kWeightExp;
+      }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2 * H; ++e) o[i][e] *= al[e >> 1];
+#pragma unroll
+        for (int i = 0; i < H; ++i) l[i] *= al[i];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) {
+          s[j][i] = fast_exp2(s[j][i] - mn[i >> 1]);
+          l[i >> 1] += s[j][i];
+        }
+      const uint4 pa =
+          make_uint4(h2_u32(__floats2half2_rn(s[0][0], s[0][1])), h2_u32(__floats2half2_rn(s[0][2], s[0][3])),
+                     h2_u32(__floats2half2_rn(s[1][0], s[1][1])), h2_u32(__floats2half2_rn(s[1][2], s[1][3])));
       typename Vec<D / 16>::type vc[4];
       uint32_t vm[4];
 #pragma unroll
@@ -440,8 +432,7 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
           dequant4(__byte_perm(word_of(vc[2], wd), word_of(vc[3], wd), sel), st1, lo1, v1);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][wd * 8 + 2 * j + odd], pa[mt], v0[j], v1[j]);
+            mma16816(o[wd * 8 + 2 * j + odd], pa, v0[j], v1[j]);
         }
       }
     }
@@ -451,68 +442,63 @@ __global__ void __launch_bounds__(kAttThreads, MT == 1 ? 3 : 2) kv4_attention_ke
     if (t0 == 0 && t1 < rq.tiles && threadIdx.x == 0)
       *cut = CutSegment{b, h, rt, line.pieces(static_cast<int>(blockIdx.x), rq.tiles, t1)};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        float x = l[mt][i];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (t == 0) {
-          sh.m[warp][mt * 16 + g + 8 * i] = m[mt][i];
-          sh.l[warp][mt * 16 + g + 8 * i] = x;
-        }
+    for (int i = 0; i < H; ++i) {
+      float x = l[i];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if (t == 0) {
+        sh.m[warp][g + 8 * i] = m[i];
+        sh.l[warp][g + 8 * i] = x;
       }
+    }
     __syncthreads();
+    float f[H];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float f[H];
+    for (int i = 0; i < H; ++i) {
+      const int r = g + 8 * i;
+      float top = sh.m[0][r];
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const int r = mt * 16 + g + 8 * i;
-        float top = sh.m[0][r];
+      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+      f[i] = m[i] == neg_inf() ? 0.0f : fast_exp2(m[i] - top);
+    }
 #pragma unroll
-        for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-        f[i] = m[mt][i] == neg_inf() ? 0.0f : fast_exp2(m[mt][i] - top);
-      }
+    for (int stage = 0; stage < 2; ++stage) {
+      // stage 0: warps 2 and 3 store; stage 1: warps 0 and 1 add
+      if ((stage == 0) == (warp >= 2)) {
 #pragma unroll
-      for (int stage = 0; stage < 2; ++stage) {
-        // stage 0: warps 2 and 3 store; stage 1: warps 0 and 1 add
-        if ((stage == 0) == (warp >= 2)) {
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-          for (int i = 0; i < H; ++i)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int c = 0; c < D / 8; c += 4) {
-                const int ch = (2 * t + e) * (D / 8) + c;
-                float4* at = reinterpret_cast<float4*>(&sh.o[warp & 1][g + 8 * i][padded(ch)]);
-                float4 x = make_float4(o[mt][c][2 * i + e] * f[i], o[mt][c + 1][2 * i + e] * f[i],
-                                       o[mt][c + 2][2 * i + e] * f[i], o[mt][c + 3][2 * i + e] * f[i]);
-                if (stage == 1) {
-                  const float4 y = *at;
-                  x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                }
-                *at = x;
+            for (int c = 0; c < D / 8; c += 4) {
+              const int ch = (2 * t + e) * (D / 8) + c;
+              float4* at = reinterpret_cast<float4*>(&sh.o[warp & 1][g + 8 * i][padded(ch)]);
+              float4 x = make_float4(o[c][2 * i + e] * f[i], o[c + 1][2 * i + e] * f[i],
+                                     o[c + 2][2 * i + e] * f[i], o[c + 3][2 * i + e] * f[i]);
+              if (stage == 1) {
+                const float4 y = *at;
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
               }
-        }
-        __syncthreads();
-      }
-      for (int i = threadIdx.x; i < 8 * H * (D / 4); i += kAttThreads) {
-        const int rr = i / (D / 4), ch = (i - rr * (D / 4)) * 4, r = mt * 16 + rr;
-        if (r >= rows) continue;
-        const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][rr][padded(ch)]);
-        const float4 y = *reinterpret_cast<const float4*>(&sh.o[1][rr][padded(ch)]);
-        const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-        float top = sh.m[0][r], sum = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w)
-          if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
-        attn_store<D>(a, rq, r0 + r, R, ch, acc, top, sum, part);
+              *at = x;
+            }
       }
       __syncthreads();
     }
+    for (int i = threadIdx.x; i < 8 * H * (D / 4); i += kAttThreads) {
+      const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
+      if (r >= rows) continue;
+      const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][padded(ch)]);
+      const float4 y = *reinterpret_cast<const float4*>(&sh.o[1][r][padded(ch)]);
+      const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      float top = sh.m[0][r], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w)
+        if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
+      attn_store<D>(a, rq, r0 + r, R, ch, acc, top, sum, part);
+    }
+    __syncthreads();
   }
   cp_async_wait<0>();
 }
@@ -775,13 +761,18 @@ int launch_rows(AttnArgs& a, int dev, size_t smem, int ctas, cudaStream_t s) {
 template <int D>
 int launch_few(AttnArgs& a, int R, int dev, int sms, cudaStream_t s) {
   if (R == 8) return launch_rows<kv4_attention8_kernel<D>, D, 8>(a, dev, sizeof(AttShared8<D>), sms * 3, s);
-  if (R == 16) return launch_rows<kv4_attention_kernel<D, 1>, D, 16>(a, dev, sizeof(AttShared<D, 1>), sms * 3, s);
-  return launch_rows<kv4_attention_kernel<D, 2>, D, 32>(a, dev, sizeof(AttShared<D, 2>), sms * 2, s);
+  return launch_rows<kv4_attention_kernel<D>, D, 16>(a, dev, sizeof(AttShared<D>), sms * 3, s);
 }
 
-// Rows of a row tile here: 8 or 16 where they suffice, else 32; 0: more rows
-// than that go to the tensor-memory kernel (kv4_tree.cu).
-int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 0)); }
+// Rows of a row tile here: 8 or 16 where they suffice; 0: more rows than that
+// go to the tensor-memory kernel (kv4_tree.cu), whose time hardly depends on
+// them.  Contexts 16..2048, 8 KV heads of 128, in us:
+//   B=128:  4 rows 77 (as 16: 115), 8 rows 82 (126), 16 rows 146 (kv4_tree.cu:
+//           148), 24 rows 149 there (two fragments of 16 here: 208), 32: 151
+//           (231)
+//   B=8:    16 rows 18.5 (24.9), 32 rows 26.6 there (26.1)
+//   B=1:    16 rows 12.5 (16.8), 32 rows 17.8 there (15.8)
+int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 0); }
 
 }  // namespace
 }  // namespace specdec

@@ -15,7 +15,14 @@
 //       fp16 slabs; Q likewise.
 // 16 warps an SM leave each thread 128 registers: with a warp more for the
 // issue (96 registers) the codes read ahead spilled, and a spill waits for
-// its load (64-node trees, B=128: 323 us).
+// its load.  The softmax goes over a row 32 columns at a time for the same
+// reason (64-node trees, B=128, 32 heads over 8 of 128, contexts 16..2048:
+// 323 us with the issuing warp, 281 without, 266 with 32 columns).
+// Bound by the softmax passes (without them 182 us) and by the hand-overs
+// between the roles (155 cycles each); the tensor pipe works 23% of the time.
+// Unpacking with twice the threads took 286 us, weights in shared memory
+// instead of tensor memory 326, no search for a maximum (weights watched for
+// their size instead) 267.
 // With MT = 2 the exponentials of one accumulator run under the products of
 // the other, on one CTA per SM with two stages of K and V; with MT = 1 two
 // CTAs share an SM to the same end.
@@ -637,6 +644,9 @@ int launch_tree(AttnArgs a, int dev, int sms, cudaStream_t s) {
 }  // namespace
 
 int launch_tree_attention(AttnArgs a, int D, int dev, int sms, cudaStream_t s) {
+  // two accumulators where there are rows for them (B=128, 8 KV heads of 128,
+  // contexts 16..2048: 160 rows 255 us, 307 with one; 128 rows 243, 168 with
+  // one)
   const bool two = static_cast<int64_t>(a.N) * a.G > kTreeRows;
   if (D == 128) return two ? launch_tree<128, 2>(a, dev, sms, s) : launch_tree<128, 1>(a, dev, sms, s);
   return two ? launch_tree<64, 2>(a, dev, sms, s) : launch_tree<64, 1>(a, dev, sms, s);
