@@ -17,8 +17,8 @@
 // issue (96 registers) the codes read ahead spilled, and a spill waits for
 // its load.  The softmax goes over a row 32 columns at a time for the same
 // reason (64-node trees, B=128, 32 heads over 8 of 128, contexts 16..2048:
-// 323 us with the issuing warp, 281 without, 266 with 32 columns).
-// Bound by the softmax passes (without them 182 us) and by the hand-overs
+// 323 us with the issuing warp, 281 without, 266 with 32 columns, 259 with K
+// read ahead sooner).  Bound by the softmax passes (without them 182 of 266) and by the hand-overs
 // between the roles (155 cycles each); the tensor pipe works 23% of the time.
 // Unpacking with twice the threads took 286 us, weights in shared memory
 // instead of tensor memory 326, no search for a maximum (weights watched for
@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
     // with two slabs, groups 2 and 3 store their units in the order 2, 3, 0, 1:
     // the eight lanes of a store phase then hit eight different units
     const bool swap = CH == 4 && g >= 2;
-    // the cursor that reads ahead: slots two tiles before their use, codes one
+    // the cursor that reads ahead: slots two tiles before their use, codes one:
+    // with two accumulators K's as soon as the tile before has left its
+    // registers (B=128, 256 rows: 266 us behind V's instead, 259 so), with one
+    // behind V's, since registers spill otherwise (64 rows: 162 us, 168)
     auto ahead = walk;
     Part ap;
     int at = -1;  // tile of the slots below, -1: the line is at its end
@@ -270,21 +273,21 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
     };
     Chunk k[kPer], v[kPer];
     uint32_t have = 0;  // bit i: position i of this thread has a slot
-    auto load_chunks = [&]() {
-      have = 0;
+    auto load_chunks = [&](bool of_k, bool of_v) {
+      if (of_k) have = 0;
       if (at < 0) return;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        k[i].c = v[i].c = make_uint4(0, 0, 0, 0);
-        k[i].m = v[i].m = 0;
+        if (of_k) k[i] = Chunk{make_uint4(0, 0, 0, 0), 0};
+        if (of_v) v[i] = Chunk{make_uint4(0, 0, 0, 0), 0};
         if (slot[i] >= 0 && slot[i] < a.num_slots) {
           const uint8_t* s = head + slot[i] * a.slot_stride;
-          k[i].c = __ldg(reinterpret_cast<const uint4*>(s) + g);
-          v[i].c = __ldg(reinterpret_cast<const uint4*>(s + D / 2) + g);
-          k[i].m = __ldg(reinterpret_cast<const uint32_t*>(s + D) + g);
-          v[i].m = __ldg(reinterpret_cast<const uint32_t*>(s + D + D / 8) + g);
-          have |= 1u << i;
-        } else if (count && slot[i] != -2) {
+          if (of_k) k[i].c = __ldg(reinterpret_cast<const uint4*>(s) + g);
+          if (of_v) v[i].c = __ldg(reinterpret_cast<const uint4*>(s + D / 2) + g);
+          if (of_k) k[i].m = __ldg(reinterpret_cast<const uint32_t*>(s + D) + g);
+          if (of_v) v[i].m = __ldg(reinterpret_cast<const uint32_t*>(s + D + D / 8) + g);
+          if (of_k) have |= 1u << i;
+        } else if (of_k && count && slot[i] != -2) {
           bump(a.stats, SPEC_STAT_BAD_REQUEST);
         }
       }
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
       }
     };
     load_slots();
-    load_chunks();
+    load_chunks(true, true);
     load_slots();
     Part p;
     bool ok = true;
@@ -401,6 +404,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&k_full[j & 3]);
+        if (MT == 2) load_chunks(true, false);
         if (tile == p.t0) {
           if (j > 0)
             for (int m = 0; m < MT && ok; ++m) ok = wait_warp(&s_full[m], (j - 1) & 1, &s_abort);
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&v_full[j & 1]);
-        load_chunks();
+        load_chunks(MT == 1, true);
         load_slots();
       }
       ++seg;
