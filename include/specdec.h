@@ -9,6 +9,11 @@
  * positive residual), accepted-path KV-slot compaction, and the TLI
  * heterogeneous-vocabulary constraint and id remapping.
  *
+ * Around the target's forward over the tree, whose projections are the
+ * caller's: the 4-bit KV cache in the kv_pool rows, the attention of the
+ * nodes over it under the tree mask, and the adjustment of the target logits
+ * (penalties, biases, grammar masks) node by node.
+ *
  * Sources (web pages, cited by title and section):
  *   [HB]  ai-infra-handbooks, "EAGLE speculative decoding in four parts: why
  *         it became a worker" -- "Drafting, verification and slots".
