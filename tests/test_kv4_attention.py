@@ -369,3 +369,29 @@ def test_smallest_and_largest_scales(gpu, N, scale):
     c["q"] = (c["q"].float() * (2.0 ** -23 if scale > 1 else 2.0 ** -3)).to(torch.bfloat16)
     out, lse = run(c)
     check(out, lse, expected(c))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,Hq,lens", [(1, 1, 6), (3, 4, 5), (5, 4, 4), (9, 16, 300)])
+def test_few_requests_far_apart_in_the_largest_batch(gpu, N, Hq, lens):
+    """65535 requests of which five have nodes: the skipped ones cost no wait its limit and are left as they were."""
+    B, live = 65535, [0, 1, 40000, 65533, 65534]
+    c = make_case(91, len(live), N, Hq, 1, 64, [lens] * len(live), page=1)
+    nodes = torch.zeros(B, dtype=torch.int32, device="cuda")
+    nodes[live] = N
+    seq = torch.zeros(B, dtype=torch.int32, device="cuda")
+    seq[live] = torch.from_numpy(c["lens"]).cuda()
+    table = torch.zeros((B, c["table"].shape[1]), dtype=torch.int32, device="cuda")
+    table[live] = torch.from_numpy(c["table"]).cuda()
+    mask = torch.zeros((B, N, N), dtype=torch.uint8, device="cuda")
+    mask[live] = torch.from_numpy(c["mask"]).cuda()
+    q = torch.zeros((B, N, Hq, 64), dtype=torch.bfloat16, device="cuda")
+    q[live] = c["q"].cuda()
+    out = torch.full_like(q, 7.0)
+    stats = sd.new_stats("cuda")
+    sd.spec_kv4_attention(q, torch.from_numpy(c["rows"]).cuda(), table, seq, 1, tree_mask=mask, num_nodes=nodes, out=out,
+                          scale=c["scale"], stats=stats)
+    assert stats.sum().item() == 0
+    check(out[live], None, expected(c))
+    out[live] = 7.0
+    assert bool((out == 7.0).all())
