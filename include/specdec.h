@@ -593,15 +593,15 @@ int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* poo
  *     [h Hq/Hkv, (h + 1) Hq/Hkv) share KV head h.
  *   out [B, N, Hq, D] bf16 contiguous; lse_or_null [B, N, Hq] fp32: the
  *     natural logarithm of sum_p exp(scale q . k_p).
- * Every position that is attended has to have been appended.  Values enter
- * the products in fp16 (relative 2^-11), sums are fp32.  A row that attends
- * to nothing gives zeros and lse -inf.  Rows n >= num_nodes[b] are left as
- * they were.  out must not overlap q; 2^-20 <= scale <= 2^20.  A position
- * whose slot is out of range is not attended, and a
- * request with seq_len < 0 or seq_len + num_nodes > max_ctx gives zeros
- * (SPEC_STAT_BAD_REQUEST each).  q, pool and out 16-byte aligned, q_stride a
- * multiple of 8, slot_stride a multiple of 16 below 2^31, Hq <= 4096, B <=
- * 65535 (SPEC_ERR_UNSUPPORTED otherwise).
+ * Every position that is attended has to have been appended; a node that
+ * tree_mask hides from every row need not be.  Values enter the products in
+ * fp16 (relative 2^-11), sums are fp32.  A row that attends to nothing gives
+ * zeros and lse -inf.  Rows n >= num_nodes[b] are left as they were.  out must
+ * not overlap q; 2^-20 <= scale <= 2^20.  A position whose slot is out of
+ * range is not attended, and a request with seq_len < 0 or seq_len +
+ * num_nodes > max_ctx gives zeros (SPEC_STAT_BAD_REQUEST each).  q, pool and
+ * out 16-byte aligned, q_stride a multiple of 8, slot_stride a multiple of 16
+ * below 2^31, Hq <= 4096, B <= 65535 (SPEC_ERR_UNSUPPORTED otherwise).
  *   ws: spec_kv4_attention_ws_size bytes (0 for sizes that are not
  *   supported), 16-byte aligned; calls that may overlap need their own. */
 size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D);

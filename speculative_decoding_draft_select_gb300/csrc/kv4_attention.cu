@@ -269,6 +269,14 @@ __device__ void load_q(const AttnArgs& a, AttShared<D>& sh, int b, int h, int r0
   }
 }
 
+// In a tile with nodes: (step, lo) of four positions of V, zero where no append
+// can have written them.
+__device__ __forceinline__ void drop_unwritten(uint32_t& st0, uint32_t& lo0, uint32_t& st1, uint32_t& lo1) {
+  const uint32_t k0 = finite_values(st0, lo0), k1 = finite_values(st1, lo1);
+  st0 &= k0, lo0 &= k0;
+  st1 &= k1, lo1 &= k1;
+}
+
 // Four channels of a row's weighted values: the result, or this CTA's partial.
 template <int D>
 __device__ __forceinline__ void attn_store(const AttnArgs& a, const Part& p, int r, int R, int ch, const float4& acc,
@@ -418,8 +426,9 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
       uint32_t vm[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) St::v(s8, 2 * t + (j & 1) + 8 * (j >> 1), g, vc[j], vm[j]);
-      const uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
-      const uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
+      uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
+      uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
+      if (!whole) drop_unwritten(st0, lo0, st1, lo1);
 #pragma unroll
       for (int wd = 0; wd < D / 64; ++wd) {
         // even channels of a word lie in its low half, odd ones in its high
@@ -620,7 +629,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][i] *= cr[i & 1];
-      if (there != 0xffffffffu || p0 + 32 > rq.start) {
+      const bool whole = there == 0xffffffffu && p0 + 32 <= rq.start;
+      if (!whole) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -670,8 +680,9 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
         uint32_t vm[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) St::v(s8, 16 * u + 2 * t + (j & 1) + 8 * (j >> 1), g, vc[j], vm[j]);
-        const uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
-        const uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
+        uint32_t st0 = __byte_perm(vm[0], vm[1], 0x5410), lo0 = __byte_perm(vm[0], vm[1], 0x7632);
+        uint32_t st1 = __byte_perm(vm[2], vm[3], 0x5410), lo1 = __byte_perm(vm[2], vm[3], 0x7632);
+        if (!whole) drop_unwritten(st0, lo0, st1, lo1);
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
           uint32_t v[2][2][4];  // odd channel, upper positions, pair of channels

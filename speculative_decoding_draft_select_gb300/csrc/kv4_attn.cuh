@@ -205,6 +205,17 @@ __device__ __forceinline__ void dequant4(uint32_t x, uint32_t step2, uint32_t lo
   }
 }
 
+// Which halves of a (step, lo) pair of registers decode to finite values alone,
+// as a mask: every lo + c * step lies between lo and lo + 15 * step, and the sum
+// is an infinity or NaN where one of its terms is.  Appended rows pass.  A node
+// that every row's mask hides may never have been appended; its weights are
+// zero, and its values, taken as zeros where they do not pass, add nothing to
+// any row (0 times an infinity or NaN would).
+__device__ __forceinline__ uint32_t finite_values(uint32_t step2, uint32_t lo2) {
+  const __half2 last = __hfma2(u32_h2(step2), u32_h2(0x4b804b80u), u32_h2(lo2));  // 15
+  return __hle2_mask(__habs2(last), u32_h2(0x7bff7bffu));                          // the largest finite
+}
+
 __device__ __forceinline__ uint16_t f_bf16(float x) {
   uint16_t r;
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));

@@ -292,9 +292,15 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         }
       }
     };
-    auto unpack_to = [&](uint8_t* dst, const Chunk& c, int pos) {
+    // nodes: V of a tile with nodes, whose bytes may never have been written
+    auto unpack_to = [&](uint8_t* dst, const Chunk& c, int pos, bool nodes) {
       uint8_t* slab = dst + (g >> 1) * C::kSlab;
-      const uint32_t st = __byte_perm(c.m, 0, 0x1010), lo = __byte_perm(c.m, 0, 0x3232);
+      uint32_t st = __byte_perm(c.m, 0, 0x1010), lo = __byte_perm(c.m, 0, 0x3232);
+      if (nodes) {
+        const uint32_t keep = finite_values(st, lo);
+        st &= keep;
+        lo &= keep;
+      }
       const uint32_t w[4] = {swap ? c.c.z : c.c.x, swap ? c.c.w : c.c.y, swap ? c.c.x : c.c.z, swap ? c.c.y : c.c.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         if (j >= S) ok = wait_warp(&k_empty[st], static_cast<uint32_t>(j / S - 1) & 1u, &s_abort);
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) unpack_to(sm_k + st * C::kOperand, k[i], p_of + i * kStep);
+        for (int i = 0; i < kPer; ++i) unpack_to(sm_k + st * C::kOperand, k[i], p_of + i * kStep, false);
         // which of this warp's positions have a slot: 32 / CH in a row from
         // uw 32 / CH + i kStep on, CH lanes each
         const bool all = __all_sync(0xffffffffu, have == (1u << kPer) - 1u);
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         if (j >= S) ok = wait_warp(&v_empty[st], static_cast<uint32_t>(j / S - 1) & 1u, &s_abort);
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) unpack_to(sm_v + st * C::kOperand, v[i], p_of + i * kStep);
+        for (int i = 0; i < kPer; ++i) unpack_to(sm_v + st * C::kOperand, v[i], p_of + i * kStep, (tile + 1) * kTT > p.start);
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&v_full[j & 1]);

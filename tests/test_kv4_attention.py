@@ -395,3 +395,34 @@ def test_few_requests_far_apart_in_the_largest_batch(gpu, N, Hq, lens):
     check(out[live], None, expected(c))
     out[live] = 7.0
     assert bool((out == 7.0).all())
+
+
+# rows per KV head by kernel: up to 8, up to 16, one accumulator, two
+KERNELS = [(1, 4), (3, 2), (3, 5), (12, 1), (24, 1), (48, 2), (48, 4)]
+
+
+def never_appended(rows, slots, D):
+    """Bytes in `slots` that no append wrote: NaN, infinities, and finite (step, lo) whose values leave fp16."""
+    head = rows.reshape(rows.shape[0], -1, D + D // 4)
+    kinds = [(np.nan, np.nan), (np.inf, 0.0), (0.0, -np.inf), (np.inf, -np.inf), (60000.0, 0.0), (-60000.0, -60000.0),
+             (1.0, np.nan), (7000.0, 57344.0)]
+    for i, slot in enumerate(slots):
+        head[slot] = 255
+        if i:
+            head[slot, :, D:] = np.tile(np.array(kinds[i % len(kinds)], np.float16), D // 16).view(np.uint8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", KERNELS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_masked_nodes_that_were_never_appended(gpu, N, G, D):
+    """A padded tree without num_nodes: columns that the mask hides from every row."""
+    c = make_case(N + G + D, 2, N, 2 * G, 2, D, [20, 173], page=1)
+    hidden = [0] if N == 1 else list(range(1, N))[-8:]
+    c["mask"][:, :, hidden] = 0
+    c["mask"][1, hidden[-1]] = 0  # and a row of the context alone
+    never_appended(c["rows"], [c["table"][b, c["lens"][b] + n] for n in hidden for b in range(2)], D)
+    with np.errstate(invalid="ignore"):
+        r = expected(c)
+    out, lse = run(c)
+    check(out, lse, r)
