@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
         const float base_m = mn[i] == neg_inf() ? 0.0f : mn[i];
         al[i] = fast_exp2(m[i] - base_m);
         m[i] = mn[i];
-        mn[i] = base_m - kWeightExp;
+        mn[i] = weight_base(base_m, kWeightExp);
       }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
         const float base_m = mn[e] == neg_inf() ? 0.0f : mn[e];
         al[e] = fast_exp2(m[e] - base_m);
         m[e] = mn[e];
-        mn[e] = base_m - kWeightExp;
+        mn[e] = weight_base(base_m, kWeightExp);
       }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll

@@ -222,6 +222,12 @@ __device__ __forceinline__ uint16_t f_bf16(float x) {
   return r;
 }
 
+// Weights are 2^(x - base) with base = max - held, rounded up: beyond 2^24 the
+// difference is no fp32 number, and rounded down it would let weights pass
+// 2^held and fp16's largest.  (Weights then lose held's powers of two; scores
+// that far from zero differ by more than that or not at all.)
+__device__ __forceinline__ float weight_base(float top, float held) { return __fadd_ru(top, -held); }
+
 // The result of a row from its weighted values, weights' sum and maximum: no
 // position gives zeros, NaN stays.
 __device__ __forceinline__ float attn_inv(float sum) { return sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum); }

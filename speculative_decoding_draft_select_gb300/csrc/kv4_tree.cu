@@ -151,8 +151,15 @@ __device__ __forceinline__ float row_max(uint32_t col, const uint32_t* see) {
   }
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-__device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, float c, float base) {
+// far: the maximum is so far from zero that the rounding of S c in it would
+// show in 2^(S c - base), where S c is not rounded: the weights then start from
+// the rounded products too.
+constexpr float kFar = 0x1p20f;  // S c is rounded by 2^-4 at most up to here
+__device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, float c, float base, bool far) {
   uint32_t x[32], y[16];
+  const bool any_far = __any_sync(0xffffffffu, far);
+  const float before = far ? c : 1.0f;
+  if (far) c = 1.0f;
   const float2 c2 = splat(c), nb2 = splat(-base);
   float2 acc[2] = {splat(0.0f), splat(0.0f)};
 #pragma unroll 1
@@ -160,6 +167,10 @@ __device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, 
     const uint32_t sw = pick(see, w);
     tc::ld32(col + 32 * w, x);
     tc::wait_ld32(x);
+    if (any_far) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__fmul_rn(__uint_as_float(x[i]), before));
+    }
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const float2 e = exp2_2(fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, nb2));
@@ -513,7 +524,9 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
           for (int i = 0; i < 4; ++i) see[i] &= s_there[j & 3][i];
           float mx = row_max(s_col, see);
           mx = mx == neg_inf() ? mx : mx * c;
-          const bool grow = mx > top + kLagExp || (top == neg_inf() && mx > top);
+          // the difference, since far from zero top + 8 may round up by more than
+          // the weights have room for
+          const bool grow = mx - top > kLagExp;  // from -inf too; never to it
           if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? (top == neg_inf() ? 0.0f : fast_exp2(top - mx)) : 1.0f;
             if (grow) top = mx;
@@ -530,8 +543,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
               }
             }
           }
-          const float base = (top == neg_inf() ? 0.0f : top) - kHeldExp;
-          sum += row_weights(s_col, see, c, base);
+          const float from = top == neg_inf() ? 0.0f : top;
+          sum += row_weights(s_col, see, c, weight_base(from, kHeldExp), fabsf(from) > kFar);
           tc::wait_st();
         }
         tc::fence_before();

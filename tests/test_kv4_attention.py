@@ -426,3 +426,31 @@ def test_masked_nodes_that_were_never_appended(gpu, N, G, D):
         r = expected(c)
     out, lse = run(c)
     check(out, lse, r)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", KERNELS)
+@pytest.mark.parametrize("peak", [1.0, 0.7, 1.3])
+@pytest.mark.parametrize("power", [20, 24, 25, 26, 27, 28, 30, 33, 60, 126])
+def test_largest_q(gpu, N, G, power, peak):
+    """q up to bf16's largest.  K differs in one channel alone: two positions far apart hold the largest, so one row's
+    result is the mean of these two and, with q's sign turned, that of all others; every other weight is below 2^-1000."""
+    D, ctx = 64, 700
+    c = make_case(power, 1, N, G, 1, D, [ctx], page=1)
+    k, v = ref.kv4_values(c["rows"], 1, D)
+    k[:] = 0
+    k[:, 0, 0] = 0.5 * peak
+    k[c["table"][0, [5, ctx - 9]], 0, 0] = peak
+    k[c["table"][0, ctx:], 0, 0] = 0.75 * peak  # the nodes are neither
+    c["rows"] = ref.kv4_rows(k, v)
+    q = torch.zeros_like(c["q"])
+    q[0, :, :, 0] = 2.0 ** power
+    q[0, -1, -1, 0] = -(2.0 ** power) * (1.9921875 if power == 127 else 1.0)
+    c["q"] = q
+    r = expected(c)
+    out, lse = run(c)
+    # equal scores are equal in any precision and the others do not count: no error of scores
+    check(out, None, dict(r, dot_abs=0 * r["dot_abs"], part_abs=0 * r["part_abs"]))
+    # k in fp16 and a few fp32 operations; log2 of the weights' sum (2^10 at most), held 2^15, is absolute
+    slack = np.abs(r["lse"]) * (2.0**-11 + 2.0**-20) + 24
+    assert (np.abs(lse.cpu().numpy().astype(np.float64) - r["lse"]) <= slack).all()
