@@ -595,8 +595,9 @@ int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* poo
  *     natural logarithm of sum_p exp(scale q . k_p).
  * Every position that is attended has to have been appended; a node that
  * tree_mask hides from every row need not be.  Values enter the products in
- * fp16 (relative 2^-11), sums are fp32.  A row that attends to nothing gives
- * zeros and lse -inf.  Rows n >= num_nodes[b] are left as they were.  out must
+ * fp16 (relative 2^-11), sums are fp32: scores times log2(e), and scale log2(e)
+ * times a row's largest |q|, have to stay in fp32's range.  A row that attends
+ * to nothing gives zeros and lse -inf.  Rows n >= num_nodes[b] are left as they were.  out must
  * not overlap q; 2^-20 <= scale <= 2^20.  A position whose slot is out of
  * range is not attended, and a request with seq_len < 0 or seq_len +
  * num_nodes > max_ctx gives zeros (SPEC_STAT_BAD_REQUEST each).  q, pool and

@@ -241,9 +241,11 @@ __device__ __forceinline__ void q_row(const AttnArgs& a, int b, int h, int r, bo
   mx = warp_max(mx);
 }
 // The power of two that brings mx into [1, 2) (1 for zeros, infinities and NaN;
-// 2^126 at most); the row's scores are multiplied by *factor.
+// 2^126 at most and 2^-126 at least, which leaves the largest mx below 4); the
+// row's scores are multiplied by *factor.
 __device__ __forceinline__ float q_scale(float mx, float scale_log2, float* factor) {
-  const int e = max(mx > 0.0f && isfinite(mx) ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0, -126);
+  const int bits = static_cast<int>(__float_as_uint(mx) >> 23);
+  const int e = mx > 0.0f && isfinite(mx) ? min(max(bits - 127, -126), 126) : 0;
   if ((threadIdx.x & 31) == 0) *factor = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }

@@ -370,9 +370,10 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
           const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
-          // 2^e <= max < 2^(e + 1); zeros, and rows with an infinity or NaN, are
-          // taken as they are
-          const int e = bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -126);
+          // 2^e <= max < 2^(e + 1), but 126 at most (2^-127 is no normal number;
+          // the largest is then below 4); zeros, and rows with an infinity or NaN,
+          // are taken as they are
+          const int e = bits == 0 || bits >= 0x7f80 ? 0 : min(max((bits >> 7) - 127, -126), 126);
           // the sign of the scale goes into q, so that a larger S is a larger score
           const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), a.scale_log2);
           if (sub == 0) s_c[seg & 1][r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);

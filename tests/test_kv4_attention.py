@@ -431,7 +431,7 @@ def test_masked_nodes_that_were_never_appended(gpu, N, G, D):
 @pytest.mark.gpu
 @pytest.mark.parametrize("N,G", KERNELS)
 @pytest.mark.parametrize("peak", [1.0, 0.7, 1.3])
-@pytest.mark.parametrize("power", [20, 24, 25, 26, 27, 28, 30, 33, 60, 126])
+@pytest.mark.parametrize("power", [20, 24, 25, 26, 27, 28, 30, 33, 60, 126, 127])
 def test_largest_q(gpu, N, G, power, peak):
     """q up to bf16's largest.  K differs in one channel alone: two positions far apart hold the largest, so one row's
     result is the mean of these two and, with q's sign turned, that of all others; every other weight is below 2^-1000."""
