@@ -279,6 +279,20 @@ __device__ __forceinline__ void drop_unwritten(uint32_t& st0, uint32_t& lo0, uin
   st1 &= k1, lo1 &= k1;
 }
 
+// Row r's maximum and sum of weights over the warps.  A warp without a maximum
+// has a sum of zero, or NaN where q has one (its scores have no maximum): it
+// counts as it is.
+template <int R>
+__device__ __forceinline__ void warps_sum(const float (&m)[kAttWarps][R], const float (&l)[kAttWarps][R], int r,
+                                          float& top, float& sum) {
+  top = m[0][r];
+#pragma unroll
+  for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, m[w][r]);
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kAttWarps; ++w) sum += l[w][r] * (m[w][r] == neg_inf() ? 1.0f : fast_exp2(m[w][r] - top));
+}
+
 // Four channels of a row's weighted values: the result, or this CTA's partial.
 template <int D>
 __device__ __forceinline__ void attn_store(const AttnArgs& a, const Part& p, int r, int R, int ch, const float4& acc,
@@ -501,12 +515,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
       const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][padded(ch)]);
       const float4 y = *reinterpret_cast<const float4*>(&sh.o[1][r][padded(ch)]);
       const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-      float top = sh.m[0][r], sum = 0.0f;
-#pragma unroll
-      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w)
-        if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
+      float top, sum;
+      warps_sum(sh.m, sh.l, r, top, sum);
       attn_store<D>(a, rq, r0 + r, R, ch, acc, top, sum, part);
     }
     __syncthreads();
@@ -746,12 +756,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
       const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
       const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][ch]), y = *reinterpret_cast<const float4*>(&sh.o[1][r][ch]);
       const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-      float top = sh.m[0][r], sum = 0.0f;
-#pragma unroll
-      for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w)
-        if (sh.m[w][r] != neg_inf()) sum += sh.l[w][r] * fast_exp2(sh.m[w][r] - top);
+      float top, sum;
+      warps_sum(sh.m, sh.l, r, top, sum);
       attn_store<D>(a, rq, r, R, ch, acc, top, sum, part);
     }
     __syncthreads();

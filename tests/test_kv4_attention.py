@@ -454,3 +454,16 @@ def test_largest_q(gpu, N, G, power, peak):
     # k in fp16 and a few fp32 operations; log2 of the weights' sum (2^10 at most), held 2^15, is absolute
     slack = np.abs(r["lse"]) * (2.0**-11 + 2.0**-20) + 24
     assert (np.abs(lse.cpu().numpy().astype(np.float64) - r["lse"]) <= slack).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", KERNELS)
+def test_nan_in_q_is_nan_in_both_results(gpu, N, G):
+    c = make_case(41 + N, 1, N, G, 1, 64, [333], page=1)
+    want, want_lse = run(c)
+    c["q"][0, N - 1, G - 1, 7] = float("nan")
+    out, lse = run(c)
+    assert torch.isnan(out[0, N - 1, G - 1]).all() and torch.isnan(lse[0, N - 1, G - 1])
+    other = torch.ones((1, N, G), dtype=torch.bool, device="cuda")
+    other[0, N - 1, G - 1] = False
+    assert torch.equal(out[other], want[other]) and torch.equal(lse[other], want_lse[other])
