@@ -462,12 +462,9 @@ extern "C" int spec_adjust_logits(int B, int N, int64_t V, int dtype, const void
   while (chunk > kAdjMinChunk && static_cast<int64_t>(B) * ((V + chunk - 1) / chunk) < 1000) chunk /= 2;
   const size_t smem = sizeof(uint32_t) * (static_cast<size_t>(chunk) * (max_bias > 0 ? 2 : 1) + chunk / 2 +
                                           (draft_token_or_null ? 4 * static_cast<size_t>(N) : 0));
-  auto kernel = dtype == SPEC_BF16 ? adjust_kernel<SPEC_BF16> : adjust_kernel<SPEC_F32>;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
+  if (!(dtype == SPEC_BF16 ? allow_smem<adjust_kernel<SPEC_BF16>>(smem) : allow_smem<adjust_kernel<SPEC_F32>>(smem)))
     return SPEC_ERR_CUDA;
-  }
+  auto kernel = dtype == SPEC_BF16 ? adjust_kernel<SPEC_BF16> : adjust_kernel<SPEC_F32>;
   // chunks in order, each for all requests: frequent ids crowd at the front of a
   // vocabulary, and the CTAs with the most to do should not come last
   const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((V + chunk - 1) / chunk));

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
 #include <utility>
 
 #include "specdec.h"
@@ -207,6 +209,34 @@ struct LaunchCfg {
   }
   LaunchCfg(const LaunchCfg&) = delete;
 };
+
+// Lets KERNEL be launched on the current device with `bytes` of dynamic shared
+// memory.  A block's fixed part counts towards the default 48 KB too (kFixedSmem
+// is more than any kernel here has), and the limit of a kernel is never taken
+// back below what an earlier call needed: another thread may be between its
+// call of this and its launch.
+constexpr size_t kFixedSmem = 9 * 1024;
+template <auto KERNEL>
+inline bool allow_smem(size_t bytes) {
+  if (bytes + kFixedSmem <= 48 * 1024) return true;
+  constexpr int kDevices = 64;
+  static std::atomic<size_t> known[kDevices];
+  static std::mutex order;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) {
+    cudaGetLastError();
+    return false;
+  }
+  if (known[dev].load(std::memory_order_acquire) >= bytes) return true;
+  const std::lock_guard<std::mutex> lock(order);
+  if (known[dev].load(std::memory_order_relaxed) >= bytes) return true;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  known[dev].store(bytes, std::memory_order_release);
+  return true;
+}
 
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kc(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

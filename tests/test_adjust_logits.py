@@ -274,3 +274,26 @@ def test_empty_shapes_through_the_binding(gpu):
                                  allowed=i(1, 2)).shape == (0, 3, 64)
     with pytest.raises(sd.SpecError):
         sd.spec_adjust_logits(torch.zeros((2, 3, 0), device="cuda"), allowed=i(2, 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,V,N,biases", [(1000, 64, 511, True), (1000, 64, 512, True), (1000, 64, 513, True),
+                                          (1000, 64, 1536, False), (500, 64, 1792, True), (1000, 64, 2048, True)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_shared_memory_around_the_default_limit(gpu, B, V, N, biases, dtype):
+    """Node counts at which a block's shared memory, the fixed part included, passes 48 KB; most rows are not live."""
+    rng = np.random.default_rng(N)
+    live = 3
+    x = torch.zeros((B, N, V), dtype=dtype, device="cuda")
+    c = make_case(N, B, live, V, dtype, edges=False)
+    x[:, :live] = c["x"].cuda()
+    keep = ("history", "history_lens", "rep", "freq", "draft") + (("bias_ids", "bias_vals") if biases else ())
+    args = on_gpu(c, keep)
+    args["draft_token"] = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+    args["draft_token"][:, :live] = torch.from_numpy(c["draft"]).cuda()
+    nodes = torch.full((B,), live, dtype=torch.int32, device="cuda")
+    sd.spec_adjust_logits(x, num_nodes=nodes, **args)
+    some = rng.integers(0, B, 40)
+    want = expected({k: (v if k != "x" else v)[some] for k, v in c.items() if k == "x" or k in keep}, keep)
+    same(x[torch.from_numpy(some).cuda(), :live], want)
+    assert not bool(x[:, live:].any())
