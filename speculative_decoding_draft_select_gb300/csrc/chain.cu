@@ -583,9 +583,7 @@ int launch_chain(ChainParams& p, const QSrc& qsrc, cudaStream_t s) {
   auto kernel = chain_verify_kernel<DT, QSrc>;
   const size_t smem = sizeof(uint4) * kRingItems * kCT +
                       sizeof(float) * (static_cast<size_t>(cdf_part_tiles<kCT, kCE, 1>(p.V)) * kCT + p.ntiles);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return SPEC_ERR_CUDA;
+  if (!allow_smem<chain_verify_kernel<DT, QSrc>>(smem)) return SPEC_ERR_CUDA;
   // as much shared memory as the SM has (more CTAs resident: more rows in flight)
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return SPEC_ERR_CUDA;

@@ -1029,10 +1029,7 @@ int launch_softmax_topk_t2(const void* logits, int64_t R, int64_t V, float c, fl
                            int32_t* topk_idx, float* probs, float* row_stats, int32_t* stats, const ExpandArgs& ex,
                            cudaStream_t s) {
   constexpr size_t smem = draft_smem_bytes<K>();
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(softmax_topk_kernel<DT, K, THREADS, TWO>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess)
-    return SPEC_ERR_CUDA;
+  if (!allow_smem<softmax_topk_kernel<DT, K, THREADS, TWO>>(smem)) return SPEC_ERR_CUDA;
   launch_k(softmax_topk_kernel<DT, K, THREADS, TWO>, static_cast<unsigned>(R), THREADS, smem, s, logits, V, c, c1, k,
            topk_p, topk_idx, probs, row_stats, stats, ex);
   return launch_status();
@@ -1155,17 +1152,11 @@ int softmax_sample_impl(const void* logits, int dtype, int64_t R, int64_t V, flo
   const size_t smem = sizeof(float) * static_cast<size_t>(ntiles > 0 ? ntiles : 1) * kFusedThreads;
   const unsigned grid = static_cast<unsigned>(R);
   if (dtype == SPEC_BF16) {
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(softmax_sample_kernel<SPEC_BF16>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem)) != cudaSuccess)
-      return SPEC_ERR_CUDA;
+    if (!allow_smem<softmax_sample_kernel<SPEC_BF16>>(smem)) return SPEC_ERR_CUDA;
     launch_k(softmax_sample_kernel<SPEC_BF16>, grid, kFusedThreads, smem, s, logits, V, c, u, out_token,
              out_prob_or_null, row_stats_or_null, probs_or_null, stats_or_null, ex);
   } else {
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(softmax_sample_kernel<SPEC_F32>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem)) != cudaSuccess)
-      return SPEC_ERR_CUDA;
+    if (!allow_smem<softmax_sample_kernel<SPEC_F32>>(smem)) return SPEC_ERR_CUDA;
     launch_k(softmax_sample_kernel<SPEC_F32>, grid, kFusedThreads, smem, s, logits, V, c, u, out_token,
              out_prob_or_null, row_stats_or_null, probs_or_null, stats_or_null, ex);
   }
@@ -1203,11 +1194,10 @@ extern "C" int spec_sample(const void* logits_or_null, int dtype, const float* p
   const size_t smem = sizeof(float) * static_cast<size_t>(cdf_smem_floats<kSampleThreads>(V));
   const float c = probs_or_null ? 0.0f : kLog2e / T;
   const unsigned grid = static_cast<unsigned>(R);
-  if (smem > 48 * 1024) {
-    cudaFuncSetAttribute(sample_kernel<SPEC_F32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cudaFuncSetAttribute(sample_kernel<SPEC_F32, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cudaFuncSetAttribute(sample_kernel<SPEC_BF16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  }
+  if (!(probs_or_null          ? allow_smem<sample_kernel<SPEC_F32, true>>(smem)
+        : dtype == SPEC_BF16 ? allow_smem<sample_kernel<SPEC_BF16, false>>(smem)
+                             : allow_smem<sample_kernel<SPEC_F32, false>>(smem)))
+    return SPEC_ERR_CUDA;
   if (probs_or_null)
     launch_k(sample_kernel<SPEC_F32, true>, grid, kSampleThreads, smem, s, nullptr, probs_or_null, V, c, u, out_token,
              out_prob_or_null, nullptr, stats_or_null);

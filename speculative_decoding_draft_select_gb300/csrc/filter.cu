@@ -629,11 +629,8 @@ extern "C" int spec_filter_logits(void* logits, int dtype, int64_t R, int64_t V,
   const int64_t grid = std::min<int64_t>(R, static_cast<int64_t>(sms) * 2);
   constexpr size_t smem = sizeof(FShared);
   auto kernel = dtype == SPEC_BF16 ? filter_kernel<SPEC_BF16> : filter_kernel<SPEC_F32>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess) {
-    cudaGetLastError();
+  if (!(dtype == SPEC_BF16 ? allow_smem<filter_kernel<SPEC_BF16>>(smem) : allow_smem<filter_kernel<SPEC_F32>>(smem)))
     return SPEC_ERR_CUDA;
-  }
   launch_k(kernel, static_cast<unsigned>(grid), kFT, smem, s, logits, R, V, c, top_k, top_p, stats_or_null);
   return launch_status();
 }

@@ -495,10 +495,7 @@ extern "C" int tli_pruned_head(int64_t M, int64_t H, int64_t K, const void* hidd
   if (!bf16_map(&tm_h, hidden, M, H, kBM) || !bf16_map(&tm_w128, weight, K, H, kBN) ||
       !bf16_map(&tm_w16, weight, K, H, kSubRows))
     return SPEC_ERR_CUDA;
-  static const bool smem_ok =
-      cudaFuncSetAttribute(pruned_head_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kHeadSmem)) == cudaSuccess;
-  if (!smem_ok) return SPEC_ERR_CUDA;
+  if (!allow_smem<pruned_head_kernel>(kHeadSmem)) return SPEC_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const float c = kLog2e / T;
   float4* partial = static_cast<float4*>(ws);

@@ -766,11 +766,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
 }
 
 template <auto KERNEL, int D, int R>
-int launch_rows(AttnArgs& a, int dev, size_t smem, int ctas, cudaStream_t s) {
-  if (!attn_smem<KERNEL>(dev, smem)) {
-    cudaGetLastError();
-    return SPEC_ERR_CUDA;
-  }
+int launch_rows(AttnArgs& a, size_t smem, int ctas, cudaStream_t s) {
+  if (!allow_smem<KERNEL>(smem)) return SPEC_ERR_CUDA;
   a.ctas = ctas < kMaxCtas ? ctas : kMaxCtas;
   launch_k(KERNEL, static_cast<unsigned>(a.ctas), kAttThreads, smem, s, a);
   launch_merge<D>(a, R, kWeightExp, s);
@@ -778,9 +775,9 @@ int launch_rows(AttnArgs& a, int dev, size_t smem, int ctas, cudaStream_t s) {
 }
 
 template <int D>
-int launch_few(AttnArgs& a, int R, int dev, int sms, cudaStream_t s) {
-  if (R == 8) return launch_rows<kv4_attention8_kernel<D>, D, 8>(a, dev, sizeof(AttShared8<D>), sms * 3, s);
-  return launch_rows<kv4_attention_kernel<D>, D, 16>(a, dev, sizeof(AttShared<D>), sms * 3, s);
+int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
+  if (R == 8) return launch_rows<kv4_attention8_kernel<D>, D, 8>(a, sizeof(AttShared8<D>), sms * 3, s);
+  return launch_rows<kv4_attention_kernel<D>, D, 16>(a, sizeof(AttShared<D>), sms * 3, s);
 }
 
 // Rows of a row tile here: 8 or 16 where they suffice; 0: more rows than that
@@ -832,8 +829,7 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
   const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
   const int64_t tokens = static_cast<int64_t>(B) * N, wide = static_cast<int64_t>(Hq) * D;
   if (q0 < o0 + 2 * tokens * wide && o0 < q0 + 2 * ((tokens - 1) * q_stride + wide)) return SPEC_ERR_INVALID_ARG;
-  int dev = 0;
-  const int sms = attn_sms(dev);
+  const int sms = attn_sms();
   if (sms == 0) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
@@ -844,6 +840,6 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
              scale * kLog2e, static_cast<uint16_t*>(out), lse_or_null, static_cast<float*>(ws), 0, stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int R = rows_of(static_cast<int64_t>(N) * a.G);
-  if (R == 0) return launch_tree_attention(a, D, dev, sms, s);
-  return D == 128 ? launch_few<128>(a, R, dev, sms, s) : launch_few<64>(a, R, dev, sms, s);
+  if (R == 0) return launch_tree_attention(a, D, sms, s);
+  return D == 128 ? launch_few<128>(a, R, sms, s) : launch_few<64>(a, R, sms, s);
 }

@@ -2,8 +2,6 @@
 // the division of the work, the unpacking of codes and the merge of partials.
 #pragma once
 
-#include <atomic>
-
 #include "kv4.cuh"
 
 namespace specdec {
@@ -332,10 +330,11 @@ void launch_merge(const AttnArgs& a, int R, float held, cudaStream_t s) {
   launch_k(kv4_merge_kernel<D>, grid, kMergeThreads, 0, s, a, R, held);
 }
 
-// The current device and its number of SMs (0: no answer), asked once a
-// device: a query is a noticeable part of a call of a few microseconds.
-inline int attn_sms(int& dev) {
+// The number of SMs of the current device (0: no answer), asked once a device:
+// a query is a noticeable part of a call of a few microseconds.
+inline int attn_sms() {
   static std::atomic<int> known[64];
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::atomic<int>& k = known[dev & 63];
   int sms = dev < 64 ? k.load(std::memory_order_relaxed) : 0;
@@ -345,22 +344,9 @@ inline int attn_sms(int& dev) {
   }
   return sms;
 }
-// Dynamic shared memory of a kernel beyond 48 KB, likewise once a device and
-// kernel.
-template <auto KERNEL>
-bool attn_smem(int dev, size_t bytes) {
-  static std::atomic<uint64_t> done{0};
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return true;
-  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-    return false;
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return true;
-}
-
 // Limits of the tensor-memory kernel's launches (kv4_tree.cu) and its entry.
 constexpr int kTreeRows = 128;     // rows of an accumulator
 constexpr int kTreeMaxCtas = 304;  // two on each of 152 SMs (one with two accumulators)
-int launch_tree_attention(AttnArgs a, int D, int dev, int sms, cudaStream_t s);
+int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s);
 
 }  // namespace specdec

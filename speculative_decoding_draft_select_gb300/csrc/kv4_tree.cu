@@ -650,14 +650,11 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 }
 
 template <int D, int MT>
-int launch_tree(AttnArgs a, int dev, int sms, cudaStream_t s) {
+int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
   using C = TreeCfg<D, MT>;
   constexpr int R = kTreeRows * MT;
   constexpr auto kernel = kv4_tree_kernel<D, MT>;
-  if (!attn_smem<kernel>(dev, C::kSmem)) {
-    cudaGetLastError();
-    return SPEC_ERR_CUDA;
-  }
+  if (!allow_smem<kernel>(C::kSmem)) return SPEC_ERR_CUDA;
   a.ctas = sms * (MT == 2 ? 1 : 2);
   a.ctas = a.ctas < kTreeMaxCtas / MT ? a.ctas : kTreeMaxCtas / MT;
   launch_k(kernel, static_cast<unsigned>(a.ctas), C::kThreads, C::kSmem, s, a);
@@ -667,13 +664,13 @@ int launch_tree(AttnArgs a, int dev, int sms, cudaStream_t s) {
 
 }  // namespace
 
-int launch_tree_attention(AttnArgs a, int D, int dev, int sms, cudaStream_t s) {
+int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s) {
   // two accumulators where there are rows for them (B=128, 8 KV heads of 128,
   // contexts 16..2048: 160 rows 255 us, 307 with one; 128 rows 243, 168 with
   // one)
   const bool two = static_cast<int64_t>(a.N) * a.G > kTreeRows;
-  if (D == 128) return two ? launch_tree<128, 2>(a, dev, sms, s) : launch_tree<128, 1>(a, dev, sms, s);
-  return two ? launch_tree<64, 2>(a, dev, sms, s) : launch_tree<64, 1>(a, dev, sms, s);
+  if (D == 128) return two ? launch_tree<128, 2>(a, sms, s) : launch_tree<128, 1>(a, sms, s);
+  return two ? launch_tree<64, 2>(a, sms, s) : launch_tree<64, 1>(a, sms, s);
 }
 
 }  // namespace specdec

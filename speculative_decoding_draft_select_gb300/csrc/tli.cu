@@ -826,11 +826,7 @@ bool launch_planned(int64_t R, int64_t Vd, int64_t Vt, const void* draft, const 
   cap &= ~int64_t(7);
   if (cap < 8) return false;
   const size_t smem = static_cast<size_t>((fixed + cap * esz + 15) & ~int64_t(15));
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(tli_planned_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
+  if (!allow_smem<tli_planned_kernel<DT>>(smem)) return false;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, tli_planned_kernel<DT>, kResThreads, smem) !=
           cudaSuccess ||

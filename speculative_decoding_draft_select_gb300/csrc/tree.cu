@@ -242,11 +242,7 @@ extern "C" int spec_build_tree(int B, int k, int num_steps, int N, const float* 
   int64_t L = 1;
   while (L < P - 1) L <<= 1;
   const size_t smem = sizeof(uint64_t) * L + sizeof(int32_t) * (P + 3 * static_cast<int64_t>(N));
-  if (smem > 48 * 1024) {
-    if (cudaFuncSetAttribute(build_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return SPEC_ERR_CUDA;
-  }
+  if (!allow_smem<build_tree_kernel>(smem)) return SPEC_ERR_CUDA;
   launch_k(build_tree_kernel, B, kBuildThreads, smem, reinterpret_cast<cudaStream_t>(stream), N, P, L, pool_score,
            pool_token, pool_parent, pool_qrow, root_token, seq_lens, draft_token, parent, positions, tree_mask,
            retrieve_index, retrieve_next_token, retrieve_next_sibling, q_row);

@@ -747,12 +747,7 @@ template <int DT, class QSrc, int C, bool WOR>
 int64_t walk_capacity(size_t smem) {
   auto kernel = sample_verify_kernel<DT, QSrc, C, WOR>;
   if (smem > kMaxDynSmem) return 0;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-          cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
+  if (!allow_smem<sample_verify_kernel<DT, QSrc, C, WOR>>(smem)) return 0;
   if (C == 1) {
     int dev = 0, sms = 0, per = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -1498,3 +1498,61 @@ def test_filtered_verify_law_monte_carlo_gpu(top_k, top_p):
     seqs = spec_rounds_with(verify, logP, Q, 0, M, width, depth, 100000, seed=5 + top_k)
     counts = np.bincount(np.ravel_multi_index(seqs.T, (V,) * M), minlength=V ** M)
     assert chi2_pvalue(counts, probs) > 1e-4
+
+
+# ------------------------------------------- sizes at the shared-memory limit
+
+# Sizes whose shared memory, a block's fixed part included, lies just above
+# the 48 KB a launch may use without asking.
+
+@pytest.mark.parametrize("V,dtype", [(196608, torch.float32), (393216, torch.bfloat16)])
+def test_softmax_sample_at_the_shared_memory_limit(V, dtype):
+    test_softmax_sample_parity(V, dtype)
+
+
+@pytest.mark.parametrize("use_probs", [True, False])
+def test_sample_at_the_shared_memory_limit(use_probs):
+    V, R = 2957000, 2
+    rng = np.random.default_rng(5)
+    x = make_logits(rng, R, V, torch.float32)
+    u = np.array([0.25, 0.75], np.float32)
+    if use_probs:
+        probs = _softmax64(x.numpy(), 1.0).astype(np.float32)
+        tok, _ = sd.spec_sample(dev(u), probs=dev(probs))
+        otok, _, margin, _ = oracle.sample(u, probs=probs)
+    else:
+        tok, _ = sd.spec_sample(dev(u), logits=dev(x))
+        otok, _, margin, _ = oracle.sample(u, logits=np_logits(x), T=1.0)
+    diff = tok.cpu().numpy() != otok
+    assert not (diff & (margin >= BOUNDARY)).any()
+
+
+@pytest.mark.parametrize("N", [410, 415, 421])
+def test_tree_at_the_shared_memory_limit(N):
+    test_tree_parity(2, 16, 12, N, False)
+
+
+@pytest.mark.parametrize("N,without_replacement", [(434, False), (437, False), (440, False), (325, True), (330, True)])
+def test_verify_sample_at_the_shared_memory_limit(N, without_replacement):
+    B, V = 2, 64
+    rng = np.random.default_rng(N)
+    nt, ns = chain_meta(B, N)
+    target = rng.normal(0, 1, (B, N, V)).astype(np.float32)
+    q = _softmax64(target, 1.0).astype(np.float32)  # p = q: every draft is accepted
+    dt = rng.integers(0, V, (B, N)).astype(np.int32)
+    coins = (rng.random((B, N)) * 0.98).astype(np.float32)
+    dt[1, N // 2] = 3
+    q[1, N // 2 - 1, 3] *= 400                      # but for one
+    uf = rng.random(B).astype(np.float32)
+    g = sd.spec_verify_sample(dev(target), 1.0, dev(q), dev(dt), dev(nt), dev(ns), dev(coins), dev(uf),
+                              without_replacement=without_replacement)
+    o = oracle.verify_sample(target, 1.0, q, dt, nt, ns, coins, uf, without_replacement=without_replacement)
+    torch.cuda.synchronize()
+    verify_compare(g, o, 0, 0, "sample")
+    assert int(g["accept_length"][0]) == N - 1
+    # request 1 ends with a draw from the residual max(p - q, 0), where p - q is the rounding of q to fp32 (relative
+    # 2^-24) but at the token that was raised: less than the fp32 error of p, so any token may come of it
+    n = int(o["accept_length"][1])
+    assert n < N // 2 and int(g["accept_length"][1]) == n
+    for name, k in (("accept_path", N), ("committed", n)):
+        np.testing.assert_array_equal(g[name][1, :k].cpu().numpy(), o[name][1, :k], err_msg=name)
