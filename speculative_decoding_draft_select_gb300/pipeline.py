@@ -182,16 +182,20 @@ def run_kv4_append(buf: StepBuffers, k, v, seq_lens, req_to_token, kv_pool, num_
 
 
 def run_attention(buf: StepBuffers, q, seq_lens, req_to_token, kv_pool, num_kv_heads, scale=None, num_nodes=None,
-                  out=None, lse=None):
+                  out=None, lse=None, ws=None):
     """Attention of q [B, N, Hq, D] of buf.tree's nodes over context and tree
-    (their K and V appended before).  The workspace of a size is allocated by
-    the first call that needs it and kept as long as buf, so that a captured
-    step's stays its own."""
-    B, N, Hq, D = q.shape
-    need = spec_kv4_attention_ws_size(B, N, Hq, int(num_kv_heads), D)
-    ws = buf.attention_ws.get(need)
+    (their K and V appended before).  Without ``ws``, the workspace of a size
+    is allocated by the first call that needs it and kept as long as buf, so
+    that a captured step's stays its own; like buf's other buffers it serves
+    calls that follow one another.  Calls of one buf that may run at the same
+    time (layers on several streams, two graphs replayed side by side) pass a
+    ``ws`` each, of spec_kv4_attention_ws_size bytes."""
     if ws is None:
-        ws = buf.attention_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
+        B, N, Hq, D = q.shape
+        need = spec_kv4_attention_ws_size(B, N, Hq, int(num_kv_heads), D)
+        ws = buf.attention_ws.get(need)
+        if ws is None:
+            ws = buf.attention_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
     return spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask=buf.tree["tree_mask"],
                               scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=ws, stats=buf.stats)
 

@@ -184,3 +184,30 @@ def test_under_the_bounds_checking_build():
     tail = (r.stdout + r.stderr)[-4000:]
     assert r.returncode == 0, tail
     assert " passed" in r.stdout and " error" not in r.stdout, tail
+
+
+@pytest.mark.gpu
+def test_two_layers_on_two_streams(gpu):
+    """Two layers of one layout at once, each with a workspace of its own; the buffers' is not touched."""
+    page = 16
+    x = {k: v.cuda() for k, v in inputs(9, page).items()}
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=page)
+    pl.run_draft(buf, x["draft"], 1.0, x["root"], x["lens"])
+    fill(x)
+    pl.run_kv4_append(buf, x["k"], x["v"], x["lens"], x["table"], x["pool"])
+    q2 = -x["q"]
+    size = sd.spec_kv4_attention_ws_size(B, N, HQ, HKV, D)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = [torch.empty_like(x["q"]) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            pl.run_attention(buf, q2, x["lens"], x["table"], x["pool"], HKV, out=out[1], ws=ws[1])
+        pl.run_attention(buf, x["q"], x["lens"], x["table"], x["pool"], HKV, out=out[0], ws=ws[0])
+    torch.cuda.synchronize()
+    assert not buf.attention_ws
+    mask = buf.tree["tree_mask"].cpu().numpy()
+    for q, o in ((x["q"], out[0]), (q2, out[1])):
+        check(o, None, ref.kv4_attention(q.float().cpu().numpy(), x["pool"].cpu().numpy(), x["table"].cpu().numpy(),
+                                         x["lens"].cpu().numpy(), HKV, D ** -0.5, tree_mask=mask))
