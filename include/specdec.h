@@ -604,7 +604,10 @@ int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* poo
  * out 16-byte aligned, q_stride a multiple of 8, slot_stride a multiple of 16
  * below 2^31, Hq <= 4096, B <= 65535 (SPEC_ERR_UNSUPPORTED otherwise).
  *   ws: spec_kv4_attention_ws_size bytes (0 for sizes that are not
- *   supported), 16-byte aligned; calls that may overlap need their own. */
+ *   supported), 16-byte aligned; calls that may overlap need their own.
+ * Above 16 rows (nodes times query heads) per KV head its waits are bounded:
+ * one that runs out is counted in SPEC_STAT_WAIT_TIMEOUT (results void), so a
+ * caller who has to know passes stats. */
 size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D);
 int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const void* pool,
                        int64_t num_slots, int64_t slot_stride, const int32_t* num_nodes_or_null,

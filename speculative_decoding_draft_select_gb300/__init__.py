@@ -665,7 +665,8 @@ def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_ma
     tree_mask [B, N, N] is set (None: a chain).  scale: None is D ** -0.5.
     lse [B, N, Hq] f32 (optional) receives the log of the weights' sum.  ws:
     a uint8 workspace of spec_kv4_attention_ws_size bytes to reuse between
-    calls that do not overlap.  Returns out [B, N, Hq, D] bf16."""
+    calls that do not overlap.  stats: counts requests and slots out of range,
+    and waits that ran out (results void).  Returns out [B, N, Hq, D] bf16."""
     dev = _device(q, "q")
     qs = _rows(q, "q")
     if q.dtype is not torch.bfloat16:
