@@ -26,9 +26,10 @@ struct AttnArgs {
   int32_t* stats;
 };
 
-// Row r of a KV head is query head r % G of node r / G.  r < 2^23 and G <= 2^12
-// (both checked by the host), so r times the excess of g_inv G over 2^40 stays
-// below 2^40 / G and the quotient is exact.
+// Row r of a KV head is query head r % G of node r / G.  With r < 2^23 and G <=
+// 2^12 (both checked by the host), r g_inv is r 2^40 / G and an excess of r
+// (g_inv G - 2^40) / G < r <= 2^23, which is less than the 2^40 / G >= 2^28 that
+// the next quotient is away: the shift is exact.
 __device__ __forceinline__ int attn_node(const AttnArgs& a, int r) {
   return static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
 }

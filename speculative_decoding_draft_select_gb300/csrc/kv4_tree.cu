@@ -374,9 +374,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
           // the largest is then below 4); zeros, and rows with an infinity or NaN,
           // are taken as they are
           const int e = bits == 0 || bits >= 0x7f80 ? 0 : min(max((bits >> 7) - 127, -126), 126);
-          // the sign of the scale goes into q, so that a larger S is a larger score
-          const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), a.scale_log2);
-          if (sub == 0) s_c[seg & 1][r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (sub == 0) s_c[seg & 1][r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
           for (int i = 0; i < per / 8; ++i) {
             uint32_t y[4];

@@ -467,3 +467,14 @@ def test_nan_in_q_is_nan_in_both_results(gpu, N, G):
     other = torch.ones((1, N, G), dtype=torch.bool, device="cuda")
     other[0, N - 1, G - 1] = False
     assert torch.equal(out[other], want[other]) and torch.equal(lse[other], want_lse[other])
+
+
+def test_division_by_the_number_of_heads():
+    """The kernels' row / heads as a product with ceil(2^40 / heads), over every number of heads and the rows around
+    each multiple up to 2^23."""
+    for G in (*range(1, 70), 127, 128, 129, 1000, 2047, 4093, 4094, 4095, 4096):
+        inv = ((1 << 40) + G - 1) // G
+        n = np.arange(0, min((1 << 23) // G + 1, 2049), dtype=np.int64) * G
+        r = np.concatenate((n, n + G - 1, n + G // 2))
+        r = r[r < 1 << 23]
+        assert np.array_equal(r * inv >> 40, r // G)
