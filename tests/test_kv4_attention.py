@@ -478,3 +478,52 @@ def test_division_by_the_number_of_heads():
         r = np.concatenate((n, n + G - 1, n + G // 2))
         r = r[r < 1 << 23]
         assert np.array_equal(r * inv >> 40, r // G)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", KERNELS)
+def test_large_q_over_small_k(gpu, N, G):
+    """Large elements of q whose scores stay moderate: the bounds mean something in every row."""
+    D = 128
+    c = make_case(31 + N, 2, N, G, 1, D, [61, 200], page=5)
+    k, v = ref.kv4_values(c["rows"], 1, D)
+    c["rows"] = ref.kv4_rows(k * 2.0**-9, v)
+    c["q"] = (c["q"].float() * 400).to(torch.bfloat16)
+    r = expected(c)
+    assert np.expm1(score_error(r, D)).max() < 0.1
+    out, lse = run(c)
+    check(out, lse, r)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,lens", [(2, 129, 2, 1, 64, [0, 130]), (1, 200, 4, 2, 128, [61]),
+                                               (2, 300, 3, 1, 64, [33, 257]), (1, 257, 1, 1, 128, [1000]),
+                                               (2, 128, 2, 1, 128, [5, 127])])
+@pytest.mark.parametrize("tree", [True, False])
+def test_more_nodes_than_a_tile(gpu, B, N, Hq, Hkv, D, lens, tree):
+    c = make_case(N + D, B, N, Hq, Hkv, D, lens, page=5, tree=tree)
+    nodes = np.array([N, N - 70][:B], np.int32)
+    for nn in (None, nodes):
+        out, lse = run(c, num_nodes=None if nn is None else torch.from_numpy(nn).cuda())
+        live = np.arange(N)[None] < (nodes if nn is not None else np.full(B, N))[:, None]
+        check(out, lse, expected(c, nn), live)
+
+
+@pytest.mark.gpu
+def test_most_nodes_and_heads(gpu):
+    """2048 nodes of 4095 query heads on one KV head: 2^23 - 2048 rows.  Each node sees itself alone."""
+    N, Hq, D = 2048, 4095, 64
+    rng = np.random.default_rng(17)
+    v = rng.normal(0, 1, (N, 1, D)).astype(np.float32)
+    rows = ref.kv4_rows(v, v)
+    q = torch.empty((1, N, Hq, D), dtype=torch.bfloat16, device="cuda").normal_()
+    out = sd.spec_kv4_attention(q, torch.from_numpy(rows).cuda(), torch.arange(N, dtype=torch.int32, device="cuda")[None],
+                                torch.zeros(1, dtype=torch.int32, device="cuda"), 1,
+                                tree_mask=torch.eye(N, dtype=torch.uint8, device="cuda")[None])
+    want = torch.from_numpy(ref.kv4_values(rows, 1, D)[1]).cuda()  # [N, 1, D] fp64
+    # v and its weight in fp16, the exponential's 2^-20 and the division; then bf16
+    move = want.abs() * (2 * 2.0**-11 + 2.0**-18) + 2.0**-25
+    bound = move + 2.0**-8 * (want.abs() + move)
+    for n in range(0, N, 256):
+        off = (out[0, n:n + 256].double() - want[n:n + 256]).abs()
+        assert bool((off <= bound[n:n + 256]).all())
