@@ -475,6 +475,7 @@ int spec_filter_logits(void* logits, int dtype, int64_t R, int64_t V, float T, i
  *     (in place).  Rows n >= num_nodes[b] (NULL: N) are left as they were.
  *   history [B, max_history] int32, the first history_lens[b] entries (NULL:
  *     all) count; ids outside [0, V) are ignored.  NULL: no history.
+ *     prompt_lens NULL: 0, all of it is answer.
  *   rep / freq / pres [B] fp32; NULL: 1 / 0 / 0.  A rep that is not > 0 is
  *     taken as 1 (SPEC_STAT_BAD_REQUEST).
  *   draft_token [B, N], tree_mask [B, N, N] u8 as spec_build_tree writes

@@ -5,7 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
 #include <mutex>
 #include <utility>
 
@@ -212,29 +211,23 @@ struct LaunchCfg {
 
 // Lets KERNEL be launched on the current device with `bytes` of dynamic shared
 // memory.  A block's fixed part counts towards the default 48 KB too (kFixedSmem
-// is more than any kernel here has), and the limit of a kernel is never taken
-// back below what an earlier call needed: another thread may be between its
-// call of this and its launch.
-constexpr size_t kFixedSmem = 9 * 1024;
+// is more than any kernel has that may come below it), and the limit is never
+// taken back below what an earlier call needed: another thread may be between
+// its call of this and its launch.  Set every time (0.2 us), so that a context
+// that the caller has reset has it too.
+constexpr size_t kFixedSmem = 8 * 1024;
 template <auto KERNEL>
 inline bool allow_smem(size_t bytes) {
   if (bytes + kFixedSmem <= 48 * 1024) return true;
-  constexpr int kDevices = 64;
-  static std::atomic<size_t> known[kDevices];
   static std::mutex order;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) {
-    cudaGetLastError();
-    return false;
-  }
-  if (known[dev].load(std::memory_order_acquire) >= bytes) return true;
+  static size_t most = 0;
   const std::lock_guard<std::mutex> lock(order);
-  if (known[dev].load(std::memory_order_relaxed) >= bytes) return true;
-  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+  const size_t want = bytes > most ? bytes : most;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(want)) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  known[dev].store(bytes, std::memory_order_release);
+  most = want;
   return true;
 }
 

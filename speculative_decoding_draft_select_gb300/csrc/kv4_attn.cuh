@@ -2,6 +2,8 @@
 // the division of the work, the unpacking of codes and the merge of partials.
 #pragma once
 
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace specdec {
