@@ -216,10 +216,14 @@ int kv4_check(int B, int64_t N, int Hkv, int D, int dtype, int64_t max_ctx, int6
   const int64_t groups = 2 * static_cast<int64_t>(Hkv) * (D / kKv4Group);
   const int64_t tokens = static_cast<int64_t>(B) * N;
   if (tokens > INT32_MAX / groups) return SPEC_ERR_UNSUPPORTED;
-  // groups of a warp, 8 a step: as many as the token has, up to four steps
-  // (64-node trees, 8 heads of 128: 37 us for one step there and back, 27 for
-  // four); one step where the warps are few and latency is all there is (128
-  // tokens: 3.5 us, 5.2 with four)
+  // groups of a warp, 8 a step: as many as the token has, up to four steps; one
+  // step where the warps are few and latency is all there is.  8 heads of 128,
+  // bf16, append / gather in us with one, two and four steps:
+  //   128 tokens   1.8 2.2 3.0 / 1.7 1.9 2.2     2048    6.1  5.5  5.8 /  4.8  4.1  3.7
+  //   512          2.6 2.7 3.1 / 2.3 2.2 2.2     8192   20.0 17.5 17.0 / 14.9 11.0  9.3
+  //   1024         4.0 4.6 3.9 / 3.3 2.8 2.6     32768  76.6 65.5 60.6 / 64.8 43.6 33.9
+  // and of 32768 tokens of 8 groups (2 heads of 64) 10.7 16.4 28.9 / 8.1 8.8
+  // 10.1, of 16 groups (4 heads of 64, fp32) 20.3 18.2 29.5 / 16.0 14.7 13.7
   *steps = groups <= 8 || tokens * groups <= 8 * 8192 ? 1 : (groups <= 16 ? 2 : 4);
   *per_token = (groups + 8 * *steps - 1) / (8 * *steps);
   *units = tokens * *per_token;

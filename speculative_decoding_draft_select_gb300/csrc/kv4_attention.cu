@@ -26,11 +26,15 @@
 // between CTAs leaves partial (max, sum, weighted values) in the workspace,
 // which a second kernel merges in a fixed order.  The host knows no lengths.
 //
-// Bound by the instructions that unpack the codes, not by the bytes: 960 a
-// warp and 32 positions of 8 rows, 536 of them unpacking, at 12 warps an SM
-// (164 registers hold O and the codes at hand).  Measured at D = 128, 8 KV
-// heads: B=128, 32 heads, contexts 16..2048: 80 us for 172 MB; B=4, 64 heads,
-// contexts 60001..131001: 153 us for 491 MB.
+// Bound by latency at three warps a scheduler (164 registers hold O and the
+// codes at hand), neither by the issue slots (46% in use) nor by the memory: per
+// issue 0.9 warps each wait for memory, for shared memory and for the
+// instruction before, and 0.6 for the CTA's other warps, which meet five times
+// a segment of nine tiles on average.  960 instructions a warp and 32 positions
+// of 8 rows, 536 of them unpacking.  Measured at D = 128, 8 KV heads: B=128, 32
+// heads, contexts 16..2048: 80 us for 172 MB (227 MB from DRAM: the 160 bytes
+// of a head touch three 64-byte pieces, and other CTAs read the neighbours at
+// other times); B=4, 64 heads, contexts 60001..131001: 153 us for 491 MB.
 #include "kv4_attn.cuh"
 
 namespace specdec {
@@ -533,9 +537,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
 // weights (position g, rows 2t, 2t + 1) become the B fragment (positions 2t,
 // 2t + 1, row g) by one 8 x 8 transposition a block (movmatrix).  A warp takes
 // 32 positions at a time: what a tile costs beside the unpacking (the slots,
-// the copies' addresses, the maximum) is shared by more positions.  Bound by
-// the instructions that unpack the codes: 26 a position and lane of 128
-// channels.
+// the copies' addresses, the maximum) is shared by more positions.  The most of
+// its instructions unpack the codes: 26 a position and lane of 128 channels.
 template <int D>
 struct AttShared8 {
   static constexpr int kRow = D + 4;
@@ -782,12 +785,20 @@ int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
 
 // Rows of a row tile here: 8 or 16 where they suffice; 0: more rows than that
 // go to the tensor-memory kernel (kv4_tree.cu), whose time hardly depends on
-// them.  Contexts 16..2048, 8 KV heads of 128, in us:
-//   B=128:  4 rows 77 (as 16: 115), 8 rows 82 (126), 16 rows 146 (kv4_tree.cu:
-//           148), 24 rows 149 there (two fragments of 16 here: 208), 32: 151
-//           (231)
-//   B=8:    16 rows 18.5 (24.9), 32 rows 26.6 there (26.1)
-//   B=1:    16 rows 12.5 (16.8), 32 rows 17.8 there (15.8)
+// them.  8 KV heads, contexts 16..2048 (B=1: 777), in us, as row tiles of 8 /
+// of 16 / in kv4_tree.cu:
+//            D=128                                    D=64
+//            B=1            B=8            B=128      B=1            B=8            B=128
+//   1 row    8.4/9.7/15.0   14.2/14.8/22.9 73/128/137 7.2/8.6/13.1   10.8/11.6/19.7 60/59/99
+//   4 rows   8.8/10.5/15.6  15.0/15.8/23.4 77/127/138 7.9/9.9/13.8   12.2/12.9/20.8 63/60/99
+//   8 rows   9.6/11.5/16.3  16.3/17.1/23.9 79/127/139 8.6/11.2/14.7  13.8/14.7/21.8 64/66/99
+//   12 rows    -/11.8/16.4    -/17.3/24.1   -/136/140   -/11.9/14.8    -/15.1/22.0   -/76/100
+//   16 rows    -/12.3/16.4    -/17.8/24.2   -/138/141   -/12.1/14.8    -/15.3/22.1   -/82/100
+//   24 rows    -/12.8/16.9    -/24.6/25.0   -/258/143   -/12.4/15.3    -/17.4/22.7   -/140/101
+//   32 rows    -/13.0/17.1    -/25.7/25.4   -/261/144   -/12.7/15.4    -/18.3/22.9   -/153/101
+// Few requests of 17 to 48 rows would do better with several row tiles of 16
+// (the first row tile's codes are then in the L2 cache for the next); the host
+// knows B but not the lengths that decide it, so the rule looks at rows alone.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 0); }
 
 }  // namespace

@@ -664,9 +664,11 @@ int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
 }  // namespace
 
 int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s) {
-  // two accumulators where there are rows for them (B=128, 8 KV heads of 128,
-  // contexts 16..2048: 160 rows 255 us, 307 with one; 128 rows 243, 168 with
-  // one)
+  // two accumulators where there are rows for them (8 KV heads, contexts
+  // 16..2048, in us with one / with two: D=128, B=128: 96 rows 160 / 223, 128
+  // rows 161 / 226, 160 rows 291 / 246; B=8: 128 rows 31.1 / 31.6, 160 rows 36.8
+  // / 34.8; D=64, B=128: 128 rows 118 / 190, 160 rows 208 / 213; B=8: 128 rows
+  // 27.5 / 27.7, 160 rows 31.8 / 31.2)
   const bool two = static_cast<int64_t>(a.N) * a.G > kTreeRows;
   if (D == 128) return two ? launch_tree<128, 2>(a, sms, s) : launch_tree<128, 1>(a, sms, s);
   return two ? launch_tree<64, 2>(a, sms, s) : launch_tree<64, 1>(a, sms, s);
