@@ -801,13 +801,18 @@ int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
 // knows B but not the lengths that decide it, so the rule looks at rows alone.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 0); }
 
+// The upper limits of a call's sizes.
+bool attn_sizes(int B, int N, int Hq, int Hkv, int D) {
+  return spec_kv4_slot_bytes(Hkv, D) >= 0 && N <= SPEC_MAX_NODES && Hq <= SPEC_KV4_MAX_HEADS * 16 && B <= 65535;
+}
+
 }  // namespace
 }  // namespace specdec
 
 using namespace specdec;
 
 extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D) {
-  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || spec_kv4_slot_bytes(Hkv, D) < 0) return 0;
+  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !attn_sizes(B, N, Hq, Hkv, D)) return 0;
   const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
   const int R = rows_of(rows);
   return align256(R == 0 ? attn_ws_bytes(kTreeMaxCtas, kTreeRows, D) : attn_ws_bytes(kMaxCtas, R, D));
@@ -823,7 +828,7 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
       !isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   const int64_t row = spec_kv4_slot_bytes(Hkv, D);
-  if (row < 0 || N > SPEC_MAX_NODES || Hq > SPEC_KV4_MAX_HEADS * 16 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (!attn_sizes(B, N, Hq, Hkv, D)) return SPEC_ERR_UNSUPPORTED;
   // a row's factor, scale log2(e) times a power of two down to 2^-126, must not vanish
   if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
   if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;

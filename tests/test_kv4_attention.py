@@ -527,3 +527,13 @@ def test_most_nodes_and_heads(gpu):
     for n in range(0, N, 256):
         off = (out[0, n:n + 256].double() - want[n:n + 256]).abs()
         assert bool((off <= bound[n:n + 256]).all())
+
+
+def test_no_workspace_for_sizes_that_are_refused():
+    build()
+    size = sd.lib().spec_kv4_attention_ws_size
+    assert size(65535, 1, 8, 8, 128) > 0 and size(1, 2048, 8, 8, 128) > 0 and size(1, 1, 4096, 1, 64) > 0
+    for bad in ((65536, 1, 8, 8, 128), (1, 2049, 8, 8, 128), (1, 1, 4097, 1, 64), (1, 1, 514, 257, 64)):
+        assert size(*bad) == 0
+        with pytest.raises(sd.SpecError):
+            sd.spec_kv4_attention_ws_size(*bad)
