@@ -598,9 +598,9 @@ int spec_kv4_gather(int B, int64_t N, int Hkv, int D, int dtype, const void* poo
  * tree_mask hides from every row need not be.  Values enter the products in
  * fp16 (relative 2^-11), sums are fp32: scores times log2(e), and scale log2(e)
  * times a row's largest |q|, have to stay in fp32's range.  A row that attends
- * to nothing gives zeros and lse -inf.  Rows n >= num_nodes[b] are left as they were.  out must
- * not overlap q; 2^-20 <= scale <= 2^20.  A position whose slot is out of
- * range is not attended, and a request with seq_len < 0 or seq_len +
+ * to nothing gives zeros and lse -inf.  Rows n >= num_nodes[b] are left as they
+ * were.  out must not overlap q; 2^-20 <= scale <= 2^20.  A position whose slot
+ * is out of range is not attended, and a request with seq_len < 0 or seq_len +
  * num_nodes > max_ctx gives zeros (SPEC_STAT_BAD_REQUEST each).  q, pool and
  * out 16-byte aligned, q_stride a multiple of 8, slot_stride a multiple of 16
  * below 2^31, Hq <= 4096, B <= 65535 (SPEC_ERR_UNSUPPORTED otherwise).
