@@ -297,3 +297,32 @@ def test_shared_memory_around_the_default_limit(gpu, B, V, N, biases, dtype):
     want = expected({k: (v if k != "x" else v)[some] for k, v in c.items() if k == "x" or k in keep}, keep)
     same(x[torch.from_numpy(some).cuda(), :live], want)
     assert not bool(x[:, live:].any())
+
+
+@pytest.mark.gpu
+def test_two_threads_of_different_sizes(gpu):
+    """Launches that need much and little shared memory beyond the default, from two threads at once."""
+    import threading
+
+    B, V, failed = 1000, 64, []
+
+    def work(N):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                x = torch.ones((B, N, V), device="cuda")
+                draft = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+                ids = torch.full((B, 1), 5, dtype=torch.int32, device="cuda")
+                vals, one = torch.ones((B, 1), device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+                for _ in range(300):
+                    sd.spec_adjust_logits(x, draft_token=draft, bias_ids=ids, bias_vals=vals, num_nodes=one)
+                torch.cuda.current_stream().synchronize()
+                assert bool((x[:, 0, 5] == 301).all()) and bool((x[:, 1:] == 1).all())
+        except Exception as e:  # noqa: BLE001
+            failed.append((N, e))
+
+    threads = [threading.Thread(target=work, args=(N,)) for N in (513, 1400)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
