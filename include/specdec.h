@@ -616,6 +616,24 @@ int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int6
                        const uint8_t* tree_mask_or_null, float scale, void* out, float* lse_or_null,
                        int32_t* stats_or_null, void* ws, size_t ws_bytes, spec_stream_t stream);
 
+/* spec_kv4_attention with a sliding window and sinks: of what a node attends to
+ * there, it keeps the positions p < sinks (the text's first tokens, which stay
+ * visible) and p > P - window, P its own position.  Node n's position is
+ * positions[b][n] (spec_build_tree's: seq_lens[b] + depth), taken as the
+ * nearest of [seq_lens[b], seq_lens[b] + n] where it lies outside; NULL:
+ * seq_lens[b] + n, a chain.  A node m of the path counts by its position, its
+ * slot is at seq_lens[b] + m as before.  sinks >= 0, window >= 1 (the node
+ * itself).  Positions from sinks to seq_lens[b] - window are neither read nor
+ * looked up: their slots may have been freed.  Everything else, the workspace
+ * included, is as in spec_kv4_attention; with sinks + window above every
+ * length it gives the same values. */
+int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const void* pool,
+                              int64_t num_slots, int64_t slot_stride, const int32_t* num_nodes_or_null,
+                              const int32_t* seq_lens, const int32_t* positions_or_null, const int32_t* req_to_token,
+                              int64_t max_ctx, const uint8_t* tree_mask_or_null, int32_t sinks, int32_t window,
+                              float scale, void* out, float* lse_or_null, int32_t* stats_or_null, void* ws,
+                              size_t ws_bytes, spec_stream_t stream);
+
 /* -------------------------------------------------------------------- TLI */
 
 /* TLI constrain + top-1 + map ([TLI] Modifications: constrain_draft_logits

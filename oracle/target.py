@@ -68,14 +68,18 @@ def kv4_values(rows, H: int, D: int):
     return out
 
 
-def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, num_nodes=None):
+def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, num_nodes=None, window=None, sinks=0,
+                  positions=None):
     """Attention in 64 bits of q [B, N, Hq, D]: a dict of out [B, N, Hq, D],
     lse [B, N, Hq], and what error bounds need: mean_abs [B, N, Hq, D] (the
     weighted mean of |v|), dot_abs [B, N, Hq] (the largest |scale| sum |q| |k|
     of an attended position), part_abs (the largest |scale| (max |q| sum |k| +
     sum |q|)) and count [B, N, Hq] (attended positions).  Rows
     n >= num_nodes[b] are NaN.  A position whose slot is out of range is not
-    attended; a request whose positions are out of range gives zeros."""
+    attended; a request whose positions are out of range gives zeros.  With a
+    window a node at position P sees, of this, the positions below sinks and
+    those above P - window (positions [B, N], seq_len + n without; taken into
+    [seq_len, seq_len + n])."""
     q = np.asarray(q, np.float64)
     B, N, Hq, D = q.shape
     G = Hq // Hkv
@@ -92,6 +96,11 @@ def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, n
         k, v = kv4_values(rows[np.where(there, slot, 0)], Hkv, D)
         see = np.ones((nn, s + nn), bool)
         see[:, s:] = np.tril(np.ones((nn, nn), bool)) if tree_mask is None else tree_mask[b, :nn, :nn] != 0
+        if window is not None:
+            at = np.arange(s + nn)
+            if positions is not None:
+                at[s:] = np.clip(np.asarray(positions[b, :nn], np.int64), s, s + np.arange(nn))
+            see &= (at < sinks)[None] | (at[None] > at[s:, None] - window)
         see &= there
         for n in range(nn):
             at = np.flatnonzero(see[n])

@@ -26,7 +26,7 @@ __all__ = [
     "tli_map_ids",
     "tli_check_config", "tli_pruned_head", "spec_filter_logits", "spec_wait_probe", "spec_debug_bounds",
     "new_stats", "new_pool", "spec_kv4_slot_bytes", "spec_kv4_append", "spec_kv4_gather",
-    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_adjust_logits",
+    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_adjust_logits",
 ]
 
 F32 = 0
@@ -92,6 +92,8 @@ _SIGS = {
     "spec_kv4_attention_ws_size": (_SZ, [_I, _I, _I, _I, _I]),
     "spec_kv4_attention": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _F, _P, _P, _P, _P,
                                 _SZ, _P]),
+    "spec_kv4_attention_window": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32, _I32,
+                                       _F, _P, _P, _P, _P, _SZ, _P]),
     "spec_adjust_logits": (_I, [_I, _I, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P,
                                 _I64, _P, _P, _P]),
     "tli_pruned_head_ws_size": (_SZ, [_I64, _I64]),
@@ -667,6 +669,21 @@ def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_ma
     a uint8 workspace of spec_kv4_attention_ws_size bytes to reuse between
     calls that do not overlap.  stats: counts requests and slots out of range,
     and waits that ran out (results void).  Returns out [B, N, Hq, D] bf16."""
+    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
+                      None)
+
+
+def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, sinks, window, positions=None,
+                              tree_mask=None, scale=None, num_nodes=None, out=None, lse=None, ws=None, stats=None):
+    """spec_kv4_attention with a sliding window: a node at position P sees, of
+    what it would see there, the positions below ``sinks`` and those above P -
+    ``window``.  positions [B, N] int32: spec_build_tree's (None: a chain).
+    Positions between the sinks and the window are not read."""
+    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
+                      (positions, int(sinks), int(window)))
+
+
+def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats, window):
     dev = _device(q, "q")
     qs = _rows(q, "q")
     if q.dtype is not torch.bfloat16:
@@ -685,14 +702,18 @@ def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_ma
         return out
     if ws is None:
         ws = torch.empty(spec_kv4_attention_ws_size(B, N, Hq, num_kv_heads, D), dtype=torch.uint8, device=q.device)
-    rc = lib().spec_kv4_attention(B, N, Hq, num_kv_heads, D, q.data_ptr(), qs, pool, slots, stride,
-                                  _arg(num_nodes, i32, (B,), dev, "num_nodes"),
-                                  _arg(seq_lens, i32, (B,), dev, "seq_lens"), table, ctx, mask,
-                                  D ** -0.5 if scale is None else scale, dst, lse_at,
-                                  _arg(stats, i32, (NUM_STATS,), dev, "stats"),
-                                  _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel(), _stream())
+    what = (B, N, Hq, num_kv_heads, D, q.data_ptr(), qs, pool, slots, stride,
+            _arg(num_nodes, i32, (B,), dev, "num_nodes"), _arg(seq_lens, i32, (B,), dev, "seq_lens"))
+    rest = (D ** -0.5 if scale is None else scale, dst, lse_at, _arg(stats, i32, (NUM_STATS,), dev, "stats"),
+            _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel(), _stream())
+    if window is None:
+        rc = lib().spec_kv4_attention(*what, table, ctx, mask, *rest)
+    else:
+        positions, sinks, width = window
+        rc = lib().spec_kv4_attention_window(*what, _arg(positions, i32, (B, N), dev, "positions"), table, ctx, mask,
+                                             sinks, width, *rest)
     if rc:
-        raise SpecError("spec_kv4_attention", rc)
+        raise SpecError("spec_kv4_attention" if window is None else "spec_kv4_attention_window", rc)
     return out
 
 

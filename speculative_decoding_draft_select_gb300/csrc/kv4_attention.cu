@@ -109,17 +109,17 @@ struct Stage {
 // P for each of four warps.  A pair of lanes copies a position's 32-byte
 // sectors (one instruction: 16 positions), so the addresses are two shuffles a
 // 16 positions and constants.
-template <int D, int P, int RING, int E, int R>
+template <int D, int P, int RING, int E, int R, bool WIN>
 struct Filler {
   using St = Stage<D, P>;
   static constexpr int kTile = 4 * P;
-  Walk<kTile, E, R> ahead;
+  Walk<kTile, E, R, WIN> ahead;
   Part ap;
   bool more, loaded;
   int next_tile;
   int32_t slot;  // of position lane % P of the warp's; -2: no position
   const uint8_t* head;
-  const int32_t* row;  // the request's slots from this lane's position of tile 0 on
+  const int32_t* row;  // the request's slots from this lane's place of tile 0 on
   unsigned ring;
   unsigned* there;  // [RING]: positions of a stage that have a slot
 
@@ -128,7 +128,7 @@ struct Filler {
     head = a.pool + ap.h * kv4_head_bytes(D);
     row = a.table + static_cast<int64_t>(ap.b) * a.max_ctx + (threadIdx.x >> 5) * P + (threadIdx.x & (P - 1));
   }
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R>& walk, uint8_t* stages, unsigned* t) {
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R, WIN>& walk, uint8_t* stages, unsigned* t) {
     ahead = walk;
     more = ahead.next(a, ap);
     segment(a);
@@ -145,7 +145,9 @@ struct Filler {
     loaded = more;
     if (!more) return;
     const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + static_cast<int>(threadIdx.x & (P - 1));
-    slot = pos < ap.end && spec_in(pos, ap.end, nullptr) ? __ldg(row + next_tile * kTile) : -2;
+    slot = pos < ap.end && spec_in(pos, ap.end, nullptr) 
+               ? __ldg(row + next_tile * kTile + (WIN && pos >= ap.cut ? ap.gap : 0))
+               : -2;
     ++next_tile;
   }
   // Copies the tile whose slots were loaded last; one commit group, empty
@@ -319,7 +321,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, const Part& p, int
   if (a.lse && ch == 0) a.lse[at] = attn_lse(top, sum, kWeightExp);
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const AttnArgs a) {
   pdl_enter();
   constexpr int R = 16, H = 2;  // halves of a fragment's rows
@@ -331,10 +333,10 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
   if (threadIdx.x == 0) *cut = CutSegment{0, 0, 0, 0};
   Line line;
-  Walk<kTile, kEnds, R> walk;
-  if (!attn_stretch<kTile, kEnds, R, kAttThreads>(a, line, walk)) return;
+  Walk<kTile, kEnds, R, WIN> walk;
+  if (!attn_stretch<kAttThreads>(a, line, walk)) return;
 
-  Filler<D, 16, kRing, kEnds, R> fill;
+  Filler<D, 16, kRing, kEnds, R, WIN> fill;
   fill.begin(a, walk, sh.ring[warp][0], sh.there[warp]);
   int st = 0;  // stage of the tile at hand
 
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
       // scores in units of log2, masked; s[j][i]: row g + 8 (i / 2),
       // position 8 j + 2 t + i % 2
       const int p0 = tile * kTile + warp * 16;
-      const bool whole = there == 0xffffu && p0 + 16 <= rq.start;
+      const bool whole = there == 0xffffu && attn_context<WIN>(a, rq, p0, p0 + 16);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -400,13 +402,10 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention_kernel(const Att
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 2 * H; ++i) {
-            const int at = 8 * j + 2 * t + (i & 1), node = p0 + at - rq.start;
+            const int at = 8 * j + 2 * t + (i & 1), r = g + 8 * (i >> 1);
             bool see = (there >> at) & 1u;
-            if (see && node >= 0) {
-              const int r = g + 8 * (i >> 1), n = attn_node(a, r0 + r);
-              see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
-                    (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
-            }
+            if (see && (WIN || p0 + at >= rq.start))
+              see = r < rows && attn_sees<WIN>(a, rq, attn_node(a, r0 + r), p0 + at);
             if (!see) s[j][i] = neg_inf();
           }
       }
@@ -556,7 +555,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const AttnArgs a) {
   pdl_enter();
   constexpr int R = 8, T = 4 * 32;
@@ -568,9 +567,9 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
   if (threadIdx.x == 0) *cut = CutSegment{0, 0, 0, 0};
   Line line;
-  Walk<T, kEnds8, R> walk;
-  if (!attn_stretch<T, kEnds8, R, kAttThreads>(a, line, walk)) return;
-  Filler<D, 32, kRing8, kEnds8, R> fill;
+  Walk<T, kEnds8, R, WIN> walk;
+  if (!attn_stretch<kAttThreads>(a, line, walk)) return;
+  Filler<D, 32, kRing8, kEnds8, R, WIN> fill;
   fill.begin(a, walk, sh.ring[warp][0], sh.there[warp]);
   int st = 0;  // stage of the tile at hand
 
@@ -644,19 +643,15 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][i] *= cr[i & 1];
-      const bool whole = there == 0xffffffffu && p0 + 32 <= rq.start;
+      const bool whole = there == 0xffffffffu && attn_context<WIN>(a, rq, p0, p0 + 32);
       if (!whole) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int at = 16 * u + g + 8 * (i >> 1), node = p0 + at - rq.start, r = 2 * t + (i & 1);
+            const int at = 16 * u + g + 8 * (i >> 1), r = 2 * t + (i & 1);
             bool see = (there >> at) & 1u;
-            if (see && node >= 0) {
-              const int n = attn_node(a, r);
-              see = r < rows && spec_in(n, a.N, a.stats) && spec_in(node, a.N, a.stats) &&
-                    (a.mask ? __ldg(a.mask + (static_cast<int64_t>(b) * a.N + n) * a.N + node) != 0 : node <= n);
-            }
+            if (see && (WIN || p0 + at >= rq.start)) see = r < rows && attn_sees<WIN>(a, rq, attn_node(a, r), p0 + at);
             if (!see) s[u][i] = neg_inf();
           }
       }
@@ -777,10 +772,10 @@ int launch_rows(AttnArgs& a, size_t smem, int ctas, cudaStream_t s) {
   return launch_status();
 }
 
-template <int D>
+template <int D, bool WIN>
 int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
-  if (R == 8) return launch_rows<kv4_attention8_kernel<D>, D, 8>(a, sizeof(AttShared8<D>), sms * 3, s);
-  return launch_rows<kv4_attention_kernel<D>, D, 16>(a, sizeof(AttShared<D>), sms * 3, s);
+  if (R == 8) return launch_rows<kv4_attention8_kernel<D, WIN>, D, 8>(a, sizeof(AttShared8<D>), sms * 3, s);
+  return launch_rows<kv4_attention_kernel<D, WIN>, D, 16>(a, sizeof(AttShared<D>), sms * 3, s);
 }
 
 // Rows of a row tile here: 8 or 16 where they suffice; 0: more rows than that
@@ -806,24 +801,12 @@ bool attn_sizes(int B, int N, int Hq, int Hkv, int D) {
   return spec_kv4_slot_bytes(Hkv, D) >= 0 && N <= SPEC_MAX_NODES && Hq <= SPEC_KV4_MAX_HEADS * 16 && B <= 65535;
 }
 
-}  // namespace
-}  // namespace specdec
-
-using namespace specdec;
-
-extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D) {
-  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !attn_sizes(B, N, Hq, Hkv, D)) return 0;
-  const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
-  const int R = rows_of(rows);
-  return align256(R == 0 ? attn_ws_bytes(kTreeMaxCtas, kTreeRows, D) : attn_ws_bytes(kMaxCtas, R, D));
-}
-
-extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,
-                                  const void* pool, int64_t num_slots, int64_t slot_stride,
-                                  const int32_t* num_nodes_or_null, const int32_t* seq_lens,
-                                  const int32_t* req_to_token, int64_t max_ctx, const uint8_t* tree_mask_or_null,
-                                  float scale, void* out, float* lse_or_null, int32_t* stats_or_null, void* ws,
-                                  size_t ws_bytes, spec_stream_t stream) {
+// Both entry points; window 0: none.
+int attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const void* pool,
+              int64_t num_slots, int64_t slot_stride, const int32_t* num_nodes, const int32_t* seq_lens,
+              const int32_t* positions, const int32_t* req_to_token, int64_t max_ctx, const uint8_t* tree_mask,
+              int sinks, int window, float scale, void* out, float* lse, int32_t* stats, void* ws, size_t ws_bytes,
+              spec_stream_t stream) {
   if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !(scale > 0.0f) ||
       !isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
@@ -852,10 +835,47 @@ extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const vo
   }
   AttnArgs a{static_cast<const uint16_t*>(q), q_stride, B, N, Hq, Hkv, Hq / Hkv,
              ((1ull << 40) + Hq / Hkv - 1) / (Hq / Hkv), static_cast<const uint8_t*>(pool),
-             num_slots, slot_stride, req_to_token, max_ctx, seq_lens, num_nodes_or_null, tree_mask_or_null,
-             scale * kLog2e, static_cast<uint16_t*>(out), lse_or_null, static_cast<float*>(ws), 0, stats_or_null};
+             num_slots, slot_stride, req_to_token, max_ctx, seq_lens, num_nodes, tree_mask, positions, sinks, window,
+             scale * kLog2e, static_cast<uint16_t*>(out), lse, static_cast<float*>(ws), 0, stats};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int R = rows_of(static_cast<int64_t>(N) * a.G);
   if (R == 0) return launch_tree_attention(a, D, sms, s);
-  return D == 128 ? launch_few<128>(a, R, sms, s) : launch_few<64>(a, R, sms, s);
+  if (window != 0) return D == 128 ? launch_few<128, true>(a, R, sms, s) : launch_few<64, true>(a, R, sms, s);
+  return D == 128 ? launch_few<128, false>(a, R, sms, s) : launch_few<64, false>(a, R, sms, s);
+}
+
+}  // namespace
+}  // namespace specdec
+
+using namespace specdec;
+
+extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !attn_sizes(B, N, Hq, Hkv, D)) return 0;
+  const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
+  const int R = rows_of(rows);
+  return align256(R == 0 ? attn_ws_bytes(kTreeMaxCtas, kTreeRows, D) : attn_ws_bytes(kMaxCtas, R, D));
+}
+
+extern "C" int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,
+                                  const void* pool, int64_t num_slots, int64_t slot_stride,
+                                  const int32_t* num_nodes_or_null, const int32_t* seq_lens,
+                                  const int32_t* req_to_token, int64_t max_ctx, const uint8_t* tree_mask_or_null,
+                                  float scale, void* out, float* lse_or_null, int32_t* stats_or_null, void* ws,
+                                  size_t ws_bytes, spec_stream_t stream) {
+  return attention(B, N, Hq, Hkv, D, q, q_stride, pool, num_slots, slot_stride, num_nodes_or_null, seq_lens, nullptr,
+                   req_to_token, max_ctx, tree_mask_or_null, 0, 0, scale, out, lse_or_null, stats_or_null, ws, ws_bytes,
+                   stream);
+}
+
+extern "C" int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,
+                                         const void* pool, int64_t num_slots, int64_t slot_stride,
+                                         const int32_t* num_nodes_or_null, const int32_t* seq_lens,
+                                         const int32_t* positions_or_null, const int32_t* req_to_token,
+                                         int64_t max_ctx, const uint8_t* tree_mask_or_null, int32_t sinks,
+                                         int32_t window, float scale, void* out, float* lse_or_null,
+                                         int32_t* stats_or_null, void* ws, size_t ws_bytes, spec_stream_t stream) {
+  if (sinks < 0 || window < 1) return SPEC_ERR_INVALID_ARG;
+  return attention(B, N, Hq, Hkv, D, q, q_stride, pool, num_slots, slot_stride, num_nodes_or_null, seq_lens,
+                   positions_or_null, req_to_token, max_ctx, tree_mask_or_null, sinks, window, scale, out, lse_or_null,
+                   stats_or_null, ws, ws_bytes, stream);
 }

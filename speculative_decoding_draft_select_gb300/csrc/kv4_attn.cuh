@@ -20,6 +20,8 @@ struct AttnArgs {
   const int32_t* seq_lens;
   const int32_t* num_nodes;
   const uint8_t* mask;
+  const int32_t* positions;  // with a window: of the nodes (null: a chain)
+  int sinks, window;
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -50,12 +52,18 @@ __device__ __forceinline__ int64_t attn_q(const AttnArgs& a, int b, int h, int r
 // Request b: nodes, positions [0, end) of which [start, end) are nodes, tiles
 // of T positions and row tiles of R rows.  A request whose positions do not
 // fit the table has no positions (its rows get zeros) and one empty tile.
+//
+// With a window (WIN) the tiles hold the positions that some row may see and no
+// others: the sinks [0, cut) and, `gap` positions further on, what the root's
+// window shows (deeper nodes see less of it).  start, end and the tiles' bounds
+// then count these places: place p is position p below cut, p + gap from there.
 struct Req {
   int nodes, start, end, tiles, row_tiles;
+  int cut, gap;
   bool bad;
 };
 
-template <int T>
+template <int T, bool WIN>
 __device__ __forceinline__ Req attn_req(const AttnArgs& a, int b, int R) {
   Req r;
   r.nodes = kv4_nodes(a.num_nodes, b, a.N);
@@ -63,6 +71,13 @@ __device__ __forceinline__ Req attn_req(const AttnArgs& a, int b, int R) {
   r.bad = r.start < 0 || static_cast<int64_t>(r.start) + r.nodes > a.max_ctx;
   r.end = r.bad ? 0 : r.start + r.nodes;
   if (r.bad) r.start = 0;
+  r.cut = r.gap = 0;
+  if (WIN) {
+    r.cut = min(a.sinks, r.start);
+    r.gap = max(r.start - a.window + 1 - r.cut, 0);
+    r.start -= r.gap;
+    r.end -= r.gap;
+  }
   r.tiles = r.nodes == 0 ? 0 : (r.bad ? 1 : (r.end + T - 1) / T);
   r.row_tiles = (r.nodes * a.G + R - 1) / R;
   return r;
@@ -81,21 +96,57 @@ __device__ __forceinline__ int64_t attn_units(const Req& r, int Hkv) {
 struct Part {
   int b, h, rt, t0, t1;
   int nodes, start, end, tiles;
+  int cut, gap;  // with a window
   bool bad;
   __device__ __forceinline__ bool complete() const { return t0 == 0 && t1 == tiles; }
 };
 
+// With a window: the depth of node n, its position less seq_len; a node has n
+// ancestors at most.
+__device__ __forceinline__ int attn_depth(const AttnArgs& a, const Part& p, int n) {
+  if (a.positions == nullptr) return n;
+  const int64_t d = static_cast<int64_t>(__ldg(a.positions + static_cast<int64_t>(p.b) * a.N + n)) - (p.start + p.gap);
+  return d < 0 ? 0 : (d > n ? n : static_cast<int>(d));
+}
+// The place that every row's window has reached: from there on, and below cut,
+// all rows see all of the context.
+__device__ __forceinline__ int attn_all_see(const AttnArgs& a, const Part& p) { return p.start + p.nodes - a.window; }
+// Whether every row sees all of the context among the places [p0, p1).
+template <bool WIN>
+__device__ __forceinline__ bool attn_context(const AttnArgs& a, const Part& p, int p0, int p1) {
+  return p1 <= p.start && (!WIN || p1 <= p.cut || max(p0, p.cut) >= attn_all_see(a, p));
+}
+// Whether node m is within node n's window, or a sink (nodes fewer than the
+// window's positions are never too far apart).
+__device__ __forceinline__ bool attn_near(const AttnArgs& a, const Part& p, int n, int m) {
+  if (a.window >= p.nodes) return true;
+  const int dm = attn_depth(a, p, m);
+  return attn_depth(a, p, n) - dm < a.window || p.start + p.gap + dm < a.sinks;
+}
+// Whether node n sees a place of its request that has a slot.
+template <bool WIN>
+__device__ __forceinline__ bool attn_sees(const AttnArgs& a, const Part& p, int n, int place) {
+  const int m = place - p.start;
+  if (!spec_in(n, a.N, a.stats)) return false;
+  if (m < 0) return !WIN || place < p.cut || place > p.start + attn_depth(a, p, n) - a.window;
+  return spec_in(m, a.N, a.stats) &&
+         (a.mask ? __ldg(a.mask + (static_cast<int64_t>(p.b) * a.N + n) * a.N + m) != 0 : m <= n) &&
+         (!WIN || attn_near(a, p, n, m));
+}
+
 // A CTA's stretch of the line, walked segment by segment.
-template <int T, int E, int R>
+template <int T, int E, int R, bool WIN>
 struct Walk {
   int64_t left;  // units
   int skip;      // units of the segment (b, h, rt) that an earlier CTA has
   int b, h, rt, row_tiles;
   int nodes, start, end, tiles;
+  int cut, gap;
   bool bad;
   __device__ __forceinline__ void request(const AttnArgs& a) {
-    const Req r = attn_req<T>(a, b, R);
+    const Req r = attn_req<T, WIN>(a, b, R);
     nodes = r.nodes, start = r.start, end = r.end, tiles = r.tiles, row_tiles = r.row_tiles, bad = r.bad;
+    cut = r.cut, gap = r.gap;
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, Part& p) {
 #pragma unroll 1
@@ -112,6 +163,7 @@ struct Walk {
       p.t0 = max(skip - E, 0);
       p.t1 = skip + take - E;
       p.b = b, p.h = h, p.rt = rt, p.nodes = nodes, p.start = start, p.end = end, p.tiles = tiles, p.bad = bad;
+      p.cut = cut, p.gap = gap;
       left -= take;
       skip = 0;
       if (++rt == row_tiles) rt = 0, ++h;
@@ -134,8 +186,8 @@ struct Line {
 
 // Finds this CTA's stretch (block-wide, every thread gets the result); false
 // when it has none.
-template <int T, int E, int R, int THREADS>
-__device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk<T, E, R>& w) {
+template <int THREADS, int T, int E, int R, bool WIN>
+__device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk<T, E, R, WIN>& w) {
   __shared__ int64_t s_warp[THREADS / 32];
   __shared__ int64_t s_off;
   __shared__ int s_b;
@@ -144,7 +196,7 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk
   const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   int64_t mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
+  for (int b = b0; b < b1; ++b) mine += attn_units<E>(attn_req<T, WIN>(a, b, R), a.Hkv);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -168,7 +220,7 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& a, Line& line, Walk
     int b = b0;
 #pragma unroll 1
     for (;; ++b) {
-      const int64_t u = attn_units<E>(attn_req<T>(a, b, R), a.Hkv);
+      const int64_t u = attn_units<E>(attn_req<T, WIN>(a, b, R), a.Hkv);
       if (lo < pre + u) break;
       pre += u;
     }
@@ -350,6 +402,7 @@ inline int attn_sms() {
 // Limits of the tensor-memory kernel's launches (kv4_tree.cu) and its entry.
 constexpr int kTreeRows = 128;     // rows of an accumulator
 constexpr int kTreeMaxCtas = 304;  // two on each of 152 SMs (one with two accumulators)
+// (a.window: 0 without one)
 int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s);
 
 }  // namespace specdec

@@ -93,6 +93,7 @@ struct Chunk {
 // at a time, ballots give the words.  All loads come first and none is behind
 // a condition of its own (a load that is tested where it was issued is a wait
 // each).
+template <bool WIN>
 __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int node, int first, uint32_t* words) {
   const int lane = threadIdx.x & 31;
   const int n_lo = __shfl_sync(0xffffffffu, node, 0), n_hi = __shfl_sync(0xffffffffu, node, 31);
@@ -112,6 +113,14 @@ __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int
       const uint8_t* row = mask + (spec_in(n, a.N, a.stats) ? n : 0) * a.N;
 #pragma unroll
       for (int w = 0; w < 4; ++w) on[q][w] = a.mask ? __ldg(row + at[w]) : static_cast<uint8_t>(at[w] <= n);
+      if (WIN && a.window < p.nodes) {
+        uint32_t near = 0;
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w)
+          near |= static_cast<uint32_t>(attn_near(a, p, n, min(max(first + 32 * w + lane, 0), p.nodes - 1))) << w;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) on[q][w] &= static_cast<uint8_t>(-static_cast<int>((near >> w) & 1u));
+      }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -194,7 +203,7 @@ __device__ __forceinline__ float row_weights(uint32_t col, const uint32_t* see, 
   return t.x + t.y;
 }
 
-template <int D, int MT>
+template <int D, int MT, bool WIN>
 __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4_tree_kernel(const AttnArgs a) {
   pdl_enter();
   using C = TreeCfg<D, MT>;
@@ -219,8 +228,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
   if (tid == 0) *cut = CutSegment{0, 0, 0, 0};
   Line line;
-  Walk<kTT, kEnds, R> walk;
-  if (!attn_stretch<kTT, kEnds, R, C::kThreads>(a, line, walk)) return;
+  Walk<kTT, kEnds, R, WIN> walk;
+  if (!attn_stretch<C::kThreads>(a, line, walk)) return;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&q_full[i], C::kUnpackThreads / 32);
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int pos = at * kTT + p_of + i * kStep;
-        slot[i] = pos < ap.end ? __ldg(row + pos) : -2;  // -2: no position, -1 or out of range: a bad slot
+        slot[i] = pos < ap.end ? __ldg(row + pos + (WIN && pos >= ap.cut ? ap.gap : 0)) : -2;  // -2: no position, -1 or out of range: a bad slot
       }
       if (++next_tile == ap.t1) {
         more = ahead.next(a, ap);
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
           const int shift = p0 - p.start;  // node of the tile's first position
           const bool keep = a.N <= kTT;    // then the words of all nodes serve every head of the request
           if (!keep || p.b != seen_b || p.rt != seen_rt) {
-            node_words(a, p, node, keep ? 0 : shift, see);
+            node_words<WIN>(a, p, node, keep ? 0 : shift, see);
             seen_b = p.b;
             seen_rt = p.rt;
             if (keep) {
@@ -510,6 +519,15 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
               see[w] = __funnelshift_r(s_seen[warp][min(max(i, 0), 5)][lane], s_seen[warp][min(max(i + 1, 0), 5)][lane],
                                        shift & 31);
             }
+          }
+        }
+        if (WIN && active && p0 + kTT > p.cut && attn_all_see(a, p) > max(p0, p.cut)) {
+          // the context before the window of this thread's node: places [cut, to)
+          const int to = min(p.start + attn_depth(a, p, node) - a.window + 1, p.start);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int lo = min(max(p.cut - p0 - 32 * w, 0), 32), hi = min(max(to - p0 - 32 * w, lo), 32);
+            see[w] &= ~(__funnelshift_lc(~0u, 0u, hi) & ~__funnelshift_lc(~0u, 0u, lo));
           }
         }
         ok = wait_warp(&s_full[m], j & 1, &s_abort);
@@ -648,11 +666,11 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
   if (tid == 0 && s_abort) bump(a.stats, SPEC_STAT_WAIT_TIMEOUT);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool WIN>
 int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
   using C = TreeCfg<D, MT>;
   constexpr int R = kTreeRows * MT;
-  constexpr auto kernel = kv4_tree_kernel<D, MT>;
+  constexpr auto kernel = kv4_tree_kernel<D, MT, WIN>;
   if (!allow_smem<kernel>(C::kSmem)) return SPEC_ERR_CUDA;
   a.ctas = sms * (MT == 2 ? 1 : 2);
   a.ctas = a.ctas < kTreeMaxCtas / MT ? a.ctas : kTreeMaxCtas / MT;
@@ -661,17 +679,22 @@ int launch_tree(AttnArgs a, int sms, cudaStream_t s) {
   return launch_status();
 }
 
-}  // namespace
-
-int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s) {
+template <bool WIN>
+int launch_tree(const AttnArgs& a, int D, int sms, cudaStream_t s) {
   // two accumulators where there are rows for them (8 KV heads, contexts
   // 16..2048, in us with one / with two: D=128, B=128: 96 rows 160 / 223, 128
   // rows 161 / 226, 160 rows 291 / 246; B=8: 128 rows 31.1 / 31.6, 160 rows 36.8
   // / 34.8; D=64, B=128: 128 rows 118 / 190, 160 rows 208 / 213; B=8: 128 rows
   // 27.5 / 27.7, 160 rows 31.8 / 31.2)
   const bool two = static_cast<int64_t>(a.N) * a.G > kTreeRows;
-  if (D == 128) return two ? launch_tree<128, 2>(a, sms, s) : launch_tree<128, 1>(a, sms, s);
-  return two ? launch_tree<64, 2>(a, sms, s) : launch_tree<64, 1>(a, sms, s);
+  if (D == 128) return two ? launch_tree<128, 2, WIN>(a, sms, s) : launch_tree<128, 1, WIN>(a, sms, s);
+  return two ? launch_tree<64, 2, WIN>(a, sms, s) : launch_tree<64, 1, WIN>(a, sms, s);
+}
+
+}  // namespace
+
+int launch_tree_attention(AttnArgs a, int D, int sms, cudaStream_t s) {
+  return a.window != 0 ? launch_tree<true>(a, D, sms, s) : launch_tree<false>(a, D, sms, s);
 }
 
 }  // namespace specdec
