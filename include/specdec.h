@@ -634,6 +634,70 @@ int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* 
                               float scale, void* out, float* lse_or_null, int32_t* stats_or_null, void* ws,
                               size_t ws_bytes, spec_stream_t stream);
 
+/* The attention that each cached position has received, summed over the
+ * committed rows and all query heads (what spec_evict_slots ranks by).  Row i <=
+ * accept_length[b] (NULL: i < N) is node accept_path[b][i] (NULL: node i) of q
+ * and lse, stands at position seq_lens[b] + i and sees p <= seq_lens[b] + i:
+ *   out[b][p] = prev[b][p] + sum over i, h of exp(scale q_ih . k_p - lse_ih)
+ * for p < seq_lens[b] + rows; other entries are left as they were.  Called
+ * behind spec_compact_slots with the seq_lens, accept_path and accept_length
+ * that it had, the accepted path's K lies in order; lse is what
+ * spec_kv4_attention returned for the same nodes.  Layers that share the slots
+ * add up by calls that follow one another.
+ *   q [B, N, Hq, D] bf16, rows (b, n) q_stride elements apart; lse [B, N, Hq]
+ *     fp32: a row whose lse is not finite adds nothing.
+ *   prev_or_null, out [B, max_ctx] fp32 (NULL: zeros); may be the same.
+ * Codes and q enter the products exactly (q's elements 2^-24 of its row's
+ * largest may round), sums are fp32 in a fixed order; scale log2(e) times a
+ * row's largest |q|, and the scores, have to stay in fp32's range.  A position
+ * whose slot is out of range receives nothing; a path entry out of range adds
+ * nothing; a request whose accept_length is outside [0, N) or whose positions
+ * do not fit max_ctx is skipped (SPEC_STAT_BAD_REQUEST each).  q and pool
+ * 16-byte aligned, q_stride a multiple of 8, slot_stride a multiple of 16
+ * below 2^31, 2^-20 <= scale <= 2^20, Hq <= 4096, B <= 65535
+ * (SPEC_ERR_UNSUPPORTED otherwise). */
+int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const float* lse,
+                         const int32_t* accept_path_or_null, const int32_t* accept_length_or_null, const void* pool,
+                         int64_t num_slots, int64_t slot_stride, const int32_t* seq_lens, const int32_t* req_to_token,
+                         int64_t max_ctx, float scale, const float* prev_or_null, float* out, int32_t* stats_or_null,
+                         spec_stream_t stream);
+
+/* Eviction: every request longer than `limit` positions is cut to `budget` of
+ * them, limit >= budget >= 1: the first `sinks`, the last `recent` (sinks +
+ * recent <= budget), and of the others those with the largest sums
+ * (spec_kv4_weight_sums), equal ones and zeros of either sign from the lower
+ * position on, NaN last (as -infinity).  They keep their order: place i takes
+ * position kept[b][i].
+ *   sums, sums_out [B, max_ctx] fp32 (the same, or apart): sums_out[b][i] =
+ *     sums[b][kept[b][i]] for i < budget, 0 from there to seq_lens[b]; a
+ *     request that is not cut has its sums copied.  Entries from seq_lens[b]
+ *     on are left as they were.
+ *   page_size == 1: req_to_token is relabelled, req_to_token[b][i] = its entry
+ *     kept[b][i]; the slots of the other positions go to freed, in the order of
+ *     b and position.  Entries from budget on are left as they were.
+ *   page_size > 1: req_to_token stays (page lp of a request holds the slots of
+ *     its positions [lp P, (lp + 1) P), the slot of position lp P being the
+ *     page's first); with kv_pool_or_null ([num_slots, bytes_per_slot] bytes)
+ *     the payload of slot kept[b][i] moves to place i's, sources being read
+ *     before they are overwritten; pages wholly behind the budget go to freed
+ *     (page id = slot / page_size), in the order of b and page.
+ *   kept [B, budget] int32 out (-1 where the request is not cut); new_kv_len
+ *     [B] = budget or seq_lens[b]; freed [freed_capacity], num_freed [1].
+ * The slots of a call are distinct.  A request with seq_len < 0 or > max_ctx is
+ * skipped (new_kv_len = -1), a move from or to a slot outside [0, num_slots)
+ * is left out (SPEC_STAT_BAD_REQUEST each).  kv_pool 16-byte aligned,
+ * bytes_per_slot a multiple of 16, B <= 65535, max_ctx < 2^30
+ * (SPEC_ERR_UNSUPPORTED otherwise).
+ *   ws: spec_evict_ws_size bytes, 16-byte aligned; calls that may overlap need
+ *   their own.  spec_evict_freed_capacity: the most entries of freed. */
+int64_t spec_evict_freed_capacity(int B, int64_t max_ctx, int page_size, int budget);
+size_t spec_evict_ws_size(int B, int page_size, int budget);
+int spec_evict_slots(int B, int page_size, int budget, int limit, int sinks, int recent, const int32_t* seq_lens,
+                     const float* sums, float* sums_out, int32_t* req_to_token, int64_t max_ctx, int32_t* kept,
+                     int32_t* freed, int64_t freed_capacity, int32_t* num_freed, int32_t* new_kv_len,
+                     void* kv_pool_or_null, int64_t num_slots, int64_t bytes_per_slot, int32_t* stats_or_null, void* ws,
+                     size_t ws_bytes, spec_stream_t stream);
+
 /* -------------------------------------------------------------------- TLI */
 
 /* TLI constrain + top-1 + map ([TLI] Modifications: constrain_draft_logits

@@ -123,6 +123,86 @@ def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, n
     return r
 
 
+def kv4_weight_sums(q, lse, rows, req_to_token, seq_lens, Hkv, scale, accept_path=None, accept_length=None, prev=None):
+    """In 64 bits, a dict of sums [B, max_ctx], prev plus the weights w that each
+    position receives, touched (the entries that are written), and what error
+    bounds need, sums over the weights: w itself, parts = w |scale| sum |q| (|lo|
+    + |k - lo|), far = w |scale| max |q| sum (|lo| + |k - lo|), size = w (|score|
+    + |lse|), and count, their number."""
+    q = np.asarray(q, np.float64)
+    B, N, Hq, D = q.shape
+    ctx = req_to_token.shape[1]
+    total = np.zeros((B, ctx)) if prev is None else np.asarray(prev, np.float64).copy()
+    r = {"sums": total, "touched": np.zeros((B, ctx), bool), "count": np.zeros((B, ctx), np.int64)}
+    for name in ("w", "parts", "far", "size"):
+        r[name] = np.zeros((B, ctx))
+    for b in range(B):
+        s, R = int(seq_lens[b]), N if accept_length is None else int(accept_length[b]) + 1
+        if s < 0 or R < 1 or R > N or s + R > ctx:
+            continue
+        r["touched"][b, :s + R] = True
+        slot = req_to_token[b, :s + R].astype(np.int64)
+        there = (slot >= 0) & (slot < rows.shape[0])
+        mine = rows[np.where(there, slot, 0)]
+        k, _ = kv4_values(mine, Hkv, D)
+        meta = np.ascontiguousarray(mine[:, :Hkv * head_bytes(D)].reshape(-1, Hkv, head_bytes(D))[..., D:D + D // 8])
+        lo = meta.view(np.float16).astype(np.float64)[..., 1::2].repeat(GROUP, -1)
+        part = np.abs(lo) + np.abs(k - lo)
+        for i in range(R):
+            n = i if accept_path is None else int(accept_path[b, i])
+            if not 0 <= n < N:
+                continue
+            see = there & (np.arange(s + R) <= s + i)
+            for h in range(Hq):
+                z = float(lse[b, n, h])
+                if not np.isfinite(z):
+                    continue
+                kv, qa = h // (Hq // Hkv), np.abs(q[b, n, h])
+                score = k[:, kv] @ q[b, n, h] * scale
+                w = np.where(see, np.exp(score - z), 0.0)
+                total[b, :s + R] += w
+                r["w"][b, :s + R] += w
+                r["parts"][b, :s + R] += w * (part[:, kv] @ qa) * abs(scale)
+                r["far"][b, :s + R] += w * part[:, kv].sum(-1) * qa.max() * abs(scale)
+                r["size"][b, :s + R] += w * (np.abs(score) + abs(z))
+                r["count"][b, :s + R] += see
+    return r
+
+
+def evict(sums, seq_lens, req_to_token, page, budget, limit, sinks, recent, rows=None):
+    """A dict of what eviction leaves: kept, freed (a list), new_kv_len, table,
+    sums and pool."""
+    r = {"table": req_to_token.copy(), "sums": np.asarray(sums, np.float32).copy(),
+         "pool": None if rows is None else rows.copy(), "freed": []}
+    B, ctx = sums.shape
+    r["kept"], r["new_kv_len"] = np.full((B, budget), -1, np.int32), np.zeros(B, np.int32)
+    for b in range(B):
+        n = int(seq_lens[b])
+        r["new_kv_len"][b] = n if 0 <= n <= ctx else -1
+        if not limit < n <= ctx:
+            continue
+        value = np.where(np.isnan(sums[b, :n]), -np.inf, sums[b, :n])
+        middle = sorted(range(sinks, n - recent), key=lambda p: (-value[p], p))[:budget - sinks - recent]
+        kept = np.array(list(range(sinks)) + sorted(middle) + list(range(n - recent, n)))
+        r["kept"][b], r["new_kv_len"][b] = kept, budget
+        r["sums"][b, :n] = 0
+        r["sums"][b, :budget] = sums[b, kept]
+        slot = req_to_token[b]
+        if page == 1:
+            gone = np.ones(n, bool)
+            gone[kept] = False
+            r["freed"] += slot[:n][gone].tolist()
+            r["table"][b, :budget] = slot[kept]
+        else:
+            r["freed"] += [int(slot[p]) // page for p in range(-(-budget // page) * page, n, page)]
+            if rows is not None:
+                ok = lambda s: 0 <= s < rows.shape[0]  # noqa: E731
+                for i, p in enumerate(kept):
+                    if ok(slot[p]) and ok(slot[i]):
+                        r["pool"][slot[i]] = rows[slot[p]]
+    return r
+
+
 def adjust_logits(x, history=None, history_lens=None, prompt_lens=None, rep=None, freq=None, pres=None, draft=None,
                   tree_mask=None, bias_ids=None, bias_vals=None, allowed=None, allowed_row=None, num_nodes=None):
     """The adjusted fp32 values of logits x [B, N, V] (fp32 of their type),

@@ -26,7 +26,8 @@ __all__ = [
     "tli_map_ids",
     "tli_check_config", "tli_pruned_head", "spec_filter_logits", "spec_wait_probe", "spec_debug_bounds",
     "new_stats", "new_pool", "spec_kv4_slot_bytes", "spec_kv4_append", "spec_kv4_gather",
-    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_adjust_logits",
+    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_kv4_weight_sums",
+    "spec_evict_freed_capacity", "spec_evict_ws_size", "spec_evict_slots", "spec_adjust_logits",
 ]
 
 F32 = 0
@@ -94,6 +95,12 @@ _SIGS = {
                                 _SZ, _P]),
     "spec_kv4_attention_window": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32, _I32,
                                        _F, _P, _P, _P, _P, _SZ, _P]),
+    "spec_kv4_weight_sums": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _P, _P,
+                                  _P]),
+    "spec_evict_freed_capacity": (_I64, [_I, _I64, _I, _I]),
+    "spec_evict_ws_size": (_SZ, [_I, _I, _I]),
+    "spec_evict_slots": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P,
+                              _SZ, _P]),
     "spec_adjust_logits": (_I, [_I, _I, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P,
                                 _I64, _P, _P, _P]),
     "tli_pruned_head_ws_size": (_SZ, [_I64, _I64]),
@@ -714,6 +721,94 @@ def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scal
                                              sinks, width, *rest)
     if rc:
         raise SpecError("spec_kv4_attention" if window is None else "spec_kv4_attention_window", rc)
+    return out
+
+
+def spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, accept_path=None, accept_length=None,
+                         prev=None, out=None, scale=None, stats=None):
+    """Adds to each cached position the attention weights that it receives from
+    the accepted path's rows, all query heads: row i <= accept_length[b] (None:
+    every i < N) is node accept_path[b, i] (None: i) of q [B, N, Hq, D] bf16 and
+    lse [B, N, Hq] f32, at position seq_lens[b] + i.  Called behind
+    spec_compact_slots with the arguments that it had.  Returns out [B, max_ctx]
+    f32 = prev plus the weights (out None: prev itself is updated, or zeros are
+    allocated when that is None too)."""
+    dev = _device(q, "q")
+    qs = _rows(q, "q")
+    if q.dtype is not torch.bfloat16:
+        raise ValueError("q must be bfloat16")
+    B, N, Hq, D = q.shape
+    pool, slots, stride, table, ctx = _kv4_pool(kv_pool, req_to_token, B, num_kv_heads, D, dev)
+    if Hq % num_kv_heads:
+        raise ValueError("the number of query heads must be a multiple of num_kv_heads")
+    i32, f32 = torch.int32, torch.float32
+    if out is None:
+        out = torch.zeros((B, ctx), dtype=f32, device=q.device) if prev is None else prev
+    before, dst = _arg(prev, f32, (B, ctx), dev, "prev"), _arg(out, f32, (B, ctx), dev, "out")
+    lse_at = _arg(lse, f32, (B, N, Hq), dev, "lse")
+    if q.numel() == 0:
+        return out
+    rc = lib().spec_kv4_weight_sums(B, N, Hq, num_kv_heads, D, q.data_ptr(), qs, lse_at,
+                                    _arg(accept_path, i32, (B, N), dev, "accept_path"),
+                                    _arg(accept_length, i32, (B,), dev, "accept_length"), pool, slots, stride,
+                                    _arg(seq_lens, i32, (B,), dev, "seq_lens"), table, ctx,
+                                    D ** -0.5 if scale is None else scale, before, dst,
+                                    _arg(stats, i32, (NUM_STATS,), dev, "stats"), _stream())
+    if rc:
+        raise SpecError("spec_kv4_weight_sums", rc)
+    return out
+
+
+# ---------------------------------------------------------------- eviction
+
+def spec_evict_freed_capacity(B, max_ctx, page_size, budget):
+    return int(lib().spec_evict_freed_capacity(int(B), int(max_ctx), int(page_size), int(budget)))
+
+
+def spec_evict_ws_size(B, page_size, budget) -> int:
+    return int(lib().spec_evict_ws_size(int(B), int(page_size), int(budget)))
+
+
+def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None, sinks=0, recent=0, kv_pool=None,
+                     sums_out=None, out=None, ws=None, stats=None):
+    """Cuts each request longer than ``limit`` (None: budget) to ``budget``
+    positions: the first ``sinks``, the last ``recent`` and the largest sums
+    [B, max_ctx] f32 among the others.  sums (or sums_out), and req_to_token with
+    pages of one token, else kv_pool [slots, bytes] uint8, are updated.  Returns
+    a dict of kept [B, budget] (-1 where nothing was cut), freed, num_freed and
+    new_kv_len."""
+    dev = _device(sums, "sums")
+    if sums.dim() != 2 or req_to_token.shape != sums.shape:
+        raise ValueError("sums and req_to_token must be [B, max_ctx]")
+    B, ctx = sums.shape
+    page_size, budget = int(page_size), int(budget)
+    i32, f32 = torch.int32, torch.float32
+    src = _arg(sums, f32, (B, ctx), dev, "sums")
+    dst = src if sums_out is None else _arg(sums_out, f32, (B, ctx), dev, "sums_out")
+    pool = slots = width = 0
+    if kv_pool is not None:
+        if kv_pool.dim() != 2:
+            raise ValueError("kv_pool must be [slots, bytes]")
+        slots, width = kv_pool.shape
+        pool = _arg(kv_pool, torch.uint8, kv_pool.shape, dev, "kv_pool")
+    if out is None:
+        cap = max(1, spec_evict_freed_capacity(B, ctx, page_size, budget))
+        out = {name: torch.empty(shape, dtype=i32, device=sums.device) for name, shape in (
+            ("kept", (B, max(budget, 0))), ("freed", (cap,)), ("num_freed", (1,)), ("new_kv_len", (B,)))}
+    freed = out["freed"]
+    if ws is None:
+        ws = torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=sums.device)
+    rc = lib().spec_evict_slots(B, page_size, budget, budget if limit is None else int(limit), int(sinks), int(recent),
+                                _arg(seq_lens, i32, (B,), dev, "seq_lens"), src, dst,
+                                _arg(req_to_token, i32, (B, ctx), dev, "req_to_token"), ctx,
+                                _arg(out["kept"], i32, (B, budget), dev, "kept"),
+                                _arg(freed, i32, (freed.numel(),), dev, "freed"), freed.numel(),
+                                _arg(out["num_freed"], i32, (1,), dev, "num_freed"),
+                                _arg(out["new_kv_len"], i32, (B,), dev, "new_kv_len"), pool or None, slots, width,
+                                _arg(stats, i32, (NUM_STATS,), dev, "stats"), _arg(ws, torch.uint8, ws.shape, dev, "ws"),
+                                ws.numel(), _stream())
+    if rc:
+        raise SpecError("spec_evict_slots", rc)
     return out
 
 

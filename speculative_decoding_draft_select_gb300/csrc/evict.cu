@@ -1,0 +1,421 @@
+// Eviction of cached positions: requests that have grown past a limit are cut
+// to a budget of positions, which keeps the first tokens (sinks), the latest
+// ones, and of the rest those whose summed attention is largest.
+//
+// The cache's rows lie in the slots that req_to_token names, so with pages of
+// one token the cut is a relabelling ("EAGLE speculative decoding in four
+// parts", ai-infra-handbooks, "Drafting, verification and slots": slots are
+// allocated, and freed, by their table); with larger pages the kept rows move
+// up, in order, and whole pages are freed.  Sums follow their positions.
+//
+// Three launches:
+//   select   a cluster per request.  Ranks are by a 32-bit key in which floats
+//            compare as unsigned integers (NaN as -inf, -0 as 0) and positions
+//            that stay in any case lie above every number.  Three counting
+//            passes (11, 11 and 10 bits) find the key of the budget's last
+//            position; the kept ones are those above it and, of equal ones, the
+//            first.  One scan in the positions' order then gives each its place.
+//   apply    writes the new table and sums, which select has put aside (the
+//            arrays are updated in place), and zeros behind them.
+//   payload  (pages of several tokens) a CTA takes a request's rows, a slice of
+//            their bytes: it reads kept rows in order, a few chunks ahead, and
+//            writes them up.  A row only ever moves towards the front: what a
+//            chunk overwrites has been read by it or a chunk before.  Slices
+//            are independent, so no CTA waits for another.
+#include <climits>
+
+#include "common.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSlice = 16384;  // keys of a CTA that stay in shared memory
+
+struct EvictArgs {
+  int B, page, budget, limit, sinks, recent;
+  const int32_t* seq_lens;
+  const float* sums;
+  float* sums_out;
+  int32_t* table;
+  int64_t max_ctx;
+  int32_t* kept;
+  int32_t* freed;
+  int64_t freed_cap;
+  int32_t* num_freed;
+  int32_t* new_len;
+  int32_t* ws_table;  // [B, budget], with pages of one token
+  float* ws_sums;     // [B, budget]
+  uint8_t* kv;
+  int64_t num_slots, bps;
+  int32_t* stats;
+};
+
+// Length of request b (-1: out of range), and whether it is cut.
+__device__ __forceinline__ int evict_len(const EvictArgs& a, int b) {
+  const int n = __ldg(a.seq_lens + b);
+  return n < 0 || n > a.max_ctx ? -1 : n;
+}
+__device__ __forceinline__ int pages_of(int n, int page) { return n / page + (n % page != 0); }
+// Entries of the freed list that a request of length n adds.
+__device__ __forceinline__ int evict_freed(const EvictArgs& a, int n) {
+  if (n <= a.limit) return 0;
+  return a.page == 1 ? n - a.budget : pages_of(n, a.page) - pages_of(a.budget, a.page);
+}
+
+__device__ __forceinline__ uint32_t sum_key(float x) {
+  const uint32_t u = __float_as_uint(order_key(x) + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+// Key of position p of a request of length n.
+__device__ __forceinline__ uint32_t evict_key(const EvictArgs& a, const float* sums, int p, int n) {
+  return p < a.sinks || p >= n - a.recent ? ~0u : sum_key(__ldg(sums + p));
+}
+
+template <typename T>
+__device__ __forceinline__ T ld_cluster(const T* local, unsigned rank) {
+  static_assert(sizeof(T) == 4, "32-bit values");
+  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
+  unsigned r, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return static_cast<T>(v);
+}
+
+// The sum over the threads before this one.
+__device__ __forceinline__ int block_before(int v, int2* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp].x = x;
+  __syncthreads();
+  int before = x - v;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w)
+    if (w < warp) before += sh[w].x;
+  return before;
+}
+
+struct SelectShared {
+  unsigned hist[kBins];
+  int2 scan[kSelWarps];
+  int64_t freed[kSelWarps];
+  unsigned digit, above;
+  int counts[2];  // this CTA's kept above the last key, and equal to it
+  uint32_t key[kSlice];
+};
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int ctas) {
+  pdl_enter();
+  extern __shared__ __align__(16) unsigned char evict_sm[];
+  SelectShared& sh = *reinterpret_cast<SelectShared*>(evict_sm);
+  if (!spec_smem_ok(sizeof(sh), a.stats)) return;
+  const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned rank = ctas > 1 ? cluster_rank() : 0u;
+
+  // entries of the freed list before this request's, and of all requests
+  int64_t before = 0, all = 0;
+  for (int i = tid; i < a.B; i += kSelThreads) {
+    const int f = evict_freed(a, evict_len(a, i));
+    all += f;
+    if (i < b) before += f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) sh.freed[warp] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) before += sh.freed[w];
+  if (blockIdx.x == 0) {
+    __syncthreads();
+    if (lane == 0) sh.freed[warp] = all;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kSelWarps; ++w) all += sh.freed[w];
+      *a.num_freed = static_cast<int32_t>(all);
+    }
+  }
+  if (b >= a.B) return;  // no request at all: the launch has this one CTA
+
+  const int n = evict_len(a, b);
+  const bool cut = n > a.limit;
+  int32_t* kept = a.kept + static_cast<int64_t>(b) * a.budget;
+  if (rank == 0 && tid == 0) {
+    a.new_len[b] = cut ? a.budget : n;
+    if (n < 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+  }
+  if (!cut) {  // the whole cluster leaves
+    for (int i = rank * kSelThreads + tid; i < a.budget; i += ctas * kSelThreads) kept[i] = -1;
+    return;
+  }
+  const float* sums = a.sums + static_cast<int64_t>(b) * a.max_ctx;
+  int32_t* table = a.table + static_cast<int64_t>(b) * a.max_ctx;
+  // this CTA's positions [p0, p0 + mine), a run of each thread's; keys beyond
+  // what shared memory holds are computed again in each pass
+  const int each = (n + ctas - 1) / ctas;
+  const int p0 = min(n, static_cast<int>(rank) * each), mine = min(each, n - p0);
+  const int held = min(mine, kSlice);
+  for (int i = tid; i < held; i += kSelThreads) sh.key[i] = evict_key(a, sums, p0 + i, n);
+  auto key_at = [&](int i) { return i < held ? sh.key[i] : evict_key(a, sums, p0 + i, n); };
+
+  uint32_t prefix = 0;
+  int need = a.budget;  // positions still to be taken among those with this prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < mine; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    if (ctas > 1) cluster_barrier();
+    else __syncthreads();
+    // bins from the top: a thread's run of four
+    constexpr int per = kBins / kSelThreads;
+    unsigned cnt[per];
+    int mine_sum = 0;
+#pragma unroll
+    for (int j = 0; j < per; ++j) {
+      const int bin = kBins - 1 - (tid * per + j);
+      cnt[j] = 0;
+      if (ctas == 1) cnt[j] = sh.hist[bin];
+      else
+        for (int c = 0; c < ctas; ++c) cnt[j] += ld_cluster(&sh.hist[bin], c);
+      mine_sum += static_cast<int>(cnt[j]);
+    }
+    int run = block_before(mine_sum, sh.scan);
+#pragma unroll
+    for (int j = 0; j < per; ++j) {
+      if (run < need && need <= run + static_cast<int>(cnt[j])) {
+        sh.digit = static_cast<unsigned>(kBins - 1 - (tid * per + j));
+        sh.above = static_cast<unsigned>(run);
+      }
+      run += static_cast<int>(cnt[j]);
+    }
+    if (ctas > 1) cluster_barrier();  // nobody reads the counts any more
+    else __syncthreads();
+    prefix = prefix << bits | sh.digit;
+    need -= static_cast<int>(sh.above);
+    __syncthreads();
+  }
+  // prefix is the last kept key; `need` of those equal to it are kept
+
+  // a run of whole words of 32 positions per warp
+  const int run = ((mine + 31) / 32 + kSelWarps - 1) / kSelWarps * 32;
+  const int i0 = min(mine, warp * run), i1 = min(mine, i0 + run);
+  int2 found = make_int2(0, 0);
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;
+    found.x += __popc(__ballot_sync(0xffffffffu, k > prefix && i + lane < i1));
+    found.y += __popc(__ballot_sync(0xffffffffu, k == prefix && i + lane < i1));
+  }
+  if (lane == 0) sh.scan[warp] = found;
+  __syncthreads();
+  int2 at = make_int2(0, 0), total = make_int2(0, 0);
+  for (int w = 0; w < kSelWarps; ++w) {
+    const int2 y = sh.scan[w];
+    if (w < warp) at.x += y.x, at.y += y.y;
+    total.x += y.x, total.y += y.y;
+  }
+  if (ctas > 1) {
+    if (tid == 0) sh.counts[0] = total.x, sh.counts[1] = total.y;
+    cluster_barrier();
+    for (unsigned c = 0; c < rank; ++c) {
+      at.x += ld_cluster(&sh.counts[0], c);
+      at.y += ld_cluster(&sh.counts[1], c);
+    }
+    cluster_barrier();  // no CTA leaves before its counts are read
+  }
+  int32_t* ws_table = a.ws_table + static_cast<int64_t>(b) * a.budget;
+  float* ws_sums = a.ws_sums + static_cast<int64_t>(b) * a.budget;
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const uint32_t k = in ? key_at(i + lane) : 0u;
+    const unsigned above = __ballot_sync(0xffffffffu, in && k > prefix), same = __ballot_sync(0xffffffffu, in && k == prefix);
+    const int p = p0 + i + lane, nth = at.y + __popc(same & below);  // among the equal ones
+    const int to = at.x + __popc(above & below) + min(nth, need);   // kept positions before this one
+    at.x += __popc(above);
+    at.y += __popc(same);
+    if (!in) continue;
+    if (k > prefix || (k == prefix && nth < need)) {
+      if (!spec_in(to, a.budget, a.stats)) continue;
+      kept[to] = p;
+      ws_sums[to] = __ldg(sums + p);
+      if (a.page == 1) ws_table[to] = table[p];
+    } else if (a.page == 1) {
+      if (spec_in(before + p - to, a.freed_cap, a.stats)) a.freed[before + p - to] = table[p];
+    }
+  }
+  if (a.page > 1 && rank == 0) {
+    const int first = pages_of(a.budget, a.page), count = pages_of(n, a.page) - first;
+    for (int i = tid; i < count; i += kSelThreads)
+      if (spec_in(before + i, a.freed_cap, a.stats))
+        a.freed[before + i] = table[static_cast<int64_t>(first + i) * a.page] / a.page;
+  }
+}
+
+constexpr int kApplyThreads = 256;
+
+__global__ void __launch_bounds__(kApplyThreads) evict_apply_kernel(const EvictArgs a) {
+  pdl_enter();
+  const int b = blockIdx.y;
+  const int n = evict_len(a, b), step = gridDim.x * kApplyThreads;
+  const bool cut = n > a.limit;
+  if (!cut && a.sums_out == a.sums) return;
+  const int64_t row = static_cast<int64_t>(b) * a.max_ctx, set = static_cast<int64_t>(b) * a.budget;
+  for (int i = blockIdx.x * kApplyThreads + threadIdx.x; i < n; i += step) {
+    float x = 0.0f;
+    if (!cut) x = a.sums[row + i];
+    else if (i < a.budget) x = a.ws_sums[set + i];
+    a.sums_out[row + i] = x;
+    if (cut && a.page == 1 && i < a.budget) a.table[row + i] = a.ws_table[set + i];
+  }
+}
+
+constexpr int kMoveThreads = 256, kMoveStages = 3;
+constexpr int kMoveVecs = 8;                            // 16-byte vectors of a slice
+constexpr int kMoveRows = 4 * kMoveThreads / kMoveVecs; // rows of a chunk: four vectors a thread
+
+__global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const EvictArgs a) {
+  pdl_enter();
+  __shared__ __align__(16) uint4 sm[kMoveStages][kMoveRows * kMoveVecs];
+  const int b = blockIdx.y;
+  if (evict_len(a, b) <= a.limit) return;
+  const int32_t* kept = a.kept + static_cast<int64_t>(b) * a.budget;
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_ctx;
+  // kept[i] - i never falls: the rows before the first that moves lie in place
+  int lo = 0, hi = a.budget;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(kept + mid) > mid) hi = mid;
+    else lo = mid + 1;
+  }
+  const int first = lo, chunks = (a.budget - first + kMoveRows - 1) / kMoveRows;
+  const int vec = threadIdx.x % kMoveVecs, r = threadIdx.x / kMoveVecs;
+  constexpr int kRowsAt = kMoveThreads / kMoveVecs;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * kMoveVecs + vec) * 16;
+  const bool in = col < a.bps;
+  auto slot_ok = [&](int32_t s) { return s >= 0 && s < a.num_slots; };
+  auto fetch = [&](int c) {
+    if (c < chunks && in) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = first + c * kMoveRows + j * kRowsAt + r;
+        if (i >= a.budget) break;
+        const int p = __ldg(kept + i);
+        const int32_t src = spec_in(p, a.max_ctx, a.stats) ? __ldg(table + p) : -1;
+        if (slot_ok(src))
+          cp_async16(&sm[c % kMoveStages][(j * kRowsAt + r) * kMoveVecs + vec], a.kv + src * a.bps + col, 16);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int c = 0; c < kMoveStages - 1; ++c) fetch(c);
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    fetch(c + kMoveStages - 1);
+    cp_async_wait<kMoveStages - 1>();
+    __syncthreads();  // the chunk has been read whole: its rows may be overwritten
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = first + c * kMoveRows + j * kRowsAt + r;
+        if (i >= a.budget) break;
+        const int p = __ldg(kept + i);
+        const int32_t src = spec_in(p, a.max_ctx, a.stats) ? __ldg(table + p) : -1, dst = __ldg(table + i);
+        if (slot_ok(src) && slot_ok(dst))
+          *reinterpret_cast<uint4*>(a.kv + dst * a.bps + col) =
+              sm[c % kMoveStages][(j * kRowsAt + r) * kMoveVecs + vec];
+        else if (blockIdx.x == 0 && vec == 0)
+          bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// CTAs of a request's cluster, by the longest request there can be: a CTA's
+// keys then fit its shared memory up to 131072 positions.
+int cluster_of(int64_t max_ctx) {
+  return max_ctx <= 4096 ? 1 : max_ctx <= 8192 ? 2 : max_ctx <= 16384 ? 4 : 8;
+}
+
+size_t evict_list(int B, int budget) { return align256(static_cast<size_t>(B) * budget * 4); }
+
+}  // namespace
+}  // namespace specdec
+
+using namespace specdec;
+
+extern "C" int64_t spec_evict_freed_capacity(int B, int64_t max_ctx, int page_size, int budget) {
+  if (B < 0 || max_ctx < 1 || max_ctx > INT_MAX || page_size < 1 || budget < 1) return -1;
+  const int64_t most = (max_ctx + page_size - 1) / page_size, stay = (static_cast<int64_t>(budget) + page_size - 1) / page_size;
+  return most > stay ? B * (most - stay) : 0;
+}
+
+extern "C" size_t spec_evict_ws_size(int B, int page_size, int budget) {
+  if (B < 1 || B > 65535 || page_size < 1 || budget < 1) return 0;
+  return evict_list(B, budget) * (page_size == 1 ? 2 : 1);
+}
+
+extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int sinks, int recent,
+                                const int32_t* seq_lens, const float* sums, float* sums_out, int32_t* req_to_token,
+                                int64_t max_ctx, int32_t* kept, int32_t* freed, int64_t freed_capacity,
+                                int32_t* num_freed, int32_t* new_kv_len, void* kv_pool_or_null, int64_t num_slots,
+                                int64_t bytes_per_slot, int32_t* stats_or_null, void* ws, size_t ws_bytes,
+                                spec_stream_t stream) {
+  if (B < 0 || page_size < 1 || budget < 1 || limit < budget || sinks < 0 || recent < 0 || max_ctx < 1 ||
+      static_cast<int64_t>(sinks) + recent > budget)
+    return SPEC_ERR_INVALID_ARG;
+  if (max_ctx > INT_MAX / 2 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (!num_freed || freed_capacity < spec_evict_freed_capacity(B, max_ctx, page_size, budget))
+    return SPEC_ERR_INVALID_ARG;
+  if (B > 0 && (!seq_lens || !sums || !sums_out || !req_to_token || !kept || !new_kv_len || !ws ||
+                (!freed && freed_capacity > 0)))
+    return SPEC_ERR_INVALID_ARG;
+  if (kv_pool_or_null) {
+    if (num_slots < 1 || bytes_per_slot < 1) return SPEC_ERR_INVALID_ARG;
+    if (bytes_per_slot % 16 != 0 || (reinterpret_cast<uintptr_t>(kv_pool_or_null) & 15) != 0 || num_slots > INT_MAX ||
+        bytes_per_slot > INT_MAX)
+      return SPEC_ERR_UNSUPPORTED;
+  }
+  if (B > 0 && (reinterpret_cast<uintptr_t>(ws) & 15) != 0) return SPEC_ERR_INVALID_ARG;
+  if (B > 0 && ws_bytes < spec_evict_ws_size(B, page_size, budget)) return SPEC_ERR_WORKSPACE;
+  // the sums are read while their new ones are written, unless they are the same
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(sums), o0 = reinterpret_cast<uintptr_t>(sums_out);
+  const uintptr_t wide = static_cast<uintptr_t>(B) * max_ctx * 4;
+  if (s0 != o0 && s0 < o0 + wide && o0 < s0 + wide) return SPEC_ERR_INVALID_ARG;
+  char* w = static_cast<char*>(ws);
+  EvictArgs a{B, page_size, budget, limit, sinks, recent, seq_lens, sums, sums_out, req_to_token, max_ctx, kept, freed,
+              freed_capacity, num_freed, new_kv_len,
+              reinterpret_cast<int32_t*>(w + (page_size == 1 && B > 0 ? evict_list(B, budget) : 0)),
+              reinterpret_cast<float*>(w), static_cast<uint8_t*>(kv_pool_or_null), num_slots, bytes_per_slot,
+              stats_or_null};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!allow_smem<evict_select_kernel>(sizeof(SelectShared))) return SPEC_ERR_CUDA;
+  const int ctas = B == 0 ? 1 : cluster_of(max_ctx);
+  launch_kc(evict_select_kernel, static_cast<unsigned>(B == 0 ? 1 : B * ctas), kSelThreads, sizeof(SelectShared), s,
+            ctas, a, ctas);
+  int e = launch_status();
+  if (e != SPEC_OK || B == 0) return e;
+  const unsigned wide_ctas = static_cast<unsigned>((max_ctx + 4 * kApplyThreads - 1) / (4 * kApplyThreads));
+  launch_k(evict_apply_kernel, dim3(wide_ctas < 64 ? wide_ctas : 64, static_cast<unsigned>(B)), kApplyThreads, 0, s, a);
+  e = launch_status();
+  if (e != SPEC_OK || page_size == 1 || !kv_pool_or_null) return e;
+  launch_k(evict_payload_kernel,
+           dim3(static_cast<unsigned>((bytes_per_slot / 16 + kMoveVecs - 1) / kMoveVecs), static_cast<unsigned>(B)),
+           kMoveThreads, 0, s, a);
+  return launch_status();
+}

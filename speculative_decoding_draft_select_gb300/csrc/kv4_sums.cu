@@ -1,0 +1,483 @@
+// The attention that every cached position has received, summed over the
+// committed rows and all query heads:
+//   out[p] = prev[p] + sum over rows i and heads h of exp(scale q_ih . k_p - lse_ih)
+// for the positions p that row i sees, p <= seq_len + i.  Rows are the nodes of
+// the accepted path, whose K compaction has put in order, and lse what their
+// attention returned ("EAGLE speculative decoding in four parts",
+// ai-infra-handbooks, "Drafting, verification and slots": only the accepted
+// path is kept, so only its rows count).  No softmax is left to do: with lse at
+// hand every position stands alone, and one pass over K's half of the cache
+// rows gives the sums.
+//
+// K is lo + c step per group of 32 channels, so
+//   q . k = sum over groups (step (q . c) + lo sum q).
+// The codes c enter the tensor cores as they are: a nibble in an fp16 register's
+// lowest bits is the subnormal c 2^-24, four bits higher c 2^-20, both exact, so
+// unpacking is a mask (and a shift for every second pair).  q is scaled by a
+// power of two per row (and by 2^-4 more where its code lies higher), exact but
+// for elements 2^-24 of the row's largest.  Products, sums and the steps are
+// fp32; lo times the group's sum of q is one matrix step more, with the sum as
+// three fp16 terms (2^-33).  The scores are then as good as fp32 sums.
+//
+// Positions are the 16 rows of a fragment, query rows its eight columns, so a
+// lane sums its positions' weights over columns, row tiles and heads in
+// registers.  A CTA takes a stretch of a request's 32-position chunks; its items
+// are (head, chunk) pairs, heads outermost, dealt to the warps in runs: a warp
+// turns its head's rows of q into fragments in registers once per run, and
+// fills its own ring of asynchronous copies.  The warps' sums meet in shared
+// memory and are added in the warps' order: no atomics.
+#include "kv4_attn.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kChunk = 32;     // positions of an item
+constexpr int kMaxChunks = 16; // chunks of a CTA's segment at most
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kStages = 4;
+
+struct SumArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const float* lse;
+  const int32_t* path;
+  const int32_t* accepted;
+  int B, N, Hq, Hkv, G;
+  uint64_t g_inv;  // ceil(2^40 / G)
+  const uint8_t* pool;
+  int64_t num_slots, slot_stride;
+  const int32_t* seq_lens;
+  const int32_t* table;
+  int64_t max_ctx;
+  float scale_log2;
+  const float* prev;
+  float* out;
+  int32_t* stats;
+};
+
+// D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct SumReq {
+  int start, rows, end;  // row i sees positions p <= start + i; end = start + rows
+  bool bad;
+};
+__device__ __forceinline__ SumReq sum_req(const SumArgs& a, int b) {
+  SumReq r;
+  r.start = __ldg(a.seq_lens + b);
+  r.rows = a.accepted ? __ldg(a.accepted + b) + 1 : a.N;
+  r.bad = r.rows < 1 || r.rows > a.N || r.start < 0 || static_cast<int64_t>(r.start) + r.rows > a.max_ctx;
+  if (r.bad) r.start = r.rows = 0;
+  r.end = r.start + r.rows;
+  return r;
+}
+__device__ __forceinline__ int sum_chunks(const SumReq& r) { return (r.end + kChunk - 1) / kChunk; }
+
+// Shared memory of a position in a stage: K's codes, then K's (step, lo); 20
+// words (D = 64: 12) apart, which makes all reads free of bank conflicts.
+template <int D>
+struct Pos {
+  static constexpr int kCodes = D / 2, kBytes = D == 128 ? 80 : 48;
+};
+
+template <int D>
+struct SumShared {
+  uint8_t ring[kWarps][kStages][kChunk * Pos<D>::kBytes];
+  float sum[kWarps][kMaxChunks * kChunk];
+  unsigned there[kWarps][kStages];
+};
+
+// The fragments of eight query rows [r0, r0 + 8) of a KV head, and of this
+// lane's columns 2t and 2t + 1 the factor that turns products into units of
+// log2, and lse in these (rows that do not count: 0 and +infinity).
+template <int D>
+struct QTile {
+  uint32_t b[D / 32][2][2];  // group, step of 16 channels, register
+  uint32_t lo[2];            // the groups' sums
+  float c[2], l[2];
+  int row[2];                // i of the columns
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0, const SumReq& rq, bool count,
+                                          QTile<D>& x) {
+  const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+  const int r = r0 + g, i = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+  bool in = i < rq.rows;
+  int n = in ? i : 0;
+  if (in && a.path) {
+    n = __ldg(a.path + static_cast<int64_t>(b) * a.N + i);
+    in = n >= 0 && n < a.N;
+    if (!in && count && t == 0 && r == i * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    if (!in) n = 0;
+  }
+  const int64_t at = static_cast<int64_t>(b) * a.N + n;
+  const int head = h * a.G + r - i * a.G;
+  float lse = in ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
+  in = in && isfinite(lse);
+  uint4 v[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (in) v[k] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
+  }
+  // the largest magnitude: bf16 bits without the sign compare as integers
+  uint32_t big = 0;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                 __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+  const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
+  // 2^e <= max < 2^(e + 1): the largest becomes [2^14, 2^15)
+  const int e = bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -113);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), half_up = up * 0.0625f;
+  float sums[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = j & 1 ? half_up : up, y0 = bf16_lo(w[j]) * f, y1 = bf16_hi(w[j]) * f;
+      x.b[k][j >> 1][j & 1] = h2_u32(__floats2half2_rn(y0, y1));
+      s += j & 1 ? (y0 + y1) * 16.0f : y0 + y1;
+    }
+    // 32 channels of at most 2^15 each, times 2^-5: fp16's range
+    s *= 0.03125f;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    sums[k] = s;
+  }
+  // groups' sums as three terms: columns of A hold lo of group 0..3 three times.
+  // Lane t has k = 2t, 2t + 1 (register 0) and 2t + 8, 2t + 9 (register 1)
+  uint32_t term[3][2];
+#pragma unroll
+  for (int z = 0; z < 3; ++z)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int k0 = 2 * k, k1 = 2 * k + 1;
+      const float s0 = k0 < D / 32 ? sums[k0 % (D / 32)] : 0.0f, s1 = k1 < D / 32 ? sums[k1 % (D / 32)] : 0.0f;
+      const __half2 y = __floats2half2_rn(s0, s1);
+      term[z][k] = h2_u32(y);
+      if (k0 < D / 32) sums[k0 % (D / 32)] -= __low2float(y);
+      if (k1 < D / 32) sums[k1 % (D / 32)] -= __high2float(y);
+    }
+  x.lo[0] = t == 0 ? term[0][0] : t == 1 ? term[0][1] : t == 2 ? term[1][0] : term[1][1];
+  x.lo[1] = t == 0 ? term[2][0] : t == 1 ? term[2][1] : 0u;
+  // of this lane's row, then of its columns
+  const float c = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 0.0f;
+  const float l = in ? lse * kLog2e : __uint_as_float(0x7f800000u);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    x.c[j] = __shfl_sync(0xffffffffu, c, (2 * t + j) * 4);
+    x.l[j] = __shfl_sync(0xffffffffu, l, (2 * t + j) * 4);
+    x.row[j] = __shfl_sync(0xffffffffu, i, (2 * t + j) * 4);
+  }
+}
+
+// A warp's run of items [at, last) of a segment with `chunks` chunks from chunk
+// `first` on: the cursor that fills the ring.
+template <int D>
+struct Ring {
+  int at, last, chunks;
+  int32_t slot;  // of position lane of the item to be copied next; -2: none
+  unsigned base;
+
+  __device__ __forceinline__ void load(const int32_t* row, int p0, int end) {
+    slot = -2;
+    if (at >= last) return;
+    const int pos = p0 + (at % chunks) * kChunk + static_cast<int>(threadIdx.x & 31);
+    if (pos < end) slot = __ldg(row + pos);
+  }
+  __device__ __forceinline__ void copy(const SumArgs& a, int st, unsigned* there, bool count) {
+    using P = Pos<D>;
+    if (at < last) {
+      const int lane = threadIdx.x & 31;
+      const bool ok = slot >= 0 && slot < a.num_slots;
+      if (!ok && slot != -2 && count && at < chunks) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      const unsigned have = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) there[st] = have;
+      const uint64_t mine = reinterpret_cast<uint64_t>(a.pool) +
+                            static_cast<uint64_t>(ok ? slot : 0) * static_cast<uint64_t>(a.slot_stride) +
+                            static_cast<uint32_t>(at / chunks) * kv4_head_bytes(D);
+      const unsigned to = base + st * (kChunk * P::kBytes);
+      // codes: D / 32 lanes a position; (step, lo) a lane each
+      constexpr int per = D / 32;
+#pragma unroll
+      for (int u = 0; u < per; ++u) {
+        const int pos = u * (32 / per) + lane / per, z = lane % per;
+        const uint64_t src = __shfl_sync(0xffffffffu, mine, pos) + z * 16;
+        put(to + pos * P::kBytes + z * 16, src, (have >> pos) & 1u ? 16u : 0u);
+      }
+      put(to + lane * P::kBytes + P::kCodes, mine + D, ok ? 16u : 0u);
+      ++at;
+    }
+    cp_async_commit();
+  }
+  __device__ __forceinline__ static void put(unsigned dst, uint64_t src, unsigned size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+  }
+};
+
+// RT: row tiles of eight that a pass over the codes takes at most.
+template <int D, int RT>
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 5 : 3) kv4_sums_kernel(const SumArgs a, int ctas) {
+  pdl_enter();
+  extern __shared__ __align__(16) unsigned char sums_sm[];
+  SumShared<D>& sh = *reinterpret_cast<SumShared<D>*>(sums_sm);
+  if (!spec_smem_ok(sizeof(sh), a.stats)) return;
+  __shared__ int64_t s_warp[kWarps], s_off;
+  __shared__ int s_b;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
+
+  // this CTA's stretch of the line of all requests' chunks
+  int64_t left;
+  int b, chunk;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+#pragma unroll 1
+    for (int i = b0; i < b1; ++i) {
+      const SumReq r = sum_req(a, i);
+      mine += sum_chunks(r);
+      if (r.bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t pre = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) pre += s_warp[i];
+      total += s_warp[i];
+    }
+    const int64_t n = min(static_cast<int64_t>(ctas), total), cta = blockIdx.x;
+    if (cta >= n) return;
+    const int64_t lo = cta * total / n;
+    left = (cta + 1) * total / n - lo;
+    if (lo >= pre && lo < pre + mine) {
+      int i = b0;
+#pragma unroll 1
+      for (;; ++i) {
+        const int u = sum_chunks(sum_req(a, i));
+        if (lo < pre + u) break;
+        pre += u;
+      }
+      s_off = lo - pre;
+      s_b = i;
+    }
+    __syncthreads();
+    b = s_b;
+    chunk = static_cast<int>(s_off);
+  }
+
+#pragma unroll 1
+  for (; left > 0; ++b, chunk = 0) {
+    const SumReq rq = sum_req(a, b);
+    const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_ctx;
+    const int tiles = (rq.rows * a.G + 7) / 8;
+#pragma unroll 1
+    for (int all = sum_chunks(rq); chunk < all && left > 0;) {
+      const int chunks = static_cast<int>(min(static_cast<int64_t>(min(all - chunk, kMaxChunks)), left));
+      const int p0 = chunk * kChunk, items = chunks * a.Hkv;
+      for (int i = lane; i < chunks * kChunk; i += 32) sh.sum[warp][i] = 0.0f;
+      __syncwarp();
+      const int from = static_cast<int>(static_cast<int64_t>(items) * warp / kWarps);
+      const int to = static_cast<int>(static_cast<int64_t>(items) * (warp + 1) / kWarps);
+#pragma unroll 1
+      for (int rt0 = 0; rt0 < tiles; rt0 += RT) {
+        Ring<D> ring;
+        ring.at = from, ring.last = to, ring.chunks = chunks;
+        ring.base = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp][0]));
+        ring.load(row, p0, rq.end);
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) {
+          ring.copy(a, i, sh.there[warp], rt0 == 0);
+          ring.load(row, p0, rq.end);
+        }
+        QTile<D> q[RT];
+        int head = -1, st = 0;
+#pragma unroll 1
+        for (int item = from; item < to; ++item) {
+          const int h = item / chunks, ch = item - h * chunks;
+          if (h != head) {
+            head = h;
+#pragma unroll
+            for (int x = 0; x < RT; ++x)
+              if (x == 0 || rt0 + x < tiles) load_tile<D>(a, b, h, (rt0 + x) * 8, rq, item == 0 && chunk == 0, q[x]);
+          }
+          __syncwarp();  // every lane has read the stage before
+          ring.copy(a, (st + kStages - 1) % kStages, sh.there[warp], rt0 == 0);
+          ring.load(row, p0, rq.end);
+          cp_async_wait<kStages - 1>();
+          __syncwarp();  // every lane's copies of this item have landed
+          const unsigned there = sh.there[warp][st];
+          const uint8_t* s8 = sh.ring[warp][st];
+          st = (st + 1) % kStages;
+
+          // s[x][u][2 i + e]: position 16 u + 8 i + g, column 2 t + e of tile x
+          float s[RT][2][4], step[D / 32][4];
+          uint32_t lo_a[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint8_t* m8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + Pos<D>::kCodes;
+              uint32_t m[4] = {0, 0, 0, 0};
+              if (D == 128) {
+                const uint4 v = *reinterpret_cast<const uint4*>(m8);
+                m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(m8);
+                m[0] = v.x, m[1] = v.y;
+              }
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) step[k][2 * u + i] = __low2float(u32_h2(m[k]));
+              const uint32_t l0 = __byte_perm(m[0], m[1], 0x7632), l1 = __byte_perm(m[2], m[3], 0x7632);
+              lo_a[u][i] = t & 1 ? l1 : l0;
+              lo_a[u][2 + i] = lo_a[u][i];
+            }
+#pragma unroll
+          for (int x = 0; x < RT; ++x)
+            if (x == 0 || rt0 + x < tiles) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                s[x][u][0] = s[x][u][1] = s[x][u][2] = s[x][u][3] = 0.0f;
+                mma16816(s[x][u], lo_a[u], q[x].lo[0], q[x].lo[1]);
+                // sums were held times 2^(14 - e - 5), products come times 2^(14 - e - 24)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[x][u][j] *= 0x1p-19f;
+              }
+            }
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t c[2][2][4];  // step of 16 channels, block of 16 positions, register
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t w =
+                    *reinterpret_cast<const uint32_t*>(s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + k * 16 + t * 4);
+                c[0][u][i] = w & 0x000f000fu;
+                c[0][u][2 + i] = w & 0x00f000f0u;
+                c[1][u][i] = (w >> 8) & 0x000f000fu;
+                c[1][u][2 + i] = (w >> 8) & 0x00f000f0u;
+              }
+#pragma unroll
+            for (int x = 0; x < RT; ++x)
+              if (x == 0 || rt0 + x < tiles) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma16816(p, c[0][u], q[x].b[k][0][0], q[x].b[k][0][1]);
+                  mma16816(p, c[1][u], q[x].b[k][1][0], q[x].b[k][1][1]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) s[x][u][j] = fmaf(step[k][2 * u + (j >> 1)], p[j], s[x][u][j]);
+                }
+              }
+          }
+          const int at0 = p0 + ch * kChunk;
+          const bool whole = there == 0xffffffffu && at0 + kChunk <= rq.start + 1;
+          float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of positions 8 j + g
+#pragma unroll
+          for (int x = 0; x < RT; ++x)
+            if (x == 0 || rt0 + x < tiles) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  // c is the row's factor for q as it was: 2^10 makes up for the codes' and q's
+                  const float y = fast_exp2(fmaf(s[x][u][j] * 0x1p10f, q[x].c[j & 1], -q[x].l[j & 1]));
+                  const int at = 16 * u + 8 * (j >> 1) + g;
+                  const bool see = whole || (((there >> at) & 1u) != 0 && at0 + at <= rq.start + q[x].row[j & 1]);
+                  w[2 * u + (j >> 1)] += see ? y : 0.0f;
+                }
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] += __shfl_xor_sync(0xffffffffu, w[j], 1);
+            w[j] += __shfl_xor_sync(0xffffffffu, w[j], 2);
+          }
+          const float mine = t == 0 ? w[0] : t == 1 ? w[1] : t == 2 ? w[2] : w[3];
+          sh.sum[warp][ch * kChunk + 8 * t + g] += mine;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+      }
+      __syncthreads();
+      const int64_t at = static_cast<int64_t>(b) * a.max_ctx + p0;
+      for (int i = threadIdx.x; i < min(chunks * kChunk, rq.end - p0); i += kThreads) {
+        float x = sh.sum[0][i];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) x += sh.sum[w][i];
+        a.out[at + i] = a.prev ? a.prev[at + i] + x : x;
+      }
+      __syncthreads();
+      chunk += chunks;
+      left -= chunks;
+    }
+  }
+}
+
+template <int D, int RT>
+int launch_sums(const SumArgs& a, int sms, cudaStream_t s) {
+  constexpr auto kernel = kv4_sums_kernel<D, RT>;
+  constexpr size_t smem = sizeof(SumShared<D>);
+  if (!allow_smem<kernel>(smem)) return SPEC_ERR_CUDA;
+  const int ctas = sms * (RT == 1 ? 5 : 3);
+  launch_k(kernel, static_cast<unsigned>(ctas), kThreads, smem, s, a, ctas);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace specdec
+
+using namespace specdec;
+
+extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,
+                                    const float* lse, const int32_t* accept_path_or_null,
+                                    const int32_t* accept_length_or_null, const void* pool, int64_t num_slots,
+                                    int64_t slot_stride, const int32_t* seq_lens, const int32_t* req_to_token,
+                                    int64_t max_ctx, float scale, const float* prev_or_null, float* out,
+                                    int32_t* stats_or_null, spec_stream_t stream) {
+  if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !(scale > 0.0f) ||
+      !isfinite(scale))
+    return SPEC_ERR_INVALID_ARG;
+  const int64_t row = spec_kv4_slot_bytes(Hkv, D);
+  if (row < 0 || N > SPEC_MAX_NODES || Hq > SPEC_KV4_MAX_HEADS * 16 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
+  if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
+  if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kChunk ||
+      slot_stride > INT32_MAX)
+    return SPEC_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return SPEC_OK;
+  if (!q || !lse || !pool || !seq_lens || !req_to_token || !out) return SPEC_ERR_INVALID_ARG;
+  for (const void* p : {q, pool})
+    if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return SPEC_ERR_UNSUPPORTED;
+  const int sms = attn_sms();
+  if (sms == 0) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
+  const int G = Hq / Hkv;
+  const SumArgs a{static_cast<const uint16_t*>(q), q_stride, lse, accept_path_or_null, accept_length_or_null, B, N, Hq,
+                  Hkv, G, ((1ull << 40) + G - 1) / G, static_cast<const uint8_t*>(pool), num_slots, slot_stride,
+                  seq_lens, req_to_token, max_ctx, scale * kLog2e, prev_or_null, out, stats_or_null};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool one = static_cast<int64_t>(N) * G <= 8;
+  if (D == 128) return one ? launch_sums<128, 1>(a, sms, s) : launch_sums<128, 4>(a, sms, s);
+  return one ? launch_sums<64, 1>(a, sms, s) : launch_sums<64, 4>(a, sms, s);
+}

@@ -29,6 +29,12 @@ kv_pool, run_attention attends over it under the tree mask, and run_adjust
 applies penalties, biases and grammar masks to the target logits of every
 node, its own path counted.  run_compact moves the same kv_pool's rows.
 
+Behind compaction, a cache that has to stay bounded: run_weight_sums adds the
+attention weights that the accepted path's rows gave each position to its sum,
+and run_evict cuts the requests that have grown past a limit to the positions
+with the largest sums, the sinks and the latest ones (run_attention takes a
+window and sinks for layers that look no further).
+
 All buffers are allocated once in ``StepBuffers``; a step only enqueues
 kernels on the current stream, so a whole step can be captured once in a
 CUDA graph (``capture_step``) and replayed: the same kernels, without the
@@ -39,7 +45,8 @@ from __future__ import annotations
 import torch
 
 from . import (new_pool, new_stats, spec_adjust_logits, spec_build_tree, spec_compact_freed_capacity,
-               spec_compact_slots, spec_kv4_append, spec_kv4_attention, spec_kv4_attention_ws_size,
+               spec_compact_slots, spec_evict_freed_capacity, spec_evict_slots, spec_evict_ws_size, spec_kv4_append,
+               spec_kv4_attention, spec_kv4_attention_window, spec_kv4_attention_ws_size, spec_kv4_weight_sums,
                spec_softmax_sample, spec_softmax_topk, spec_verify_greedy, spec_verify_sample,
                spec_verify_sample_qlogits, spec_verify_ws_size, tli_constrain_map, tli_constrain_map_qlogits,
                tli_plan_build, tli_plan_bytes)
@@ -102,6 +109,7 @@ class StepBuffers:
         self.verify_out = None
         self.stats = new_stats(dev)
         self.attention_ws = {}  # run_attention's, by their size, kept from the first call on
+        self.evict_out = {}     # run_evict's results and workspaces, by their sizes, likewise
         self.compact_out = None
         if page_size:
             cap = spec_compact_freed_capacity(B, N, page_size)
@@ -182,22 +190,27 @@ def run_kv4_append(buf: StepBuffers, k, v, seq_lens, req_to_token, kv_pool, num_
 
 
 def run_attention(buf: StepBuffers, q, seq_lens, req_to_token, kv_pool, num_kv_heads, scale=None, num_nodes=None,
-                  out=None, lse=None, ws=None):
+                  out=None, lse=None, ws=None, window=None, sinks=0):
     """Attention of q [B, N, Hq, D] of buf.tree's nodes over context and tree
     (their K and V appended before).  Without ``ws``, the workspace of a size
     is allocated by the first call that needs it and kept as long as buf, so
     that a captured step's stays its own; like buf's other buffers it serves
     calls that follow one another.  Calls of one buf that may run at the same
     time (layers on several streams, two graphs replayed side by side) pass a
-    ``ws`` each, of spec_kv4_attention_ws_size bytes."""
+    ``ws`` each, of spec_kv4_attention_ws_size bytes.  With a ``window`` a node
+    sees the first ``sinks`` positions and the window up to its own."""
     if ws is None:
         B, N, Hq, D = q.shape
         need = spec_kv4_attention_ws_size(B, N, Hq, int(num_kv_heads), D)
         ws = buf.attention_ws.get(need)
         if ws is None:
             ws = buf.attention_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
-    return spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask=buf.tree["tree_mask"],
-                              scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=ws, stats=buf.stats)
+    same = dict(tree_mask=buf.tree["tree_mask"], scale=scale, num_nodes=num_nodes, out=out, lse=lse, ws=ws,
+                stats=buf.stats)
+    if window is not None:
+        return spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, sinks, window,
+                                         positions=buf.tree["positions"], **same)
+    return spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, **same)
 
 
 def run_adjust(buf: StepBuffers, target, out=None, **penalties):
@@ -239,6 +252,35 @@ def run_compact(buf: StepBuffers, seq_lens, req_to_token, page_size, kv_pool=Non
     v = buf.verify_out
     return spec_compact_slots(seq_lens, v["accept_path"], v["accept_length"], req_to_token, page_size,
                               kv_pool=kv_pool, out=buf.compact_out, stats=buf.stats)
+
+
+def run_weight_sums(buf: StepBuffers, q, lse, seq_lens, req_to_token, kv_pool, num_kv_heads, sums, scale=None):
+    """Adds the attention weights of the accepted path's rows of q [B, N, Hq, D]
+    to sums [B, max_ctx]; behind run_compact, with the seq_lens and lse that
+    run_attention had."""
+    v = buf.verify_out
+    return spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, accept_path=v["accept_path"],
+                                accept_length=v["accept_length"], prev=sums, scale=scale, stats=buf.stats)
+
+
+def run_evict(buf: StepBuffers, sums, seq_lens, req_to_token, page_size, budget, limit=None, sinks=0, recent=0,
+              kv_pool=None):
+    """Cuts requests longer than ``limit`` to ``budget`` positions
+    (spec_evict_slots); seq_lens: run_compact's new_kv_len.  The results and the
+    workspace of a size are allocated by its first call and kept as long as buf:
+    the next call of the same sizes writes the same tensors."""
+    B, ctx = sums.shape
+    key = (B, ctx, int(page_size), int(budget))
+    held = buf.evict_out.get(key)
+    if held is None:
+        dev = sums.device
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+        held = buf.evict_out[key] = (
+            {"kept": new(B, budget), "freed": new(max(1, spec_evict_freed_capacity(B, ctx, page_size, budget))),
+             "num_freed": new(1), "new_kv_len": new(B)},
+            torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=dev))
+    return spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=limit, sinks=sinks, recent=recent,
+                            kv_pool=kv_pool, out=held[0], ws=held[1], stats=buf.stats)
 
 
 def capture_step(fn, warm=True):
