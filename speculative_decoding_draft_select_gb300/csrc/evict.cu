@@ -8,15 +8,15 @@
 // allocated, and freed, by their table); with larger pages the kept rows move
 // up, in order, and whole pages are freed.  Sums follow their positions.
 //
-// Three launches:
+// Two launches:
 //   select   a cluster per request.  Ranks are by a 32-bit key in which floats
 //            compare as unsigned integers (NaN as -inf, -0 as 0) and positions
 //            that stay in any case lie above every number.  Three counting
 //            passes (11, 11 and 10 bits) find the key of the budget's last
 //            position; the kept ones are those above it and, of equal ones, the
-//            first.  One scan in the positions' order then gives each its place.
-//   apply    writes the new table and sums, which select has put aside (the
-//            arrays are updated in place), and zeros behind them.
+//            first.  One scan in the positions' order then gives each its place; the slots
+//            and sums of the kept are put aside, and once the cluster has read
+//            all of the old ones they take the first places.
 //   payload  (pages of several tokens) a CTA takes a request's rows, a slice of
 //            their bytes: it reads kept rows in order, a few chunks ahead, and
 //            writes them up.  A row only ever moves towards the front: what a
@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCtas = 8;    // of a cluster
 constexpr int kSlice = 16384;  // keys of a CTA that stay in shared memory
 
 struct EvictArgs {
@@ -45,7 +46,7 @@ struct EvictArgs {
   int64_t freed_cap;
   int32_t* num_freed;
   int32_t* new_len;
-  int32_t* ws_table;  // [B, budget], with pages of one token
+  int32_t* ws_table;  // [B, budget]: slots of the kept positions
   float* ws_sums;     // [B, budget]
   uint8_t* kv;
   int64_t num_slots, bps;
@@ -81,6 +82,15 @@ __device__ __forceinline__ T ld_cluster(const T* local, unsigned rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
   return static_cast<T>(v);
+}
+
+__device__ __forceinline__ uint4 ld_cluster4(const unsigned* local, unsigned rank) {
+  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
+  unsigned r;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(r) : "memory");
+  return v;
 }
 
 // The sum over the threads before this one.
@@ -153,11 +163,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     a.new_len[b] = cut ? a.budget : n;
     if (n < 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
   }
+  const float* sums = a.sums + static_cast<int64_t>(b) * a.max_ctx;
+  float* sums_out = a.sums_out + static_cast<int64_t>(b) * a.max_ctx;
+  const int step = ctas * kSelThreads, t0 = static_cast<int>(rank) * kSelThreads + tid;  // of the cluster's threads
   if (!cut) {  // the whole cluster leaves
-    for (int i = rank * kSelThreads + tid; i < a.budget; i += ctas * kSelThreads) kept[i] = -1;
+    for (int i = t0; i < a.budget; i += step) kept[i] = -1;
+    if (sums_out != sums)
+      for (int i = t0; i < n; i += step) sums_out[i] = __ldg(sums + i);
     return;
   }
-  const float* sums = a.sums + static_cast<int64_t>(b) * a.max_ctx;
   int32_t* table = a.table + static_cast<int64_t>(b) * a.max_ctx;
   // this CTA's positions [p0, p0 + mine), a run of each thread's; keys beyond
   // what shared memory holds are computed again in each pass
@@ -181,18 +195,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (ctas > 1) cluster_barrier();
     else __syncthreads();
     // bins from the top: a thread's run of four
-    constexpr int per = kBins / kSelThreads;
-    unsigned cnt[per];
-    int mine_sum = 0;
+    constexpr int per = 4;
+    static_assert(per * kSelThreads == kBins, "a run of four bins each");
+    const int low = kBins - per * (tid + 1);  // the run's lowest bin
+    uint4 h = *reinterpret_cast<const uint4*>(sh.hist + low);
+    if (ctas > 1) {
+      uint4 other[kMaxCtas];  // all in flight at once: a load takes about a microsecond
 #pragma unroll
-    for (int j = 0; j < per; ++j) {
-      const int bin = kBins - 1 - (tid * per + j);
-      cnt[j] = 0;
-      if (ctas == 1) cnt[j] = sh.hist[bin];
-      else
-        for (int c = 0; c < ctas; ++c) cnt[j] += ld_cluster(&sh.hist[bin], c);
-      mine_sum += static_cast<int>(cnt[j]);
+      for (int c = 0; c < kMaxCtas; ++c)
+        if (c < ctas) other[c] = ld_cluster4(sh.hist + low, c);
+      h = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < kMaxCtas; ++c)
+        if (c < ctas) h.x += other[c].x, h.y += other[c].y, h.z += other[c].z, h.w += other[c].w;
     }
+    const unsigned cnt[per] = {h.w, h.z, h.y, h.x};
+    const int mine_sum = static_cast<int>(h.x + h.y + h.z + h.w);
     int run = block_before(mine_sum, sh.scan);
 #pragma unroll
     for (int j = 0; j < per; ++j) {
@@ -227,14 +245,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (w < warp) at.x += y.x, at.y += y.y;
     total.x += y.x, total.y += y.y;
   }
-  if (ctas > 1) {
+  if (ctas > 1) {  // no CTA leaves before its counts are read: a barrier follows
     if (tid == 0) sh.counts[0] = total.x, sh.counts[1] = total.y;
     cluster_barrier();
-    for (unsigned c = 0; c < rank; ++c) {
-      at.x += ld_cluster(&sh.counts[0], c);
-      at.y += ld_cluster(&sh.counts[1], c);
-    }
-    cluster_barrier();  // no CTA leaves before its counts are read
+    int x[kMaxCtas], y[kMaxCtas];
+#pragma unroll
+    for (unsigned c = 0; c < kMaxCtas; ++c)
+      if (c < rank) x[c] = ld_cluster(&sh.counts[0], c), y[c] = ld_cluster(&sh.counts[1], c);
+#pragma unroll
+    for (unsigned c = 0; c < kMaxCtas; ++c)
+      if (c < rank) at.x += x[c], at.y += y[c];
   }
   int32_t* ws_table = a.ws_table + static_cast<int64_t>(b) * a.budget;
   float* ws_sums = a.ws_sums + static_cast<int64_t>(b) * a.budget;
@@ -252,7 +272,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       if (!spec_in(to, a.budget, a.stats)) continue;
       kept[to] = p;
       ws_sums[to] = __ldg(sums + p);
-      if (a.page == 1) ws_table[to] = table[p];
+      ws_table[to] = table[p];
     } else if (a.page == 1) {
       if (spec_in(before + p - to, a.freed_cap, a.stats)) a.freed[before + p - to] = table[p];
     }
@@ -263,37 +283,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       if (spec_in(before + i, a.freed_cap, a.stats))
         a.freed[before + i] = table[static_cast<int64_t>(first + i) * a.page] / a.page;
   }
-}
-
-constexpr int kApplyThreads = 256;
-
-__global__ void __launch_bounds__(kApplyThreads) evict_apply_kernel(const EvictArgs a) {
-  pdl_enter();
-  const int b = blockIdx.y;
-  const int n = evict_len(a, b), step = gridDim.x * kApplyThreads;
-  const bool cut = n > a.limit;
-  if (!cut && a.sums_out == a.sums) return;
-  const int64_t row = static_cast<int64_t>(b) * a.max_ctx, set = static_cast<int64_t>(b) * a.budget;
-  for (int i = blockIdx.x * kApplyThreads + threadIdx.x; i < n; i += step) {
-    float x = 0.0f;
-    if (!cut) x = a.sums[row + i];
-    else if (i < a.budget) x = a.ws_sums[set + i];
-    a.sums_out[row + i] = x;
-    if (cut && a.page == 1 && i < a.budget) a.table[row + i] = a.ws_table[set + i];
+  // nobody reads the old slots and sums any more
+  if (ctas > 1) cluster_barrier();
+  else __syncthreads();
+  for (int i = t0; i < a.budget; i += step) {
+    sums_out[i] = ws_sums[i];
+    if (a.page == 1) table[i] = ws_table[i];
   }
+  for (int i = a.budget + t0; i < n; i += step) sums_out[i] = 0.0f;
 }
 
 constexpr int kMoveThreads = 256, kMoveStages = 3;
-constexpr int kMoveVecs = 8;                            // 16-byte vectors of a slice
-constexpr int kMoveRows = 4 * kMoveThreads / kMoveVecs; // rows of a chunk: four vectors a thread
 
+// V: 16-byte vectors of a slice.
+template <int V>
 __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const EvictArgs a) {
   pdl_enter();
-  __shared__ __align__(16) uint4 sm[kMoveStages][kMoveRows * kMoveVecs];
+  constexpr int kRowsAt = kMoveThreads / V, kRows = 4 * kRowsAt;  // rows of a chunk: four vectors a thread
+  __shared__ __align__(16) uint4 sm[kMoveStages][4 * kMoveThreads];
   const int b = blockIdx.y;
   if (evict_len(a, b) <= a.limit) return;
   const int32_t* kept = a.kept + static_cast<int64_t>(b) * a.budget;
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_ctx;
   // kept[i] - i never falls: the rows before the first that moves lie in place
   int lo = 0, hi = a.budget;
   while (lo < hi) {
@@ -301,46 +311,57 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
     if (__ldg(kept + mid) > mid) hi = mid;
     else lo = mid + 1;
   }
-  const int first = lo, chunks = (a.budget - first + kMoveRows - 1) / kMoveRows;
-  const int vec = threadIdx.x % kMoveVecs, r = threadIdx.x / kMoveVecs;
-  constexpr int kRowsAt = kMoveThreads / kMoveVecs;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x) * kMoveVecs + vec) * 16;
+  const int first = lo, chunks = (a.budget - first + kRows - 1) / kRows;
+  const int vec = threadIdx.x % V, r = threadIdx.x / V;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * V + vec) * 16;
   const bool in = col < a.bps;
-  auto slot_ok = [&](int32_t s) { return s >= 0 && s < a.num_slots; };
-  auto fetch = [&](int c) {
-    if (c < chunks && in) {
+  const int32_t* from = a.ws_table + static_cast<int64_t>(b) * a.budget;
+  const int32_t* to = a.table + static_cast<int64_t>(b) * a.max_ctx;
+  // slots of this thread's four rows of a chunk: -1 behind the last
+  auto slots = [&](const int32_t* list, int c, int32_t* s) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = first + c * kMoveRows + j * kRowsAt + r;
-        if (i >= a.budget) break;
-        const int p = __ldg(kept + i);
-        const int32_t src = spec_in(p, a.max_ctx, a.stats) ? __ldg(table + p) : -1;
-        if (slot_ok(src))
-          cp_async16(&sm[c % kMoveStages][(j * kRowsAt + r) * kMoveVecs + vec], a.kv + src * a.bps + col, 16);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int i = first + c * kRows + j * kRowsAt + r;
+      s[j] = in && i < a.budget ? __ldg(list + i) : -1;
     }
-    cp_async_commit();
   };
+  auto slot_ok = [&](int32_t s) { return s >= 0 && s < a.num_slots; };
+  int32_t src[4], dst[4];
+  unsigned read[kMoveStages];  // bit j: row j of the stage's chunk has been read
+  slots(from, 0, src);
+  auto fetch = [&](int c, int st) {
+    unsigned have = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (slot_ok(src[j])) {
+        cp_async16(&sm[st][j * kMoveThreads + threadIdx.x], a.kv + src[j] * a.bps + col, 16);
+        have |= 1u << j;
+      }
+    cp_async_commit();
+    slots(from, c + 1, src);
+    return have;
+  };
+#pragma unroll
+  for (int c = 0; c < kMoveStages - 1; ++c) read[c] = fetch(c, c);
+  slots(to, 0, dst);
 #pragma unroll 1
-  for (int c = 0; c < kMoveStages - 1; ++c) fetch(c);
-#pragma unroll 1
-  for (int c = 0; c < chunks; ++c) {
-    fetch(c + kMoveStages - 1);
-    cp_async_wait<kMoveStages - 1>();
-    __syncthreads();  // the chunk has been read whole: its rows may be overwritten
-    if (in) {
+  for (int c0 = 0; c0 < chunks; c0 += kMoveStages) {
+#pragma unroll
+    for (int s = 0; s < kMoveStages; ++s) {
+      const int c = c0 + s;
+      if (c >= chunks) break;  // the same in every thread
+      read[(s + kMoveStages - 1) % kMoveStages] = fetch(c + kMoveStages - 1, (s + kMoveStages - 1) % kMoveStages);
+      cp_async_wait<kMoveStages - 1>();
+      __syncthreads();  // the chunk has been read whole: its rows may be overwritten
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = first + c * kMoveRows + j * kRowsAt + r;
-        if (i >= a.budget) break;
-        const int p = __ldg(kept + i);
-        const int32_t src = spec_in(p, a.max_ctx, a.stats) ? __ldg(table + p) : -1, dst = __ldg(table + i);
-        if (slot_ok(src) && slot_ok(dst))
-          *reinterpret_cast<uint4*>(a.kv + dst * a.bps + col) =
-              sm[c % kMoveStages][(j * kRowsAt + r) * kMoveVecs + vec];
-        else if (blockIdx.x == 0 && vec == 0)
+        const int i = first + c * kRows + j * kRowsAt + r;
+        if (((read[s] >> j) & 1u) != 0 && slot_ok(dst[j]))
+          *reinterpret_cast<uint4*>(a.kv + dst[j] * a.bps + col) = sm[s][j * kMoveThreads + threadIdx.x];
+        else if (in && i < a.budget && blockIdx.x == 0 && vec == 0)
           bump(a.stats, SPEC_STAT_BAD_REQUEST);
       }
+      slots(to, c + 1, dst);
     }
   }
   cp_async_wait<0>();
@@ -367,7 +388,7 @@ extern "C" int64_t spec_evict_freed_capacity(int B, int64_t max_ctx, int page_si
 
 extern "C" size_t spec_evict_ws_size(int B, int page_size, int budget) {
   if (B < 1 || B > 65535 || page_size < 1 || budget < 1) return 0;
-  return evict_list(B, budget) * (page_size == 1 ? 2 : 1);
+  return evict_list(B, budget) * 2;
 }
 
 extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int sinks, int recent,
@@ -400,7 +421,7 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
   char* w = static_cast<char*>(ws);
   EvictArgs a{B, page_size, budget, limit, sinks, recent, seq_lens, sums, sums_out, req_to_token, max_ctx, kept, freed,
               freed_capacity, num_freed, new_kv_len,
-              reinterpret_cast<int32_t*>(w + (page_size == 1 && B > 0 ? evict_list(B, budget) : 0)),
+              reinterpret_cast<int32_t*>(w + (B > 0 ? evict_list(B, budget) : 0)),
               reinterpret_cast<float*>(w), static_cast<uint8_t*>(kv_pool_or_null), num_slots, bytes_per_slot,
               stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -410,12 +431,12 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
             ctas, a, ctas);
   int e = launch_status();
   if (e != SPEC_OK || B == 0) return e;
-  const unsigned wide_ctas = static_cast<unsigned>((max_ctx + 4 * kApplyThreads - 1) / (4 * kApplyThreads));
-  launch_k(evict_apply_kernel, dim3(wide_ctas < 64 ? wide_ctas : 64, static_cast<unsigned>(B)), kApplyThreads, 0, s, a);
-  e = launch_status();
-  if (e != SPEC_OK || page_size == 1 || !kv_pool_or_null) return e;
-  launch_k(evict_payload_kernel,
-           dim3(static_cast<unsigned>((bytes_per_slot / 16 + kMoveVecs - 1) / kMoveVecs), static_cast<unsigned>(B)),
-           kMoveThreads, 0, s, a);
+  if (page_size == 1 || !kv_pool_or_null) return SPEC_OK;
+  // slices of 128 bytes, or of 32 where a launch of those would leave SMs idle
+  const int64_t vecs = bytes_per_slot / 16;
+  const bool wide_slices = B * ((vecs + 7) / 8) >= 2 * 152;
+  const dim3 grid(static_cast<unsigned>(wide_slices ? (vecs + 7) / 8 : (vecs + 1) / 2), static_cast<unsigned>(B));
+  if (wide_slices) launch_k(evict_payload_kernel<8>, grid, kMoveThreads, 0, s, a);
+  else launch_k(evict_payload_kernel<2>, grid, kMoveThreads, 0, s, a);
   return launch_status();
 }

@@ -32,9 +32,9 @@ namespace specdec {
 namespace {
 
 constexpr int kChunk = 32;     // positions of an item
-constexpr int kMaxChunks = 16; // chunks of a CTA's segment at most
+constexpr int kMaxChunks = 8;  // chunks of a CTA's segment at most
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 struct SumArgs {
   const uint16_t* q;

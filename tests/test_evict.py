@@ -90,7 +90,7 @@ def test_host_checks():
     assert cap(3, 10, 1, 4) == 18 and cap(3, 10, 4, 4) == 6 and cap(3, 10, 4, 5) == 3 and cap(3, 10, 1, 11) == 0
     assert cap(-1, 10, 1, 4) == -1 and cap(1, 0, 1, 4) == -1 and cap(1, 10, 0, 4) == -1 and cap(1, 10, 1, 0) == -1
     assert lib.spec_evict_ws_size(0, 1, 4) == 0 and lib.spec_evict_ws_size(1, 1, 0) == 0
-    assert lib.spec_evict_ws_size(3, 1, 5) >= 2 * 60 and lib.spec_evict_ws_size(3, 16, 5) >= 60
+    assert lib.spec_evict_ws_size(3, 1, 5) >= 2 * 60 and lib.spec_evict_ws_size(3, 16, 5) >= 2 * 60
     if not torch.cuda.is_available():  # made-up addresses: only where nothing could run
         p, odd = ctypes.c_void_p(4096), ctypes.c_void_p(4104)
         a = dict(lens=p, sums=p, out=p, table=p, kept=p, freed=p, num=p, new=p, ws=p, wsb=1 << 40)
