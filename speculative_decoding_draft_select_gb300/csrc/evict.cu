@@ -69,9 +69,10 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
   const uint32_t u = __float_as_uint(order_key(x) + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-// Key of position p of a request of length n.
+// Whether position p of a request of length n stays in any case.
+__device__ __forceinline__ bool evict_stays(const EvictArgs& a, int p, int n) { return p < a.sinks || p >= n - a.recent; }
 __device__ __forceinline__ uint32_t evict_key(const EvictArgs& a, const float* sums, int p, int n) {
-  return p < a.sinks || p >= n - a.recent ? ~0u : sum_key(__ldg(sums + p));
+  return evict_stays(a, p, n) ? ~0u : sum_key(__ldg(sums + p));
 }
 
 template <typename T>
@@ -178,7 +179,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int each = (n + ctas - 1) / ctas;
   const int p0 = min(n, static_cast<int>(rank) * each), mine = min(each, n - p0);
   const int held = min(mine, kSlice);
-  for (int i = tid; i < held; i += kSelThreads) sh.key[i] = evict_key(a, sums, p0 + i, n);
+  constexpr int kAhead = 8;  // loads of a thread in flight
+  for (int i = tid; i < held; i += kAhead * kSelThreads) {
+    float x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = i + u * kSelThreads < held ? __ldg(sums + p0 + i + u * kSelThreads) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = i + u * kSelThreads;
+      if (j < held) sh.key[j] = evict_stays(a, p0 + j, n) ? ~0u : sum_key(x[u]);
+    }
+  }
   auto key_at = [&](int i) { return i < held ? sh.key[i] : evict_key(a, sums, p0 + i, n); };
 
   uint32_t prefix = 0;
@@ -259,22 +270,36 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int32_t* ws_table = a.ws_table + static_cast<int64_t>(b) * a.budget;
   float* ws_sums = a.ws_sums + static_cast<int64_t>(b) * a.budget;
   const unsigned below = (1u << lane) - 1u;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t k = in ? key_at(i + lane) : 0u;
-    const unsigned above = __ballot_sync(0xffffffffu, in && k > prefix), same = __ballot_sync(0xffffffffu, in && k == prefix);
-    const int p = p0 + i + lane, nth = at.y + __popc(same & below);  // among the equal ones
-    const int to = at.x + __popc(above & below) + min(nth, need);   // kept positions before this one
-    at.x += __popc(above);
-    at.y += __popc(same);
-    if (!in) continue;
-    if (k > prefix || (k == prefix && nth < need)) {
-      if (!spec_in(to, a.budget, a.stats)) continue;
-      kept[to] = p;
-      ws_sums[to] = __ldg(sums + p);
-      ws_table[to] = table[p];
-    } else if (a.page == 1) {
-      if (spec_in(before + p - to, a.freed_cap, a.stats)) a.freed[before + p - to] = table[p];
+  constexpr int kWords = 4;  // words of 32 positions whose loads are in flight together
+  for (int w0 = i0; w0 < i1; w0 += 32 * kWords) {
+    float x[kWords];
+    int32_t slot[kWords];
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int i = w0 + 32 * u + lane, p = p0 + min(i, i1 - 1);
+      x[u] = __ldg(sums + p);
+      slot[u] = table[p];
+    }
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int i = w0 + 32 * u + lane, p = p0 + i;
+      const bool in = i < i1;
+      const uint32_t k = in ? key_at(i) : 0u;
+      const unsigned above = __ballot_sync(0xffffffffu, in && k > prefix);
+      const unsigned same = __ballot_sync(0xffffffffu, in && k == prefix);
+      const int nth = at.y + __popc(same & below);                   // among the equal ones
+      const int to = at.x + __popc(above & below) + min(nth, need);  // kept positions before this one
+      at.x += __popc(above);
+      at.y += __popc(same);
+      if (!in) continue;
+      if (k > prefix || (k == prefix && nth < need)) {
+        if (!spec_in(to, a.budget, a.stats)) continue;
+        kept[to] = p;
+        ws_sums[to] = x[u];
+        ws_table[to] = slot[u];
+      } else if (a.page == 1) {
+        if (spec_in(before + p - to, a.freed_cap, a.stats)) a.freed[before + p - to] = slot[u];
+      }
     }
   }
   if (a.page > 1 && rank == 0) {
@@ -286,9 +311,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   // nobody reads the old slots and sums any more
   if (ctas > 1) cluster_barrier();
   else __syncthreads();
-  for (int i = t0; i < a.budget; i += step) {
-    sums_out[i] = ws_sums[i];
-    if (a.page == 1) table[i] = ws_table[i];
+  for (int i = t0; i < a.budget; i += kWords * step) {
+    float x[kWords];
+    int32_t slot[kWords];
+#pragma unroll
+    for (int u = 0; u < kWords; ++u)
+      if (i + u * step < a.budget) x[u] = ws_sums[i + u * step], slot[u] = ws_table[i + u * step];
+#pragma unroll
+    for (int u = 0; u < kWords; ++u)
+      if (i + u * step < a.budget) {
+        sums_out[i + u * step] = x[u];
+        if (a.page == 1) table[i + u * step] = slot[u];
+      }
   }
   for (int i = a.budget + t0; i < n; i += step) sums_out[i] = 0.0f;
 }

@@ -31,10 +31,15 @@
 namespace specdec {
 namespace {
 
-constexpr int kChunk = 32;     // positions of an item
-constexpr int kMaxChunks = 8;  // chunks of a CTA's segment at most
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kChunk = 32;      // positions of an item
+constexpr int kMaxChunks = 32;  // chunks of a CTA's segment at most
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMine = kMaxChunks / kWarps + 2;  // chunks that a warp has a part of
 constexpr int kStages = 3;
+// Tiles of eight query rows in shared memory: one a head where they fit, so
+// that a request's stay; more heads or rows take several passes over the codes.
+constexpr int kTiles = 8;       // with one tile a head
+constexpr int kTiles4 = 32;     // with up to four
 
 struct SumArgs {
   const uint16_t* q;
@@ -63,6 +68,14 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// D = A B.
+__device__ __forceinline__ void mma16816_zero(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 struct SumReq {
   int start, rows, end;  // row i sees positions p <= start + i; end = start + rows
   bool bad;
@@ -85,24 +98,27 @@ struct Pos {
   static constexpr int kCodes = D / 2, kBytes = D == 128 ? 80 : 48;
 };
 
+// A tile of eight query rows of a KV head as B fragments: lane by lane, per
+// group of 32 channels two steps of 16; the groups' sums; and of its columns
+// the factor that turns products into units of log2, lse in these (rows that
+// do not count: 0 and +infinity), and the row of the path.
 template <int D>
+struct QTile {
+  uint2 b[D / 16][32];
+  uint2 lo[32];
+  float c[8], l[8];
+  int row[8];
+};
+
+template <int D, int TILES>
 struct SumShared {
   uint8_t ring[kWarps][kStages][kChunk * Pos<D>::kBytes];
-  float sum[kWarps][kMaxChunks * kChunk];
+  QTile<D> q[TILES];
+  float sum[kWarps][kMine][kChunk];
   unsigned there[kWarps][kStages];
 };
 
-// The fragments of eight query rows [r0, r0 + 8) of a KV head, and of this
-// lane's columns 2t and 2t + 1 the factor that turns products into units of
-// log2, and lse in these (rows that do not count: 0 and +infinity).
-template <int D>
-struct QTile {
-  uint32_t b[D / 32][2][2];  // group, step of 16 channels, register
-  uint32_t lo[2];            // the groups' sums
-  float c[2], l[2];
-  int row[2];                // i of the columns
-};
-
+// Rows [r0, r0 + 8) of KV head h as a tile: a warp's work.
 template <int D>
 __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0, const SumReq& rq, bool count,
                                           QTile<D>& x) {
@@ -118,20 +134,22 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
   }
   const int64_t at = static_cast<int64_t>(b) * a.N + n;
   const int head = h * a.G + r - i * a.G;
-  float lse = in ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
-  in = in && isfinite(lse);
+  const float lse = in ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
   uint4 v[D / 32];
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     v[k] = make_uint4(0, 0, 0, 0);
     if (in) v[k] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
   }
+  in = in && isfinite(lse);
   // the largest magnitude: bf16 bits without the sign compare as integers
   uint32_t big = 0;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k)
+  for (int k = 0; k < D / 32; ++k) {
+    if (!in) v[k] = make_uint4(0, 0, 0, 0);
     big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
                                  __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+  }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
   const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
@@ -142,21 +160,24 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t y[4];
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float f = j & 1 ? half_up : up, y0 = bf16_lo(w[j]) * f, y1 = bf16_hi(w[j]) * f;
-      x.b[k][j >> 1][j & 1] = h2_u32(__floats2half2_rn(y0, y1));
+      y[j] = h2_u32(__floats2half2_rn(y0, y1));
       s += j & 1 ? (y0 + y1) * 16.0f : y0 + y1;
     }
+    x.b[2 * k][lane] = make_uint2(y[0], y[1]);
+    x.b[2 * k + 1][lane] = make_uint2(y[2], y[3]);
     // 32 channels of at most 2^15 each, times 2^-5: fp16's range
     s *= 0.03125f;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     sums[k] = s;
   }
-  // groups' sums as three terms: columns of A hold lo of group 0..3 three times.
-  // Lane t has k = 2t, 2t + 1 (register 0) and 2t + 8, 2t + 9 (register 1)
+  // groups' sums as three terms: A's columns hold lo of the groups three times.
+  // Lane t has rows 2t, 2t + 1 of B (first register) and 2t + 8, 2t + 9 (second)
   uint32_t term[3][2];
 #pragma unroll
   for (int z = 0; z < 3; ++z)
@@ -169,55 +190,69 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
       if (k0 < D / 32) sums[k0 % (D / 32)] -= __low2float(y);
       if (k1 < D / 32) sums[k1 % (D / 32)] -= __high2float(y);
     }
-  x.lo[0] = t == 0 ? term[0][0] : t == 1 ? term[0][1] : t == 2 ? term[1][0] : term[1][1];
-  x.lo[1] = t == 0 ? term[2][0] : t == 1 ? term[2][1] : 0u;
-  // of this lane's row, then of its columns
-  const float c = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 0.0f;
-  const float l = in ? lse * kLog2e : __uint_as_float(0x7f800000u);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    x.c[j] = __shfl_sync(0xffffffffu, c, (2 * t + j) * 4);
-    x.l[j] = __shfl_sync(0xffffffffu, l, (2 * t + j) * 4);
-    x.row[j] = __shfl_sync(0xffffffffu, i, (2 * t + j) * 4);
+  x.lo[lane] = make_uint2(t == 0 ? term[0][0] : t == 1 ? term[0][1] : t == 2 ? term[1][0] : term[1][1],
+                          t == 0 ? term[2][0] : t == 1 ? term[2][1] : 0u);
+  if (t == 0) {
+    // products come times 2^(14 - e - 24)
+    x.c[g] = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p10f : 0.0f;
+    x.l[g] = in ? lse * kLog2e : __uint_as_float(0x7f800000u);
+    x.row[g] = i;
   }
 }
 
-// A warp's run of items [at, last) of a segment with `chunks` chunks from chunk
-// `first` on: the cursor that fills the ring.
+// A warp's items, the cursor that fills its ring: (chunk, head) pairs, the
+// chunk's heads one after another, so that a chunk's slots and addresses are
+// found once and a cache row is read from end to end.
 template <int D>
 struct Ring {
-  int at, last, chunks;
-  int32_t slot;  // of position lane of the item to be copied next; -2: none
+  int left;         // items to be copied
+  int chunk, head;  // of the next one
+  int32_t slot;     // of position lane of the chunk behind the one at hand; -2: none
+  uint64_t src[D / 32], meta;  // where this lane's copies of the chunk's head 0 come from
+  unsigned size, have;         // bit u: the copy's position has a slot; positions that have one
   unsigned base;
 
-  __device__ __forceinline__ void load(const int32_t* row, int p0, int end) {
-    slot = -2;
-    if (at >= last) return;
-    const int pos = p0 + (at % chunks) * kChunk + static_cast<int>(threadIdx.x & 31);
-    if (pos < end) slot = __ldg(row + pos);
+  __device__ __forceinline__ void load(const int32_t* row, int at, int end) {
+    const int pos = at * kChunk + static_cast<int>(threadIdx.x & 31);
+    slot = pos < end ? __ldg(row + pos) : -2;
   }
-  __device__ __forceinline__ void copy(const SumArgs& a, int st, unsigned* there, bool count) {
-    using P = Pos<D>;
-    if (at < last) {
-      const int lane = threadIdx.x & 31;
-      const bool ok = slot >= 0 && slot < a.num_slots;
-      if (!ok && slot != -2 && count && at < chunks) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-      const unsigned have = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) there[st] = have;
-      const uint64_t mine = reinterpret_cast<uint64_t>(a.pool) +
-                            static_cast<uint64_t>(ok ? slot : 0) * static_cast<uint64_t>(a.slot_stride) +
-                            static_cast<uint32_t>(at / chunks) * kv4_head_bytes(D);
-      const unsigned to = base + st * (kChunk * P::kBytes);
-      // codes: D / 32 lanes a position; (step, lo) a lane each
-      constexpr int per = D / 32;
+  // Takes over the chunk whose slots were loaded last, and loads the next one's.
+  __device__ __forceinline__ void enter(const SumArgs& a, const int32_t* row, int at, int end, int h, bool count) {
+    constexpr int per = D / 32;
+    const int lane = threadIdx.x & 31;
+    const bool ok = slot >= 0 && slot < a.num_slots;
+    if (!ok && slot != -2 && count && h == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    have = __ballot_sync(0xffffffffu, ok);
+    const uint64_t mine = reinterpret_cast<uint64_t>(a.pool) +
+                          static_cast<uint64_t>(ok ? slot : 0) * static_cast<uint64_t>(a.slot_stride);
+    size = 0;
 #pragma unroll
-      for (int u = 0; u < per; ++u) {
-        const int pos = u * (32 / per) + lane / per, z = lane % per;
-        const uint64_t src = __shfl_sync(0xffffffffu, mine, pos) + z * 16;
-        put(to + pos * P::kBytes + z * 16, src, (have >> pos) & 1u ? 16u : 0u);
+    for (int u = 0; u < per; ++u) {
+      const int pos = u * (32 / per) + lane / per;
+      src[u] = __shfl_sync(0xffffffffu, mine, pos) + (lane % per) * 16;
+      size |= ((have >> pos) & 1u) << u;
+    }
+    meta = mine + D;
+    load(row, at + 1, end);
+  }
+  __device__ __forceinline__ void copy(const SumArgs& a, const int32_t* row, int first, int end, int h0, int heads, int st,
+                                       unsigned* there, bool count) {
+    using P = Pos<D>;
+    if (left > 0) {
+      constexpr int per = D / 32;
+      const int lane = threadIdx.x & 31;
+      const unsigned to = base + st * (kChunk * P::kBytes), off = static_cast<unsigned>(h0 + head) * kv4_head_bytes(D);
+      if (lane == 0) there[st] = have;
+#pragma unroll
+      for (int u = 0; u < per; ++u)
+        put(to + (u * (32 / per) + lane / per) * P::kBytes + (lane % per) * 16, src[u] + off, ((size >> u) & 1u) * 16u);
+      put(to + lane * P::kBytes + P::kCodes, meta + off, ((have >> lane) & 1u) * 16u);
+      --left;
+      if (++head == heads) {
+        head = 0;
+        ++chunk;
+        if (left > 0) enter(a, row, first + chunk, end, 0, count);
       }
-      put(to + lane * P::kBytes + P::kCodes, mine + D, ok ? 16u : 0u);
-      ++at;
     }
     cp_async_commit();
   }
@@ -228,10 +263,12 @@ struct Ring {
 
 // RT: row tiles of eight that a pass over the codes takes at most.
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 5 : 3) kv4_sums_kernel(const SumArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(const SumArgs a, int ctas) {
   pdl_enter();
+  constexpr int TILES = RT == 1 ? kTiles : kTiles4;
   extern __shared__ __align__(16) unsigned char sums_sm[];
-  SumShared<D>& sh = *reinterpret_cast<SumShared<D>*>(sums_sm);
+  using Shared = SumShared<D, TILES>;
+  Shared& sh = *reinterpret_cast<Shared*>(sums_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
   __shared__ int64_t s_warp[kWarps], s_off;
   __shared__ int s_b;
@@ -289,140 +326,169 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 5 : 3) kv4_sums_kernel(con
     const SumReq rq = sum_req(a, b);
     const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_ctx;
     const int tiles = (rq.rows * a.G + 7) / 8;
+    // a pass: `heads` heads, `rts` tiles of rows of each
+    const int rts = min(tiles, RT), heads = min(a.Hkv, TILES / rts);
+    const bool once = rts == tiles && heads == a.Hkv;  // then the tiles stay for the whole request
+    bool loaded = false;
 #pragma unroll 1
-    for (int all = sum_chunks(rq); chunk < all && left > 0;) {
+    for (const int all = sum_chunks(rq); chunk < all && left > 0;) {
       const int chunks = static_cast<int>(min(static_cast<int64_t>(min(all - chunk, kMaxChunks)), left));
-      const int p0 = chunk * kChunk, items = chunks * a.Hkv;
-      for (int i = lane; i < chunks * kChunk; i += 32) sh.sum[warp][i] = 0.0f;
-      __syncwarp();
-      const int from = static_cast<int>(static_cast<int64_t>(items) * warp / kWarps);
-      const int to = static_cast<int>(static_cast<int64_t>(items) * (warp + 1) / kWarps);
-#pragma unroll 1
-      for (int rt0 = 0; rt0 < tiles; rt0 += RT) {
-        Ring<D> ring;
-        ring.at = from, ring.last = to, ring.chunks = chunks;
-        ring.base = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp][0]));
-        ring.load(row, p0, rq.end);
-#pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) {
-          ring.copy(a, i, sh.there[warp], rt0 == 0);
-          ring.load(row, p0, rq.end);
-        }
-        QTile<D> q[RT];
-        int head = -1, st = 0;
-#pragma unroll 1
-        for (int item = from; item < to; ++item) {
-          const int h = item / chunks, ch = item - h * chunks;
-          if (h != head) {
-            head = h;
+      // this warp's items and their first chunk: the same in all passes but for a last one of fewer heads
 #pragma unroll
-            for (int x = 0; x < RT; ++x)
-              if (x == 0 || rt0 + x < tiles) load_tile<D>(a, b, h, (rt0 + x) * 8, rq, item == 0 && chunk == 0, q[x]);
+      for (int i = 0; i < kMine; ++i) sh.sum[warp][i][lane] = 0.0f;
+      const int from0 = chunks * warp / kWarps;  // the first chunk of any pass
+#pragma unroll 1
+      for (int h0 = 0; h0 < a.Hkv; h0 += heads)
+#pragma unroll 1
+        for (int rt0 = 0; rt0 < tiles; rt0 += RT) {
+          const int hs = min(heads, a.Hkv - h0), mine = min(rts, tiles - rt0), items = chunks * hs;
+          const int from = items * warp / kWarps, to = items * (warp + 1) / kWarps;
+          Ring<D> ring;
+          ring.left = to - from;
+          ring.chunk = from / hs, ring.head = from - ring.chunk * hs;
+          ring.base = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp][0]));
+          const bool count = rt0 == 0 && h0 == 0;
+          int ch = ring.chunk, h = ring.head;
+          if (ring.left > 0) {
+            ring.load(row, chunk + ch, rq.end);
+            ring.enter(a, row, chunk + ch, rq.end, h, count);
           }
-          __syncwarp();  // every lane has read the stage before
-          ring.copy(a, (st + kStages - 1) % kStages, sh.there[warp], rt0 == 0);
-          ring.load(row, p0, rq.end);
-          cp_async_wait<kStages - 1>();
-          __syncwarp();  // every lane's copies of this item have landed
-          const unsigned there = sh.there[warp][st];
-          const uint8_t* s8 = sh.ring[warp][st];
-          st = (st + 1) % kStages;
+#pragma unroll 1
+          for (int i = 0; i < kStages - 1; ++i) ring.copy(a, row, chunk, rq.end, h0, hs, i, sh.there[warp], count);
+          if (!loaded) {
+            if (!once) __syncthreads();  // every warp is done with the pass before
+#pragma unroll 1
+            for (int i = warp; i < hs * mine; i += kWarps) {
+              const int hh = i / mine, x = i - hh * mine;
+              load_tile<D>(a, b, h0 + hh, (rt0 + x) * 8, rq, h0 + hh == 0 && chunk == 0, sh.q[hh * rts + x]);
+            }
+            __syncthreads();
+            loaded = once;
+          }
+          int st = 0;
+          float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of positions 8 j + g of the chunk
+          auto flush = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] += __shfl_xor_sync(0xffffffffu, w[j], 1);
+              w[j] += __shfl_xor_sync(0xffffffffu, w[j], 2);
+            }
+            const float x = t == 0 ? w[0] : t == 1 ? w[1] : t == 2 ? w[2] : w[3];
+            if (spec_in(c - from0, kMine, a.stats)) sh.sum[warp][c - from0][8 * t + g] += x;
+            w[0] = w[1] = w[2] = w[3] = 0.0f;
+          };
+#pragma unroll 1
+          for (int item = from; item < to; ++item) {
+            __syncwarp();  // every lane has read the stage before
+            ring.copy(a, row, chunk, rq.end, h0, hs, (st + kStages - 1) % kStages, sh.there[warp], count);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();  // every lane's copies of this item have landed
+            const unsigned there = sh.there[warp][st];
+            const uint8_t* s8 = sh.ring[warp][st];
+            st = (st + 1) % kStages;
+            const QTile<D>* q = sh.q + h * rts;
 
-          // s[x][u][2 i + e]: position 16 u + 8 i + g, column 2 t + e of tile x
-          float s[RT][2][4], step[D / 32][4];
-          uint32_t lo_a[2][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint8_t* m8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + Pos<D>::kCodes;
-              uint32_t m[4] = {0, 0, 0, 0};
-              if (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4*>(m8);
-                m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(m8);
-                m[0] = v.x, m[1] = v.y;
-              }
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k) step[k][2 * u + i] = __low2float(u32_h2(m[k]));
-              const uint32_t l0 = __byte_perm(m[0], m[1], 0x7632), l1 = __byte_perm(m[2], m[3], 0x7632);
-              lo_a[u][i] = t & 1 ? l1 : l0;
-              lo_a[u][2 + i] = lo_a[u][i];
-            }
-#pragma unroll
-          for (int x = 0; x < RT; ++x)
-            if (x == 0 || rt0 + x < tiles) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                s[x][u][0] = s[x][u][1] = s[x][u][2] = s[x][u][3] = 0.0f;
-                mma16816(s[x][u], lo_a[u], q[x].lo[0], q[x].lo[1]);
-                // sums were held times 2^(14 - e - 5), products come times 2^(14 - e - 24)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[x][u][j] *= 0x1p-19f;
-              }
-            }
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t c[2][2][4];  // step of 16 channels, block of 16 positions, register
+            // s[x][u][2 i + e]: position 16 u + 8 i + g, column 2 t + e of tile x
+            float s[RT][2][4], step[D / 32][4];
+            uint32_t lo_a[2][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t w =
-                    *reinterpret_cast<const uint32_t*>(s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + k * 16 + t * 4);
-                c[0][u][i] = w & 0x000f000fu;
-                c[0][u][2 + i] = w & 0x00f000f0u;
-                c[1][u][i] = (w >> 8) & 0x000f000fu;
-                c[1][u][2 + i] = (w >> 8) & 0x00f000f0u;
-              }
-#pragma unroll
-            for (int x = 0; x < RT; ++x)
-              if (x == 0 || rt0 + x < tiles) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma16816(p, c[0][u], q[x].b[k][0][0], q[x].b[k][0][1]);
-                  mma16816(p, c[1][u], q[x].b[k][1][0], q[x].b[k][1][1]);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) s[x][u][j] = fmaf(step[k][2 * u + (j >> 1)], p[j], s[x][u][j]);
+                const uint8_t* m8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + Pos<D>::kCodes;
+                uint32_t m[4] = {0, 0, 0, 0};
+                if (D == 128) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(m8);
+                  m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(m8);
+                  m[0] = v.x, m[1] = v.y;
                 }
-              }
-          }
-          const int at0 = p0 + ch * kChunk;
-          const bool whole = there == 0xffffffffu && at0 + kChunk <= rq.start + 1;
-          float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of positions 8 j + g
 #pragma unroll
-          for (int x = 0; x < RT; ++x)
-            if (x == 0 || rt0 + x < tiles) {
+                for (int k = 0; k < D / 32; ++k) step[k][2 * u + i] = __low2float(u32_h2(m[k]));
+                const uint32_t l0 = __byte_perm(m[0], m[1], 0x7632), l1 = __byte_perm(m[2], m[3], 0x7632);
+                lo_a[u][i] = t & 1 ? l1 : l0;
+                lo_a[u][2 + i] = lo_a[u][i];
+              }
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t c[2][2][4];  // step of 16 channels, block of 16 positions, register
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  // c is the row's factor for q as it was: 2^10 makes up for the codes' and q's
-                  const float y = fast_exp2(fmaf(s[x][u][j] * 0x1p10f, q[x].c[j & 1], -q[x].l[j & 1]));
-                  const int at = 16 * u + 8 * (j >> 1) + g;
-                  const bool see = whole || (((there >> at) & 1u) != 0 && at0 + at <= rq.start + q[x].row[j & 1]);
-                  w[2 * u + (j >> 1)] += see ? y : 0.0f;
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t v =
+                      *reinterpret_cast<const uint32_t*>(s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + k * 16 + t * 4);
+                  c[0][u][i] = v & 0x000f000fu;
+                  c[0][u][2 + i] = v & 0x00f000f0u;
+                  c[1][u][i] = (v >> 8) & 0x000f000fu;
+                  c[1][u][2 + i] = (v >> 8) & 0x00f000f0u;
+                }
+#pragma unroll
+              for (int x = 0; x < RT; ++x)
+                if (x == 0 || x < mine) {
+                  const uint2 b0 = q[x].b[2 * k][lane], b1 = q[x].b[2 * k + 1][lane];
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    float p[4];
+                    mma16816_zero(p, c[0][u], b0.x, b0.y);
+                    mma16816(p, c[1][u], b1.x, b1.y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      s[x][u][j] = k == 0 ? step[k][2 * u + (j >> 1)] * p[j]
+                                          : fmaf(step[k][2 * u + (j >> 1)], p[j], s[x][u][j]);
+                  }
                 }
             }
+            const int at0 = (chunk + ch) * kChunk;
+            const bool whole = there == 0xffffffffu && at0 + kChunk <= rq.start + 1;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] += __shfl_xor_sync(0xffffffffu, w[j], 1);
-            w[j] += __shfl_xor_sync(0xffffffffu, w[j], 2);
+            for (int x = 0; x < RT; ++x)
+              if (x == 0 || x < mine) {
+                const uint2 lo = q[x].lo[lane];
+                const float2 c = *reinterpret_cast<const float2*>(q[x].c + 2 * t);
+                const float2 l = *reinterpret_cast<const float2*>(q[x].l + 2 * t);
+                // the groups' sums were held times 2^(14 - e - 5), the products 2^(14 - e - 24)
+                const float2 c_lo = make_float2(c.x * 0x1p-19f, c.y * 0x1p-19f);
+                const int2 i_of = *reinterpret_cast<const int2*>(q[x].row + 2 * t);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  float p[4];
+                  mma16816_zero(p, lo_a[u], lo.x, lo.y);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float y = fast_exp2(fmaf(p[j], j & 1 ? c_lo.y : c_lo.x,
+                                                   fmaf(s[x][u][j], j & 1 ? c.y : c.x, j & 1 ? -l.y : -l.x)));
+                    if (whole) {
+                      w[2 * u + (j >> 1)] += y;
+                    } else {
+                      const int at = 16 * u + 8 * (j >> 1) + g;
+                      if (((there >> at) & 1u) != 0 && at0 + at <= rq.start + (j & 1 ? i_of.y : i_of.x))
+                        w[2 * u + (j >> 1)] += y;
+                    }
+                  }
+                }
+              }
+            if (++h == hs) {
+              h = 0;
+              flush(ch);
+              ++ch;
+            }
           }
-          const float mine = t == 0 ? w[0] : t == 1 ? w[1] : t == 2 ? w[2] : w[3];
-          sh.sum[warp][ch * kChunk + 8 * t + g] += mine;
+          if (h != 0) flush(ch);
+          cp_async_wait<0>();
+          __syncwarp();
         }
-        cp_async_wait<0>();
-        __syncwarp();
-      }
       __syncthreads();
-      const int64_t at = static_cast<int64_t>(b) * a.max_ctx + p0;
-      for (int i = threadIdx.x; i < min(chunks * kChunk, rq.end - p0); i += kThreads) {
-        float x = sh.sum[0][i];
+      const int64_t at = static_cast<int64_t>(b) * a.max_ctx + static_cast<int64_t>(chunk) * kChunk;
+      for (int i = threadIdx.x; i < min(chunks * kChunk, rq.end - chunk * kChunk); i += kThreads) {
+        const int c = i / kChunk;
+        float x = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) x += sh.sum[w][i];
+        for (int w = 0; w < kWarps; ++w) {
+          const int k = c - chunks * w / kWarps;  // chunks of a warp: from its first on, in all passes
+          if (k >= 0 && k < kMine) x += sh.sum[w][k][i % kChunk];
+        }
         a.out[at + i] = a.prev ? a.prev[at + i] + x : x;
       }
       __syncthreads();
@@ -435,9 +501,9 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 5 : 3) kv4_sums_kernel(con
 template <int D, int RT>
 int launch_sums(const SumArgs& a, int sms, cudaStream_t s) {
   constexpr auto kernel = kv4_sums_kernel<D, RT>;
-  constexpr size_t smem = sizeof(SumShared<D>);
+  constexpr size_t smem = sizeof(SumShared<D, RT == 1 ? kTiles : kTiles4>);
   if (!allow_smem<kernel>(smem)) return SPEC_ERR_CUDA;
-  const int ctas = sms * (RT == 1 ? 5 : 3);
+  const int ctas = sms * (RT == 1 ? 2 : 1);
   launch_k(kernel, static_cast<unsigned>(ctas), kThreads, smem, s, a, ctas);
   return launch_status();
 }
