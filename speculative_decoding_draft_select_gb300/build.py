@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libspecdec.so")
 DEBUG_OUT_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB = os.path.join(PKG, "libspecdec_debug.so")
 SOURCES = ["draft.cu", "tree.cu", "verify.cu", "chain.cu", "compact.cu", "tli.cu", "head.cu", "filter.cu",
-           "kv4.cu", "kv4_attention.cu", "kv4_tree.cu", "kv4_sums.cu", "evict.cu", "adjust.cu"]
+           "kv4.cu", "kv4_attention.cu", "kv4_tree.cu", "kv4_sums.cu", "kv4_sums_rows.cu", "evict.cu", "adjust.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-I", INCLUDE, "-I", CSRC]

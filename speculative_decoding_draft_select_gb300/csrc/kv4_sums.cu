@@ -26,7 +26,7 @@
 // turns its head's rows of q into fragments in registers once per run, and
 // fills its own ring of asynchronous copies.  The warps' sums meet in shared
 // memory and are added in the warps' order: no atomics.
-#include "kv4_attn.cuh"
+#include "kv4_sums.cuh"
 
 namespace specdec {
 namespace {
@@ -35,29 +35,13 @@ constexpr int kChunk = 32;      // positions of an item
 constexpr int kMaxChunks = 32;  // chunks of a CTA's segment at most
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMine = kMaxChunks / kWarps + 2;  // chunks that a warp has a part of
-constexpr int kStages = 3;
-// Tiles of eight query rows in shared memory: one a head where they fit, so
-// that a request's stay; more heads or rows take several passes over the codes.
-constexpr int kTiles = 8;       // with one tile a head
-constexpr int kTiles4 = 32;     // with up to four
-
-struct SumArgs {
-  const uint16_t* q;
-  int64_t q_stride;
-  const float* lse;
-  const int32_t* path;
-  const int32_t* accepted;
-  int B, N, Hq, Hkv, G;
-  uint64_t g_inv;  // ceil(2^40 / G)
-  const uint8_t* pool;
-  int64_t num_slots, slot_stride;
-  const int32_t* seq_lens;
-  const int32_t* table;
-  int64_t max_ctx;
-  float scale_log2;
-  const float* prev;
-  float* out;
-  int32_t* stats;
+constexpr int kStages = 2;
+// Tiles of eight query rows in shared memory: all of a request's where they
+// fit; more heads or rows take several passes, the latter over the same codes.
+template <int RT>
+struct SumCfg {
+  static constexpr int kTiles = 8 * RT;
+  static constexpr int kCtas = RT == 1 ? 3 : 2;  // of an SM
 };
 
 // D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
@@ -76,20 +60,18 @@ __device__ __forceinline__ void mma16816_zero(float* d, const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-struct SumReq {
-  int start, rows, end;  // row i sees positions p <= start + i; end = start + rows
-  bool bad;
-};
-__device__ __forceinline__ SumReq sum_req(const SumArgs& a, int b) {
-  SumReq r;
-  r.start = __ldg(a.seq_lens + b);
-  r.rows = a.accepted ? __ldg(a.accepted + b) + 1 : a.N;
-  r.bad = r.rows < 1 || r.rows > a.N || r.start < 0 || static_cast<int64_t>(r.start) + r.rows > a.max_ctx;
-  if (r.bad) r.start = r.rows = 0;
-  r.end = r.start + r.rows;
-  return r;
-}
 __device__ __forceinline__ int sum_chunks(const SumReq& r) { return (r.end + kChunk - 1) / kChunk; }
+__device__ __forceinline__ int sum_tiles(const SumArgs& a, const SumReq& r) { return (r.rows * a.G + 7) / 8; }
+// What a chunk costs: copying and unpacking its codes about what a row tile does.
+__device__ __forceinline__ int sum_cost(const SumArgs& a, const SumReq& r) { return sum_tiles(a, r) + 1; }
+__device__ __forceinline__ int64_t sum_units(const SumArgs& a, const SumReq& r) {
+  return static_cast<int64_t>(sum_chunks(r)) * sum_cost(a, r);
+}
+// Chunks of this cost that begin before `units` of their request's.
+__device__ __forceinline__ int chunks_before(int64_t units, int cost) {
+  const int64_t x = units + cost - 1;
+  return static_cast<int>(x <= 0xffffffffll ? static_cast<uint32_t>(x) / static_cast<uint32_t>(cost) : x / cost);
+}
 
 // Shared memory of a position in a stage: K's codes, then K's (step, lo); 20
 // words (D = 64: 12) apart, which makes all reads free of bank conflicts.
@@ -263,20 +245,21 @@ struct Ring {
 
 // RT: row tiles of eight that a pass over the codes takes at most.
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(const SumArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(const SumArgs a, int ctas) {
   pdl_enter();
-  constexpr int TILES = RT == 1 ? kTiles : kTiles4;
+  constexpr int TILES = SumCfg<RT>::kTiles;
   extern __shared__ __align__(16) unsigned char sums_sm[];
   using Shared = SumShared<D, TILES>;
   Shared& sh = *reinterpret_cast<Shared*>(sums_sm);
   if (!spec_smem_ok(sizeof(sh), a.stats)) return;
-  __shared__ int64_t s_warp[kWarps], s_off;
+  __shared__ int64_t s_warp[kWarps], s_pre;
   __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
 
-  // this CTA's stretch of the line of all requests' chunks
-  int64_t left;
-  int b, chunk;
+  // this CTA's stretch [lo, hi) of the line of all requests' chunks, by their
+  // cost: the chunks that begin in it.  pre: where request b begins
+  int64_t lo, hi, pre;
+  int b;
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
@@ -284,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
 #pragma unroll 1
     for (int i = b0; i < b1; ++i) {
       const SumReq r = sum_req(a, i);
-      mine += sum_chunks(r);
-      if (r.bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      mine += sum_units(a, r);
+      if (r.bad && a.count_bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -295,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int64_t pre = incl - mine, total = 0;
+    int64_t total = 0;
+    pre = incl - mine;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) pre += s_warp[i];
@@ -303,36 +287,40 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
     }
     const int64_t n = min(static_cast<int64_t>(ctas), total), cta = blockIdx.x;
     if (cta >= n) return;
-    const int64_t lo = cta * total / n;
-    left = (cta + 1) * total / n - lo;
+    lo = cta * total / n;
+    hi = (cta + 1) * total / n;
     if (lo >= pre && lo < pre + mine) {
       int i = b0;
 #pragma unroll 1
       for (;; ++i) {
-        const int u = sum_chunks(sum_req(a, i));
+        const int64_t u = sum_units(a, sum_req(a, i));
         if (lo < pre + u) break;
         pre += u;
       }
-      s_off = lo - pre;
+      s_pre = pre;
       s_b = i;
     }
     __syncthreads();
     b = s_b;
-    chunk = static_cast<int>(s_off);
+    pre = s_pre;
   }
 
 #pragma unroll 1
-  for (; left > 0; ++b, chunk = 0) {
+  for (; pre < hi; ++b) {
     const SumReq rq = sum_req(a, b);
     const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_ctx;
-    const int tiles = (rq.rows * a.G + 7) / 8;
+    const int tiles = sum_tiles(a, rq), cost = sum_cost(a, rq);
+    const int64_t units = sum_units(a, rq);
+    int chunk = pre < lo ? chunks_before(lo - pre, cost) : 0;
+    const int all = pre + units <= hi ? sum_chunks(rq) : chunks_before(hi - pre, cost);
+    pre += units;
     // a pass: `heads` heads, `rts` tiles of rows of each
-    const int rts = min(tiles, RT), heads = min(a.Hkv, TILES / rts);
+    const int rts = min(tiles, RT), heads = min(a.Hkv, TILES / max(rts, 1));
     const bool once = rts == tiles && heads == a.Hkv;  // then the tiles stay for the whole request
     bool loaded = false;
 #pragma unroll 1
-    for (const int all = sum_chunks(rq); chunk < all && left > 0;) {
-      const int chunks = static_cast<int>(min(static_cast<int64_t>(min(all - chunk, kMaxChunks)), left));
+    while (chunk < all) {
+      const int chunks = min(all - chunk, kMaxChunks);
       // this warp's items and their first chunk: the same in all passes but for a last one of fewer heads
 #pragma unroll
       for (int i = 0; i < kMine; ++i) sh.sum[warp][i][lane] = 0.0f;
@@ -389,36 +377,18 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
             const QTile<D>* q = sh.q + h * rts;
 
             // s[x][u][2 i + e]: position 16 u + 8 i + g, column 2 t + e of tile x
-            float s[RT][2][4], step[D / 32][4];
-            uint32_t lo_a[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint8_t* m8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + Pos<D>::kCodes;
-                uint32_t m[4] = {0, 0, 0, 0};
-                if (D == 128) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(m8);
-                  m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
-                } else {
-                  const uint2 v = *reinterpret_cast<const uint2*>(m8);
-                  m[0] = v.x, m[1] = v.y;
-                }
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) step[k][2 * u + i] = __low2float(u32_h2(m[k]));
-                const uint32_t l0 = __byte_perm(m[0], m[1], 0x7632), l1 = __byte_perm(m[2], m[3], 0x7632);
-                lo_a[u][i] = t & 1 ? l1 : l0;
-                lo_a[u][2 + i] = lo_a[u][i];
-              }
+            float s[RT][2][4];
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
               uint32_t c[2][2][4];  // step of 16 channels, block of 16 positions, register
+              float step[4];        // of positions 8 j + g
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint32_t v =
-                      *reinterpret_cast<const uint32_t*>(s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + k * 16 + t * 4);
+                  const uint8_t* p8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes;
+                  const uint32_t v = *reinterpret_cast<const uint32_t*>(p8 + k * 16 + t * 4);
+                  step[2 * u + i] = __half2float(*reinterpret_cast<const __half*>(p8 + Pos<D>::kCodes + k * 4));
                   c[0][u][i] = v & 0x000f000fu;
                   c[0][u][2 + i] = v & 0x00f000f0u;
                   c[1][u][i] = (v >> 8) & 0x000f000fu;
@@ -435,11 +405,22 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
                     mma16816(p, c[1][u], b1.x, b1.y);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                      s[x][u][j] = k == 0 ? step[k][2 * u + (j >> 1)] * p[j]
-                                          : fmaf(step[k][2 * u + (j >> 1)], p[j], s[x][u][j]);
+                      s[x][u][j] = k == 0 ? step[2 * u + (j >> 1)] * p[j]
+                                          : fmaf(step[2 * u + (j >> 1)], p[j], s[x][u][j]);
                   }
                 }
             }
+            // lo of two groups: those of this lane's columns of A
+            uint32_t lo_a[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint8_t* m8 = s8 + (16 * u + 8 * i + g) * Pos<D>::kBytes + Pos<D>::kCodes;
+                uint2 m = make_uint2(0, 0);
+                if (D == 128 || (t & 1) == 0) m = *reinterpret_cast<const uint2*>(m8 + 8 * (t & 1));
+                lo_a[u][i] = lo_a[u][2 + i] = __byte_perm(m.x, m.y, 0x7632);
+              }
             const int at0 = (chunk + ch) * kChunk;
             const bool whole = there == 0xffffffffu && at0 + kChunk <= rq.start + 1;
 #pragma unroll
@@ -493,17 +474,18 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) kv4_sums_kernel(con
       }
       __syncthreads();
       chunk += chunks;
-      left -= chunks;
     }
   }
 }
 
+constexpr int kManyRows = 32;
+
 template <int D, int RT>
 int launch_sums(const SumArgs& a, int sms, cudaStream_t s) {
   constexpr auto kernel = kv4_sums_kernel<D, RT>;
-  constexpr size_t smem = sizeof(SumShared<D, RT == 1 ? kTiles : kTiles4>);
+  constexpr size_t smem = sizeof(SumShared<D, SumCfg<RT>::kTiles>);
   if (!allow_smem<kernel>(smem)) return SPEC_ERR_CUDA;
-  const int ctas = sms * (RT == 1 ? 2 : 1);
+  const int ctas = sms * SumCfg<RT>::kCtas;
   launch_k(kernel, static_cast<unsigned>(ctas), kThreads, smem, s, a, ctas);
   return launch_status();
 }
@@ -539,11 +521,23 @@ extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const 
     return SPEC_ERR_CUDA;
   }
   const int G = Hq / Hkv;
-  const SumArgs a{static_cast<const uint16_t*>(q), q_stride, lse, accept_path_or_null, accept_length_or_null, B, N, Hq,
-                  Hkv, G, ((1ull << 40) + G - 1) / G, static_cast<const uint8_t*>(pool), num_slots, slot_stride,
-                  seq_lens, req_to_token, max_ctx, scale * kLog2e, prev_or_null, out, stats_or_null};
+  SumArgs a{static_cast<const uint16_t*>(q), q_stride, lse, accept_path_or_null, accept_length_or_null, B, N, Hq,
+            Hkv, G, ((1ull << 40) + G - 1) / G, static_cast<const uint8_t*>(pool), num_slots, slot_stride,
+            seq_lens, req_to_token, max_ctx, scale * kLog2e, prev_or_null, out, stats_or_null, 0, INT32_MAX, true};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool one = static_cast<int64_t>(N) * G <= 8;
-  if (D == 128) return one ? launch_sums<128, 1>(a, sms, s) : launch_sums<128, 4>(a, sms, s);
-  return one ? launch_sums<64, 1>(a, sms, s) : launch_sums<64, 4>(a, sms, s);
+  const int64_t rows = static_cast<int64_t>(N) * G;
+  // the host knows how many rows there may be, the device how many there are:
+  // with accepted lengths each request goes to the kernel that suits it
+  if (rows > kManyRows) {
+    if (!accept_length_or_null) return launch_sums_rows(a, D, sms, s);
+    a.above = kManyRows;
+    const int e = launch_sums_rows(a, D, sms, s);
+    if (e != SPEC_OK) return e;
+    a.above = 0;
+    a.upto = kManyRows;
+    a.count_bad = false;
+  }
+  const bool one = rows <= 8;
+  if (D == 128) return one ? launch_sums<128, 1>(a, sms, s) : launch_sums<128, 2>(a, sms, s);
+  return one ? launch_sums<64, 1>(a, sms, s) : launch_sums<64, 2>(a, sms, s);
 }

@@ -1,0 +1,554 @@
+// Attention weights summed per cached position for many query rows (the last
+// tokens of prompts), on the fifth-generation tensor cores.  The mathematics is
+// that of kv4_sums.cu; here a step is 128 positions of one KV head and up to 128
+// of its query rows, and S^T = K Q^T lies in tensor memory with a position per
+// lane, so that a thread sums its position's weights over the columns in a
+// register.
+//
+// K = lo + c step as exact fp16 operands: c step = hi + rem, the product rounded
+// to fp16 and what it lost (a multiple of 2^-24 like step itself, so exact), and
+// one step of 16 more columns that multiply the groups' lo with the groups' sums
+// of q, three fp16 terms of each (2^-33).  All products of a step accumulate in
+// fp32 in the same columns: 2 D + 16 instead of D products an element, with
+// scores as good as fp32 sums.
+//
+// Roles of a CTA:
+//   warps 0 .. 7    weights: two groups of four warps take turns, a buffer of
+//       tensor memory each; a thread's position is its lane.
+//   warps 8 .. 15   unpack the cache, a position a thread: two groups again take
+//       turns, each with its next step's codes on their way to registers and the
+//       slots of the one behind; and the query rows of the next KV head.
+//   warp 16         issues the matrix instructions.
+// Steps go head by head over a segment of up to kSegTiles tiles of a request, so
+// that a head's rows are unpacked once a segment; the segment's sums stay in
+// shared memory until its last head.  Where there are few tiles, the CTAs of a
+// cluster share a segment's steps and add their sums through distributed shared
+// memory, in rank order.  Every wait is bounded; a wait that runs out is counted
+// in SPEC_STAT_WAIT_TIMEOUT and the CTA goes on without working (results void).
+#include "kv4_sums.cuh"
+#include "tcgen05.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kTile = 128;       // positions of a step
+constexpr int kCols = 128;       // query rows of a step at most
+constexpr int kSegTiles = 12;    // tiles of a segment at most
+constexpr int kGroupWarps = 4, kUnpackWarp = 8, kIssueWarp = 16;
+constexpr int kThreads = 17 * 32;
+
+template <int D>
+struct RowsCfg {
+  static constexpr int kSlab = kTile * 128;            // bytes: 128 rows of 64 elements
+  static constexpr int kOperand = D / 64 * kSlab;
+  static constexpr int kExtra = kTile * 32;            // 128 rows of 16 elements, no swizzle
+  static constexpr int kStage = 2 * kOperand + kExtra; // hi, rem, lo
+  static constexpr int kQ = kOperand + kExtra;
+};
+template <int D>
+struct RowsShared {
+  uint8_t k[2][RowsCfg<D>::kStage];  // 1024-byte aligned
+  uint8_t q[2][RowsCfg<D>::kQ];
+  float sum[2][kSegTiles * kTile];   // of the two groups
+  float c[2][kCols], nl[2][kCols];   // factor of a row's products, -lse in units of log2
+  int row[2][kCols];                 // row of the path
+};
+
+// Descriptor of an operand without swizzle, K-major: 8 rows of 16 bytes are a
+// block of 128 bytes; `leading` bytes between blocks along K, 128 along rows.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr, uint32_t leading) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((leading & 0x3FFFFu) >> 4) << 16 |
+         static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
+// A cluster's stretch of the line of all requests' tiles, segment by segment,
+// and this CTA's share of a segment's steps: every role walks it by itself.
+struct Segments {
+  int64_t lo, hi, pre;  // tiles; where request b begins
+  int b, tile;          // next
+  int t0, tiles, items, from, to;  // of the segment: steps [from, to) of items x tiles
+  SumReq rq;
+  int blocks;                      // of a head's rows
+
+  __device__ __forceinline__ static int tiles_of(const SumReq& r) { return (r.end + kTile - 1) / kTile; }
+  __device__ __forceinline__ bool next(const SumArgs& a, int rank, int ranks) {
+#pragma unroll 1
+    for (; pre + tile < hi; ++b, tile = 0) {
+      rq = sum_req(a, b);
+      const int all = tiles_of(rq);
+      if (tile < all) {
+        t0 = tile;
+        tiles = static_cast<int>(min(static_cast<int64_t>(min(all - tile, kSegTiles)), hi - pre - tile));
+        tile += tiles;
+        blocks = (rq.rows * a.G + kCols - 1) / kCols;
+        items = a.Hkv * blocks;
+        const int64_t steps = static_cast<int64_t>(items) * tiles;
+        from = static_cast<int>(steps * rank / ranks);
+        to = static_cast<int>(steps * (rank + 1) / ranks);
+        return true;
+      }
+      pre += all;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
+  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
+  unsigned r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put_unit(uint8_t* slab, int r, int u, const uint32_t* v) {
+  *reinterpret_cast<uint4*>(slab + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Query rows [r0, r0 + n) of KV head h as fp16 rows of buffer qb: eight lanes a
+// row, D / 8 channels a lane.
+template <int D>
+__device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, int qb, int b, int h, int r0, int n,
+                                          const SumReq& rq, bool count, int uw) {
+  constexpr int per = D / 8, vecs = per / 8;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+#pragma unroll 4
+  for (int c = uw * 4 + (lane >> 3); c < n; c += 16) {
+    const int r = r0 + c, i = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+    bool in = i < rq.rows;
+    int node = in ? i : 0;
+    if (in && a.path) {
+      node = __ldg(a.path + static_cast<int64_t>(b) * a.N + i);
+      in = node >= 0 && node < a.N;
+      if (!in && count && sub == 0 && r == i * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      if (!in) node = 0;
+    }
+    const int64_t at = static_cast<int64_t>(b) * a.N + node;
+    const int head = h * a.G + r - i * a.G;
+    const float lse = in ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
+    uint4 v[vecs];
+#pragma unroll
+    for (int z = 0; z < vecs; ++z) {
+      v[z] = make_uint4(0, 0, 0, 0);
+      if (in) v[z] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + sub * per) + z);
+    }
+    in = in && isfinite(lse);
+    uint32_t big = 0;
+#pragma unroll
+    for (int z = 0; z < vecs; ++z) {
+      if (!in) v[z] = make_uint4(0, 0, 0, 0);
+      big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[z].x & 0x7fff7fffu, v[z].y & 0x7fff7fffu),
+                                   __vmaxu2(v[z].z & 0x7fff7fffu, v[z].w & 0x7fff7fffu)));
+    }
+    const unsigned eight = 0xffu << (lane & 24);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(eight, big, o));
+    const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
+    // 2^e <= max < 2^(e + 1): the largest becomes [2^9, 2^10), a group's sum at most 2^15
+    const int e = bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -117);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
+    float s = 0.0f;
+#pragma unroll
+    for (int z = 0; z < vecs; ++z) {
+      const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float y0 = bf16_lo(w[j]) * up, y1 = bf16_hi(w[j]) * up;
+        y[j] = h2_u32(__floats2half2_rn(y0, y1));
+        s += y0 + y1;
+      }
+      const int ch = sub * per + 8 * z;
+      put_unit(sh.q[qb] + ch / 64 * RowsCfg<D>::kSlab, c, ch % 64 / 8, y);
+    }
+    // the group's sum, and its three terms, in every lane of the group
+#pragma unroll
+    for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(eight, s, o);
+    float term[3];
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+      term[z] = __half2float(__float2half_rn(s));
+      s -= term[z];
+    }
+    // 16 columns: term z of group g is column 4 z + g (D = 64: groups 2 and 3 are zeros)
+    uint32_t col[8];
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+#pragma unroll
+      for (int g = 0; g < 4; g += 2) {
+        float x[2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+          x[o] = g + o < D / 32 ? __shfl_sync(eight, term[z], (lane & 24) + (g + o) % (D / 32) * (256 / D)) : 0.0f;
+        col[2 * z + g / 2] = h2_u32(__floats2half2_rn(x[0], x[1]));
+      }
+    col[6] = col[7] = 0;
+    if (sub < 2)
+      *reinterpret_cast<uint4*>(sh.q[qb] + RowsCfg<D>::kOperand + sub * (kTile * 16) + c * 16) =
+          sub == 0 ? make_uint4(col[0], col[1], col[2], col[3]) : make_uint4(col[4], col[5], col[6], col[7]);
+    if (sub == 0) {
+      sh.c[qb][c] = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p-9f : 0.0f;
+      sh.nl[qb][c] = in ? -lse * kLog2e : neg_inf();
+      sh.row[qb][c] = i;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArgs a, int clusters, int ranks) {
+  pdl_enter();
+  using C = RowsCfg<D>;
+  using Shared = RowsShared<D>;
+  extern __shared__ uint8_t rows_sm[];
+  Shared& sh = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(rows_sm) + 1023) & ~uintptr_t(1023));
+  if (!spec_smem_ok((reinterpret_cast<uint8_t*>(&sh) - rows_sm) + sizeof(Shared), a.stats)) return;
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], s_full[2], s_empty[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_b;
+  __shared__ int64_t s_warp[kThreads / 32], s_pre;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = ranks > 1 ? static_cast<int>(cluster_rank()) : 0, cluster = blockIdx.x / ranks;
+
+  // the cluster's stretch of the line
+  Segments seg;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+#pragma unroll 1
+    for (int i = b0; i < b1; ++i) {
+      const SumReq r = sum_req(a, i);
+      mine += Segments::tiles_of(r);
+      if (r.bad && a.count_bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, pre = incl - mine;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) pre += s_warp[i];
+      total += s_warp[i];
+    }
+    const int64_t n = min(static_cast<int64_t>(clusters), total);
+    if (cluster >= n) return;  // the whole cluster
+    seg.lo = cluster * total / n;
+    seg.hi = (cluster + 1) * total / n;
+    if (seg.lo >= pre && seg.lo < pre + mine) {
+      int i = b0;
+#pragma unroll 1
+      for (;; ++i) {
+        const int u = Segments::tiles_of(sum_req(a, i));
+        if (seg.lo < pre + u) break;
+        pre += u;
+      }
+      s_pre = pre;
+      s_b = i;
+    }
+    if (tid == 0) {
+      for (int i = 0; i < 2; ++i) {
+        tc::bar_init(&q_full[i], 4);
+        tc::bar_init(&q_empty[i], 1 + 2 * kGroupWarps);
+        tc::bar_init(&k_full[i], 4);
+        tc::bar_init(&k_empty[i], 1);
+        tc::bar_init(&s_full[i], 1);
+        tc::bar_init(&s_empty[i], kGroupWarps);
+      }
+      tc::bar_init(&drain, 1);
+      s_abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tc::alloc<2 * kCols>(&s_tmem);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    seg.b = s_b;
+    seg.pre = s_pre;
+    seg.tile = static_cast<int>(seg.lo - seg.pre);
+  }
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+  unsigned j = 0, item_no = 0;  // steps and items so far: which buffer, which phase
+
+  if (warp >= kUnpackWarp && warp < kIssueWarp) {
+    // ------------------------------------------------------------- unpack
+    const int u = (warp - kUnpackWarp) >> 2, uw = warp & 3, p = uw * 32 + lane;
+    constexpr int vecs = D / 32;
+    uint4 code[vecs], code2[vecs];
+    uint32_t meta[vecs], meta2[vecs];
+    int32_t slot;  // of the group's step behind the one whose codes are on their way
+#pragma unroll 1
+    while (seg.next(a, rank, ranks)) {
+      const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
+      auto load_slot = [&](int s) {  // -2: no position
+        slot = -2;
+        if (s >= seg.to) return;
+        const int pos = (seg.t0 + s % seg.tiles) * kTile + p;
+        if (pos < seg.rq.end) slot = __ldg(row + pos);
+      };
+      auto load = [&](int s, uint4* code, uint32_t* meta) {
+#pragma unroll
+        for (int z = 0; z < vecs; ++z) code[z] = make_uint4(0, 0, 0, 0), meta[z] = 0;
+        if (slot == -2) return;
+        const int item = s / seg.tiles;
+        if (slot < 0 || slot >= a.num_slots) {
+          if (item == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+          return;
+        }
+        const uint8_t* src = a.pool + slot * a.slot_stride + item / seg.blocks * kv4_head_bytes(D);
+#pragma unroll
+        for (int z = 0; z < vecs; ++z) code[z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
+        if (D == 128) {
+          const uint4 m = __ldg(reinterpret_cast<const uint4*>(src + D));
+          meta[0] = m.x, meta[1] = m.y, meta[vecs - 2] = m.z, meta[vecs - 1] = m.w;
+        } else {
+          const uint2 m = __ldg(reinterpret_cast<const uint2*>(src + D));
+          meta[0] = m.x, meta[1] = m.y;
+        }
+      };
+      const int mine = seg.from + static_cast<int>((j ^ u) & 1);  // the group's first step
+      load_slot(mine);
+      load(mine, code2, meta2);
+      load_slot(mine + 2);
+      int held = -1;
+#pragma unroll 1
+      for (int s = seg.from; s < seg.to; ++s, ++j) {
+        const int item = s / seg.tiles, h = item / seg.blocks, block = item - h * seg.blocks, st = j & 1;
+        const bool first = item != held;
+        if (first) held = item, ++item_no;
+        if (st != u) continue;
+#pragma unroll
+        for (int z = 0; z < vecs; ++z) code[z] = code2[z], meta[z] = meta2[z];
+        load(s + 2, code2, meta2);
+        load_slot(s + 4);
+        if (first) {
+          // the group of a head's first step unpacks its rows
+          const unsigned i = item_no - 1;
+          const int qb = i & 1;
+          if (ok && i >= 2) ok = wait_warp(&q_empty[qb], ((i >> 1) - 1) & 1, &s_abort);
+          if (ok) {
+            const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+            load_rows<D>(a, sh, qb, seg.b, h, block * kCols, n, seg.rq,
+                         h == 0 && seg.t0 == 0 && s % seg.tiles == 0, uw);
+            tc::fence_smem();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&q_full[qb]);
+          }
+        }
+        if (ok && j >= 2) ok = wait_warp(&k_empty[st], ((j >> 1) - 1) & 1, &s_abort);
+        if (!ok) continue;
+        uint8_t* hi8 = sh.k[st];
+        uint8_t* rem8 = hi8 + C::kOperand;
+#pragma unroll
+        for (int z = 0; z < vecs; ++z) {
+          const uint32_t w[4] = {code[z].x, code[z].y, code[z].z, code[z].w};
+          const __half2 step = u32_h2(__byte_perm(meta[z], 0, 0x1010));
+          const __half2 k1024 = u32_h2(0xe400e400u), k16 = u32_h2(0x2c002c00u), k64 = u32_h2(0xd400d400u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t hi[4], rem[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t y = x & 2 ? w[q] >> 8 : w[q];
+              const __half2 c = x & 1 ? __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), k16, k64)
+                                      : __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), k1024);
+              const __half2 v = __hmul2_rn(c, step);
+              hi[x] = h2_u32(v);
+              rem[x] = h2_u32(__hfma2(c, step, __hneg2(v)));
+            }
+            const int slab = (z >> 1) * C::kSlab, unit = (z & 1) * 4 + q;
+            put_unit(hi8 + slab, p, unit, hi);
+            put_unit(rem8 + slab, p, unit, rem);
+          }
+        }
+        // lo of the groups, three times: columns 0..3, 4..7, 8..11
+        uint32_t lo[2];
+        lo[0] = __byte_perm(meta[0], meta[1], 0x7632);
+        lo[1] = vecs == 4 ? __byte_perm(meta[vecs - 2], meta[vecs - 1], 0x7632) : 0u;
+        uint8_t* extra = rem8 + C::kOperand;
+        *reinterpret_cast<uint4*>(extra + p * 16) = make_uint4(lo[0], lo[1], lo[0], lo[1]);
+        *reinterpret_cast<uint4*>(extra + kTile * 16 + p * 16) = make_uint4(lo[0], lo[1], 0u, 0u);
+        tc::fence_smem();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&k_full[st]);
+      }
+      if (ranks > 1) {
+        __syncwarp();
+        cluster_barrier();
+        cluster_barrier();
+      }
+    }
+  } else if (warp == kIssueWarp) {
+    // -------------------------------------------------------------- issue
+#pragma unroll 1
+    while (seg.next(a, rank, ranks)) {
+      int held = -1;
+#pragma unroll 1
+      for (int s = seg.from; s < seg.to; ++s, ++j) {
+        const int item = s / seg.tiles, st = j & 1;
+        if (item != held) {
+          held = item;
+          if (ok) ok = wait_warp(&q_full[item_no & 1], (item_no >> 1) & 1, &s_abort);
+          ++item_no;
+        }
+        const int qb = (item_no - 1) & 1;
+        if (ok) ok = wait_warp(&k_full[st], (j >> 1) & 1, &s_abort);
+        if (ok && j >= 2) ok = wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
+        if (ok && lane == 0) {
+          tc::fence_after();
+          const int block = item % seg.blocks;
+          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+          const uint32_t id = tc::idesc_f16(n, false), d = tmem + st * kCols;
+          const uint32_t k8 = tc::smem_addr(sh.k[st]), q8 = tc::smem_addr(sh.q[qb]);
+          const uint64_t qd = tc::desc(q8, 0);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint64_t kd = tc::desc(k8 + part * C::kOperand, 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4;
+              tc::mma_ss(d, kd + off, qd + off, id, part + kk != 0 ? 1u : 0u);
+            }
+          }
+          tc::mma_ss(d, desc_plain(k8 + 2 * C::kOperand, kTile * 16), desc_plain(q8 + C::kOperand, kTile * 16), id, 1u);
+          tc::commit(&s_full[st]);
+          tc::commit(&k_empty[st]);
+          if (s + 1 == seg.to || (s + 1) / seg.tiles != item) tc::commit(&q_empty[qb]);
+        }
+        __syncwarp();
+      }
+      if (ranks > 1) {
+        __syncwarp();
+        cluster_barrier();
+        cluster_barrier();
+      }
+    }
+    if (lane == 0) {
+      // nothing in flight when tensor memory is freed
+      tc::commit(&drain);
+      const long long t0 = clock64();
+      while (!tc::bar_test(&drain, 0) && clock64() - t0 < tc::kWaitCycles) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ weights
+    const int e = warp >> 2, p = (warp & 3) * 32 + lane;
+    const uint32_t col0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + e * kCols;
+#pragma unroll 1
+    while (seg.next(a, rank, ranks)) {
+      const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
+      for (int i = p; i < seg.tiles * kTile; i += kTile) sh.sum[e][i] = 0.0f;
+      int held = -1;
+#pragma unroll 1
+      for (int s = seg.from; s < seg.to; ++s, ++j) {
+        const int item = s / seg.tiles, tile = s - item * seg.tiles;
+        if (item != held) {
+          held = item;
+          if (ok) ok = wait_warp(&q_full[item_no & 1], (item_no >> 1) & 1, &s_abort);
+          ++item_no;
+        }
+        const int qb = (item_no - 1) & 1;
+        if (static_cast<int>(j & 1) == e && ok) {
+          const int pos = (seg.t0 + tile) * kTile + p, block = item % seg.blocks;
+          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+          const int32_t slot = pos < seg.rq.end ? __ldg(row + pos) : -1;
+          ok = wait_warp(&s_full[e], (j >> 1) & 1, &s_abort);
+          if (ok) {
+            tc::fence_after();
+            const bool whole = (seg.t0 + tile + 1) * kTile <= seg.rq.start + 1;
+            float2 acc[2] = {splat(0.0f), splat(0.0f)};
+#pragma unroll 1
+            for (int w = 0; w < n; w += 32) {
+              uint32_t x[32];
+              tc::ld32(col0 + w, x);
+              tc::wait_ld32(x);
+              const float4* c4 = reinterpret_cast<const float4*>(sh.c[qb] + w);
+              const float4* l4 = reinterpret_cast<const float4*>(sh.nl[qb] + w);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 c = c4[i / 4], l = l4[i / 4];
+                float2 y0 = exp2_2(fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                        make_float2(c.x, c.y), make_float2(l.x, l.y)));
+                float2 y1 = exp2_2(fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                        make_float2(c.z, c.w), make_float2(l.z, l.w)));
+                if (!whole) {
+                  const int4 i4 = *reinterpret_cast<const int4*>(sh.row[qb] + w + i);
+                  const int d = pos - seg.rq.start;
+                  if (d > i4.x) y0.x = 0.0f;
+                  if (d > i4.y) y0.y = 0.0f;
+                  if (d > i4.z) y1.x = 0.0f;
+                  if (d > i4.w) y1.y = 0.0f;
+                }
+                acc[0] = add2(acc[0], y0);
+                acc[1] = add2(acc[1], y1);
+              }
+            }
+            const float2 t = add2(acc[0], acc[1]);
+            if (slot >= 0 && slot < a.num_slots) sh.sum[e][tile * kTile + p] += t.x + t.y;
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&s_empty[e]);
+          }
+        }
+        if (s + 1 == seg.to || (s + 1) / seg.tiles != item) {
+          __syncwarp();
+          if (ok && lane == 0) tc::bar_arrive(&q_empty[qb]);
+        }
+      }
+      // the segment's sums of both groups, and of all CTAs of the cluster
+      __syncwarp();
+      if (ranks > 1) cluster_barrier();
+      else asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int64_t at = static_cast<int64_t>(seg.b) * a.max_ctx + static_cast<int64_t>(seg.t0) * kTile;
+      const int count = min(seg.tiles * kTile, seg.rq.end - seg.t0 * kTile);
+      for (int i = rank * 256 + tid; i < count; i += ranks * 256) {
+        float x = 0.0f;
+        if (ranks == 1) x = sh.sum[0][i] + sh.sum[1][i];
+        else
+          for (int z = 0; z < ranks; ++z) x += ld_cluster(&sh.sum[0][i], z) + ld_cluster(&sh.sum[1][i], z);
+        a.out[at + i] = a.prev ? a.prev[at + i] + x : x;
+      }
+      __syncwarp();
+      if (ranks > 1) cluster_barrier();
+      else asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after();
+    tc::dealloc<2 * kCols>(tmem);
+  }
+  if (tid == 0 && s_abort) bump(a.stats, SPEC_STAT_WAIT_TIMEOUT);
+}
+
+template <int D>
+int launch_rows(const SumArgs& a, int ranks, int sms, cudaStream_t s) {
+  constexpr auto kernel = kv4_sums_rows_kernel<D>;
+  constexpr size_t smem = sizeof(RowsShared<D>) + 1024;
+  static_assert(smem + 1024 <= 227 * 1024, "a CTA's shared memory");
+  if (!allow_smem<kernel>(smem)) return SPEC_ERR_CUDA;
+  const int clusters = sms / ranks;
+  launch_kc(kernel, static_cast<unsigned>(clusters * ranks), kThreads, smem, s, ranks, a, clusters, ranks);
+  return launch_status();
+}
+
+}  // namespace
+
+int launch_sums_rows(const SumArgs& a, int D, int sms, cudaStream_t s) {
+  // clusters where the longest requests there can be would leave SMs without a
+  // tile of their own
+  const int ranks = a.B * ((a.max_ctx + kTile - 1) / kTile) >= 2 * sms ? 1 : 4;
+  return D == 128 ? launch_rows<128>(a, ranks, sms, s) : launch_rows<64>(a, ranks, sms, s);
+}
+
+}  // namespace specdec

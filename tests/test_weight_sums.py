@@ -163,6 +163,45 @@ def test_long_context(gpu, N, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,N,G,Hkv,D", [(1, 9, 4, 1, 64), (2, 33, 1, 3, 128), (3, 17, 8, 2, 64), (1, 100, 3, 1, 128),
+                                         (2, 64, 8, 1, 64)])
+def test_many_rows(gpu, B, N, G, Hkv, D):
+    """33 to 512 rows of a KV head, over contexts that end in every part of a tile."""
+    c = add_rows(make_case(N, B, N, G * Hkv, Hkv, D, [1601, 130 - N, 0][:B], spread=1.0), accepted=[N - 1, N // 2, 0][:B])
+    stats = sd.new_stats()
+    got = run(c, stats=stats)
+    check(got, expected(c), D)
+    assert int(stats.sum()) == 0
+    assert torch.equal(got, run(c))
+
+
+@pytest.mark.gpu
+def test_few_and_many_rows_in_one_batch(gpu):
+    """Paths from one row to all of 40; bad entries and lengths among them."""
+    B, N = 6, 40
+    c = make_case(21, B, N, 4, 2, 64, [300, 0, 5, 700, 90, 40], spread=1.0)
+    rng = np.random.default_rng(0)
+    path = np.stack([np.concatenate(([0], 1 + rng.permutation(N - 1))) for _ in range(B)]).astype(np.int32)
+    add_rows(c, 1, [39, 0, 15, 16, 2, 30], path)
+    c["path"][0, 5], c["path"][3, 16], c["path"][4, 1] = -1, N, 2**31 - 1
+    c["accepted"][5] = N
+    stats = sd.new_stats()
+    got = run(c, stats=stats)
+    check(got, expected(c), 64)
+    assert stats.tolist()[sd.STATS["bad_request"]] == 4
+
+
+@pytest.mark.gpu
+def test_many_rows_in_many_segments(gpu):
+    """Enough tiles that CTAs work alone, over several segments and requests."""
+    c = make_case(3, 12, 6, 8, 1, 64, [5003, 4000, 3333, 17, 0, 5100, 2900, 128, 4900, 4801, 5055, 61], spread=0.8)
+    add_rows(c)
+    got = run(c)
+    check(got, expected(c), 64)
+    assert torch.equal(got, run(c))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N,G", [(1, 8), (16, 4)])
 def test_ragged_batch(gpu, N, G):
     c = add_rows(make_case(N + G, 7, N, 2 * G, 2, 64, [0, 1, 2500, 64, 0, 700, 63], page=5))
