@@ -17,8 +17,9 @@
 //       tensor memory each; a thread's position is its lane.
 //   warps 8 .. 15   unpack the cache, a position a thread: two groups again take
 //       turns, each with its next step's codes on their way to registers and the
-//       slots of the one behind; and the query rows of the next KV head.
+//       slots of the one behind.
 //   warp 16         issues the matrix instructions.
+//   warps 17 .. 19  turn the query rows of the next KV heads into fp16 rows.
 // Steps go head by head over a segment of up to kSegTiles tiles of a request, so
 // that a head's rows are unpacked once a segment; the segment's sums stay in
 // shared memory until its last head.  Where there are few tiles, the CTAs of a
@@ -33,26 +34,27 @@ namespace {
 
 constexpr int kTile = 128;       // positions of a step
 constexpr int kCols = 128;       // query rows of a step at most
-constexpr int kSegTiles = 12;    // tiles of a segment at most
-constexpr int kGroupWarps = 4, kUnpackWarp = 8, kIssueWarp = 16;
-constexpr int kThreads = 17 * 32;
+constexpr int kSegTiles = 48;    // tiles of a segment at most
+constexpr int kGroupWarps = 4, kUnpackWarp = 8, kIssueWarp = 16, kRowWarp = 17, kRowWarps = 3;
+constexpr int kThreads = 20 * 32;
 
 template <int D>
 struct RowsCfg {
-  static constexpr int kSlab = kTile * 128;            // bytes: 128 rows of 64 elements
+  static constexpr int kSlab = kCols * 128;            // bytes: 128 rows of 64 elements
   static constexpr int kOperand = D / 64 * kSlab;
   static constexpr int kExtra = kTile * 32;            // 128 rows of 16 elements, no swizzle
-  static constexpr int kStage = 2 * kOperand + kExtra; // hi, rem, lo
-  static constexpr int kQ = kOperand + kExtra;
 };
 template <int D>
 struct RowsShared {
-  uint8_t k[2][RowsCfg<D>::kStage];  // 1024-byte aligned
-  uint8_t q[2][RowsCfg<D>::kQ];
-  float sum[2][kSegTiles * kTile];   // of the two groups
-  float c[2][kCols], nl[2][kCols];   // factor of a row's products, -lse in units of log2
-  int row[2][kCols];                 // row of the path
+  uint8_t q[2][RowsCfg<D>::kOperand];  // 1024-byte aligned
+  uint8_t q_sums[2][RowsCfg<D>::kExtra];
+  uint8_t k_lo[2][RowsCfg<D>::kExtra];
+  float sum[2][kSegTiles * kTile];     // of the two groups
+  float c[2][kCols], nl[2][kCols];     // factor of a row's products, -lse in units of log2
+  int row[2][kCols];                   // row of the path
 };
+// Tensor memory: S of both buffers, then hi and rem of both stages.
+constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kCols;
 
 // Descriptor of an operand without swizzle, K-major: 8 rows of 16 bytes are a
 // block of 128 bytes; `leading` bytes between blocks along K, 128 along rows.
@@ -93,8 +95,34 @@ struct Segments {
   }
 };
 
+// A warp's wait, bounded like tc::bar_wait.  A lane that waits sleeps in the
+// hardware for up to a microsecond at a time: some fifteen warps that poll take
+// shared memory's bandwidth from the matrix instructions.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
-  return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, abort));
+  const uint32_t at = tc::smem_addr(bar);
+  const long long t0 = clock64();
+  bool ok = true;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(at), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done != 0) break;
+    if (*reinterpret_cast<volatile int*>(abort) != 0) {
+      ok = false;
+      break;
+    }
+    if (clock64() - t0 > tc::kWaitCycles) {
+      atomicExch(abort, 1);
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
@@ -104,42 +132,55 @@ __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
   return v;
 }
+// Stores 8 fp16 channels, unit `u` of row r, to a slab.
 __device__ __forceinline__ void put_unit(uint8_t* slab, int r, int u, const uint32_t* v) {
   *reinterpret_cast<uint4*>(slab + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Query rows [r0, r0 + n) of KV head h as fp16 rows of buffer qb: eight lanes a
-// row, D / 8 channels a lane.
+// row, D / 8 channels a lane, kBatch rows' loads in flight together.
 template <int D>
 __device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, int qb, int b, int h, int r0, int n,
-                                          const SumReq& rq, bool count, int uw) {
-  constexpr int per = D / 8, vecs = per / 8;
+                                          const SumReq& rq, bool count) {
+  constexpr int per = D / 8, vecs = per / 8, kBatch = 4, kStep = 4 * kRowWarps;
   const int lane = threadIdx.x & 31, sub = lane & 7;
-#pragma unroll 4
-  for (int c = uw * 4 + (lane >> 3); c < n; c += 16) {
-    const int r = r0 + c, i = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
-    bool in = i < rq.rows;
-    int node = in ? i : 0;
-    if (in && a.path) {
-      node = __ldg(a.path + static_cast<int64_t>(b) * a.N + i);
-      in = node >= 0 && node < a.N;
-      if (!in && count && sub == 0 && r == i * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-      if (!in) node = 0;
-    }
-    const int64_t at = static_cast<int64_t>(b) * a.N + node;
-    const int head = h * a.G + r - i * a.G;
-    const float lse = in ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
-    uint4 v[vecs];
+#pragma unroll 1
+  for (int c0 = ((threadIdx.x >> 5) - kRowWarp) * 4 + (lane >> 3); c0 < n; c0 += kBatch * kStep) {
+   int row[kBatch], node[kBatch];
+   float lses[kBatch];
+   uint4 vs[kBatch][vecs];
 #pragma unroll
-    for (int z = 0; z < vecs; ++z) {
-      v[z] = make_uint4(0, 0, 0, 0);
-      if (in) v[z] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + sub * per) + z);
-    }
-    in = in && isfinite(lse);
+   for (int z = 0; z < kBatch; ++z) {
+     const int r = r0 + c0 + z * kStep;
+     row[z] = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+     node[z] = c0 + z * kStep < n && row[z] < rq.rows ? row[z] : -1;
+     if (a.path && node[z] >= 0) {
+       node[z] = __ldg(a.path + static_cast<int64_t>(b) * a.N + row[z]);
+       if (node[z] >= a.N) node[z] = -1;
+       if (node[z] < 0 && count && sub == 0 && r == row[z] * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+     }
+   }
+#pragma unroll
+   for (int z = 0; z < kBatch; ++z) {
+     const int64_t at = static_cast<int64_t>(b) * a.N + node[z];
+     const int head = h * a.G + r0 + c0 + z * kStep - row[z] * a.G;
+     lses[z] = node[z] >= 0 ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
+#pragma unroll
+     for (int y = 0; y < vecs; ++y)
+       vs[z][y] = node[z] < 0 ? make_uint4(0, 0, 0, 0)
+                              : __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + sub * per) + y);
+   }
+#pragma unroll
+   for (int x = 0; x < kBatch; ++x) {
+    const int c = c0 + x * kStep, i = row[x];
+    if (c >= n) break;  // n is a multiple of 4: the same in the whole warp
+    const float lse = lses[x];
+    const bool in = isfinite(lse);
+    uint4 v[vecs];
     uint32_t big = 0;
 #pragma unroll
     for (int z = 0; z < vecs; ++z) {
-      if (!in) v[z] = make_uint4(0, 0, 0, 0);
+      v[z] = in ? vs[x][z] : make_uint4(0, 0, 0, 0);
       big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[z].x & 0x7fff7fffu, v[z].y & 0x7fff7fffu),
                                    __vmaxu2(v[z].z & 0x7fff7fffu, v[z].w & 0x7fff7fffu)));
     }
@@ -164,36 +205,26 @@ __device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, i
       const int ch = sub * per + 8 * z;
       put_unit(sh.q[qb] + ch / 64 * RowsCfg<D>::kSlab, c, ch % 64 / 8, y);
     }
-    // the group's sum, and its three terms, in every lane of the group
+    // the group's sum as three terms: term z of group g is column 4 z + g (the
+    // others are zeros)
 #pragma unroll
     for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(eight, s, o);
-    float term[3];
+    if (sub % (256 / D) == 0) {
+      const int group = sub / (256 / D);
 #pragma unroll
-    for (int z = 0; z < 3; ++z) {
-      term[z] = __half2float(__float2half_rn(s));
-      s -= term[z];
-    }
-    // 16 columns: term z of group g is column 4 z + g (D = 64: groups 2 and 3 are zeros)
-    uint32_t col[8];
-#pragma unroll
-    for (int z = 0; z < 3; ++z)
-#pragma unroll
-      for (int g = 0; g < 4; g += 2) {
-        float x[2];
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-          x[o] = g + o < D / 32 ? __shfl_sync(eight, term[z], (lane & 24) + (g + o) % (D / 32) * (256 / D)) : 0.0f;
-        col[2 * z + g / 2] = h2_u32(__floats2half2_rn(x[0], x[1]));
+      for (int z = 0; z < 3; ++z) {
+        const __half t = __float2half_rn(s);
+        s -= __half2float(t);
+        const int col = 4 * z + group;
+        *reinterpret_cast<__half*>(sh.q_sums[qb] + col / 8 * (kCols * 16) + c * 16 + col % 8 * 2) = t;
       }
-    col[6] = col[7] = 0;
-    if (sub < 2)
-      *reinterpret_cast<uint4*>(sh.q[qb] + RowsCfg<D>::kOperand + sub * (kTile * 16) + c * 16) =
-          sub == 0 ? make_uint4(col[0], col[1], col[2], col[3]) : make_uint4(col[4], col[5], col[6], col[7]);
+    }
     if (sub == 0) {
       sh.c[qb][c] = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p-9f : 0.0f;
       sh.nl[qb][c] = in ? -lse * kLog2e : neg_inf();
       sh.row[qb][c] = i;
     }
+   }
   }
 }
 
@@ -255,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     }
     if (tid == 0) {
       for (int i = 0; i < 2; ++i) {
-        tc::bar_init(&q_full[i], 4);
+        tc::bar_init(&q_full[i], kRowWarps);
         tc::bar_init(&q_empty[i], 1 + 2 * kGroupWarps);
         tc::bar_init(&k_full[i], 4);
         tc::bar_init(&k_empty[i], 1);
@@ -266,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
       s_abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) tc::alloc<2 * kCols>(&s_tmem);
+    if (warp == 0) tc::alloc<kTmemCols>(&s_tmem);
+    for (int i = tid; i < 2 * C::kExtra / 16; i += kThreads) reinterpret_cast<uint4*>(sh.q_sums)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -278,7 +310,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   bool ok = true;
   unsigned j = 0, item_no = 0;  // steps and items so far: which buffer, which phase
 
-  if (warp >= kUnpackWarp && warp < kIssueWarp) {
+  if (warp >= kRowWarp) {
+    // --------------------------------------------------------------- rows
+#pragma unroll 1
+    while (seg.next(a, rank, ranks)) {
+#pragma unroll 1
+      for (int s = seg.from; s < seg.to; ++item_no) {
+        const int item = s / seg.tiles, h = item / seg.blocks, block = item - h * seg.blocks, qb = item_no & 1;
+        if (ok && item_no >= 2) ok = wait_warp(&q_empty[qb], ((item_no >> 1) - 1) & 1, &s_abort);
+        if (ok) {
+          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+          load_rows<D>(a, sh, qb, seg.b, h, block * kCols, n, seg.rq, h == 0 && seg.t0 == 0 && s % seg.tiles == 0);
+          tc::fence_smem();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&q_full[qb]);
+        }
+        s = (item + 1) * seg.tiles;  // the next item's first step
+      }
+      if (ranks > 1) {
+        __syncwarp();
+        cluster_barrier();
+        cluster_barrier();
+      }
+    }
+  } else if (warp >= kUnpackWarp && warp < kIssueWarp) {
     // ------------------------------------------------------------- unpack
     const int u = (warp - kUnpackWarp) >> 2, uw = warp & 3, p = uw * 32 + lane;
     constexpr int vecs = D / 32;
@@ -318,64 +373,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
       load_slot(mine);
       load(mine, code2, meta2);
       load_slot(mine + 2);
-      int held = -1;
 #pragma unroll 1
       for (int s = seg.from; s < seg.to; ++s, ++j) {
-        const int item = s / seg.tiles, h = item / seg.blocks, block = item - h * seg.blocks, st = j & 1;
-        const bool first = item != held;
-        if (first) held = item, ++item_no;
+        const int st = j & 1;
         if (st != u) continue;
 #pragma unroll
         for (int z = 0; z < vecs; ++z) code[z] = code2[z], meta[z] = meta2[z];
         load(s + 2, code2, meta2);
         load_slot(s + 4);
-        if (first) {
-          // the group of a head's first step unpacks its rows
-          const unsigned i = item_no - 1;
-          const int qb = i & 1;
-          if (ok && i >= 2) ok = wait_warp(&q_empty[qb], ((i >> 1) - 1) & 1, &s_abort);
-          if (ok) {
-            const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
-            load_rows<D>(a, sh, qb, seg.b, h, block * kCols, n, seg.rq,
-                         h == 0 && seg.t0 == 0 && s % seg.tiles == 0, uw);
-            tc::fence_smem();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(&q_full[qb]);
-          }
-        }
         if (ok && j >= 2) ok = wait_warp(&k_empty[st], ((j >> 1) - 1) & 1, &s_abort);
         if (!ok) continue;
-        uint8_t* hi8 = sh.k[st];
-        uint8_t* rem8 = hi8 + C::kOperand;
+        tc::fence_after();
+        const uint32_t to = tmem + (static_cast<uint32_t>(uw * 32) << 16) + kTmemA + st * D;
 #pragma unroll
         for (int z = 0; z < vecs; ++z) {
           const uint32_t w[4] = {code[z].x, code[z].y, code[z].z, code[z].w};
           const __half2 step = u32_h2(__byte_perm(meta[z], 0, 0x1010));
           const __half2 k1024 = u32_h2(0xe400e400u), k16 = u32_h2(0x2c002c00u), k64 = u32_h2(0xd400d400u);
+          uint32_t hi[16], rem[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t hi[4], rem[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t y = x & 2 ? w[q] >> 8 : w[q];
-              const __half2 c = x & 1 ? __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), k16, k64)
-                                      : __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), k1024);
-              const __half2 v = __hmul2_rn(c, step);
-              hi[x] = h2_u32(v);
-              rem[x] = h2_u32(__hfma2(c, step, __hneg2(v)));
-            }
-            const int slab = (z >> 1) * C::kSlab, unit = (z & 1) * 4 + q;
-            put_unit(hi8 + slab, p, unit, hi);
-            put_unit(rem8 + slab, p, unit, rem);
+          for (int x = 0; x < 16; ++x) {
+            const uint32_t y = x & 2 ? w[x >> 2] >> 8 : w[x >> 2];
+            const __half2 c = x & 1 ? __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), k16, k64)
+                                    : __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), k1024);
+            const __half2 v = __hmul2_rn(c, step);
+            hi[x] = h2_u32(v);
+            rem[x] = h2_u32(__hfma2(c, step, __hneg2(v)));
           }
+          tc::st16(to + z * 16, hi);
+          tc::st16(to + D / 2 + z * 16, rem);
         }
         // lo of the groups, three times: columns 0..3, 4..7, 8..11
         uint32_t lo[2];
         lo[0] = __byte_perm(meta[0], meta[1], 0x7632);
         lo[1] = vecs == 4 ? __byte_perm(meta[vecs - 2], meta[vecs - 1], 0x7632) : 0u;
-        uint8_t* extra = rem8 + C::kOperand;
-        *reinterpret_cast<uint4*>(extra + p * 16) = make_uint4(lo[0], lo[1], lo[0], lo[1]);
-        *reinterpret_cast<uint4*>(extra + kTile * 16 + p * 16) = make_uint4(lo[0], lo[1], 0u, 0u);
+        *reinterpret_cast<uint4*>(sh.k_lo[st] + p * 16) = make_uint4(lo[0], lo[1], lo[0], lo[1]);
+        *reinterpret_cast<uint4*>(sh.k_lo[st] + kTile * 16 + p * 16) = make_uint4(lo[0], lo[1], 0u, 0u);
+        tc::wait_st();
+        tc::fence_before();
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&k_full[st]);
@@ -407,18 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
           const int block = item % seg.blocks;
           const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
           const uint32_t id = tc::idesc_f16(n, false), d = tmem + st * kCols;
-          const uint32_t k8 = tc::smem_addr(sh.k[st]), q8 = tc::smem_addr(sh.q[qb]);
-          const uint64_t qd = tc::desc(q8, 0);
+          const uint64_t qd = tc::desc(tc::smem_addr(sh.q[qb]), 0);
+          const uint32_t k_at = tmem + kTmemA + st * D;
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint64_t kd = tc::desc(k8 + part * C::kOperand, 0);
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4;
-              tc::mma_ss(d, kd + off, qd + off, id, part + kk != 0 ? 1u : 0u);
-            }
-          }
-          tc::mma_ss(d, desc_plain(k8 + 2 * C::kOperand, kTile * 16), desc_plain(q8 + C::kOperand, kTile * 16), id, 1u);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4), id,
+                         part + kk != 0 ? 1u : 0u);
+          tc::mma_ss(d, desc_plain(tc::smem_addr(sh.k_lo[st]), kTile * 16),
+                     desc_plain(tc::smem_addr(sh.q_sums[qb]), kCols * 16), id, 1u);
           tc::commit(&s_full[st]);
           tc::commit(&k_empty[st]);
           if (s + 1 == seg.to || (s + 1) / seg.tiles != item) tc::commit(&q_empty[qb]);
@@ -526,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   __syncthreads();
   if (warp == 0) {
     tc::fence_after();
-    tc::dealloc<2 * kCols>(tmem);
+    tc::dealloc<kTmemCols>(tmem);
   }
   if (tid == 0 && s_abort) bump(a.stats, SPEC_STAT_WAIT_TIMEOUT);
 }
