@@ -51,10 +51,13 @@ struct RowsShared {
   uint8_t k_lo[2][RowsCfg<D>::kExtra];
   float sum[2][kSegTiles * kTile];     // of the two groups
   float c[2][kCols], nl[2][kCols];     // factor of a row's products, -lse in units of log2
-  int row[2][kCols];                   // row of the path
+  int row[2][kCols], node[2][kCols];   // row of the path, and of q
+  int fold[2];                         // the rows have one factor, and lse is in the products
 };
 // Tensor memory: S of both buffers, then hi and rem of both stages.
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kCols;
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // Descriptor of an operand without swizzle, K-major: 8 rows of 16 bytes are a
 // block of 128 bytes; `leading` bytes between blocks along K, 128 along rows.
@@ -95,13 +98,13 @@ struct Segments {
   }
 };
 
-// A warp's wait, bounded like tc::bar_wait.  A lane that waits sleeps in the
-// hardware for up to a microsecond at a time: some fifteen warps that poll take
-// shared memory's bandwidth from the matrix instructions.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+// A wait, bounded like tc::bar_wait.  A lane that waits sleeps in the hardware
+// for up to a microsecond at a time: some fifteen warps that poll take shared
+// memory's bandwidth from the matrix instructions.
+__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, int* abort) {
+  if (tc::bar_test(bar, parity)) return true;
   const uint32_t at = tc::smem_addr(bar);
   const long long t0 = clock64();
-  bool ok = true;
   for (;;) {
     uint32_t done;
     asm volatile(
@@ -111,18 +114,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* a
         : "=r"(done)
         : "r"(at), "r"(parity), "r"(1000u)
         : "memory");
-    if (done != 0) break;
-    if (*reinterpret_cast<volatile int*>(abort) != 0) {
-      ok = false;
-      break;
-    }
+    if (done != 0) return true;
+    if (*reinterpret_cast<volatile int*>(abort) != 0) return false;
     if (clock64() - t0 > tc::kWaitCycles) {
       atomicExch(abort, 1);
-      ok = false;
-      break;
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  return __all_sync(0xffffffffu, wait_lane(bar, parity, abort));
 }
 __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
@@ -137,95 +138,153 @@ __device__ __forceinline__ void put_unit(uint8_t* slab, int r, int u, const uint
   *reinterpret_cast<uint4*>(slab + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// Query rows [r0, r0 + n) of KV head h as fp16 rows of buffer qb: eight lanes a
-// row, D / 8 channels a lane, kBatch rows' loads in flight together.
+// A row of q that a lane holds D / 8 channels of, eight lanes a row.
 template <int D>
-__device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, int qb, int b, int h, int r0, int n,
-                                          const SumReq& rq, bool count) {
-  constexpr int per = D / 8, vecs = per / 8, kBatch = 4, kStep = 4 * kRowWarps;
-  const int lane = threadIdx.x & 31, sub = lane & 7;
-#pragma unroll 1
-  for (int c0 = ((threadIdx.x >> 5) - kRowWarp) * 4 + (lane >> 3); c0 < n; c0 += kBatch * kStep) {
-   int row[kBatch], node[kBatch];
-   float lses[kBatch];
-   uint4 vs[kBatch][vecs];
+struct RowPart {
+  static constexpr int kVecs = D / 64;
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const SumArgs& a, int64_t at, int head, bool in) {
+    const uint16_t* src = a.q + at * a.q_stride + static_cast<int64_t>(head) * D + (threadIdx.x & 7) * (D / 8);
 #pragma unroll
-   for (int z = 0; z < kBatch; ++z) {
-     const int r = r0 + c0 + z * kStep;
-     row[z] = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
-     node[z] = c0 + z * kStep < n && row[z] < rq.rows ? row[z] : -1;
-     if (a.path && node[z] >= 0) {
-       node[z] = __ldg(a.path + static_cast<int64_t>(b) * a.N + row[z]);
-       if (node[z] >= a.N) node[z] = -1;
-       if (node[z] < 0 && count && sub == 0 && r == row[z] * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-     }
-   }
-#pragma unroll
-   for (int z = 0; z < kBatch; ++z) {
-     const int64_t at = static_cast<int64_t>(b) * a.N + node[z];
-     const int head = h * a.G + r0 + c0 + z * kStep - row[z] * a.G;
-     lses[z] = node[z] >= 0 ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
-#pragma unroll
-     for (int y = 0; y < vecs; ++y)
-       vs[z][y] = node[z] < 0 ? make_uint4(0, 0, 0, 0)
-                              : __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + sub * per) + y);
-   }
-#pragma unroll
-   for (int x = 0; x < kBatch; ++x) {
-    const int c = c0 + x * kStep, i = row[x];
-    if (c >= n) break;  // n is a multiple of 4: the same in the whole warp
-    const float lse = lses[x];
-    const bool in = isfinite(lse);
-    uint4 v[vecs];
+    for (int z = 0; z < kVecs; ++z) v[z] = in ? __ldg(reinterpret_cast<const uint4*>(src) + z) : make_uint4(0, 0, 0, 0);
+  }
+  // Exponent of the row's largest element: 2^e <= it < 2^(e + 1), at least
+  // -117 (zeros, and rows with an infinity or NaN: 0).
+  __device__ __forceinline__ int exponent(unsigned eight) const {
     uint32_t big = 0;
 #pragma unroll
-    for (int z = 0; z < vecs; ++z) {
-      v[z] = in ? vs[x][z] : make_uint4(0, 0, 0, 0);
+    for (int z = 0; z < kVecs; ++z)
       big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[z].x & 0x7fff7fffu, v[z].y & 0x7fff7fffu),
                                    __vmaxu2(v[z].z & 0x7fff7fffu, v[z].w & 0x7fff7fffu)));
-    }
-    const unsigned eight = 0xffu << (lane & 24);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(eight, big, o));
     const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
-    // 2^e <= max < 2^(e + 1): the largest becomes [2^9, 2^10), a group's sum at most 2^15
-    const int e = bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -117);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
-    float s = 0.0f;
-#pragma unroll
-    for (int z = 0; z < vecs; ++z) {
-      const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-      uint32_t y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float y0 = bf16_lo(w[j]) * up, y1 = bf16_hi(w[j]) * up;
-        y[j] = h2_u32(__floats2half2_rn(y0, y1));
-        s += y0 + y1;
-      }
-      const int ch = sub * per + 8 * z;
-      put_unit(sh.q[qb] + ch / 64 * RowsCfg<D>::kSlab, c, ch % 64 / 8, y);
-    }
-    // the group's sum as three terms: term z of group g is column 4 z + g (the
-    // others are zeros)
-#pragma unroll
-    for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(eight, s, o);
-    if (sub % (256 / D) == 0) {
-      const int group = sub / (256 / D);
-#pragma unroll
-      for (int z = 0; z < 3; ++z) {
-        const __half t = __float2half_rn(s);
-        s -= __half2float(t);
-        const int col = 4 * z + group;
-        *reinterpret_cast<__half*>(sh.q_sums[qb] + col / 8 * (kCols * 16) + c * 16 + col % 8 * 2) = t;
-      }
-    }
-    if (sub == 0) {
-      sh.c[qb][c] = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p-9f : 0.0f;
-      sh.nl[qb][c] = in ? -lse * kLog2e : neg_inf();
-      sh.row[qb][c] = i;
-    }
-   }
+    return bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -117);
   }
+};
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Query rows [r0, r0 + n) of KV head h as fp16 rows of buffer qb, by the warps
+// from kRowWarp on.  Rows of similar size (the common case) are scaled by one
+// power of two, and each row's -lse, in units of the products, joins the columns
+// of the groups' sums: a weight is then 2^(S c) with one factor c, and nothing is
+// read per column.  Else every row has its own power of two, factor and lse.
+template <int D>
+__device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, int qb, int b, int h, int r0, int n,
+                                          const SumReq& rq, bool count) {
+  constexpr int kStep = 4 * kRowWarps, kBatch = 4;  // rows of a turn, turns at a time
+  const int lane = threadIdx.x & 31, sub = lane & 7, first = ((threadIdx.x >> 5) - kRowWarp) * 4 + (lane >> 3);
+  const unsigned eight = 0xffu << (lane & 24);
+  // where the rows are, their lse and their size; n is a multiple of 4, so that
+  // a warp's lanes take the same turns.  The loads of kBatch turns fly together
+#pragma unroll 1
+  for (int c0 = first; c0 < n; c0 += kBatch * kStep) {
+    int row[kBatch], node[kBatch];
+    float lse[kBatch];
+    RowPart<D> x[kBatch];
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int r = r0 + c0 + z * kStep;
+      row[z] = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+      node[z] = c0 + z * kStep < n && row[z] < rq.rows ? row[z] : -1;
+      if (a.path && node[z] >= 0) node[z] = __ldg(a.path + static_cast<int64_t>(b) * a.N + row[z]);
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int r = r0 + c0 + z * kStep;
+      if (a.path && (node[z] < 0 || node[z] >= a.N)) {
+        if (count && sub == 0 && c0 + z * kStep < n && row[z] < rq.rows && r == row[z] * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+        node[z] = -1;
+      }
+      const int64_t at = static_cast<int64_t>(b) * a.N + max(node[z], 0);
+      const int head = h * a.G + r - row[z] * a.G;
+      lse[z] = node[z] >= 0 ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
+      x[z].load(a, at, head, node[z] >= 0);
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int c = c0 + z * kStep, e = x[z].exponent(eight);
+      if (sub == 0 && c < n) {
+        sh.c[qb][c] = __int_as_float(e);
+        sh.nl[qb][c] = isfinite(lse[z]) ? -lse[z] * kLog2e : neg_inf();
+        sh.row[qb][c] = row[z];
+        sh.node[qb][c] = node[z];
+      }
+    }
+  }
+  asm volatile("bar.sync 2, 96;" ::: "memory");
+  int top = -127;
+  for (int c = lane; c < n; c += 32)
+    if (sh.nl[qb][c] != neg_inf()) top = max(top, __float_as_int(sh.c[qb][c]));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // products come times 2^(9 - e)
+  const float one = a.scale_log2 * pow2(max(top, -117)) * 0x1p-9f;
+  bool fold = one >= 0x1p-17f && one <= 0x1p100f;
+  for (int c = lane; c < n; c += 32) {
+    const float nl = sh.nl[qb][c];
+    if (nl != neg_inf()) fold = fold && __float_as_int(sh.c[qb][c]) >= top - 16 && fabsf(nl) < one * 0x1p25f;
+  }
+  fold = __all_sync(0xffffffffu, fold);
+  asm volatile("bar.sync 2, 96;" ::: "memory");
+#pragma unroll 1
+  for (int c0 = first; c0 < n; c0 += kBatch * kStep) {
+    RowPart<D> x[kBatch];
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int c = min(c0 + z * kStep, n - 1);
+      x[z].load(a, static_cast<int64_t>(b) * a.N + max(sh.node[qb][c], 0), h * a.G + r0 + c - sh.row[qb][c] * a.G,
+                sh.nl[qb][c] != neg_inf());
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int c = c0 + z * kStep;
+      if (c >= n) break;
+      const float nl = sh.nl[qb][c];
+      const int e = fold ? top : __float_as_int(sh.c[qb][c]);
+      const bool in = nl != neg_inf();
+      // the largest becomes at most [2^9, 2^10), a group's sum at most 2^15
+      const float up = pow2(9 - e);
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < RowPart<D>::kVecs; ++v) {
+        const uint32_t w[4] = {x[z].v[v].x, x[z].v[v].y, x[z].v[v].z, x[z].v[v].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y0 = bf16_lo(w[j]) * up, y1 = bf16_hi(w[j]) * up;
+          y[j] = h2_u32(__floats2half2_rn(y0, y1));
+          s += y0 + y1;
+        }
+        const int ch = sub * (D / 8) + 8 * v;
+        put_unit(sh.q[qb] + ch / 64 * RowsCfg<D>::kSlab, c, ch % 64 / 8, y);
+      }
+      // 16 more columns: the group's sum as three terms, term z of group g in
+      // column 4 z + g (D = 64: two groups, zeros beside them), and -lse as three
+      // terms, 2^-10 of it, in columns 12 to 14
+#pragma unroll
+      for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(eight, s, o);
+      float t = s;
+      int col = sub / (256 / D), step = 4;
+      if (sub == 1) {  // a lane beside group 0's first writes lse's
+        t = !fold ? 0.0f : in ? nl / one * 0x1p-10f : -65504.0f;
+        col = 12;
+        step = 1;
+      }
+      if (sub % (256 / D) == 0 || sub == 1) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const __half y = __float2half_rn(t);
+          t -= __half2float(y);
+          *reinterpret_cast<__half*>(sh.q_sums[qb] + col / 8 * (kCols * 16) + c * 16 + col % 8 * 2) = y;
+          col += step;
+        }
+      }
+      __syncwarp();
+      if (sub == 0) sh.c[qb][c] = fold ? one : in ? a.scale_log2 * pow2(e) * 0x1p-9f : 0.0f;
+    }
+  }
+  if (threadIdx.x == kRowWarp * 32) sh.fold[qb] = fold;
 }
 
 template <int D>
@@ -236,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   extern __shared__ uint8_t rows_sm[];
   Shared& sh = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(rows_sm) + 1023) & ~uintptr_t(1023));
   if (!spec_smem_ok((reinterpret_cast<uint8_t*>(&sh) - rows_sm) + sizeof(Shared), a.stats)) return;
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], s_full[2], s_empty[2], drain;
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], k_full[2], s_full[2], s_empty[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b;
   __shared__ int64_t s_warp[kThreads / 32], s_pre;
@@ -289,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         tc::bar_init(&q_full[i], kRowWarps);
         tc::bar_init(&q_empty[i], 1 + 2 * kGroupWarps);
         tc::bar_init(&k_full[i], 4);
-        tc::bar_init(&k_empty[i], 1);
         tc::bar_init(&s_full[i], 1);
         tc::bar_init(&s_empty[i], kGroupWarps);
       }
@@ -381,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         for (int z = 0; z < vecs; ++z) code[z] = code2[z], meta[z] = meta2[z];
         load(s + 2, code2, meta2);
         load_slot(s + 4);
-        if (ok && j >= 2) ok = wait_warp(&k_empty[st], ((j >> 1) - 1) & 1, &s_abort);
+        // the stage is free once the products of two steps before are there
+        if (ok && j >= 2) ok = wait_warp(&s_full[st], ((j >> 1) - 1) & 1, &s_abort);
         if (!ok) continue;
         tc::fence_after();
         const uint32_t to = tmem + (static_cast<uint32_t>(uw * 32) << 16) + kTmemA + st * D;
@@ -408,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         lo[0] = __byte_perm(meta[0], meta[1], 0x7632);
         lo[1] = vecs == 4 ? __byte_perm(meta[vecs - 2], meta[vecs - 1], 0x7632) : 0u;
         *reinterpret_cast<uint4*>(sh.k_lo[st] + p * 16) = make_uint4(lo[0], lo[1], lo[0], lo[1]);
-        *reinterpret_cast<uint4*>(sh.k_lo[st] + kTile * 16 + p * 16) = make_uint4(lo[0], lo[1], 0u, 0u);
+        *reinterpret_cast<uint4*>(sh.k_lo[st] + kTile * 16 + p * 16) =
+            make_uint4(lo[0], lo[1], 0x64006400u, 0x00006400u);  // 1024 beside lse's terms
         tc::wait_st();
         tc::fence_before();
         tc::fence_smem();
@@ -423,40 +483,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     }
   } else if (warp == kIssueWarp) {
     // -------------------------------------------------------------- issue
+    // one lane, with nothing between two steps but the waits: the products are
+    // what a step takes longest for
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
-      int held = -1;
+      if (lane == 0) {
+        int item = seg.from / seg.tiles, left = min((item + 1) * seg.tiles, seg.to) - seg.from;  // steps of the item
+        int block = item % seg.blocks;
 #pragma unroll 1
-      for (int s = seg.from; s < seg.to; ++s, ++j) {
-        const int item = s / seg.tiles, st = j & 1;
-        if (item != held) {
-          held = item;
-          if (ok) ok = wait_warp(&q_full[item_no & 1], (item_no >> 1) & 1, &s_abort);
-          ++item_no;
-        }
-        const int qb = (item_no - 1) & 1;
-        if (ok) ok = wait_warp(&k_full[st], (j >> 1) & 1, &s_abort);
-        if (ok && j >= 2) ok = wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
-        if (ok && lane == 0) {
-          tc::fence_after();
-          const int block = item % seg.blocks;
+        for (int s = seg.from; ok && s < seg.to;) {
+          const int qb = item_no & 1;
           const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
-          const uint32_t id = tc::idesc_f16(n, false), d = tmem + st * kCols;
+          const uint32_t id = tc::idesc_f16(n, false);
           const uint64_t qd = tc::desc(tc::smem_addr(sh.q[qb]), 0);
-          const uint32_t k_at = tmem + kTmemA + st * D;
+          const uint64_t sums = desc_plain(tc::smem_addr(sh.q_sums[qb]), kCols * 16);
+          ok = wait_lane(&q_full[qb], (item_no >> 1) & 1, &s_abort);
+#pragma unroll 1
+          for (int i = 0; ok && i < left; ++i, ++j) {
+            const int st = j & 1;
+            const uint32_t d = tmem + st * kCols, k_at = tmem + kTmemA + st * D;
+            const uint64_t lo = desc_plain(tc::smem_addr(sh.k_lo[st]), kTile * 16);
+            ok = wait_lane(&k_full[st], (j >> 1) & 1, &s_abort);
+            if (j >= 2) ok = ok && wait_lane(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
+            if (!ok) break;
+            tc::fence_after();
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4), id,
-                         part + kk != 0 ? 1u : 0u);
-          tc::mma_ss(d, desc_plain(tc::smem_addr(sh.k_lo[st]), kTile * 16),
-                     desc_plain(tc::smem_addr(sh.q_sums[qb]), kCols * 16), id, 1u);
-          tc::commit(&s_full[st]);
-          tc::commit(&k_empty[st]);
-          if (s + 1 == seg.to || (s + 1) / seg.tiles != item) tc::commit(&q_empty[qb]);
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4), id,
+                           part + kk != 0 ? 1u : 0u);
+            tc::mma_ss(d, lo, sums, id, 1u);
+            tc::commit(&s_full[st]);
+          }
+          if (ok) tc::commit(&q_empty[qb]);
+          s += left;
+          left = min(seg.tiles, seg.to - s);
+          ++item;
+          ++item_no;
+          if (++block == seg.blocks) block = 0;
         }
-        __syncwarp();
       }
       if (ranks > 1) {
         __syncwarp();
@@ -464,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         cluster_barrier();
       }
     }
+    __syncwarp();
     if (lane == 0) {
       // nothing in flight when tensor memory is freed
       tc::commit(&drain);
@@ -498,32 +565,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
           if (ok) {
             tc::fence_after();
             const bool whole = (seg.t0 + tile + 1) * kTile <= seg.rq.start + 1;
+            const bool fold = sh.fold[qb] != 0;
+            const float2 one = splat(sh.c[qb][0]);
+            const int d = pos - seg.rq.start;  // rows from this one on see the position
             float2 acc[2] = {splat(0.0f), splat(0.0f)};
 #pragma unroll 1
             for (int w = 0; w < n; w += 32) {
               uint32_t x[32];
               tc::ld32(col0 + w, x);
               tc::wait_ld32(x);
-              const float4* c4 = reinterpret_cast<const float4*>(sh.c[qb] + w);
-              const float4* l4 = reinterpret_cast<const float4*>(sh.nl[qb] + w);
+              if (fold) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 c = c4[i / 4], l = l4[i / 4];
-                float2 y0 = exp2_2(fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                        make_float2(c.x, c.y), make_float2(l.x, l.y)));
-                float2 y1 = exp2_2(fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                        make_float2(c.z, c.w), make_float2(l.z, l.w)));
-                if (!whole) {
-                  const int4 i4 = *reinterpret_cast<const int4*>(sh.row[qb] + w + i);
-                  const int d = pos - seg.rq.start;
-                  if (d > i4.x) y0.x = 0.0f;
-                  if (d > i4.y) y0.y = 0.0f;
-                  if (d > i4.z) y1.x = 0.0f;
-                  if (d > i4.w) y1.y = 0.0f;
+                for (int i = 0; i < 32; i += 2) {
+                  const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), one);
+                  x[i] = __float_as_uint(y.x);
+                  x[i + 1] = __float_as_uint(y.y);
                 }
-                acc[0] = add2(acc[0], y0);
-                acc[1] = add2(acc[1], y1);
+              } else {
+                const float4* c4 = reinterpret_cast<const float4*>(sh.c[qb] + w);
+                const float4* l4 = reinterpret_cast<const float4*>(sh.nl[qb] + w);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 c = c4[i / 4], l = l4[i / 4];
+                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c.x, l.x));
+                  x[i + 1] = __float_as_uint(fmaf(__uint_as_float(x[i + 1]), c.y, l.y));
+                  x[i + 2] = __float_as_uint(fmaf(__uint_as_float(x[i + 2]), c.z, l.z));
+                  x[i + 3] = __float_as_uint(fmaf(__uint_as_float(x[i + 3]), c.w, l.w));
+                }
               }
+              if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (d > sh.row[qb][w + i]) x[i] = 0xff800000u;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], exp2_2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]))));
             }
             const float2 t = add2(acc[0], acc[1]);
             if (slot >= 0 && slot < a.num_slots) sh.sum[e][tile * kTile + p] += t.x + t.y;
