@@ -655,12 +655,18 @@ int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* 
  * do not fit max_ctx is skipped (SPEC_STAT_BAD_REQUEST each).  q and pool
  * 16-byte aligned, q_stride a multiple of 8, slot_stride a multiple of 16
  * below 2^31, 2^-20 <= scale <= 2^20, Hq <= 4096, B <= 65535
- * (SPEC_ERR_UNSUPPORTED otherwise). */
+ * (SPEC_ERR_UNSUPPORTED otherwise).
+ *   ws: spec_kv4_weight_sums_ws_size bytes, 16-byte aligned; calls that may
+ *   overlap need their own.  0 bytes (NULL will do) for up to 32 rows N Hq / Hkv
+ *   a KV head, and for sizes that are not supported.  With more its waits are
+ *   bounded: one that runs out is counted in SPEC_STAT_WAIT_TIMEOUT (results
+ *   void). */
+size_t spec_kv4_weight_sums_ws_size(int B, int N, int Hq, int Hkv, int D);
 int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const float* lse,
                          const int32_t* accept_path_or_null, const int32_t* accept_length_or_null, const void* pool,
                          int64_t num_slots, int64_t slot_stride, const int32_t* seq_lens, const int32_t* req_to_token,
                          int64_t max_ctx, float scale, const float* prev_or_null, float* out, int32_t* stats_or_null,
-                         spec_stream_t stream);
+                         void* ws, size_t ws_bytes, spec_stream_t stream);
 
 /* Eviction: every request longer than `limit` positions is cut to `budget` of
  * them, limit >= budget >= 1: the first `sinks`, the last `recent` (sinks +

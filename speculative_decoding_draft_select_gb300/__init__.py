@@ -26,7 +26,7 @@ __all__ = [
     "tli_map_ids",
     "tli_check_config", "tli_pruned_head", "spec_filter_logits", "spec_wait_probe", "spec_debug_bounds",
     "new_stats", "new_pool", "spec_kv4_slot_bytes", "spec_kv4_append", "spec_kv4_gather",
-    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_kv4_weight_sums",
+    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_kv4_weight_sums", "spec_kv4_weight_sums_ws_size",
     "spec_evict_freed_capacity", "spec_evict_ws_size", "spec_evict_slots", "spec_adjust_logits",
 ]
 
@@ -96,7 +96,8 @@ _SIGS = {
     "spec_kv4_attention_window": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32, _I32,
                                        _F, _P, _P, _P, _P, _SZ, _P]),
     "spec_kv4_weight_sums": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _P, _P,
-                                  _P]),
+                                  _P, _SZ, _P]),
+    "spec_kv4_weight_sums_ws_size": (_SZ, [_I, _I, _I, _I, _I]),
     "spec_evict_freed_capacity": (_I64, [_I, _I64, _I, _I]),
     "spec_evict_ws_size": (_SZ, [_I, _I, _I]),
     "spec_evict_slots": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P,
@@ -724,15 +725,22 @@ def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scal
     return out
 
 
+@functools.lru_cache(maxsize=256)  # of the sizes alone
+def spec_kv4_weight_sums_ws_size(B, N, Hq, Hkv, D) -> int:
+    return int(lib().spec_kv4_weight_sums_ws_size(int(B), int(N), int(Hq), int(Hkv), int(D)))
+
+
 def spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, accept_path=None, accept_length=None,
-                         prev=None, out=None, scale=None, stats=None):
+                         prev=None, out=None, scale=None, ws=None, stats=None):
     """Adds to each cached position the attention weights that it receives from
     the accepted path's rows, all query heads: row i <= accept_length[b] (None:
     every i < N) is node accept_path[b, i] (None: i) of q [B, N, Hq, D] bf16 and
     lse [B, N, Hq] f32, at position seq_lens[b] + i.  Called behind
     spec_compact_slots with the arguments that it had.  Returns out [B, max_ctx]
     f32 = prev plus the weights (out None: prev itself is updated, or zeros are
-    allocated when that is None too)."""
+    allocated when that is None too).  ws: a uint8 workspace of
+    spec_kv4_weight_sums_ws_size bytes (none for few rows) to reuse between calls
+    that do not overlap."""
     dev = _device(q, "q")
     qs = _rows(q, "q")
     if q.dtype is not torch.bfloat16:
@@ -748,12 +756,17 @@ def spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, 
     lse_at = _arg(lse, f32, (B, N, Hq), dev, "lse")
     if q.numel() == 0:
         return out
+    if ws is None:
+        need = spec_kv4_weight_sums_ws_size(B, N, Hq, num_kv_heads, D)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     rc = lib().spec_kv4_weight_sums(B, N, Hq, num_kv_heads, D, q.data_ptr(), qs, lse_at,
                                     _arg(accept_path, i32, (B, N), dev, "accept_path"),
                                     _arg(accept_length, i32, (B,), dev, "accept_length"), pool, slots, stride,
                                     _arg(seq_lens, i32, (B,), dev, "seq_lens"), table, ctx,
                                     D ** -0.5 if scale is None else scale, before, dst,
-                                    _arg(stats, i32, (NUM_STATS,), dev, "stats"), _stream())
+                                    _arg(stats, i32, (NUM_STATS,), dev, "stats"),
+                                    None if ws is None else _arg(ws, torch.uint8, ws.shape, dev, "ws"),
+                                    0 if ws is None else ws.numel(), _stream())
     if rc:
         raise SpecError("spec_kv4_weight_sums", rc)
     return out

@@ -243,6 +243,151 @@ struct Ring {
   }
 };
 
+// A row of q that a lane holds D / 8 channels of, eight lanes a row.
+template <int D>
+struct RowPart {
+  static constexpr int kVecs = D / 64;
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const SumArgs& a, int64_t at, int head, bool in) {
+    const uint16_t* src = a.q + at * a.q_stride + static_cast<int64_t>(head) * D + (threadIdx.x & 7) * (D / 8);
+#pragma unroll
+    for (int z = 0; z < kVecs; ++z) v[z] = in ? __ldg(reinterpret_cast<const uint4*>(src) + z) : make_uint4(0, 0, 0, 0);
+  }
+  // Exponent of the row's largest element: 2^e <= it < 2^(e + 1), at least
+  // -117 (zeros, and rows with an infinity or NaN: 0).
+  __device__ __forceinline__ int exponent() const {
+    uint32_t big = 0;
+#pragma unroll
+    for (int z = 0; z < kVecs; ++z)
+      big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[z].x & 0x7fff7fffu, v[z].y & 0x7fff7fffu),
+                                   __vmaxu2(v[z].z & 0x7fff7fffu, v[z].w & 0x7fff7fffu)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
+    return bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -117);
+  }
+};
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Rows [r0, r0 + 128) of KV head h as a block in the workspace: a CTA's work,
+// four rows a warp at a time.
+template <int D>
+__device__ __forceinline__ void write_block(const SumArgs& a, int b, int h, int r0, const SumReq& rq, RowsBlock<D>& out) {
+  constexpr int kTurns = kRowsBlock / (4 * kWarps);
+  __shared__ int s_top[kWarps], s_fold[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, c0 = warp * 4 + (lane >> 3);
+  RowPart<D> x[kTurns];
+  int row[kTurns], e[kTurns];
+  float nl[kTurns];
+  int top = -127;
+#pragma unroll
+  for (int z = 0; z < kTurns; ++z) {
+    const int r = r0 + c0 + z * 4 * kWarps;
+    row[z] = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
+    int node = row[z] < rq.rows ? row[z] : -1;
+    if (a.path && node >= 0) {
+      node = __ldg(a.path + static_cast<int64_t>(b) * a.N + row[z]);
+      if (node < 0 || node >= a.N) {
+        if (h == 0 && sub == 0 && r == row[z] * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+        node = -1;
+      }
+    }
+    const int64_t at = static_cast<int64_t>(b) * a.N + max(node, 0);
+    const int head = h * a.G + r - row[z] * a.G;
+    const float lse = node >= 0 ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
+    nl[z] = isfinite(lse) ? -lse * kLog2e : neg_inf();
+    x[z].load(a, at, head, isfinite(lse));
+  }
+#pragma unroll
+  for (int z = 0; z < kTurns; ++z) {
+    e[z] = x[z].exponent();
+    if (nl[z] != neg_inf()) top = max(top, e[z]);
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, s_top[w]);
+  // products come times 2^(9 - e)
+  const float one = a.scale_log2 * pow2(max(top, -117)) * 0x1p-9f;
+  bool fold = one >= 0x1p-17f && one <= 0x1p100f;
+#pragma unroll
+  for (int z = 0; z < kTurns; ++z)
+    if (nl[z] != neg_inf()) fold = fold && e[z] >= top - 16 && fabsf(nl[z]) < one * 0x1p25f;
+  fold = __all_sync(0xffffffffu, fold);
+  if (lane == 0) s_fold[warp] = fold;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) fold = fold && s_fold[w] != 0;
+#pragma unroll
+  for (int z = 0; z < kTurns; ++z) {
+    const int c = c0 + z * 4 * kWarps;
+    const bool in = nl[z] != neg_inf();
+    // the largest becomes at most [2^9, 2^10), a group's sum at most 2^15
+    const float up = pow2(9 - (fold ? top : e[z]));
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < RowPart<D>::kVecs; ++v) {
+      const uint32_t w[4] = {x[z].v[v].x, x[z].v[v].y, x[z].v[v].z, x[z].v[v].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float y0 = bf16_lo(w[j]) * up, y1 = bf16_hi(w[j]) * up;
+        y[j] = h2_u32(__floats2half2_rn(y0, y1));
+        s += y0 + y1;
+      }
+      const int ch = sub * (D / 8) + 8 * v;
+      *reinterpret_cast<uint4*>(out.q + ch / 64 * RowsBlock<D>::kSlab + c * 128 + ((ch % 64 / 8 ^ (c & 7)) << 4)) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+    }
+#pragma unroll
+    for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    // a lane writes three terms: a group's first lane the group's, lane 1 lse's;
+    // the columns between are zeros where D = 64 has two groups, 15 always
+    const bool of_lse = sub == 1;
+    float t = of_lse ? (!fold ? 0.0f : in ? nl[z] / one * 0x1p-10f : -65504.0f) : s;
+    if (of_lse || sub % (256 / D) == 0) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const __half y = __float2half_rn(t);
+        t -= __half2float(y);
+        const int col = of_lse ? 12 + k : 4 * k + sub / (256 / D);
+        *reinterpret_cast<__half*>(out.sums + col / 8 * (kRowsBlock * 16) + c * 16 + col % 8 * 2) = y;
+      }
+    } else if (D == 64 && (sub == 2 || sub == 3)) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int col = 4 * k + sub;
+        *reinterpret_cast<uint16_t*>(out.sums + col / 8 * (kRowsBlock * 16) + c * 16 + col % 8 * 2) = 0;
+      }
+    }
+    if (sub == 7) *reinterpret_cast<uint16_t*>(out.sums + kRowsBlock * 16 + c * 16 + 14) = 0;
+    if (sub == 0) {
+      out.c[c] = fold ? one : in ? a.scale_log2 * pow2(e[z]) * 0x1p-9f : 0.0f;
+      out.nl[c] = nl[z];
+      out.row[c] = row[z];
+    }
+  }
+  if (threadIdx.x == 0) out.fold = fold;
+  __syncthreads();
+}
+
+// The blocks of the requests that go to the tensor-memory kernel.
+template <int D>
+__device__ __noinline__ void write_blocks(const SumArgs& a) {
+  const int blocks = (a.N * a.G + kRowsBlock - 1) / kRowsBlock, each = a.Hkv * blocks;
+  const int64_t all = static_cast<int64_t>(a.B) * each;
+#pragma unroll 1
+  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+    const int b = static_cast<int>(i / each), k = static_cast<int>(i - static_cast<int64_t>(b) * each);
+    const int h = k / blocks, block = k - h * blocks;
+    const SumReq rq = any_req(a, b);
+    if (rq.rows * a.G > a.upto && block * kRowsBlock < rq.rows * a.G)
+      write_block<D>(a, b, h, block * kRowsBlock, rq, static_cast<RowsBlock<D>*>(a.ws)[i]);
+  }
+}
+
 // RT: row tiles of eight that a pass over the codes takes at most.
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(const SumArgs a, int ctas) {
@@ -255,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
   __shared__ int64_t s_warp[kWarps], s_pre;
   __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
+  if (RT > 1 && a.ws != nullptr) write_blocks<D>(a);
 
   // this CTA's stretch [lo, hi) of the line of all requests' chunks, by their
   // cost: the chunks that begin in it.  pre: where request b begins
@@ -268,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
     for (int i = b0; i < b1; ++i) {
       const SumReq r = sum_req(a, i);
       mine += sum_units(a, r);
-      if (r.bad && a.count_bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+      if (r.bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -478,7 +624,13 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
   }
 }
 
+// Rows of a KV head above which the tensor-memory kernel takes a request.
 constexpr int kManyRows = 32;
+
+// The upper limits of a call's sizes.
+bool sum_sizes(int B, int N, int Hq, int Hkv, int D) {
+  return spec_kv4_slot_bytes(Hkv, D) >= 0 && N <= SPEC_MAX_NODES && Hq <= SPEC_KV4_MAX_HEADS * 16 && B <= 65535;
+}
 
 template <int D, int RT>
 int launch_sums(const SumArgs& a, int sms, cudaStream_t s) {
@@ -495,17 +647,25 @@ int launch_sums(const SumArgs& a, int sms, cudaStream_t s) {
 
 using namespace specdec;
 
+extern "C" size_t spec_kv4_weight_sums_ws_size(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !sum_sizes(B, N, Hq, Hkv, D)) return 0;
+  const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
+  if (rows <= kManyRows) return 0;
+  return static_cast<size_t>(B) * Hkv * ((rows + kRowsBlock - 1) / kRowsBlock) *
+         (D == 128 ? sizeof(RowsBlock<128>) : sizeof(RowsBlock<64>));
+}
+
 extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride,
                                     const float* lse, const int32_t* accept_path_or_null,
                                     const int32_t* accept_length_or_null, const void* pool, int64_t num_slots,
                                     int64_t slot_stride, const int32_t* seq_lens, const int32_t* req_to_token,
                                     int64_t max_ctx, float scale, const float* prev_or_null, float* out,
-                                    int32_t* stats_or_null, spec_stream_t stream) {
+                                    int32_t* stats_or_null, void* ws, size_t ws_bytes, spec_stream_t stream) {
   if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !(scale > 0.0f) ||
       !isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   const int64_t row = spec_kv4_slot_bytes(Hkv, D);
-  if (row < 0 || N > SPEC_MAX_NODES || Hq > SPEC_KV4_MAX_HEADS * 16 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (!sum_sizes(B, N, Hq, Hkv, D)) return SPEC_ERR_UNSUPPORTED;
   if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
   if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
   if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kChunk ||
@@ -515,6 +675,9 @@ extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const 
   if (!q || !lse || !pool || !seq_lens || !req_to_token || !out) return SPEC_ERR_INVALID_ARG;
   for (const void* p : {q, pool})
     if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return SPEC_ERR_UNSUPPORTED;
+  const size_t need = spec_kv4_weight_sums_ws_size(B, N, Hq, Hkv, D);
+  if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < need) return SPEC_ERR_WORKSPACE;
   const int sms = attn_sms();
   if (sms == 0) {
     cudaGetLastError();
@@ -523,21 +686,19 @@ extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const 
   const int G = Hq / Hkv;
   SumArgs a{static_cast<const uint16_t*>(q), q_stride, lse, accept_path_or_null, accept_length_or_null, B, N, Hq,
             Hkv, G, ((1ull << 40) + G - 1) / G, static_cast<const uint8_t*>(pool), num_slots, slot_stride,
-            seq_lens, req_to_token, max_ctx, scale * kLog2e, prev_or_null, out, stats_or_null, 0, INT32_MAX, true};
+            seq_lens, req_to_token, max_ctx, scale * kLog2e, prev_or_null, out, stats_or_null, nullptr, 0, INT32_MAX};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(N) * G;
   // the host knows how many rows there may be, the device how many there are:
-  // with accepted lengths each request goes to the kernel that suits it
-  if (rows > kManyRows) {
-    if (!accept_length_or_null) return launch_sums_rows(a, D, sms, s);
-    a.above = kManyRows;
-    const int e = launch_sums_rows(a, D, sms, s);
-    if (e != SPEC_OK) return e;
-    a.above = 0;
-    a.upto = kManyRows;
-    a.count_bad = false;
-  }
+  // each request goes to the kernel that suits it
+  const bool many = rows > kManyRows;
+  a.upto = many ? kManyRows : INT32_MAX;
+  a.ws = many ? ws : nullptr;
   const bool one = rows <= 8;
-  if (D == 128) return one ? launch_sums<128, 1>(a, sms, s) : launch_sums<128, 2>(a, sms, s);
-  return one ? launch_sums<64, 1>(a, sms, s) : launch_sums<64, 2>(a, sms, s);
+  const int e = D == 128 ? (one ? launch_sums<128, 1>(a, sms, s) : launch_sums<128, 2>(a, sms, s))
+                         : (one ? launch_sums<64, 1>(a, sms, s) : launch_sums<64, 2>(a, sms, s));
+  if (e != SPEC_OK || !many) return e;
+  a.above = kManyRows;
+  a.upto = INT32_MAX;
+  return launch_sums_rows(a, D, sms, s);
 }

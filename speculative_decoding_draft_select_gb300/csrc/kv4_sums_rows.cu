@@ -13,13 +13,14 @@
 // scores as good as fp32 sums.
 //
 // Roles of a CTA:
-//   warps 0 .. 7    weights: two groups of four warps take turns, a buffer of
-//       tensor memory each; a thread's position is its lane.
-//   warps 8 .. 15   unpack the cache, a position a thread: two groups again take
-//       turns, each with its next step's codes on their way to registers and the
+//   warps 0 .. 7    weights: a thread's position is its lane; two groups of four
+//       warps share a step's columns, since the next products but one wait for it.
+//   warps 8 .. 15   unpack the cache, a position a thread: two groups take turns,
+//       each with its next step's codes on their way to registers and the
 //       slots of the one behind.
 //   warp 16         issues the matrix instructions.
-//   warps 17 .. 19  turn the query rows of the next KV heads into fp16 rows.
+//   warp 17         copies the next KV head's rows, which kv4_sums_kernel has laid
+//       out in the workspace.
 // Steps go head by head over a segment of up to kSegTiles tiles of a request, so
 // that a head's rows are unpacked once a segment; the segment's sums stay in
 // shared memory until its last head.  Where there are few tiles, the CTAs of a
@@ -33,26 +34,16 @@ namespace specdec {
 namespace {
 
 constexpr int kTile = 128;       // positions of a step
-constexpr int kCols = 128;       // query rows of a step at most
+constexpr int kCols = kRowsBlock;  // query rows of a step at most
 constexpr int kSegTiles = 48;    // tiles of a segment at most
-constexpr int kGroupWarps = 4, kUnpackWarp = 8, kIssueWarp = 16, kRowWarp = 17, kRowWarps = 3;
-constexpr int kThreads = 20 * 32;
+constexpr int kUnpackWarp = 8, kIssueWarp = 16, kRowWarp = 17;
+constexpr int kThreads = 18 * 32;
 
 template <int D>
-struct RowsCfg {
-  static constexpr int kSlab = kCols * 128;            // bytes: 128 rows of 64 elements
-  static constexpr int kOperand = D / 64 * kSlab;
-  static constexpr int kExtra = kTile * 32;            // 128 rows of 16 elements, no swizzle
-};
-template <int D>
 struct RowsShared {
-  uint8_t q[2][RowsCfg<D>::kOperand];  // 1024-byte aligned
-  uint8_t q_sums[2][RowsCfg<D>::kExtra];
-  uint8_t k_lo[2][RowsCfg<D>::kExtra];
-  float sum[2][kSegTiles * kTile];     // of the two groups
-  float c[2][kCols], nl[2][kCols];     // factor of a row's products, -lse in units of log2
-  int row[2][kCols], node[2][kCols];   // row of the path, and of q
-  int fold[2];                         // the rows have one factor, and lse is in the products
+  RowsBlock<D> q[2];                // 1024-byte aligned
+  uint8_t k_lo[2][kTile * 32];      // 128 rows of 16 elements, no swizzle
+  float sum[2][kSegTiles * kTile];  // of the two groups
 };
 // Tensor memory: S of both buffers, then hi and rem of both stages.
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kCols;
@@ -133,164 +124,9 @@ __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
   return v;
 }
-// Stores 8 fp16 channels, unit `u` of row r, to a slab.
-__device__ __forceinline__ void put_unit(uint8_t* slab, int r, int u, const uint32_t* v) {
-  *reinterpret_cast<uint4*>(slab + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// A row of q that a lane holds D / 8 channels of, eight lanes a row.
-template <int D>
-struct RowPart {
-  static constexpr int kVecs = D / 64;
-  uint4 v[kVecs];
-  __device__ __forceinline__ void load(const SumArgs& a, int64_t at, int head, bool in) {
-    const uint16_t* src = a.q + at * a.q_stride + static_cast<int64_t>(head) * D + (threadIdx.x & 7) * (D / 8);
-#pragma unroll
-    for (int z = 0; z < kVecs; ++z) v[z] = in ? __ldg(reinterpret_cast<const uint4*>(src) + z) : make_uint4(0, 0, 0, 0);
-  }
-  // Exponent of the row's largest element: 2^e <= it < 2^(e + 1), at least
-  // -117 (zeros, and rows with an infinity or NaN: 0).
-  __device__ __forceinline__ int exponent(unsigned eight) const {
-    uint32_t big = 0;
-#pragma unroll
-    for (int z = 0; z < kVecs; ++z)
-      big = __vmaxu2(big, __vmaxu2(__vmaxu2(v[z].x & 0x7fff7fffu, v[z].y & 0x7fff7fffu),
-                                   __vmaxu2(v[z].z & 0x7fff7fffu, v[z].w & 0x7fff7fffu)));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(eight, big, o));
-    const int bits = static_cast<int>(max(big & 0xffffu, big >> 16));
-    return bits == 0 || bits >= 0x7f80 ? 0 : max((bits >> 7) - 127, -117);
-  }
-};
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-
-// Query rows [r0, r0 + n) of KV head h as fp16 rows of buffer qb, by the warps
-// from kRowWarp on.  Rows of similar size (the common case) are scaled by one
-// power of two, and each row's -lse, in units of the products, joins the columns
-// of the groups' sums: a weight is then 2^(S c) with one factor c, and nothing is
-// read per column.  Else every row has its own power of two, factor and lse.
-template <int D>
-__device__ __forceinline__ void load_rows(const SumArgs& a, RowsShared<D>& sh, int qb, int b, int h, int r0, int n,
-                                          const SumReq& rq, bool count) {
-  constexpr int kStep = 4 * kRowWarps, kBatch = 4;  // rows of a turn, turns at a time
-  const int lane = threadIdx.x & 31, sub = lane & 7, first = ((threadIdx.x >> 5) - kRowWarp) * 4 + (lane >> 3);
-  const unsigned eight = 0xffu << (lane & 24);
-  // where the rows are, their lse and their size; n is a multiple of 4, so that
-  // a warp's lanes take the same turns.  The loads of kBatch turns fly together
-#pragma unroll 1
-  for (int c0 = first; c0 < n; c0 += kBatch * kStep) {
-    int row[kBatch], node[kBatch];
-    float lse[kBatch];
-    RowPart<D> x[kBatch];
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      const int r = r0 + c0 + z * kStep;
-      row[z] = static_cast<int>(static_cast<uint64_t>(r) * a.g_inv >> 40);
-      node[z] = c0 + z * kStep < n && row[z] < rq.rows ? row[z] : -1;
-      if (a.path && node[z] >= 0) node[z] = __ldg(a.path + static_cast<int64_t>(b) * a.N + row[z]);
-    }
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      const int r = r0 + c0 + z * kStep;
-      if (a.path && (node[z] < 0 || node[z] >= a.N)) {
-        if (count && sub == 0 && c0 + z * kStep < n && row[z] < rq.rows && r == row[z] * a.G) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-        node[z] = -1;
-      }
-      const int64_t at = static_cast<int64_t>(b) * a.N + max(node[z], 0);
-      const int head = h * a.G + r - row[z] * a.G;
-      lse[z] = node[z] >= 0 ? __ldg(a.lse + at * a.Hq + head) : neg_inf();
-      x[z].load(a, at, head, node[z] >= 0);
-    }
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      const int c = c0 + z * kStep, e = x[z].exponent(eight);
-      if (sub == 0 && c < n) {
-        sh.c[qb][c] = __int_as_float(e);
-        sh.nl[qb][c] = isfinite(lse[z]) ? -lse[z] * kLog2e : neg_inf();
-        sh.row[qb][c] = row[z];
-        sh.node[qb][c] = node[z];
-      }
-    }
-  }
-  asm volatile("bar.sync 2, 96;" ::: "memory");
-  int top = -127;
-  for (int c = lane; c < n; c += 32)
-    if (sh.nl[qb][c] != neg_inf()) top = max(top, __float_as_int(sh.c[qb][c]));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // products come times 2^(9 - e)
-  const float one = a.scale_log2 * pow2(max(top, -117)) * 0x1p-9f;
-  bool fold = one >= 0x1p-17f && one <= 0x1p100f;
-  for (int c = lane; c < n; c += 32) {
-    const float nl = sh.nl[qb][c];
-    if (nl != neg_inf()) fold = fold && __float_as_int(sh.c[qb][c]) >= top - 16 && fabsf(nl) < one * 0x1p25f;
-  }
-  fold = __all_sync(0xffffffffu, fold);
-  asm volatile("bar.sync 2, 96;" ::: "memory");
-#pragma unroll 1
-  for (int c0 = first; c0 < n; c0 += kBatch * kStep) {
-    RowPart<D> x[kBatch];
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      const int c = min(c0 + z * kStep, n - 1);
-      x[z].load(a, static_cast<int64_t>(b) * a.N + max(sh.node[qb][c], 0), h * a.G + r0 + c - sh.row[qb][c] * a.G,
-                sh.nl[qb][c] != neg_inf());
-    }
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      const int c = c0 + z * kStep;
-      if (c >= n) break;
-      const float nl = sh.nl[qb][c];
-      const int e = fold ? top : __float_as_int(sh.c[qb][c]);
-      const bool in = nl != neg_inf();
-      // the largest becomes at most [2^9, 2^10), a group's sum at most 2^15
-      const float up = pow2(9 - e);
-      float s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < RowPart<D>::kVecs; ++v) {
-        const uint32_t w[4] = {x[z].v[v].x, x[z].v[v].y, x[z].v[v].z, x[z].v[v].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float y0 = bf16_lo(w[j]) * up, y1 = bf16_hi(w[j]) * up;
-          y[j] = h2_u32(__floats2half2_rn(y0, y1));
-          s += y0 + y1;
-        }
-        const int ch = sub * (D / 8) + 8 * v;
-        put_unit(sh.q[qb] + ch / 64 * RowsCfg<D>::kSlab, c, ch % 64 / 8, y);
-      }
-      // 16 more columns: the group's sum as three terms, term z of group g in
-      // column 4 z + g (D = 64: two groups, zeros beside them), and -lse as three
-      // terms, 2^-10 of it, in columns 12 to 14
-#pragma unroll
-      for (int o = 1; o < 256 / D; o <<= 1) s += __shfl_xor_sync(eight, s, o);
-      float t = s;
-      int col = sub / (256 / D), step = 4;
-      if (sub == 1) {  // a lane beside group 0's first writes lse's
-        t = !fold ? 0.0f : in ? nl / one * 0x1p-10f : -65504.0f;
-        col = 12;
-        step = 1;
-      }
-      if (sub % (256 / D) == 0 || sub == 1) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const __half y = __float2half_rn(t);
-          t -= __half2float(y);
-          *reinterpret_cast<__half*>(sh.q_sums[qb] + col / 8 * (kCols * 16) + c * 16 + col % 8 * 2) = y;
-          col += step;
-        }
-      }
-      __syncwarp();
-      if (sub == 0) sh.c[qb][c] = fold ? one : in ? a.scale_log2 * pow2(e) * 0x1p-9f : 0.0f;
-    }
-  }
-  if (threadIdx.x == kRowWarp * 32) sh.fold[qb] = fold;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArgs a, int clusters, int ranks) {
   pdl_enter();
-  using C = RowsCfg<D>;
   using Shared = RowsShared<D>;
   extern __shared__ uint8_t rows_sm[];
   Shared& sh = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(rows_sm) + 1023) & ~uintptr_t(1023));
@@ -312,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     for (int i = b0; i < b1; ++i) {
       const SumReq r = sum_req(a, i);
       mine += Segments::tiles_of(r);
-      if (r.bad && a.count_bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -345,18 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     }
     if (tid == 0) {
       for (int i = 0; i < 2; ++i) {
-        tc::bar_init(&q_full[i], kRowWarps);
-        tc::bar_init(&q_empty[i], 1 + 2 * kGroupWarps);
+        tc::bar_init(&q_full[i], 1);
+        tc::bar_init(&q_empty[i], 1 + kUnpackWarp);
         tc::bar_init(&k_full[i], 4);
         tc::bar_init(&s_full[i], 1);
-        tc::bar_init(&s_empty[i], kGroupWarps);
+        tc::bar_init(&s_empty[i], kUnpackWarp);
       }
       tc::bar_init(&drain, 1);
       s_abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tc::alloc<kTmemCols>(&s_tmem);
-    for (int i = tid; i < 2 * C::kExtra / 16; i += kThreads) reinterpret_cast<uint4*>(sh.q_sums)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -372,18 +206,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     // --------------------------------------------------------------- rows
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
+      if (lane == 0) {
+        const int blocks = (a.N * a.G + kCols - 1) / kCols;  // of the workspace's heads
 #pragma unroll 1
-      for (int s = seg.from; s < seg.to; ++item_no) {
-        const int item = s / seg.tiles, h = item / seg.blocks, block = item - h * seg.blocks, qb = item_no & 1;
-        if (ok && item_no >= 2) ok = wait_warp(&q_empty[qb], ((item_no >> 1) - 1) & 1, &s_abort);
-        if (ok) {
-          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
-          load_rows<D>(a, sh, qb, seg.b, h, block * kCols, n, seg.rq, h == 0 && seg.t0 == 0 && s % seg.tiles == 0);
-          tc::fence_smem();
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(&q_full[qb]);
+        for (int s = seg.from; ok && s < seg.to; ++item_no) {
+          const int item = s / seg.tiles, h = item / seg.blocks, qb = item_no & 1;
+          if (item_no >= 2) ok = wait_lane(&q_empty[qb], ((item_no >> 1) - 1) & 1, &s_abort);
+          if (!ok) break;
+          const RowsBlock<D>* src = static_cast<const RowsBlock<D>*>(a.ws) +
+                                    (static_cast<int64_t>(seg.b) * a.Hkv + h) * blocks + item - h * seg.blocks;
+          const uint32_t bar = tc::smem_addr(&q_full[qb]);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                       "r"(static_cast<uint32_t>(sizeof(RowsBlock<D>)))
+                       : "memory");
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           tc::smem_addr(&sh.q[qb])),
+                       "l"(src), "r"(static_cast<uint32_t>(sizeof(RowsBlock<D>))), "r"(bar)
+                       : "memory");
+          s = (item + 1) * seg.tiles;  // the next item's first step
         }
-        s = (item + 1) * seg.tiles;  // the next item's first step
       }
       if (ranks > 1) {
         __syncwarp();
@@ -391,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         cluster_barrier();
       }
     }
+    __syncwarp();
   } else if (warp >= kUnpackWarp && warp < kIssueWarp) {
     // ------------------------------------------------------------- unpack
     const int u = (warp - kUnpackWarp) >> 2, uw = warp & 3, p = uw * 32 + lane;
@@ -495,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
           const int qb = item_no & 1;
           const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
           const uint32_t id = tc::idesc_f16(n, false);
-          const uint64_t qd = tc::desc(tc::smem_addr(sh.q[qb]), 0);
-          const uint64_t sums = desc_plain(tc::smem_addr(sh.q_sums[qb]), kCols * 16);
+          const uint64_t qd = tc::desc(tc::smem_addr(sh.q[qb].q), 0);
+          const uint64_t sums = desc_plain(tc::smem_addr(sh.q[qb].sums), kCols * 16);
           ok = wait_lane(&q_full[qb], (item_no >> 1) & 1, &s_abort);
 #pragma unroll 1
           for (int i = 0; ok && i < left; ++i, ++j) {
@@ -511,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * C::kSlab + (kk % 4) * 32) >> 4), id,
+                tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * RowsBlock<D>::kSlab + (kk % 4) * 32) >> 4), id,
                            part + kk != 0 ? 1u : 0u);
             tc::mma_ss(d, lo, sums, id, 1u);
             tc::commit(&s_full[st]);
@@ -542,35 +384,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   } else {
     // ------------------------------------------------------------ weights
     const int e = warp >> 2, p = (warp & 3) * 32 + lane;
-    const uint32_t col0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + e * kCols;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
       const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
       for (int i = p; i < seg.tiles * kTile; i += kTile) sh.sum[e][i] = 0.0f;
-      int held = -1;
+      int item = seg.from / seg.tiles, tile = seg.from - item * seg.tiles, block = item % seg.blocks;
+      bool fresh = true;
 #pragma unroll 1
       for (int s = seg.from; s < seg.to; ++s, ++j) {
-        const int item = s / seg.tiles, tile = s - item * seg.tiles;
-        if (item != held) {
-          held = item;
-          if (ok) ok = wait_warp(&q_full[item_no & 1], (item_no >> 1) & 1, &s_abort);
-          ++item_no;
-        }
-        const int qb = (item_no - 1) & 1;
-        if (static_cast<int>(j & 1) == e && ok) {
-          const int pos = (seg.t0 + tile) * kTile + p, block = item % seg.blocks;
+        const int qb = item_no & 1, st = j & 1;
+        if (fresh && ok) ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
+        fresh = false;
+        if (ok) {
+          const int pos = (seg.t0 + tile) * kTile + p;
           const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
           const int32_t slot = pos < seg.rq.end ? __ldg(row + pos) : -1;
-          ok = wait_warp(&s_full[e], (j >> 1) & 1, &s_abort);
+          const uint32_t col0 = lanes + st * kCols;
+          ok = wait_warp(&s_full[st], (j >> 1) & 1, &s_abort);
           if (ok) {
             tc::fence_after();
             const bool whole = (seg.t0 + tile + 1) * kTile <= seg.rq.start + 1;
-            const bool fold = sh.fold[qb] != 0;
-            const float2 one = splat(sh.c[qb][0]);
+            const RowsBlock<D>& q = sh.q[qb];
+            const bool fold = q.fold != 0;
+            const float2 one = splat(q.c[0]);
             const int d = pos - seg.rq.start;  // rows from this one on see the position
             float2 acc[2] = {splat(0.0f), splat(0.0f)};
 #pragma unroll 1
-            for (int w = 0; w < n; w += 32) {
+            for (int w = 32 * e; w < n; w += 64) {  // a group's columns
               uint32_t x[32];
               tc::ld32(col0 + w, x);
               tc::wait_ld32(x);
@@ -582,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
                   x[i + 1] = __float_as_uint(y.y);
                 }
               } else {
-                const float4* c4 = reinterpret_cast<const float4*>(sh.c[qb] + w);
-                const float4* l4 = reinterpret_cast<const float4*>(sh.nl[qb] + w);
+                const float4* c4 = reinterpret_cast<const float4*>(q.c + w);
+                const float4* l4 = reinterpret_cast<const float4*>(q.nl + w);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                   const float4 c = c4[i / 4], l = l4[i / 4];
@@ -596,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
               if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (d > sh.row[qb][w + i]) x[i] = 0xff800000u;
+                  if (d > q.row[w + i]) x[i] = 0xff800000u;
               }
 #pragma unroll
               for (int i = 0; i < 32; i += 2)
@@ -606,12 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             if (slot >= 0 && slot < a.num_slots) sh.sum[e][tile * kTile + p] += t.x + t.y;
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(&s_empty[e]);
+            if (lane == 0) tc::bar_arrive(&s_empty[st]);
           }
         }
-        if (s + 1 == seg.to || (s + 1) / seg.tiles != item) {
+        if (++tile == seg.tiles || s + 1 == seg.to) {
           __syncwarp();
           if (ok && lane == 0) tc::bar_arrive(&q_empty[qb]);
+          tile = 0;
+          ++item_no;
+          if (++block == seg.blocks) block = 0;
+          fresh = true;
         }
       }
       // the segment's sums of both groups, and of all CTAs of the cluster

@@ -47,6 +47,7 @@ import torch
 from . import (new_pool, new_stats, spec_adjust_logits, spec_build_tree, spec_compact_freed_capacity,
                spec_compact_slots, spec_evict_freed_capacity, spec_evict_slots, spec_evict_ws_size, spec_kv4_append,
                spec_kv4_attention, spec_kv4_attention_window, spec_kv4_attention_ws_size, spec_kv4_weight_sums,
+               spec_kv4_weight_sums_ws_size,
                spec_softmax_sample, spec_softmax_topk, spec_verify_greedy, spec_verify_sample,
                spec_verify_sample_qlogits, spec_verify_ws_size, tli_constrain_map, tli_constrain_map_qlogits,
                tli_plan_build, tli_plan_bytes)
@@ -109,6 +110,7 @@ class StepBuffers:
         self.verify_out = None
         self.stats = new_stats(dev)
         self.attention_ws = {}  # run_attention's, by their size, kept from the first call on
+        self.sums_ws = {}       # run_weight_sums's, likewise
         self.evict_out = {}     # run_evict's results and workspaces, by their sizes, likewise
         self.compact_out = None
         if page_size:
@@ -257,10 +259,14 @@ def run_compact(buf: StepBuffers, seq_lens, req_to_token, page_size, kv_pool=Non
 def run_weight_sums(buf: StepBuffers, q, lse, seq_lens, req_to_token, kv_pool, num_kv_heads, sums, scale=None):
     """Adds the attention weights of the accepted path's rows of q [B, N, Hq, D]
     to sums [B, max_ctx]; behind run_compact, with the seq_lens and lse that
-    run_attention had."""
+    run_attention had.  The workspace is kept as run_attention's."""
     v = buf.verify_out
+    need = spec_kv4_weight_sums_ws_size(*q.shape[:3], int(num_kv_heads), q.shape[3])
+    ws = buf.sums_ws.get(need)
+    if need and ws is None:
+        ws = buf.sums_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
     return spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, accept_path=v["accept_path"],
-                                accept_length=v["accept_length"], prev=sums, scale=scale, stats=buf.stats)
+                                accept_length=v["accept_length"], prev=sums, scale=scale, ws=ws, stats=buf.stats)
 
 
 def run_evict(buf: StepBuffers, sums, seq_lens, req_to_token, page_size, budget, limit=None, sinks=0, recent=0,

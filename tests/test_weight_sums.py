@@ -81,9 +81,12 @@ def test_host_checks():
     lib, null = sd.lib(), None
 
     def call(B=1, N=1, Hq=2, Hkv=1, D=64, q=null, qs=128, lse=null, pool=null, slots=8, stride=80, lens=null, table=null,
-             ctx=8, scale=1.0, out=null):
+             ctx=8, scale=1.0, out=null, ws=null, wsb=0):
         return lib.spec_kv4_weight_sums(B, N, Hq, Hkv, D, q, qs, lse, null, null, pool, slots, stride, lens, table, ctx,
-                                        scale, null, out, null, null)
+                                        scale, null, out, null, ws, wsb, null)
+    size = lib.spec_kv4_weight_sums_ws_size
+    assert size(1, 1, 32, 1, 128) == 0 and size(1, 8, 32, 8, 64) == 0 and size(1, 33, 1, 1, 128) > 128 * 128 * 2
+    assert size(3, 33, 8, 2, 64) == 6 * size(1, 33, 4, 1, 64) and size(1, 2049, 1, 1, 64) == 0 and size(0, 64, 1, 1, 64) == 0
     assert call(B=-1) == -1 and call(N=-1) == -1 and call(Hkv=0) == -1 and call(Hq=3, Hkv=2) == -1 and call(ctx=0) == -1
     assert call(slots=0) == -1 and call(scale=float("nan")) == -1 and call(scale=-1.0) == -1
     assert call(D=96) == -2 and call(N=2049) == -2 and call(B=65536) == -2 and call(Hq=4097) == -2 and call(scale=1e-9) == -2
@@ -96,6 +99,8 @@ def test_host_checks():
             assert call(**{**a, name: odd}) == -2
         for name in a:
             assert call(**{**a, name: null}) == -1
+        many = dict(a, N=17, qs=128)
+        assert call(**many) == -1 and call(**many, ws=odd) == -1 and call(**many, ws=p, wsb=64) == -4
 
 
 def test_binding_refuses_host_tensors():
