@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
   __shared__ int64_t s_warp[kWarps], s_pre;
   __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
-  if (RT > 1 && a.ws != nullptr) write_blocks<D>(a);
 
   // this CTA's stretch [lo, hi) of the line of all requests' chunks, by their
   // cost: the chunks that begin in it.  pre: where request b begins
@@ -410,10 +409,12 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     int64_t mine = 0;
+    bool others = false;  // requests for the tensor-memory kernel
 #pragma unroll 1
     for (int i = b0; i < b1; ++i) {
-      const SumReq r = sum_req(a, i);
-      mine += sum_units(a, r);
+      const SumReq r = any_req(a, i);
+      if (r.rows * a.G <= a.upto) mine += sum_units(a, r);
+      else others = true;
       if (r.bad && blockIdx.x == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
     }
     int64_t incl = mine;
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
       if (lane >= o) incl += y;
     }
     if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
+    others = __syncthreads_or(others) != 0;
+    if (RT > 1 && others) write_blocks<D>(a);
     int64_t total = 0;
     pre = incl - mine;
 #pragma unroll

@@ -243,44 +243,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
       const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
-      auto load_slot = [&](int s) {  // -2: no position
-        slot = -2;
-        if (s >= seg.to) return;
-        const int pos = (seg.t0 + s % seg.tiles) * kTile + p;
-        if (pos < seg.rq.end) slot = __ldg(row + pos);
-      };
-      auto load = [&](int s, uint4* code, uint32_t* meta) {
-#pragma unroll
-        for (int z = 0; z < vecs; ++z) code[z] = make_uint4(0, 0, 0, 0), meta[z] = 0;
-        if (slot == -2) return;
-        const int item = s / seg.tiles;
-        if (slot < 0 || slot >= a.num_slots) {
-          if (item == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
-          return;
+      // where a step is: KV head and tile of the segment
+      struct At {
+        int s, tile, block, h;
+        __device__ __forceinline__ At(const Segments& seg, int step) : s(step) {
+          const int item = step / seg.tiles;
+          tile = step - item * seg.tiles, h = item / seg.blocks, block = item - h * seg.blocks;
         }
-        const uint8_t* src = a.pool + slot * a.slot_stride + item / seg.blocks * kv4_head_bytes(D);
-#pragma unroll
-        for (int z = 0; z < vecs; ++z) code[z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
-        if (D == 128) {
-          const uint4 m = __ldg(reinterpret_cast<const uint4*>(src + D));
-          meta[0] = m.x, meta[1] = m.y, meta[vecs - 2] = m.z, meta[vecs - 1] = m.w;
-        } else {
-          const uint2 m = __ldg(reinterpret_cast<const uint2*>(src + D));
-          meta[0] = m.x, meta[1] = m.y;
+        __device__ __forceinline__ void next(const Segments& seg) {  // the group's next step
+          s += 2;
+          tile += 2;
+          while (tile >= seg.tiles) {
+            tile -= seg.tiles;
+            if (++block == seg.blocks) block = 0, ++h;
+          }
         }
       };
       const int mine = seg.from + static_cast<int>((j ^ u) & 1);  // the group's first step
-      load_slot(mine);
-      load(mine, code2, meta2);
-      load_slot(mine + 2);
+      At of_slot(seg, mine), of_code(seg, mine);
+      auto load_slot = [&]() {  // -2: no position
+        slot = -2;
+        const int pos = (seg.t0 + of_slot.tile) * kTile + p;
+        if (of_slot.s < seg.to && pos < seg.rq.end) slot = __ldg(row + pos);
+        of_slot.next(seg);
+      };
+      auto load = [&](uint4* code, uint32_t* meta) {
+        if (slot >= 0 && slot < a.num_slots) {
+          const uint8_t* src = a.pool + slot * a.slot_stride + of_code.h * kv4_head_bytes(D);
+#pragma unroll
+          for (int z = 0; z < vecs; ++z) code[z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
+          if (D == 128) {
+            const uint4 m = __ldg(reinterpret_cast<const uint4*>(src + D));
+            meta[0] = m.x, meta[1] = m.y, meta[vecs - 2] = m.z, meta[vecs - 1] = m.w;
+          } else {
+            const uint2 m = __ldg(reinterpret_cast<const uint2*>(src + D));
+            meta[0] = m.x, meta[1] = m.y;
+          }
+        } else {
+#pragma unroll
+          for (int z = 0; z < vecs; ++z) code[z] = make_uint4(0, 0, 0, 0), meta[z] = 0;
+          if (slot != -2 && of_code.h == 0 && of_code.block == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+        }
+        of_code.next(seg);
+      };
+      load_slot();
+      load(code2, meta2);
+      load_slot();
 #pragma unroll 1
       for (int s = seg.from; s < seg.to; ++s, ++j) {
         const int st = j & 1;
         if (st != u) continue;
 #pragma unroll
         for (int z = 0; z < vecs; ++z) code[z] = code2[z], meta[z] = meta2[z];
-        load(s + 2, code2, meta2);
-        load_slot(s + 4);
+        load(code2, meta2);
+        load_slot();
         // the stage is free once the products of two steps before are there
         if (ok && j >= 2) ok = wait_warp(&s_full[st], ((j >> 1) - 1) & 1, &s_abort);
         if (!ok) continue;
@@ -389,75 +405,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     while (seg.next(a, rank, ranks)) {
       const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
       for (int i = p; i < seg.tiles * kTile; i += kTile) sh.sum[e][i] = 0.0f;
-      int item = seg.from / seg.tiles, tile = seg.from - item * seg.tiles, block = item % seg.blocks;
-      bool fresh = true;
+      int tile = seg.from % seg.tiles, block = seg.from / seg.tiles % seg.blocks;
 #pragma unroll 1
-      for (int s = seg.from; s < seg.to; ++s, ++j) {
-        const int qb = item_no & 1, st = j & 1;
-        if (fresh && ok) ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
-        fresh = false;
-        if (ok) {
-          const int pos = (seg.t0 + tile) * kTile + p;
-          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
-          const int32_t slot = pos < seg.rq.end ? __ldg(row + pos) : -1;
-          const uint32_t col0 = lanes + st * kCols;
+      for (int s = seg.from; ok && s < seg.to; ++item_no) {
+        const int qb = item_no & 1, count = min(seg.tiles - tile, seg.to - s);  // tiles of this head's rows
+        ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
+        if (!ok) break;
+        const RowsBlock<D>& q = sh.q[qb];
+        const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+        const bool fold = q.fold != 0;
+        const float2 one = splat(q.c[0]);
+        float* sum = sh.sum[e] + tile * kTile + p;
+        int d = (seg.t0 + tile) * kTile + p - seg.rq.start;  // rows from this one on see the position
+#pragma unroll 1
+        for (int i = 0; i < count; ++i, ++j, d += kTile, sum += kTile) {
+          const int st = j & 1;
           ok = wait_warp(&s_full[st], (j >> 1) & 1, &s_abort);
-          if (ok) {
-            tc::fence_after();
-            const bool whole = (seg.t0 + tile + 1) * kTile <= seg.rq.start + 1;
-            const RowsBlock<D>& q = sh.q[qb];
-            const bool fold = q.fold != 0;
-            const float2 one = splat(q.c[0]);
-            const int d = pos - seg.rq.start;  // rows from this one on see the position
-            float2 acc[2] = {splat(0.0f), splat(0.0f)};
+          if (!ok) break;
+          tc::fence_after();
+          const bool whole = d - p + kTile <= 1;
+          float2 acc[2] = {splat(0.0f), splat(0.0f)};
 #pragma unroll 1
-            for (int w = 32 * e; w < n; w += 64) {  // a group's columns
-              uint32_t x[32];
-              tc::ld32(col0 + w, x);
-              tc::wait_ld32(x);
-              if (fold) {
+          for (int w = 32 * e; w < n; w += 64) {  // a group's columns
+            uint32_t x[32];
+            tc::ld32(lanes + st * kCols + w, x);
+            tc::wait_ld32(x);
+            if (fold) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), one);
-                  x[i] = __float_as_uint(y.x);
-                  x[i + 1] = __float_as_uint(y.y);
-                }
-              } else {
-                const float4* c4 = reinterpret_cast<const float4*>(q.c + w);
-                const float4* l4 = reinterpret_cast<const float4*>(q.nl + w);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 c = c4[i / 4], l = l4[i / 4];
-                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c.x, l.x));
-                  x[i + 1] = __float_as_uint(fmaf(__uint_as_float(x[i + 1]), c.y, l.y));
-                  x[i + 2] = __float_as_uint(fmaf(__uint_as_float(x[i + 2]), c.z, l.z));
-                  x[i + 3] = __float_as_uint(fmaf(__uint_as_float(x[i + 3]), c.w, l.w));
-                }
+              for (int k = 0; k < 32; k += 2) {
+                const float2 y = mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), one);
+                x[k] = __float_as_uint(y.x);
+                x[k + 1] = __float_as_uint(y.y);
               }
-              if (!whole) {
+            } else {
+              const float4* c4 = reinterpret_cast<const float4*>(q.c + w);
+              const float4* l4 = reinterpret_cast<const float4*>(q.nl + w);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (d > q.row[w + i]) x[i] = 0xff800000u;
+              for (int k = 0; k < 32; k += 4) {
+                const float4 c = c4[k / 4], l = l4[k / 4];
+                x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), c.x, l.x));
+                x[k + 1] = __float_as_uint(fmaf(__uint_as_float(x[k + 1]), c.y, l.y));
+                x[k + 2] = __float_as_uint(fmaf(__uint_as_float(x[k + 2]), c.z, l.z));
+                x[k + 3] = __float_as_uint(fmaf(__uint_as_float(x[k + 3]), c.w, l.w));
               }
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], exp2_2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]))));
             }
-            const float2 t = add2(acc[0], acc[1]);
-            if (slot >= 0 && slot < a.num_slots) sh.sum[e][tile * kTile + p] += t.x + t.y;
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(&s_empty[st]);
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (d > q.row[w + k]) x[k] = 0xff800000u;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2)
+              acc[(k >> 1) & 1] = add2(acc[(k >> 1) & 1], exp2_2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))));
           }
-        }
-        if (++tile == seg.tiles || s + 1 == seg.to) {
+          tc::fence_before();
           __syncwarp();
-          if (ok && lane == 0) tc::bar_arrive(&q_empty[qb]);
-          tile = 0;
-          ++item_no;
-          if (++block == seg.blocks) block = 0;
-          fresh = true;
+          if (lane == 0) tc::bar_arrive(&s_empty[st]);
+          const float2 t = add2(acc[0], acc[1]);
+          *sum += t.x + t.y;
         }
+        __syncwarp();
+        if (ok && lane == 0) tc::bar_arrive(&q_empty[qb]);
+        s += count;
+        tile = 0;
+        if (++block == seg.blocks) block = 0;
       }
       // the segment's sums of both groups, and of all CTAs of the cluster
       __syncwarp();
@@ -470,6 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         if (ranks == 1) x = sh.sum[0][i] + sh.sum[1][i];
         else
           for (int z = 0; z < ranks; ++z) x += ld_cluster(&sh.sum[0][i], z) + ld_cluster(&sh.sum[1][i], z);
+        // a position without a slot has been a row of zeros so far
+        const int32_t slot = __ldg(row + seg.t0 * kTile + i);
+        if (slot < 0 || slot >= a.num_slots) x = 0.0f;
         a.out[at + i] = a.prev ? a.prev[at + i] + x : x;
       }
       __syncwarp();
