@@ -73,13 +73,6 @@ __device__ __forceinline__ int chunks_before(int64_t units, int cost) {
   return static_cast<int>(x <= 0xffffffffll ? static_cast<uint32_t>(x) / static_cast<uint32_t>(cost) : x / cost);
 }
 
-// Shared memory of a position in a stage: K's codes, then K's (step, lo); 20
-// words (D = 64: 12) apart, which makes all reads free of bank conflicts.
-template <int D>
-struct Pos {
-  static constexpr int kCodes = D / 2, kBytes = D == 128 ? 80 : 48;
-};
-
 // A tile of eight query rows of a KV head as B fragments: lane by lane, per
 // group of 32 channels two steps of 16; the groups' sums; and of its columns
 // the factor that turns products into units of log2, lse in these (rows that
@@ -227,8 +220,8 @@ struct Ring {
       if (lane == 0) there[st] = have;
 #pragma unroll
       for (int u = 0; u < per; ++u)
-        put(to + (u * (32 / per) + lane / per) * P::kBytes + (lane % per) * 16, src[u] + off, ((size >> u) & 1u) * 16u);
-      put(to + lane * P::kBytes + P::kCodes, meta + off, ((have >> lane) & 1u) * 16u);
+        put_async(to + (u * (32 / per) + lane / per) * P::kBytes + (lane % per) * 16, src[u] + off, ((size >> u) & 1u) * 16u);
+      put_async(to + lane * P::kBytes + P::kCodes, meta + off, ((have >> lane) & 1u) * 16u);
       --left;
       if (++head == heads) {
         head = 0;
@@ -237,9 +230,6 @@ struct Ring {
       }
     }
     cp_async_commit();
-  }
-  __device__ __forceinline__ static void put(unsigned dst, uint64_t src, unsigned size) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
   }
 };
 

@@ -67,6 +67,16 @@ struct RowsBlock {
 };
 static_assert(sizeof(RowsBlock<128>) % 1024 == 0 && sizeof(RowsBlock<64>) % 1024 == 0, "blocks lie one after another");
 
+// A position of a stage in shared memory: K's codes, then K's (step, lo); 20
+// words (D = 64: 12) apart, which makes all reads free of bank conflicts.
+template <int D>
+struct Pos {
+  static constexpr int kCodes = D / 2, kBytes = D == 128 ? 80 : 48;
+};
+__device__ __forceinline__ void put_async(unsigned dst, uint64_t src, unsigned size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+
 // The tensor-memory kernel's entry (kv4_sums_rows.cu).
 int launch_sums_rows(const SumArgs& a, int D, int sms, cudaStream_t s);
 

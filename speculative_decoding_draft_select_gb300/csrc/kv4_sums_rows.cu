@@ -16,17 +16,16 @@
 //   warps 0 .. 7    weights: a thread's position is its lane; two groups of four
 //       warps share a step's columns, since the next products but one wait for it.
 //   warps 8 .. 15   unpack the cache, a position a thread: two groups take turns,
-//       each with its next step's codes on their way to registers and the
-//       slots of the one behind.
+//       each warp with a ring of asynchronous copies of its 32 positions.
 //   warp 16         issues the matrix instructions.
 //   warp 17         copies the next KV head's rows, which kv4_sums_kernel has laid
 //       out in the workspace.
 // Steps go head by head over a segment of up to kSegTiles tiles of a request, so
-// that a head's rows are unpacked once a segment; the segment's sums stay in
-// shared memory until its last head.  Where there are few tiles, the CTAs of a
-// cluster share a segment's steps and add their sums through distributed shared
-// memory, in rank order.  Every wait is bounded; a wait that runs out is counted
-// in SPEC_STAT_WAIT_TIMEOUT and the CTA goes on without working (results void).
+// that a head's rows are copied once a segment; the segment's sums stay in shared
+// memory until its last head.  The CTAs of a cluster share a segment's steps and
+// add their sums through distributed shared memory, in rank order.  Every wait is
+// bounded; a wait that runs out is counted in SPEC_STAT_WAIT_TIMEOUT and the CTA
+// goes on without working (results void).
 #include "kv4_sums.cuh"
 #include "tcgen05.cuh"
 
@@ -38,12 +37,14 @@ constexpr int kCols = kRowsBlock;  // query rows of a step at most
 constexpr int kSegTiles = 48;    // tiles of a segment at most
 constexpr int kUnpackWarp = 8, kIssueWarp = 16, kRowWarp = 17;
 constexpr int kThreads = 18 * 32;
+constexpr int kRing = 3;         // stages of an unpacking warp
 
 template <int D>
 struct RowsShared {
   RowsBlock<D> q[2];                // 1024-byte aligned
   uint8_t k_lo[2][kTile * 32];      // 128 rows of 16 elements, no swizzle
   float sum[2][kSegTiles * kTile];  // of the two groups
+  uint8_t ring[8][kRing][32 * Pos<D>::kBytes];  // of the unpacking warps
 };
 // Tensor memory: S of both buffers, then hi and rem of both stages.
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kCols;
@@ -116,6 +117,16 @@ __device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, int* a
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
   return __all_sync(0xffffffffu, wait_lane(bar, parity, abort));
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
   unsigned r;
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   __shared__ int s_abort, s_b;
   __shared__ int64_t s_warp[kThreads / 32], s_pre;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = ranks > 1 ? static_cast<int>(cluster_rank()) : 0, cluster = blockIdx.x / ranks;
+  const int rank = static_cast<int>(cluster_rank()), cluster = blockIdx.x / ranks;
 
   // the cluster's stretch of the line
   Segments seg;
@@ -226,20 +237,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
           s = (item + 1) * seg.tiles;  // the next item's first step
         }
       }
-      if (ranks > 1) {
-        __syncwarp();
-        cluster_barrier();
-        cluster_barrier();
-      }
+      __syncwarp();
+      cluster_barrier();
+      cluster_barrier();
     }
     __syncwarp();
   } else if (warp >= kUnpackWarp && warp < kIssueWarp) {
     // ------------------------------------------------------------- unpack
     const int u = (warp - kUnpackWarp) >> 2, uw = warp & 3, p = uw * 32 + lane;
     constexpr int vecs = D / 32;
-    uint4 code[vecs], code2[vecs];
-    uint32_t meta[vecs], meta2[vecs];
-    int32_t slot;  // of the group's step behind the one whose codes are on their way
+    const unsigned ring = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp - kUnpackWarp][0]));
+    int32_t slot;  // of this lane's position in the group's step to be copied next
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
       const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
@@ -267,36 +275,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         if (of_slot.s < seg.to && pos < seg.rq.end) slot = __ldg(row + pos);
         of_slot.next(seg);
       };
-      auto load = [&](uint4* code, uint32_t* meta) {
-        if (slot >= 0 && slot < a.num_slots) {
-          const uint8_t* src = a.pool + slot * a.slot_stride + of_code.h * kv4_head_bytes(D);
+      auto copy = [&](int to) {  // the positions' codes and (step, lo) to a stage; one commit group
+        if (of_code.s < seg.to) {
+          using P = Pos<D>;
+          constexpr int per = D / 32;  // lanes of a position's codes
+          const bool here = slot >= 0 && slot < a.num_slots;
+          if (!here && slot != -2 && of_code.h == 0 && of_code.block == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+          const unsigned have = __ballot_sync(0xffffffffu, here);
+          const uint64_t mine = reinterpret_cast<uint64_t>(a.pool) +
+                                static_cast<uint64_t>(here ? slot : 0) * static_cast<uint64_t>(a.slot_stride) +
+                                static_cast<uint32_t>(of_code.h) * kv4_head_bytes(D);
+          const unsigned at = ring + to * (32 * P::kBytes);
 #pragma unroll
-          for (int z = 0; z < vecs; ++z) code[z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
-          if (D == 128) {
-            const uint4 m = __ldg(reinterpret_cast<const uint4*>(src + D));
-            meta[0] = m.x, meta[1] = m.y, meta[vecs - 2] = m.z, meta[vecs - 1] = m.w;
-          } else {
-            const uint2 m = __ldg(reinterpret_cast<const uint2*>(src + D));
-            meta[0] = m.x, meta[1] = m.y;
+          for (int z = 0; z < per; ++z) {
+            const int pos = z * (32 / per) + lane / per;
+            const uint64_t src = __shfl_sync(0xffffffffu, mine, pos) + lane % per * 16;
+            put_async(at + pos * P::kBytes + lane % per * 16, src, ((have >> pos) & 1u) * 16u);
           }
-        } else {
-#pragma unroll
-          for (int z = 0; z < vecs; ++z) code[z] = make_uint4(0, 0, 0, 0), meta[z] = 0;
-          if (slot != -2 && of_code.h == 0 && of_code.block == 0) bump(a.stats, SPEC_STAT_BAD_REQUEST);
+          put_async(at + lane * P::kBytes + P::kCodes, mine + D, here ? 16u : 0u);
         }
+        cp_async_commit();
         of_code.next(seg);
       };
       load_slot();
-      load(code2, meta2);
-      load_slot();
+#pragma unroll 1
+      for (int i = 0; i < kRing - 1; ++i) {
+        copy(i);
+        load_slot();
+      }
+      int stage = 0;
 #pragma unroll 1
       for (int s = seg.from; s < seg.to; ++s, ++j) {
         const int st = j & 1;
         if (st != u) continue;
-#pragma unroll
-        for (int z = 0; z < vecs; ++z) code[z] = code2[z], meta[z] = meta2[z];
-        load(code2, meta2);
+        __syncwarp();  // every lane has read the stage before
+        copy(stage == 0 ? kRing - 1 : stage - 1);
         load_slot();
+        cp_async_wait<kRing - 1>();
+        __syncwarp();  // every lane's copies of this step have landed
+        uint4 code[vecs];
+        uint32_t meta[vecs];
+        const uint8_t* from = sh.ring[warp - kUnpackWarp][stage] + lane * Pos<D>::kBytes;
+#pragma unroll
+        for (int z = 0; z < vecs; ++z) {
+          code[z] = *reinterpret_cast<const uint4*>(from + 16 * z);
+          meta[z] = *reinterpret_cast<const uint32_t*>(from + Pos<D>::kCodes + 4 * z);
+        }
+        stage = stage + 1 == kRing ? 0 : stage + 1;
         // the stage is free once the products of two steps before are there
         if (ok && j >= 2) ok = wait_warp(&s_full[st], ((j >> 1) - 1) & 1, &s_abort);
         if (!ok) continue;
@@ -333,38 +358,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&k_full[st]);
       }
-      if (ranks > 1) {
-        __syncwarp();
-        cluster_barrier();
-        cluster_barrier();
-      }
+      __syncwarp();
+      cluster_barrier();
+      cluster_barrier();
     }
   } else if (warp == kIssueWarp) {
     // -------------------------------------------------------------- issue
-    // one lane, with nothing between two steps but the waits: the products are
-    // what a step takes longest for
+    // the whole warp walks the steps, so that the operands' addresses are known to
+    // be the same in all lanes (uniform registers); one lane issues
+    const bool leader = elect_one();
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
-      if (lane == 0) {
-        int item = seg.from / seg.tiles, left = min((item + 1) * seg.tiles, seg.to) - seg.from;  // steps of the item
-        int block = item % seg.blocks;
+      int left = min((seg.from / seg.tiles + 1) * seg.tiles, seg.to) - seg.from;  // steps of the item
+      int block = seg.from / seg.tiles % seg.blocks;
 #pragma unroll 1
-        for (int s = seg.from; ok && s < seg.to;) {
-          const int qb = item_no & 1;
-          const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
-          const uint32_t id = tc::idesc_f16(n, false);
-          const uint64_t qd = tc::desc(tc::smem_addr(sh.q[qb].q), 0);
-          const uint64_t sums = desc_plain(tc::smem_addr(sh.q[qb].sums), kCols * 16);
-          ok = wait_lane(&q_full[qb], (item_no >> 1) & 1, &s_abort);
+      for (int s = seg.from; ok && s < seg.to;) {
+        const int qb = uniform(item_no & 1);
+        const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
+        const uint32_t id = uniform(tc::idesc_f16(n, false));
+        const uint64_t qd = tc::desc(tc::smem_addr(sh.q[0].q) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), 0);
+        const uint64_t sums = desc_plain(tc::smem_addr(sh.q[0].sums) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), kCols * 16);
+        ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
 #pragma unroll 1
-          for (int i = 0; ok && i < left; ++i, ++j) {
-            const int st = j & 1;
-            const uint32_t d = tmem + st * kCols, k_at = tmem + kTmemA + st * D;
-            const uint64_t lo = desc_plain(tc::smem_addr(sh.k_lo[st]), kTile * 16);
-            ok = wait_lane(&k_full[st], (j >> 1) & 1, &s_abort);
-            if (j >= 2) ok = ok && wait_lane(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
-            if (!ok) break;
-            tc::fence_after();
+        for (int i = 0; ok && i < left; ++i, ++j) {
+          const int st = uniform(j & 1);
+          const uint32_t d = uniform(tmem) + st * kCols, k_at = uniform(tmem) + kTmemA + st * D;
+          const uint64_t lo = desc_plain(tc::smem_addr(sh.k_lo[0]) + st * static_cast<uint32_t>(sizeof(sh.k_lo[0])), kTile * 16);
+          ok = wait_warp(&k_full[st], (j >> 1) & 1, &s_abort);
+          if (j >= 2) ok = ok && wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
+          if (!ok) break;
+          tc::fence_after();
+          if (leader) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -374,22 +398,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             tc::mma_ss(d, lo, sums, id, 1u);
             tc::commit(&s_full[st]);
           }
-          if (ok) tc::commit(&q_empty[qb]);
-          s += left;
-          left = min(seg.tiles, seg.to - s);
-          ++item;
-          ++item_no;
-          if (++block == seg.blocks) block = 0;
+          __syncwarp();
         }
-      }
-      if (ranks > 1) {
+        if (ok && leader) tc::commit(&q_empty[qb]);
         __syncwarp();
-        cluster_barrier();
-        cluster_barrier();
+        s += left;
+        left = min(seg.tiles, seg.to - s);
+        ++item_no;
+        if (++block == seg.blocks) block = 0;
       }
+      __syncwarp();
+      cluster_barrier();
+      cluster_barrier();
     }
     __syncwarp();
-    if (lane == 0) {
+    if (leader) {
       // nothing in flight when tensor memory is freed
       tc::commit(&drain);
       const long long t0 = clock64();
@@ -472,23 +495,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
       }
       // the segment's sums of both groups, and of all CTAs of the cluster
       __syncwarp();
-      if (ranks > 1) cluster_barrier();
-      else asm volatile("bar.sync 1, 256;" ::: "memory");
+      cluster_barrier();
       const int64_t at = static_cast<int64_t>(seg.b) * a.max_ctx + static_cast<int64_t>(seg.t0) * kTile;
       const int count = min(seg.tiles * kTile, seg.rq.end - seg.t0 * kTile);
       for (int i = rank * 256 + tid; i < count; i += ranks * 256) {
         float x = 0.0f;
-        if (ranks == 1) x = sh.sum[0][i] + sh.sum[1][i];
-        else
-          for (int z = 0; z < ranks; ++z) x += ld_cluster(&sh.sum[0][i], z) + ld_cluster(&sh.sum[1][i], z);
+        for (int z = 0; z < ranks; ++z) x += ld_cluster(&sh.sum[0][i], z) + ld_cluster(&sh.sum[1][i], z);
         // a position without a slot has been a row of zeros so far
         const int32_t slot = __ldg(row + seg.t0 * kTile + i);
         if (slot < 0 || slot >= a.num_slots) x = 0.0f;
         a.out[at + i] = a.prev ? a.prev[at + i] + x : x;
       }
       __syncwarp();
-      if (ranks > 1) cluster_barrier();
-      else asm volatile("bar.sync 1, 256;" ::: "memory");
+      cluster_barrier();
     }
   }
   tc::fence_before();
@@ -516,7 +535,7 @@ int launch_rows(const SumArgs& a, int ranks, int sms, cudaStream_t s) {
 int launch_sums_rows(const SumArgs& a, int D, int sms, cudaStream_t s) {
   // clusters where the longest requests there can be would leave SMs without a
   // tile of their own
-  const int ranks = a.B * ((a.max_ctx + kTile - 1) / kTile) >= 2 * sms ? 1 : 4;
+  const int ranks = a.B * ((a.max_ctx + kTile - 1) / kTile) <= sms / 4 ? 4 : 2;
   return D == 128 ? launch_rows<128>(a, ranks, sms, s) : launch_rows<64>(a, ranks, sms, s);
 }
 
