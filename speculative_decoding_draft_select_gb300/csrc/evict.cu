@@ -31,8 +31,8 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCtas = 8;    // of a cluster
-constexpr int kSlice = 16384;  // keys of a CTA that stay in shared memory
+constexpr int kMaxCtas = 16;   // of a cluster
+constexpr int kSlice = 131072 / kMaxCtas;  // keys of a CTA that stay in shared memory
 
 struct EvictArgs {
   int B, page, budget, limit, sinks, recent;
@@ -94,6 +94,13 @@ __device__ __forceinline__ uint4 ld_cluster4(const unsigned* local, unsigned ran
   return v;
 }
 
+__device__ __forceinline__ void st_cluster4(unsigned* local, unsigned rank, const uint4& v) {
+  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
+  unsigned r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(r), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // The sum over the threads before this one.
 __device__ __forceinline__ int block_before(int v, int2* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -113,7 +120,7 @@ __device__ __forceinline__ int block_before(int v, int2* sh) {
 }
 
 struct SelectShared {
-  unsigned hist[kBins];
+  unsigned hist[kBins], total[kBins];  // this CTA's, the cluster's
   int2 scan[kSelWarps];
   int64_t freed[kSelWarps];
   unsigned digit, above;
@@ -191,6 +198,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
   }
   auto key_at = [&](int i) { return i < held ? sh.key[i] : evict_key(a, sums, p0 + i, n); };
+  // visit(key, i) for i = from, from + every, ... below to; kAhead keys at a time
+  // where shared memory holds them all
+  auto for_keys = [&](int from, int to, int every, auto&& visit) {
+    int i = from;
+    if (held == mine) {
+      for (; i + (kAhead - 1) * every < to; i += kAhead * every) {
+        uint32_t k[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) k[u] = sh.key[i + u * every];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) visit(k[u], i + u * every);
+      }
+    }
+    for (; i < to; i += every) visit(key_at(i), i);
+  };
 
   uint32_t prefix = 0;
   int need = a.budget;  // positions still to be taken among those with this prefix
@@ -199,27 +221,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < mine; i += kSelThreads) {
-      const uint32_t k = key_at(i);
+    for_keys(tid, mine, kSelThreads, [&](uint32_t k, int) {
       if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-    }
+    });
     if (ctas > 1) cluster_barrier();
     else __syncthreads();
+    // each CTA adds its share of the bins up and tells the others
+    const unsigned* bins = sh.hist;
+    if (ctas > 1) {
+      const int quads = kBins / 4 / ctas;
+      if (tid < quads) {
+        const int at = (static_cast<int>(rank) * quads + tid) * 4;
+        uint4 h = make_uint4(0, 0, 0, 0), other[kMaxCtas];  // all loads in flight at once
+#pragma unroll
+        for (int c = 0; c < kMaxCtas; ++c)
+          if (c < ctas) other[c] = ld_cluster4(sh.hist + at, c);
+#pragma unroll
+        for (int c = 0; c < kMaxCtas; ++c)
+          if (c < ctas) h.x += other[c].x, h.y += other[c].y, h.z += other[c].z, h.w += other[c].w;
+#pragma unroll
+        for (int c = 0; c < kMaxCtas; ++c)
+          if (c < ctas) st_cluster4(sh.total + at, c, h);
+      }
+      bins = sh.total;
+      cluster_barrier();
+    }
     // bins from the top: a thread's run of four
     constexpr int per = 4;
     static_assert(per * kSelThreads == kBins, "a run of four bins each");
-    const int low = kBins - per * (tid + 1);  // the run's lowest bin
-    uint4 h = *reinterpret_cast<const uint4*>(sh.hist + low);
-    if (ctas > 1) {
-      uint4 other[kMaxCtas];  // all in flight at once: a load takes about a microsecond
-#pragma unroll
-      for (int c = 0; c < kMaxCtas; ++c)
-        if (c < ctas) other[c] = ld_cluster4(sh.hist + low, c);
-      h = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < kMaxCtas; ++c)
-        if (c < ctas) h.x += other[c].x, h.y += other[c].y, h.z += other[c].z, h.w += other[c].w;
-    }
+    const uint4 h = *reinterpret_cast<const uint4*>(bins + kBins - per * (tid + 1));
     const unsigned cnt[per] = {h.w, h.z, h.y, h.x};
     const int mine_sum = static_cast<int>(h.x + h.y + h.z + h.w);
     int run = block_before(mine_sum, sh.scan);
@@ -231,8 +261,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
       run += static_cast<int>(cnt[j]);
     }
-    if (ctas > 1) cluster_barrier();  // nobody reads the counts any more
-    else __syncthreads();
+    __syncthreads();
     prefix = prefix << bits | sh.digit;
     need -= static_cast<int>(sh.above);
     __syncthreads();
@@ -243,11 +272,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int run = ((mine + 31) / 32 + kSelWarps - 1) / kSelWarps * 32;
   const int i0 = min(mine, warp * run), i1 = min(mine, i0 + run);
   int2 found = make_int2(0, 0);
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;
-    found.x += __popc(__ballot_sync(0xffffffffu, k > prefix && i + lane < i1));
-    found.y += __popc(__ballot_sync(0xffffffffu, k == prefix && i + lane < i1));
-  }
+  for_keys(i0 + lane, i1, 32, [&](uint32_t k, int) {
+    found.x += k > prefix;
+    found.y += k == prefix;
+  });
+  found.x = warp_sum_int(found.x);
+  found.y = warp_sum_int(found.y);
   if (lane == 0) sh.scan[warp] = found;
   __syncthreads();
   int2 at = make_int2(0, 0), total = make_int2(0, 0);
@@ -270,16 +300,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int32_t* ws_table = a.ws_table + static_cast<int64_t>(b) * a.budget;
   float* ws_sums = a.ws_sums + static_cast<int64_t>(b) * a.budget;
   const unsigned below = (1u << lane) - 1u;
-  constexpr int kWords = 4;  // words of 32 positions whose loads are in flight together
-  for (int w0 = i0; w0 < i1; w0 += 32 * kWords) {
-    float x[kWords];
-    int32_t slot[kWords];
+  constexpr int kWords = 4;  // words of 32 positions: loads in flight for the next ones while these find their places
+  float x[kWords], x2[kWords];
+  int32_t slot[kWords], slot2[kWords];
+  auto fetch = [&](int w0) {
 #pragma unroll
     for (int u = 0; u < kWords; ++u) {
-      const int i = w0 + 32 * u + lane, p = p0 + min(i, i1 - 1);
-      x[u] = __ldg(sums + p);
-      slot[u] = table[p];
+      const int p = p0 + min(w0 + 32 * u + lane, i1 - 1);
+      x2[u] = __ldg(sums + p);
+      slot2[u] = table[p];
     }
+  };
+  if (i0 < i1) fetch(i0);
+  for (int w0 = i0; w0 < i1; w0 += 32 * kWords) {
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) x[u] = x2[u], slot[u] = slot2[u];
+    if (w0 + 32 * kWords < i1) fetch(w0 + 32 * kWords);
 #pragma unroll
     for (int u = 0; u < kWords; ++u) {
       const int i = w0 + 32 * u + lane, p = p0 + i;
@@ -312,8 +348,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   if (ctas > 1) cluster_barrier();
   else __syncthreads();
   for (int i = t0; i < a.budget; i += kWords * step) {
-    float x[kWords];
-    int32_t slot[kWords];
 #pragma unroll
     for (int u = 0; u < kWords; ++u)
       if (i + u * step < a.budget) x[u] = ws_sums[i + u * step], slot[u] = ws_table[i + u * step];
@@ -404,7 +438,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
 // CTAs of a request's cluster, by the longest request there can be: a CTA's
 // keys then fit its shared memory up to 131072 positions.
 int cluster_of(int64_t max_ctx) {
-  return max_ctx <= 4096 ? 1 : max_ctx <= 8192 ? 2 : max_ctx <= 16384 ? 4 : 8;
+  return max_ctx <= 4096 ? 1 : max_ctx <= 8192 ? 2 : max_ctx <= 16384 ? 4 : max_ctx <= 32768 ? 8 : 16;
 }
 
 size_t evict_list(int B, int budget) { return align256(static_cast<size_t>(B) * budget * 4); }
@@ -460,6 +494,11 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
               stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!allow_smem<evict_select_kernel>(sizeof(SelectShared))) return SPEC_ERR_CUDA;
+  // clusters of 16 are not portable: allowed here
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
   const int ctas = B == 0 ? 1 : cluster_of(max_ctx);
   launch_kc(evict_select_kernel, static_cast<unsigned>(B == 0 ? 1 : B * ctas), kSelThreads, sizeof(SelectShared), s,
             ctas, a, ctas);
