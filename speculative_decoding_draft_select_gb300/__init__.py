@@ -778,6 +778,7 @@ def spec_evict_freed_capacity(B, max_ctx, page_size, budget):
     return int(lib().spec_evict_freed_capacity(int(B), int(max_ctx), int(page_size), int(budget)))
 
 
+@functools.lru_cache(maxsize=256)  # of the sizes alone
 def spec_evict_ws_size(B, page_size, budget) -> int:
     return int(lib().spec_evict_ws_size(int(B), int(page_size), int(budget)))
 

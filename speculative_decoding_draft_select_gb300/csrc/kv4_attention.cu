@@ -42,7 +42,11 @@ namespace {
 
 constexpr int kTile = 64;        // positions of a tile: 16 per warp
 constexpr int kEnds = 2;         // tiles that a segment's beginning and end cost
-constexpr int kEnds8 = 1;        // of four times 32 positions
+// Of four times 32 positions.  With a window the segments are short and alike,
+// and nearly all CTAs cut one (8 KV heads, B=128, window 2048: 116 us with 1,
+// 109 with 2, 111 with 4).
+template <bool WIN>
+constexpr int kEnds8 = WIN ? 2 : 1;
 constexpr int kAttThreads = 128;
 constexpr int kAttWarps = kAttThreads / 32;
 constexpr float kWeightExp = 15.0f;  // weights are held times 2^15
@@ -567,9 +571,9 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
   CutSegment* cut = reinterpret_cast<CutSegment*>(a.ws) + blockIdx.x;
   if (threadIdx.x == 0) *cut = CutSegment{0, 0, 0, 0};
   Line line;
-  Walk<T, kEnds8, R, WIN> walk;
+  Walk<T, kEnds8<WIN>, R, WIN> walk;
   if (!attn_stretch<kAttThreads>(a, line, walk)) return;
-  Filler<D, 32, kRing8, kEnds8, R, WIN> fill;
+  Filler<D, 32, kRing8, kEnds8<WIN>, R, WIN> fill;
   fill.begin(a, walk, sh.ring[warp][0], sh.there[warp]);
   int st = 0;  // stage of the tile at hand
 
