@@ -21,11 +21,27 @@
 //
 // Positions are the 16 rows of a fragment, query rows its eight columns, so a
 // lane sums its positions' weights over columns, row tiles and heads in
-// registers.  A CTA takes a stretch of a request's 32-position chunks; its items
-// are (head, chunk) pairs, heads outermost, dealt to the warps in runs: a warp
-// turns its head's rows of q into fragments in registers once per run, and
-// fills its own ring of asynchronous copies.  The warps' sums meet in shared
-// memory and are added in the warps' order: no atomics.
+// registers.  A CTA takes a stretch of 32-position chunks, cut by their cost; its
+// items are (chunk, head) pairs, a chunk's heads one after another (a cache row
+// is read from end to end, and its address found once), dealt evenly to the
+// warps.  The rows of q are turned into fragments in shared memory once a request,
+// every warp fills its own ring of asynchronous copies, and the warps' sums meet
+// in shared memory and are added in the warps' order: no atomics.
+//
+// More than 32 rows a KV head go to kv4_sums_rows.cu, request by request; this
+// launch then lays their rows out for it.
+//
+// Bound by the memory: DRAM delivers whole 128-byte lines, and K's codes and
+// (step, lo) of two heads touch all lines of a row, V's half included (180 MB read
+// for 87 MB asked at B=128, 32 heads over 8 of 128, contexts 16..2048).  Measured
+// there: one token 37 us, of which about 6 are the launch, the lengths' scan and
+// the first loads, and the slope over the length is 6.1 TB/s of whole lines;
+// accepted paths of 1 to 7 tokens 58 us (63 with the second launch, which finds
+// nothing to do), where the second pass over the codes of longer paths shows.
+// Before: heads outermost with fragments in registers 48 us (twice the lines,
+// since other warps read a row's other heads at other times); chunks dealt out
+// evenly instead of by cost 72 us for the paths; four row tiles a pass instead of
+// two 63 to 90 (registers: one CTA an SM, or spills).
 #include "kv4_sums.cuh"
 
 namespace specdec {
@@ -38,6 +54,8 @@ constexpr int kMine = kMaxChunks / kWarps + 2;  // chunks that a warp has a part
 constexpr int kStages = 2;
 // Tiles of eight query rows in shared memory: all of a request's where they
 // fit; more heads or rows take several passes, the latter over the same codes.
+// Up to eight rows take the kernel with one tile a pass (one token, B=128: 37 us
+// with it, 41 with two tiles; its 80 registers leave room for three CTAs).
 template <int RT>
 struct SumCfg {
   static constexpr int kTiles = 8 * RT;
@@ -616,7 +634,15 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
   }
 }
 
-// Rows of a KV head above which the tensor-memory kernel takes a request.
+// Rows of a KV head above which the tensor-memory kernel takes a request, whose
+// time hardly depends on them up to 128.  8 KV heads of 128, in us, here / there
+// (two launches):
+//              B=1, 4000     B=4, 60000     B=128, 1000
+//   16 rows     8.8 / 14.6    59 /  99       44 / 88
+//   24 rows    12.4 / 14.8   105 /  99       72 / 88
+//   32 rows    14.1 / 14.8   112 /  99       80 / 89
+//   36 rows    17.6 / 14.9   154 / 101         -
+//   64 rows    24.5 / 15.0   215 / 102         -
 constexpr int kManyRows = 32;
 
 // The upper limits of a call's sizes.

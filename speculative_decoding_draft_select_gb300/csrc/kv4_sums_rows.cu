@@ -26,24 +26,37 @@
 // add their sums through distributed shared memory, in rank order.  Every wait is
 // bounded; a wait that runs out is counted in SPEC_STAT_WAIT_TIMEOUT and the CTA
 // goes on without working (results void).
+//
+// Measured at 32 heads over 8 of 128, 32 rows each, B=4, contexts 60001..131001
+// (100 GFLOP of scores, 391 M exponentials): 182 us with the launch that lays the
+// rows out.  A step takes 1830 cycles, of which the tensor pipe works 1090 (57% of
+// the time).  All products of a step go through one accumulator, one after the
+// other, and two steps' S and operands fill the tensor memory.  The
+// weights take 1350 cycles, the unpacking 2000 for two groups.  786 MB come from
+// DRAM for 489 MB of rows, since the heads of a tile are some twenty steps apart;
+// shorter segments read less and take longer (8 tiles: 204 us).  Steps on the way
+// here: K's operands in shared memory 319 us (the matrix instructions then share
+// its bandwidth), factor and lse read per column and rows converted by every CTA
+// 289, groups of weights on alternate steps 206, one lane of a diverged warp
+// issuing 204 instead of 182.
 #include "kv4_sums.cuh"
 #include "tcgen05.cuh"
 
 namespace specdec {
 namespace {
 
-constexpr int kTile = 128;       // positions of a step
+constexpr int kTile = 128;         // positions of a step
 constexpr int kCols = kRowsBlock;  // query rows of a step at most
-constexpr int kSegTiles = 48;    // tiles of a segment at most
+constexpr int kSegTiles = 48;      // tiles of a segment at most
 constexpr int kUnpackWarp = 8, kIssueWarp = 16, kRowWarp = 17;
 constexpr int kThreads = 18 * 32;
-constexpr int kRing = 3;         // stages of an unpacking warp
+constexpr int kRing = 3;           // stages of an unpacking warp
 
 template <int D>
 struct RowsShared {
   RowsBlock<D> q[2];                // 1024-byte aligned
   uint8_t k_lo[2][kTile * 32];      // 128 rows of 16 elements, no swizzle
-  float sum[2][kSegTiles * kTile];  // of the two groups
+  float sum[2][kSegTiles * kTile];  // of the two groups of weights
   uint8_t ring[8][kRing][32 * Pos<D>::kBytes];  // of the unpacking warps
 };
 // Tensor memory: S of both buffers, then hi and rem of both stages.
@@ -135,6 +148,7 @@ __device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
   return v;
 }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArgs a, int clusters, int ranks) {
   pdl_enter();
@@ -240,6 +254,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
       __syncwarp();
       cluster_barrier();
       cluster_barrier();
+    }
+    if (lane == 0) {
+      // no copy in flight when the CTA ends, although a wait has run out: the last
+      // two items' are all that can be
+      const long long t0 = clock64();
+      for (unsigned i = item_no < 2 ? 0 : item_no - 2; i < item_no; ++i)
+        while (!tc::bar_test(&q_full[i & 1], (i >> 1) & 1) && clock64() - t0 < tc::kWaitCycles) {
+        }
     }
     __syncwarp();
   } else if (warp >= kUnpackWarp && warp < kIssueWarp) {
@@ -533,8 +555,11 @@ int launch_rows(const SumArgs& a, int ranks, int sms, cudaStream_t s) {
 }  // namespace
 
 int launch_sums_rows(const SumArgs& a, int D, int sms, cudaStream_t s) {
-  // clusters where the longest requests there can be would leave SMs without a
-  // tile of their own
+  // wider clusters where even the longest requests there can be give each no more
+  // than a tile (128 rows, 8 KV heads; in us with 1, 2, 4, 8 CTAs: B=1, 4000
+  // positions 26, 21, 17, 24; B=1, 16000: 27, 25, 36, 35; B=8, 2000: 28, 26, 37, 41;
+  // B=4, 60000, 96 rows: 130, 127, 241, 253: clusters of four and more leave SMs
+  // without one)
   const int ranks = a.B * ((a.max_ctx + kTile - 1) / kTile) <= sms / 4 ? 4 : 2;
   return D == 128 ? launch_rows<128>(a, ranks, sms, s) : launch_rows<64>(a, ranks, sms, s);
 }
