@@ -17,18 +17,19 @@
 //            first.  One scan in the positions' order then gives each its place; the slots
 //            and sums of the kept are put aside, and once the cluster has read
 //            all of the old ones they take the first places.
-//   payload  (pages of several tokens) a CTA takes a request's rows, a slice of
-//            their bytes: it reads kept rows in order, a few chunks ahead, and
-//            writes them up.  A row only ever moves towards the front: what a
-//            chunk overwrites has been read by it or a chunk before.  Slices
-//            are independent, so no CTA waits for another.
+//   payload  (pages of several tokens) a CTA, or a cluster where there are few,
+//            takes a request's rows, a slice of their bytes: it reads kept rows
+//            in order, two chunks ahead, and writes them up.  A row only ever
+//            moves towards the front: what a chunk overwrites has been read by it
+//            or a chunk before, so a barrier between a chunk's reads and its
+//            writes is enough.  Slices are independent.
 //
 // Latency: a chain of counting passes with barriers between (for one request of
 // 1500 positions 13.7k cycles: 3.1k for lengths and keys, 1.9k a pass, 2 x 1.7k for
 // the scan, 1k for the copies).  Measured (us): one request, 1500 to 1024 positions
 // 7.1; 4 of 60001..131001 to 32768 21 (with clusters of 8 26, and 33 with every CTA
 // reading all others' counts); 128 of 16..2048 to 768 with rows of 4096 bytes in
-// pages of 16 82, of them 72 for 346 MB of payload (0.72 of the copy rate for all
+// pages of 16 81, of them 72 for 346 MB of payload (0.73 of the copy rate for all
 // of the call's bytes); without the slots read a chunk ahead the payload took twice
 // as long.
 #include <climits>
@@ -372,11 +373,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 
 constexpr int kMoveThreads = 256, kMoveStages = 3;
 
-// V: 16-byte vectors of a slice.
-template <int V>
-__global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const EvictArgs a) {
+constexpr int kSliceVecs = 8;  // 16-byte vectors of a slice: a line of memory
+constexpr int kRowsAt = kMoveThreads / kSliceVecs, kRows = 4 * kRowsAt;  // rows of a CTA's chunk: four vectors a thread
+
+__global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const EvictArgs a, int ctas) {
   pdl_enter();
-  constexpr int kRowsAt = kMoveThreads / V, kRows = 4 * kRowsAt;  // rows of a chunk: four vectors a thread
   __shared__ __align__(16) uint4 sm[kMoveStages][4 * kMoveThreads];
   const int b = blockIdx.y;
   if (evict_len(a, b) <= a.limit) return;
@@ -388,9 +389,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
     if (__ldg(kept + mid) > mid) hi = mid;
     else lo = mid + 1;
   }
-  const int first = lo, chunks = (a.budget - first + kRows - 1) / kRows;
-  const int vec = threadIdx.x % V, r = threadIdx.x / V;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x) * V + vec) * 16;
+  const int rows = kRows * ctas;  // of the cluster's chunk
+  const int chunks = (a.budget - lo + rows - 1) / rows;
+  const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0, slice = blockIdx.x / ctas;
+  const int vec = threadIdx.x % kSliceVecs, first = lo + rank * kRows + threadIdx.x / kSliceVecs;
+  const int64_t col = (static_cast<int64_t>(slice) * kSliceVecs + vec) * 16;
   const bool in = col < a.bps;
   const int32_t* from = a.ws_table + static_cast<int64_t>(b) * a.budget;
   const int32_t* to = a.table + static_cast<int64_t>(b) * a.max_ctx;
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
   auto slots = [&](const int32_t* list, int c, int32_t* s) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = first + c * kRows + j * kRowsAt + r;
+      const int i = first + c * rows + j * kRowsAt;
       s[j] = in && i < a.budget ? __ldg(list + i) : -1;
     }
   };
@@ -429,19 +432,33 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
       if (c >= chunks) break;  // the same in every thread
       read[(s + kMoveStages - 1) % kMoveStages] = fetch(c + kMoveStages - 1, (s + kMoveStages - 1) % kMoveStages);
       cp_async_wait<kMoveStages - 1>();
-      __syncthreads();  // the chunk has been read whole: its rows may be overwritten
+      // the chunk has been read whole (it lies in shared memory): its rows may be
+      // overwritten.  Nothing written before has to be seen, so the cluster's
+      // barrier does not wait for the stores of the chunk before
+      if (ctas > 1)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+      else
+        __syncthreads();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = first + c * kRows + j * kRowsAt + r;
+        const int i = first + c * rows + j * kRowsAt;
         if (((read[s] >> j) & 1u) != 0 && slot_ok(dst[j]))
           *reinterpret_cast<uint4*>(a.kv + dst[j] * a.bps + col) = sm[s][j * kMoveThreads + threadIdx.x];
-        else if (in && i < a.budget && blockIdx.x == 0 && vec == 0)
+        else if (in && i < a.budget && slice == 0 && vec == 0)
           bump(a.stats, SPEC_STAT_BAD_REQUEST);
       }
       slots(to, c + 1, dst);
     }
   }
   cp_async_wait<0>();
+}
+
+// Clusters of 16 are not portable and have to be allowed.
+template <auto KERNEL>
+bool allow_wide_clusters() {
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 // CTAs of a request's cluster, by the longest request there can be: a CTA's
@@ -506,23 +523,22 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
               stats_or_null};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!allow_smem<evict_select_kernel>(sizeof(SelectShared))) return SPEC_ERR_CUDA;
-  // clusters of 16 are not portable: allowed here
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();
-    return SPEC_ERR_CUDA;
-  }
+  if (!allow_wide_clusters<evict_select_kernel>()) return SPEC_ERR_CUDA;
   const int ctas = B == 0 ? 1 : cluster_of(max_ctx);
   launch_kc(evict_select_kernel, static_cast<unsigned>(B == 0 ? 1 : B * ctas), kSelThreads, sizeof(SelectShared), s,
             ctas, a, ctas);
   int e = launch_status();
   if (e != SPEC_OK || B == 0) return e;
   if (page_size == 1 || !kv_pool_or_null) return SPEC_OK;
-  // slices of 128 bytes, or of 32 where a launch of those would leave SMs idle
-  // (128 rows of 4096 bytes: 81 us with 128, 129 with 32; 37 of 320: 19.6 and 18.5)
-  const int64_t vecs = bytes_per_slot / 16;
-  const bool wide_slices = B * ((vecs + 7) / 8) >= 2 * 152;
-  const dim3 grid(static_cast<unsigned>(wide_slices ? (vecs + 7) / 8 : (vecs + 1) / 2), static_cast<unsigned>(B));
-  if (wide_slices) launch_k(evict_payload_kernel<8>, grid, kMoveThreads, 0, s, a);
-  else launch_k(evict_payload_kernel<2>, grid, kMoveThreads, 0, s, a);
+  // CTAs of a slice's cluster: more until the launch fills the SMs twice or a
+  // chunk takes all rows.  In us with one CTA / this rule: 1 request of 100000 to
+  // 50000 positions, rows of 1280 bytes 311 / 56; 4 of 30000 to 20000 166 / 60; 16
+  // of 4000 to 3000, 640 bytes 30 / 23; 128 of 2000 to 1000, 1280 bytes 73 / 73
+  const int64_t slices = (bytes_per_slot / 16 + kSliceVecs - 1) / kSliceVecs;
+  int c = 1;
+  while (c < kMaxCtas && B * slices * c < 2 * 152 && c * kRows < budget) c *= 2;
+  if (!allow_wide_clusters<evict_payload_kernel>()) return SPEC_ERR_CUDA;
+  launch_kc(evict_payload_kernel, dim3(static_cast<unsigned>(slices * c), static_cast<unsigned>(B)), kMoveThreads, 0, s, c,
+            a, c);
   return launch_status();
 }
