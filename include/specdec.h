@@ -12,7 +12,9 @@
  * Around the target's forward over the tree, whose projections are the
  * caller's: the 4-bit KV cache in the kv_pool rows, the attention of the
  * nodes over it under the tree mask, and the adjustment of the target logits
- * (penalties, biases, grammar masks) node by node.
+ * (penalties, biases, grammar masks) node by node.  For a cache that stays
+ * bounded: the attention with a sliding window and sinks, the attention
+ * weights summed per cached position, and eviction by these sums.
  *
  * Sources (web pages, cited by title and section):
  *   [HB]  ai-infra-handbooks, "EAGLE speculative decoding in four parts: why
