@@ -648,7 +648,7 @@ int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* 
  * add up by calls that follow one another.
  *   q [B, N, Hq, D] bf16, rows (b, n) q_stride elements apart; lse [B, N, Hq]
  *     fp32: a row whose lse is not finite adds nothing.
- *   prev_or_null, out [B, max_ctx] fp32 (NULL: zeros); may be the same.
+ *   prev_or_null, out [B, max_ctx] fp32 (NULL: zeros): the same, or apart.
  * Codes and q enter the products exactly (q's elements 2^-24 of its row's
  * largest may round), sums are fp32 in a fixed order; scale log2(e) times a
  * row's largest |q|, and the scores, have to stay in fp32's range.  A position
@@ -688,13 +688,14 @@ int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, in
  *     page's first); with kv_pool_or_null ([num_slots, bytes_per_slot] bytes)
  *     the payload of slot kept[b][i] moves to place i's, sources being read
  *     before they are overwritten; pages wholly behind the budget go to freed
- *     (page id = slot / page_size), in the order of b and page.
+ *     (page id = slot / page_size, -1 of a negative slot), in the order of b and
+ *     page.
  *   kept [B, budget] int32 out (-1 where the request is not cut); new_kv_len
  *     [B] = budget or seq_lens[b]; freed [freed_capacity], num_freed [1].
  * The slots of a call are distinct.  A request with seq_len < 0 or > max_ctx is
  * skipped (new_kv_len = -1), a move from or to a slot outside [0, num_slots)
  * is left out (SPEC_STAT_BAD_REQUEST each).  kv_pool 16-byte aligned,
- * bytes_per_slot a multiple of 16, B <= 65535, max_ctx < 2^30
+ * bytes_per_slot a multiple of 16, B <= 65535, max_ctx and budget < 2^30
  * (SPEC_ERR_UNSUPPORTED otherwise).
  *   ws: spec_evict_ws_size bytes, 16-byte aligned; calls that may overlap need
  *   their own.  spec_evict_freed_capacity: the most entries of freed. */

@@ -194,7 +194,7 @@ def evict(sums, seq_lens, req_to_token, page, budget, limit, sinks, recent, rows
             r["freed"] += slot[:n][gone].tolist()
             r["table"][b, :budget] = slot[kept]
         else:
-            r["freed"] += [int(slot[p]) // page for p in range(-(-budget // page) * page, n, page)]
+            r["freed"] += [max(-1, int(slot[p]) // page) for p in range(-(-budget // page) * page, n, page)]
             if rows is not None:
                 ok = lambda s: 0 <= s < rows.shape[0]  # noqa: E731
                 for i, p in enumerate(kept):

@@ -47,6 +47,7 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_INT_MAX = 2**31 - 1
 
 _SIGS = {
     "spec_softmax_topk": (_I, [_P, _I, _I64, _I64, _F, _F, _I, _P, _P, _P, _P, _P, _P]),
@@ -688,7 +689,7 @@ def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, 
     ``window``.  positions [B, N] int32: spec_build_tree's (None: a chain).
     Positions between the sinks and the window are not read."""
     return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
-                      (positions, int(sinks), int(window)))
+                      (positions, min(int(sinks), _INT_MAX), min(int(window), _INT_MAX)))  # beyond every position
 
 
 def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats, window):
@@ -796,6 +797,8 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
         raise ValueError("sums and req_to_token must be [B, max_ctx]")
     B, ctx = sums.shape
     page_size, budget = int(page_size), int(budget)
+    if max(page_size, budget, int(sinks), int(recent)) > _INT_MAX:
+        raise ValueError("page_size, budget, sinks and recent must be 32-bit numbers")
     i32, f32 = torch.int32, torch.float32
     src = _arg(sums, f32, (B, ctx), dev, "sums")
     dst = src if sums_out is None else _arg(sums_out, f32, (B, ctx), dev, "sums_out")
@@ -812,7 +815,7 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
     freed = out["freed"]
     if ws is None:
         ws = torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=sums.device)
-    rc = lib().spec_evict_slots(B, page_size, budget, budget if limit is None else int(limit), int(sinks), int(recent),
+    rc = lib().spec_evict_slots(B, page_size, budget, budget if limit is None else min(int(limit), _INT_MAX), int(sinks), int(recent),
                                 _arg(seq_lens, i32, (B,), dev, "seq_lens"), src, dst,
                                 _arg(req_to_token, i32, (B, ctx), dev, "req_to_token"), ctx,
                                 _arg(out["kept"], i32, (B, budget), dev, "kept"),

@@ -350,9 +350,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   if (a.page > 1 && rank == 0) {
     const int first = pages_of(a.budget, a.page), count = pages_of(n, a.page) - first;
-    for (int i = tid; i < count; i += kSelThreads)
-      if (spec_in(before + i, a.freed_cap, a.stats))
-        a.freed[before + i] = table[static_cast<int64_t>(first + i) * a.page] / a.page;
+    for (int i = tid; i < count; i += kSelThreads) {
+      const int32_t slot = table[static_cast<int64_t>(first + i) * a.page];
+      if (spec_in(before + i, a.freed_cap, a.stats)) a.freed[before + i] = slot < 0 ? -1 : slot / a.page;
+    }
   }
   // nobody reads the old slots and sums any more
   if (ctas > 1) cluster_barrier();
@@ -497,7 +498,7 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
   if (B < 0 || page_size < 1 || budget < 1 || limit < budget || sinks < 0 || recent < 0 || max_ctx < 1 ||
       static_cast<int64_t>(sinks) + recent > budget)
     return SPEC_ERR_INVALID_ARG;
-  if (max_ctx > INT_MAX / 2 || B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (max_ctx > INT_MAX / 2 || budget > INT_MAX / 2 || B > 65535) return SPEC_ERR_UNSUPPORTED;
   if (!num_freed || freed_capacity < spec_evict_freed_capacity(B, max_ctx, page_size, budget))
     return SPEC_ERR_INVALID_ARG;
   if (B > 0 && (!seq_lens || !sums || !sums_out || !req_to_token || !kept || !new_kv_len || !ws ||

@@ -686,13 +686,17 @@ extern "C" int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const 
   if (!sum_sizes(B, N, Hq, Hkv, D)) return SPEC_ERR_UNSUPPORTED;
   if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
   if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
-  if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kChunk ||
+  if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kRowsBlock ||
       slot_stride > INT32_MAX)
     return SPEC_ERR_UNSUPPORTED;
   if (B == 0 || N == 0) return SPEC_OK;
   if (!q || !lse || !pool || !seq_lens || !req_to_token || !out) return SPEC_ERR_INVALID_ARG;
   for (const void* p : {q, pool})
     if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return SPEC_ERR_UNSUPPORTED;
+  // the old sums are read while others' new ones are written, unless they are the same
+  const uintptr_t p0 = reinterpret_cast<uintptr_t>(prev_or_null), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t wide = static_cast<uintptr_t>(B) * max_ctx * 4;
+  if (prev_or_null && p0 != o0 && p0 < o0 + wide && o0 < p0 + wide) return SPEC_ERR_INVALID_ARG;
   const size_t need = spec_kv4_weight_sums_ws_size(B, N, Hq, Hkv, D);
   if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return SPEC_ERR_INVALID_ARG;
   if (ws_bytes < need) return SPEC_ERR_WORKSPACE;

@@ -85,7 +85,7 @@ def test_host_checks():
     assert call(B=-1) == -1 and call(page=0) == -1 and call(budget=0) == -1 and call(limit=3) == -1 and call(ctx=0) == -1
     assert call(sinks=-1) == -1 and call(recent=-1) == -1 and call(sinks=2, recent=3) == -1
     assert call(sinks=2**31 - 1, recent=2**31 - 1) == -1
-    assert call(B=65536) == -2 and call(ctx=2**30) == -2 and call() == -1
+    assert call(B=65536) == -2 and call(ctx=2**30) == -2 and call(budget=2**30, limit=2**30) == -2 and call() == -1
     cap = lib.spec_evict_freed_capacity
     assert cap(3, 10, 1, 4) == 18 and cap(3, 10, 4, 4) == 6 and cap(3, 10, 4, 5) == 3 and cap(3, 10, 1, 11) == 0
     assert cap(-1, 10, 1, 4) == -1 and cap(1, 0, 1, 4) == -1 and cap(1, 10, 0, 4) == -1 and cap(1, 10, 1, 0) == -1
@@ -189,6 +189,26 @@ def test_bad_requests_and_slots(gpu, page):
     c["table"][3, [50, 59, 2]] = [10**9, -5, -1]               # page > 1: two sources at the end, one place
     run_and_check(c, page, 20, 20, 2, 18, stats=stats)
     assert int(stats[BAD]) == 2 + (3 if page > 1 else 0)
+
+
+@pytest.mark.gpu
+def test_pages_whose_slots_are_none(gpu):
+    """A freed page is named by its first slot: none of a negative one, and never page 0."""
+    c = make(14, [64, 64], 64, 16, width=16)
+    c["table"][0, 48], c["table"][1, 32] = -1, -17
+    got = run_and_check(c, 16, 20, 20, 0, 0)
+    freed = got["freed"][:int(got["num_freed"])].tolist()
+    assert freed[1] == -1 and freed[2] < 0
+
+
+@pytest.mark.gpu
+def test_limits_beyond_32_bits(gpu):
+    c = make(15, [40, 64], 64, 1)
+    x = {k: on(v) for k, v in c.items()}
+    got = sd.spec_evict_slots(x["sums"], x["lens"], x["table"], 1, 20, limit=2**40)
+    assert got["new_kv_len"].tolist() == [40, 64] and int(got["num_freed"]) == 0
+    with pytest.raises(ValueError):
+        sd.spec_evict_slots(x["sums"], x["lens"], x["table"], 1, 2**40)
 
 
 @pytest.mark.gpu

@@ -81,9 +81,9 @@ def test_host_checks():
     lib, null = sd.lib(), None
 
     def call(B=1, N=1, Hq=2, Hkv=1, D=64, q=null, qs=128, lse=null, pool=null, slots=8, stride=80, lens=null, table=null,
-             ctx=8, scale=1.0, out=null, ws=null, wsb=0):
+             ctx=8, scale=1.0, prev=null, out=null, ws=null, wsb=0):
         return lib.spec_kv4_weight_sums(B, N, Hq, Hkv, D, q, qs, lse, null, null, pool, slots, stride, lens, table, ctx,
-                                        scale, null, out, null, ws, wsb, null)
+                                        scale, prev, out, null, ws, wsb, null)
     size = lib.spec_kv4_weight_sums_ws_size
     assert size(1, 1, 32, 1, 128) == 0 and size(1, 8, 32, 8, 64) == 0 and size(1, 33, 1, 1, 128) > 128 * 128 * 2
     assert size(3, 33, 8, 2, 64) == 6 * size(1, 33, 4, 1, 64) and size(1, 2049, 1, 1, 64) == 0 and size(0, 64, 1, 1, 64) == 0
@@ -99,6 +99,7 @@ def test_host_checks():
             assert call(**{**a, name: odd}) == -2
         for name in a:
             assert call(**{**a, name: null}) == -1
+        assert call(**a, prev=ctypes.c_void_p(4100)) == -1        # sums and their new ones overlap in part
         many = dict(a, N=17, qs=128)
         assert call(**many) == -1 and call(**many, ws=odd) == -1 and call(**many, ws=p, wsb=64) == -4
 
