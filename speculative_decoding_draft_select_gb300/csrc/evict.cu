@@ -24,14 +24,15 @@
 //            or a chunk before, so a barrier between a chunk's reads and its
 //            writes is enough.  Slices are independent.
 //
-// Latency: a chain of counting passes with barriers between (for one request of
-// 1500 positions 13.7k cycles: 3.1k for lengths and keys, 1.9k a pass, 2 x 1.7k for
-// the scan, 1k for the copies).  Measured (us): one request, 1500 to 1024 positions
-// 7.1; 4 of 60001..131001 to 32768 21 (with clusters of 8 26, and 33 with every CTA
-// reading all others' counts); 128 of 16..2048 to 768 with rows of 4096 bytes in
-// pages of 16 81, of them 72 for 346 MB of payload (0.73 of the copy rate for all
-// of the call's bytes); without the slots read a chunk ahead the payload took twice
-// as long.
+// Latency: a chain of counting passes with barriers between.  One request of 1500
+// positions takes 13.7k cycles: 3.1k for lengths and keys, 1.9k a pass, 2 x 1.7k for
+// the scan, 1k for the copies; the third pass, told by the second that it has all
+// keys of its digits, is then left out (7.2 to 6.6 us).  Measured (us): that
+// request 6.6; 4 of 60001..131001 to 32768 20 (with clusters of 8 26, and 33 with
+// every CTA reading all others' counts); 128 of 16..2048 to 768 with rows of 4096
+// bytes in pages of 16 78, of them 69 for 346 MB of payload (0.76 of the copy rate
+// for all of the call's bytes).  Without the slots read a chunk ahead the payload
+// took twice as long; with a search by halves for the first row that moves 3 more.
 #include <climits>
 
 #include "common.cuh"
@@ -134,6 +135,7 @@ struct SelectShared {
   int2 scan[kSelWarps];
   int64_t freed[kSelWarps];
   unsigned digit, above;
+  int whole;
   int counts[2];  // this CTA's kept above the last key, and equal to it
   uint32_t key[kSlice];
 };
@@ -268,15 +270,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       if (run < need && need <= run + static_cast<int>(cnt[j])) {
         sh.digit = static_cast<unsigned>(kBins - 1 - (tid * per + j));
         sh.above = static_cast<unsigned>(run);
+        sh.whole = need - run == static_cast<int>(cnt[j]);
       }
       run += static_cast<int>(cnt[j]);
     }
     __syncthreads();
     prefix = prefix << bits | sh.digit;
     need -= static_cast<int>(sh.above);
+    const bool whole = sh.whole != 0;
     __syncthreads();
+    if (whole) {  // all keys with these digits are kept: the rest need not be told apart
+      prefix = (prefix << shift) - 1;  // no key has digits of zeros alone
+      need = 0;
+      break;
+    }
   }
-  // prefix is the last kept key; `need` of those equal to it are kept
+  // keys above prefix are kept, and `need` of those equal to it
 
   // a run of whole words of 32 positions per warp
   const int run = ((mine + 31) / 32 + kSelWarps - 1) / kSelWarps * 32;
@@ -383,12 +392,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_payload_kernel(const Evict
   const int b = blockIdx.y;
   if (evict_len(a, b) <= a.limit) return;
   const int32_t* kept = a.kept + static_cast<int64_t>(b) * a.budget;
-  // kept[i] - i never falls: the rows before the first that moves lie in place
+  // kept[i] - i never falls: the rows before the first that moves lie in place.
+  // The block looks at 256 places at a time, since a search by halves is a chain of
+  // ten loads and more
   int lo = 0, hi = a.budget;
+#pragma unroll 1
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(kept + mid) > mid) hi = mid;
-    else lo = mid + 1;
+    const int step = (hi - lo + kMoveThreads - 1) / kMoveThreads, at = lo + static_cast<int>(threadIdx.x) * step;
+    const int still = __syncthreads_count(at < hi && __ldg(kept + at) == at);  // places before the first that moves
+    if (still == 0) break;
+    hi = min(hi, lo + still * step);
+    lo += (still - 1) * step + 1;
   }
   const int rows = kRows * ctas;  // of the cluster's chunk
   const int chunks = (a.budget - lo + rows - 1) / rows;
@@ -466,9 +480,14 @@ bool allow_wide_clusters() {
 // keys then fit its shared memory up to 131072 positions.  Counts of a cluster
 // cost two of its barriers a pass, so short requests have one CTA (37 requests of
 // up to 4093 positions: 18.4 us with one, 21.4 with two; 131001: 26.1 with 8, 21.2
-// with 16).
-int cluster_of(int64_t max_ctx) {
-  return max_ctx <= 4096 ? 1 : max_ctx <= 8192 ? 2 : max_ctx <= 16384 ? 4 : max_ctx <= 32768 ? 8 : 16;
+// with 16).  In a large batch most are shorter than that, and its requests fill
+// the SMs by themselves (128 requests of 2000 positions in a table of 131072: 220 us
+// with clusters of 16, 23 with two CTAs); keys that do not fit are then computed
+// again in each pass.
+int cluster_of(int B, int64_t max_ctx) {
+  int ctas = max_ctx <= 4096 ? 1 : max_ctx <= 8192 ? 2 : max_ctx <= 16384 ? 4 : max_ctx <= 32768 ? 8 : kMaxCtas;
+  while (ctas > 1 && static_cast<int64_t>(B) * ctas > 2 * 152) ctas /= 2;
+  return ctas;
 }
 
 size_t evict_list(int B, int budget) { return align256(static_cast<size_t>(B) * budget * 4); }
@@ -525,16 +544,16 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!allow_smem<evict_select_kernel>(sizeof(SelectShared))) return SPEC_ERR_CUDA;
   if (!allow_wide_clusters<evict_select_kernel>()) return SPEC_ERR_CUDA;
-  const int ctas = B == 0 ? 1 : cluster_of(max_ctx);
-  launch_kc(evict_select_kernel, static_cast<unsigned>(B == 0 ? 1 : B * ctas), kSelThreads, sizeof(SelectShared), s,
+  const int ctas = cluster_of(B, max_ctx);
+  launch_kc(evict_select_kernel, static_cast<unsigned>(B == 0 ? ctas : B * ctas), kSelThreads, sizeof(SelectShared), s,
             ctas, a, ctas);
   int e = launch_status();
   if (e != SPEC_OK || B == 0) return e;
   if (page_size == 1 || !kv_pool_or_null) return SPEC_OK;
   // CTAs of a slice's cluster: more until the launch fills the SMs twice or a
   // chunk takes all rows.  In us with one CTA / this rule: 1 request of 100000 to
-  // 50000 positions, rows of 1280 bytes 311 / 56; 4 of 30000 to 20000 166 / 60; 16
-  // of 4000 to 3000, 640 bytes 30 / 23; 128 of 2000 to 1000, 1280 bytes 73 / 73
+  // 50000 positions, rows of 1280 bytes 311 / 53; 4 of 30000 to 20000 166 / 56; 16
+  // of 4000 to 3000, 640 bytes 30 / 19; 128 of 2000 to 1000, 1280 bytes 73 / 70
   const int64_t slices = (bytes_per_slot / 16 + kSliceVecs - 1) / kSliceVecs;
   int c = 1;
   while (c < kMaxCtas && B * slices * c < 2 * 152 && c * kRows < budget) c *= 2;

@@ -317,12 +317,14 @@ __device__ __forceinline__ void write_block(const SumArgs& a, int b, int h, int 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = max(top, s_top[w]);
-  // products come times 2^(9 - e)
+  // products come times 2^(9 - e).  Rows 2^-8 of the largest still lose nothing
+  // above 2^-25 of their own largest element; one is large enough for a row that
+  // does not count to come out as 2^-512, and for lse's terms to fit
   const float one = a.scale_log2 * pow2(max(top, -117)) * 0x1p-9f;
   bool fold = one >= 0x1p-17f && one <= 0x1p100f;
 #pragma unroll
   for (int z = 0; z < kTurns; ++z)
-    if (nl[z] != neg_inf()) fold = fold && e[z] >= top - 16 && fabsf(nl[z]) < one * 0x1p25f;
+    if (nl[z] != neg_inf()) fold = fold && e[z] >= top - 8 && fabsf(nl[z]) < one * 0x1p25f;
   fold = __all_sync(0xffffffffu, fold);
   if (lane == 0) s_fold[warp] = fold;
   __syncthreads();

@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     // the whole warp walks the steps, so that the operands' addresses are known to
     // be the same in all lanes (uniform registers); one lane issues
     const bool leader = elect_one();
+    const uint32_t base = uniform(tmem);
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
       int left = min((seg.from / seg.tiles + 1) * seg.tiles, seg.to) - seg.from;  // steps of the item
@@ -401,14 +402,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         const uint64_t qd = tc::desc(tc::smem_addr(sh.q[0].q) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), 0);
         const uint64_t sums = desc_plain(tc::smem_addr(sh.q[0].sums) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), kCols * 16);
         ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
+        const unsigned steps = uniform(static_cast<uint32_t>(left));
+        j = uniform(j);
 #pragma unroll 1
-        for (int i = 0; ok && i < left; ++i, ++j) {
-          const int st = uniform(j & 1);
-          const uint32_t d = uniform(tmem) + st * kCols, k_at = uniform(tmem) + kTmemA + st * D;
+        for (unsigned i = 0; i < steps; ++i, ++j) {
+          const int st = j & 1;
+          const uint32_t d = base + st * kCols, k_at = base + kTmemA + st * D;
           const uint64_t lo = desc_plain(tc::smem_addr(sh.k_lo[0]) + st * static_cast<uint32_t>(sizeof(sh.k_lo[0])), kTile * 16);
-          ok = wait_warp(&k_full[st], (j >> 1) & 1, &s_abort);
-          if (j >= 2) ok = ok && wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort);
-          if (!ok) break;
+          if (!wait_warp(&k_full[st], (j >> 1) & 1, &s_abort) ||
+              (j >= 2 && !wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort))) {
+            ok = false;
+            break;
+          }
           tc::fence_after();
           if (leader) {
 #pragma unroll

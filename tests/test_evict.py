@@ -168,6 +168,16 @@ def test_keys_beyond_shared_memory(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [20, 160, 310])
+def test_large_batches_in_a_wide_table(gpu, B):
+    """Fewer CTAs a request, so that the longest one's keys do not all fit."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 300, B)
+    lens[B // 2], lens[-1] = 40000, 9000
+    run_and_check(make(B, lens, 40000, 1), 1, 120, 150, 4, 10)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [16, 112, 128, 144, 4096])
 def test_payload_widths(gpu, width):
     c = make(6, [700, 90, 1200], 1201, 16, width=width)

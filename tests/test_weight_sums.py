@@ -261,6 +261,20 @@ def test_rows_far_from_one(gpu, size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("spread", [3, 8, 9, 17, 60])
+@pytest.mark.parametrize("N", [6, 40])
+def test_rows_of_different_sizes(gpu, N, spread):
+    """Rows from 2^-spread of the largest on, some without a finite lse, some zero."""
+    c = make_case(17, 2, N, 4, 2, 128, [200, 60])
+    size = 2.0 ** -np.random.default_rng(spread).integers(0, spread + 1, (2, N, 4))
+    size[0, 1] = 0
+    c["q"] = (c["q"].float() * torch.from_numpy(size)[..., None].float()).to(torch.bfloat16)
+    add_rows(c)
+    c["lse"][1, N // 2, 1] = float("-inf")
+    check(run(c), expected(c), 128)
+
+
+@pytest.mark.gpu
 def test_elements_far_below_their_row(gpu):
     c = make_case(15, 2, 3, 4, 2, 128, [90, 40])
     c["q"][..., ::2] *= 2.0**-22
