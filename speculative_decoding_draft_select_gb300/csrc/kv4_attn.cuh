@@ -118,10 +118,11 @@ __device__ __forceinline__ bool attn_context(const AttnArgs& a, const Part& p, i
 }
 // Whether node m is within node n's window, or a sink (nodes fewer than the
 // window's positions are never too far apart).
+__device__ __forceinline__ bool attn_near_depths(const AttnArgs& a, const Part& p, int dn, int dm) {
+  return dn - dm < a.window || p.start + p.gap + dm < a.sinks;
+}
 __device__ __forceinline__ bool attn_near(const AttnArgs& a, const Part& p, int n, int m) {
-  if (a.window >= p.nodes) return true;
-  const int dm = attn_depth(a, p, m);
-  return attn_depth(a, p, n) - dm < a.window || p.start + p.gap + dm < a.sinks;
+  return a.window >= p.nodes || attn_near_depths(a, p, attn_depth(a, p, n), attn_depth(a, p, m));
 }
 // Whether node n sees a place of its request that has a slot.
 template <bool WIN>

@@ -108,6 +108,11 @@ __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int
     nd[w] = first + 32 * w + lane;
     at[w] = min(max(nd[w], 0), p.nodes - 1);
   }
+  int depth[4] = {0, 0, 0, 0};
+  if (WIN && a.window < p.nodes) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) depth[w] = attn_depth(a, p, at[w]);
+  }
 #pragma unroll 1
   for (int nb = n_lo; nb <= n_hi; nb += 4) {
     uint8_t on[4][4];
@@ -118,12 +123,10 @@ __device__ __forceinline__ void node_words(const AttnArgs& a, const Part& p, int
 #pragma unroll
       for (int w = 0; w < 4; ++w) on[q][w] = a.mask ? __ldg(row + at[w]) : static_cast<uint8_t>(at[w] <= n);
       if (WIN && a.window < p.nodes) {
-        uint32_t near = 0;
-#pragma unroll 1
-        for (int w = 0; w < 4; ++w)
-          near |= static_cast<uint32_t>(attn_near(a, p, n, min(max(first + 32 * w + lane, 0), p.nodes - 1))) << w;
+        const int dn = attn_depth(a, p, n);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) on[q][w] &= static_cast<uint8_t>(-static_cast<int>((near >> w) & 1u));
+        for (int w = 0; w < 4; ++w)
+          if (!attn_near_depths(a, p, dn, depth[w])) on[q][w] = 0;
       }
     }
 #pragma unroll
