@@ -627,8 +627,7 @@ int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int6
  * slot is at seq_lens[b] + m as before.  sinks >= 0, window >= 1 (the node
  * itself).  Positions from sinks to seq_lens[b] - window are neither read nor
  * looked up: their slots may have been freed.  Everything else, the workspace
- * included, is as in spec_kv4_attention; with sinks + window above every
- * length it gives the same values. */
+ * included, is as in spec_kv4_attention. */
 int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_stride, const void* pool,
                               int64_t num_slots, int64_t slot_stride, const int32_t* num_nodes_or_null,
                               const int32_t* seq_lens, const int32_t* positions_or_null, const int32_t* req_to_token,

@@ -808,6 +808,20 @@ int launch_few(AttnArgs& a, int R, int sms, cudaStream_t s) {
 // knows B but not the lengths that decide it, so the rule looks at rows alone.
 int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 0); }
 
+// With a window the host knows how many places a row sees at most: calls of more
+// than 16 rows whose row tiles of 16 fit in few tiles go to the kernel of 16, whose
+// segments cost less to begin and end (a window that shows the whole table takes
+// the kernel that the call without one takes).  In us, in kv4_tree.cu / here, by
+// tiles:
+//   D=128  552: 23.3/18.1   1081: 22.5/17.4   2073: 24.6/25.1   4416: 65/88
+//   D=64   811: 19.8/13.5   4264: 30.3/27.5   6490: 33.4/38.2
+constexpr int64_t kFewTiles = 2000;
+bool few_tiles(int B, int N, int Hkv, int64_t rows, int64_t max_ctx, int sinks, int window) {
+  const int64_t places = static_cast<int64_t>(sinks) + window + N;
+  const int64_t tiles = (places + kTile - 1) / kTile;
+  return places < max_ctx && static_cast<int64_t>(B) * Hkv * ((rows + 15) / 16) * tiles <= kFewTiles;
+}
+
 // The upper limits of a call's sizes.
 bool attn_sizes(int B, int N, int Hq, int Hkv, int D) {
   return spec_kv4_slot_bytes(Hkv, D) >= 0 && N <= SPEC_MAX_NODES && Hq <= SPEC_KV4_MAX_HEADS * 16 && B <= 65535;
@@ -822,11 +836,11 @@ int attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_str
   if (B < 0 || N < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_ctx < 1 || num_slots < 1 || !(scale > 0.0f) ||
       !isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
-  const int64_t row = spec_kv4_slot_bytes(Hkv, D);
+  const int64_t row_bytes = spec_kv4_slot_bytes(Hkv, D);
   if (!attn_sizes(B, N, Hq, Hkv, D)) return SPEC_ERR_UNSUPPORTED;
   // a row's factor, scale log2(e) times a power of two down to 2^-126, must not vanish
   if (scale < 0x1p-20f || scale > 0x1p20f) return SPEC_ERR_UNSUPPORTED;
-  if (slot_stride < row || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
+  if (slot_stride < row_bytes || q_stride < static_cast<int64_t>(Hq) * D) return SPEC_ERR_INVALID_ARG;
   if (slot_stride % 16 != 0 || q_stride % 8 != 0 || num_slots > INT32_MAX || max_ctx > INT32_MAX - 2 * kTile ||
       slot_stride > INT32_MAX)
     return SPEC_ERR_UNSUPPORTED;
@@ -850,7 +864,9 @@ int attention(int B, int N, int Hq, int Hkv, int D, const void* q, int64_t q_str
              num_slots, slot_stride, req_to_token, max_ctx, seq_lens, num_nodes, tree_mask, positions, sinks, window,
              scale * kLog2e, static_cast<uint16_t*>(out), lse, static_cast<float*>(ws), 0, stats};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int R = rows_of(static_cast<int64_t>(N) * a.G);
+  const int64_t rows = static_cast<int64_t>(N) * a.G;
+  int R = rows_of(rows);
+  if (R == 0 && window != 0 && few_tiles(B, N, Hkv, rows, max_ctx, sinks, window)) R = 16;
   if (R == 0) return launch_tree_attention(a, D, sms, s);
   if (window != 0) return D == 128 ? launch_few<128, true>(a, R, sms, s) : launch_few<64, true>(a, R, sms, s);
   return D == 128 ? launch_few<128, false>(a, R, sms, s) : launch_few<64, false>(a, R, sms, s);
@@ -865,6 +881,8 @@ extern "C" size_t spec_kv4_attention_ws_size(int B, int N, int Hq, int Hkv, int 
   if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !attn_sizes(B, N, Hq, Hkv, D)) return 0;
   const int64_t rows = static_cast<int64_t>(N) * (Hq / Hkv);
   const int R = rows_of(rows);
+  // more than 16 rows may go to the kernel of 16 (few_tiles), which needs less
+  static_assert(kMaxCtas * 16 <= kTreeMaxCtas * kTreeRows, "either kernel's partials");
   return align256(R == 0 ? attn_ws_bytes(kTreeMaxCtas, kTreeRows, D) : attn_ws_bytes(kMaxCtas, R, D));
 }
 

@@ -117,6 +117,34 @@ def test_matches_64_bits(gpu, B, N, Hq, Hkv, D, lens, page, sinks, window, tree)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,N,Hq,Hkv,D", [(90, 34, 8, 8, 64), (60, 40, 16, 4, 128), (85, 20, 16, 8, 128)])
+@pytest.mark.parametrize("sinks,window", [(0, 1), (4, 3), (7, 40), (130, 100), (3, 300)])
+def test_large_batches(gpu, B, N, Hq, Hkv, D, sinks, window):
+    """More row tiles than the few that go to the kernel of 16 rows: the tensor
+    memory's, with one accumulator and with two.  Padded requests, positions from
+    depths and at random, and nothing but NaN and no slots out of sight."""
+    rng = np.random.default_rng(N + window)
+    lens = rng.integers(0, 400, B)
+    lens[:3] = [0, 1, window]
+    c = make_case(N, B, N, Hq, Hkv, D, lens, page=5)
+    nn = rng.integers(0, N + 1, B).astype(np.int32)
+    nn[:2] = N
+    pos = c["lens"][:, None] + depths(c["mask"])
+    pos[B // 2:] = rng.integers(-5, 500, pos[B // 2:].shape)
+    want = expected(c, sinks, window, positions=pos, num_nodes=nn)
+    for b, n in enumerate(c["lens"]):
+        gone = slice(sinks, max(sinks, n - window + 1))
+        c["rows"][c["table"][b, gone]] = 0xff
+        c["table"][b, gone][::3] = -1
+    stats = sd.new_stats()
+    out = torch.full(c["q"].shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = run(c, sinks, window, positions=pos, num_nodes=torch.from_numpy(nn).cuda(), out=out, stats=stats)
+    rows = np.arange(N)[None] < nn[:, None]
+    check(out, lse, want, rows)
+    assert (out.cpu()[torch.from_numpy(~rows)] == 3.0).all() and int(stats.sum()) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [3, 12, 70])
 def test_window_that_reaches_everything(gpu, N):
     """A window beyond every length: the plain attention, bit for bit."""
