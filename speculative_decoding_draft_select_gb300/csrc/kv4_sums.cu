@@ -132,7 +132,8 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     v[k] = make_uint4(0, 0, 0, 0);
-    if (in) v[k] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
+    if (in)
+      v[k] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
   }
   in = in && isfinite(lse);
   // the largest magnitude: bf16 bits without the sign compare as integers

@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         const int n = min(kCols, (seg.rq.rows * a.G - block * kCols + 31) / 32 * 32);
         const uint32_t id = uniform(tc::idesc_f16(n, false));
         const uint64_t qd = tc::desc(tc::smem_addr(sh.q[0].q) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), 0);
-        const uint64_t sums = desc_plain(tc::smem_addr(sh.q[0].sums) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), kCols * 16);
+        const uint64_t sums =
+            desc_plain(tc::smem_addr(sh.q[0].sums) + qb * static_cast<uint32_t>(sizeof(sh.q[0])), kCols * 16);
         ok = wait_warp(&q_full[qb], (item_no >> 1) & 1, &s_abort);
         const unsigned steps = uniform(static_cast<uint32_t>(left));
         j = uniform(j);
@@ -408,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         for (unsigned i = 0; i < steps; ++i, ++j) {
           const int st = j & 1;
           const uint32_t d = base + st * kCols, k_at = base + kTmemA + st * D;
-          const uint64_t lo = desc_plain(tc::smem_addr(sh.k_lo[0]) + st * static_cast<uint32_t>(sizeof(sh.k_lo[0])), kTile * 16);
+          const uint64_t lo =
+              desc_plain(tc::smem_addr(sh.k_lo[0]) + st * static_cast<uint32_t>(sizeof(sh.k_lo[0])), kTile * 16);
           if (!wait_warp(&k_full[st], (j >> 1) & 1, &s_abort) ||
               (j >= 2 && !wait_warp(&s_empty[st], ((j >> 1) - 1) & 1, &s_abort))) {
             ok = false;
@@ -420,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_ts(d, k_at + part * (D / 2) + kk * 8, qd + (((kk / 4) * RowsBlock<D>::kSlab + (kk % 4) * 32) >> 4), id,
-                           part + kk != 0 ? 1u : 0u);
+                tc::mma_ts(d, k_at + part * (D / 2) + kk * 8,
+                           qd + (((kk / 4) * RowsBlock<D>::kSlab + (kk % 4) * 32) >> 4), id, part + kk != 0 ? 1u : 0u);
             tc::mma_ss(d, lo, sums, id, 1u);
             tc::commit(&s_full[st]);
           }
@@ -506,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             }
 #pragma unroll
             for (int k = 0; k < 32; k += 2)
-              acc[(k >> 1) & 1] = add2(acc[(k >> 1) & 1], exp2_2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))));
+              acc[(k >> 1) & 1] =
+                  add2(acc[(k >> 1) & 1], exp2_2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))));
           }
           tc::fence_before();
           __syncwarp();
