@@ -12,6 +12,13 @@
 // fp32 in the same columns: 2 D + 16 instead of D products an element, with
 // scores as good as fp32 sums.
 //
+// c step is the distance from the group's least value, up to 15 steps, which
+// passes fp16's largest where a group spans more than that (steps above 4366;
+// append's are below 7650).  Groups with steps from 4096 on are taken about their
+// middle, K = lo + 8 step + (c - 8) step: |c - 8| step stays below 61200 and
+// splits exactly as before, and 8 step, exact too, multiplies the groups' sums of
+// q in 16 columns more.  Only products of tiles with such a group have them.
+//
 // Roles of a CTA:
 //   warps 0 .. 7    weights: a thread's position is its lane; two groups of four
 //       warps share a step's columns, since the next products but one wait for it.
@@ -28,17 +35,17 @@
 // goes on without working (results void).
 //
 // Measured at 32 heads over 8 of 128, 32 rows each, B=4, contexts 60001..131001
-// (100 GFLOP of scores, 391 M exponentials): 182 us with the launch that lays the
-// rows out.  A step takes 1830 cycles, of which the tensor pipe works 1090 (57% of
-// the time).  All products of a step go through one accumulator, one after the
-// other, and two steps' S and operands fill the tensor memory.  The
-// weights take 1350 cycles, the unpacking 2000 for two groups.  786 MB come from
-// DRAM for 489 MB of rows, since the heads of a tile are some twenty steps apart;
-// shorter segments read less and take longer (8 tiles: 204 us).  Steps on the way
-// here: K's operands in shared memory 319 us (the matrix instructions then share
-// its bandwidth), factor and lse read per column and rows converted by every CTA
-// 289, groups of weights on alternate steps 206, one lane of a diverged warp
-// issuing 204 instead of 182.
+// (100 GFLOP of scores, 391 M exponentials): 184 us with the launch that lays the
+// rows out (180 without the look for wide groups).  A step takes 1850 cycles, of
+// which the tensor pipe works 1090.  All products of a step go through one
+// accumulator, one after the other, and two steps' S and operands fill the tensor
+// memory.  The weights take 1350 cycles, the unpacking 2000 for two groups.  786
+// MB come from DRAM for 489 MB of rows, since the heads of a tile are some twenty
+// steps apart; shorter segments read less and take longer (8 tiles: 204 us).
+// Steps on the way here: K's operands in shared memory 319 us (the matrix
+// instructions then share its bandwidth), factor and lse read per column and rows
+// converted by every CTA 289, groups of weights on alternate steps 206, one lane
+// of a diverged warp issuing 204 instead of 182.
 #include "kv4_sums.cuh"
 #include "tcgen05.cuh"
 
@@ -58,9 +65,12 @@ struct RowsShared {
   uint8_t k_lo[2][kTile * 32];      // 128 rows of 16 elements, no swizzle
   float sum[2][kSegTiles * kTile];  // of the two groups of weights
   uint8_t ring[8][kRing][32 * Pos<D>::kBytes];  // of the unpacking warps
+  uint8_t k_mid[2][kTile * 32];     // as k_lo: 8 step of wide groups, zeros of the others
 };
 // Tensor memory: S of both buffers, then hi and rem of both stages.
 constexpr uint32_t kTmemCols = 512, kTmemA = 2 * kCols;
+
+constexpr uint32_t kWideStep = 0x6c00u;  // 4096 in fp16: steps from here on make a group wide
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
@@ -159,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], k_full[2], s_full[2], s_empty[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_b;
+  __shared__ uint32_t s_wide[2];  // a byte per unpacking warp: its rows of the stage's k_mid are not all zeros
   __shared__ int64_t s_warp[kThreads / 32], s_pre;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank()), cluster = blockIdx.x / ranks;
@@ -270,6 +281,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
     constexpr int vecs = D / 32;
     const unsigned ring = static_cast<unsigned>(__cvta_generic_to_shared(sh.ring[warp - kUnpackWarp][0]));
     int32_t slot;  // of this lane's position in the group's step to be copied next
+    // a group's 32 channels, hi and rem, to tensor memory; less1024, less64: -1024 and
+    // -64 as half2, or 8 less for codes less 8
+    auto unpack = [](const uint4& code, uint32_t meta, uint32_t less1024, uint32_t less64, uint32_t to) {
+      const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+      const __half2 step = u32_h2(__byte_perm(meta, 0, 0x1010)), sixteenth = u32_h2(0x2c002c00u);
+      uint32_t hi[16], rem[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const uint32_t y = x & 2 ? w[x >> 2] >> 8 : w[x >> 2];
+        const __half2 c = x & 1 ? __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), sixteenth, u32_h2(less64))
+                                : __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), u32_h2(less1024));
+        const __half2 v = __hmul2_rn(c, step);
+        hi[x] = h2_u32(v);
+        rem[x] = h2_u32(__hfma2(c, step, __hneg2(v)));
+      }
+      tc::st16(to, hi);
+      tc::st16(to + D / 2, rem);
+    };
+    // this thread's row of k_mid, in the one stage that its group fills
+    auto put_mid = [&](uint32_t a01, uint32_t a23) {  // three times, as lo
+      uint8_t* row = sh.k_mid[u] + p * 16;
+      *reinterpret_cast<uint4*>(row) = make_uint4(a01, a23, a01, a23);
+      *reinterpret_cast<uint4*>(row + kTile * 16) = make_uint4(a01, a23, 0u, 0u);
+    };
+    put_mid(0u, 0u);
+    if (lane == 0) reinterpret_cast<uint8_t*>(&s_wide[u])[uw] = 0;
+    bool mid_set = false;  // the warp's rows of k_mid are not all zeros
 #pragma unroll 1
     while (seg.next(a, rank, ranks)) {
       const int32_t* row = a.table + static_cast<int64_t>(seg.b) * a.max_ctx;
@@ -350,22 +388,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
         tc::fence_after();
         const uint32_t to = tmem + (static_cast<uint32_t>(uw * 32) << 16) + kTmemA + st * D;
 #pragma unroll
-        for (int z = 0; z < vecs; ++z) {
-          const uint32_t w[4] = {code[z].x, code[z].y, code[z].z, code[z].w};
-          const __half2 step = u32_h2(__byte_perm(meta[z], 0, 0x1010));
-          const __half2 k1024 = u32_h2(0xe400e400u), k16 = u32_h2(0x2c002c00u), k64 = u32_h2(0xd400d400u);
-          uint32_t hi[16], rem[16];
+        for (int z = 0; z < vecs; ++z) unpack(code[z], meta[z], 0xe400e400u, 0xd400d400u, to + z * 16);
+        uint32_t most = meta[0];  // its lower half: the largest step
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const uint32_t y = x & 2 ? w[x >> 2] >> 8 : w[x >> 2];
-            const __half2 c = x & 1 ? __hfma2(u32_h2((y & 0x00f000f0u) | 0x64006400u), k16, k64)
-                                    : __hadd2(u32_h2((y & 0x000f000fu) | 0x64006400u), k1024);
-            const __half2 v = __hmul2_rn(c, step);
-            hi[x] = h2_u32(v);
-            rem[x] = h2_u32(__hfma2(c, step, __hneg2(v)));
+        for (int z = 1; z < vecs; ++z) most = __vmaxu2(most, meta[z]);
+        const bool wide = (most & 0xffffu) >= kWideStep;
+        if (__any_sync(0xffffffffu, wide || mid_set)) {
+          // wide groups again, from the stage and in a loop: few positions need it, and
+          // code that every step fetches costs more than it computes
+          uint32_t mid[2] = {0u, 0u};
+          tc::wait_st();
+#pragma unroll 1
+          for (int z = 0; z < vecs; ++z) {
+            const uint32_t m = *reinterpret_cast<const uint32_t*>(from + Pos<D>::kCodes + 4 * z);
+            const bool about = (m & 0xffffu) >= kWideStep;
+            unpack(*reinterpret_cast<const uint4*>(from + 16 * z), m, about ? 0xe408e408u : 0xe400e400u,
+                   about ? 0xd480d480u : 0xd400d400u, to + z * 16);
+            const uint32_t eight = about ? h2_u32(__hmul2_rn(u32_h2(m & 0xffffu), u32_h2(0x4800u))) : 0u;  // steps
+            if (z < 2) mid[0] |= eight << (16 * z);
+            else mid[1] |= eight << (16 * (z - 2));
           }
-          tc::st16(to + z * 16, hi);
-          tc::st16(to + D / 2 + z * 16, rem);
+          put_mid(mid[0], mid[1]);
+          mid_set = __any_sync(0xffffffffu, wide);
+          if (lane == 0) reinterpret_cast<uint8_t*>(&s_wide[u])[uw] = mid_set;
         }
         // lo of the groups, three times: columns 0..3, 4..7, 8..11
         uint32_t lo[2];
@@ -417,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
             break;
           }
           tc::fence_after();
+          const uint32_t wide = *reinterpret_cast<volatile uint32_t*>(&s_wide[st]);
           if (leader) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)
@@ -425,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArg
                 tc::mma_ts(d, k_at + part * (D / 2) + kk * 8,
                            qd + (((kk / 4) * RowsBlock<D>::kSlab + (kk % 4) * 32) >> 4), id, part + kk != 0 ? 1u : 0u);
             tc::mma_ss(d, lo, sums, id, 1u);
+            if (wide != 0) tc::mma_ss(d, lo + ((offsetof(Shared, k_mid) - offsetof(Shared, k_lo)) >> 4), sums, id, 1u);
             tc::commit(&s_full[st]);
           }
           __syncwarp();

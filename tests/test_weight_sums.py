@@ -318,3 +318,33 @@ def test_strided_captured_on_another_stream(gpu):
     t = r["touched"]
     check(torch.where(torch.from_numpy(t).cuda(), sums, 55.0), r, 64)
     assert torch.equal(sums[torch.from_numpy(~t).cuda()], x["prev"][torch.from_numpy(~t).cuda()])
+
+
+def wide_groups(rng, slots, Hkv, D, span):
+    """K whose groups of 32 channels reach from one value to another `span`
+    further on: the cache's whole range, spans on both sides of fp16's largest
+    over the groups, or every third group far wider than the others."""
+    u = rng.random((slots, Hkv, D // 32, 32))
+    u[..., 0], u[..., 1] = 0, 1
+    width = {"all": np.full(u.shape[:3], 2 * 57344.0), "border": rng.uniform(65000, 66500, u.shape[:3]),
+             "some": np.where(rng.random(u.shape[:3]) < 1 / 3, 2 * 57344.0, 3.0)}[span][..., None]
+    least = np.where(width < 100, -1.5, -57344.0 + rng.random(width.shape) * (2 * 57344.0 - width))
+    return (least + u * width).reshape(slots, Hkv, D).astype(np.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,G", [(4, 4), (12, 4), (33, 4)])
+@pytest.mark.parametrize("span", ["all", "border", "some"])
+def test_groups_wider_than_half_precision(gpu, D, N, G, span):
+    """The cache holds K up to +-57344, so code times step may pass fp16's
+    largest; q is small enough that scores stay near one."""
+    c = make_case(18, 2, N, 2 * G, 2, D, [300, 45])
+    rng = np.random.default_rng(D + N)
+    slots = c["rows"].shape[0]
+    c["rows"] = ref.kv4_rows(wide_groups(rng, slots, 2, D, span), rng.normal(0, 1, (slots, 2, D)).astype(np.float32))
+    c["q"] = (c["q"].float() * 2.0**-15).to(torch.bfloat16)
+    add_rows(c)
+    got = run(c)
+    check(got, expected(c), D)
+    assert torch.equal(got, run(c))
