@@ -620,11 +620,12 @@ int spec_kv4_attention(int B, int N, int Hq, int Hkv, int D, const void* q, int6
 
 /* spec_kv4_attention with a sliding window and sinks: of what a node attends to
  * there, it keeps the positions p < sinks (the text's first tokens, which stay
- * visible) and p > P - window, P its own position.  Node n's position is
- * positions[b][n] (spec_build_tree's: seq_lens[b] + depth), taken as the
- * nearest of [seq_lens[b], seq_lens[b] + n] where it lies outside; NULL:
- * seq_lens[b] + n, a chain.  A node m of the path counts by its position, its
- * slot is at seq_lens[b] + m as before.  sinks >= 0, window >= 1 (the node
+ * visible) and p > P - window, P its own position, seq_lens[b] + its depth.
+ * Node n's depth is positions[b][n] - positions[b][0] (spec_build_tree's
+ * positions, whatever length of the text they start from: after an eviction it is
+ * beyond the cache's), taken as the nearest of [0, n] where it lies outside;
+ * NULL: n, a chain.  A node m of the path counts by its position, its slot is at
+ * seq_lens[b] + m as before.  sinks >= 0, window >= 1 (the node
  * itself).  Positions from sinks to seq_lens[b] - window are neither read nor
  * looked up: their slots may have been freed.  Everything else, the workspace
  * included, is as in spec_kv4_attention. */
@@ -691,6 +692,9 @@ int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, in
  *     page.
  *   kept [B, budget] int32 out (-1 where the request is not cut); new_kv_len
  *     [B] = budget or seq_lens[b]; freed [freed_capacity], num_freed [1].
+ * From then on a request has two lengths: new_kv_len, which the calls on the
+ * cache take, and the text's, which the caller keeps and gives to spec_build_tree,
+ * since the rows that stay were made at their old positions.
  * The slots of a call are distinct.  A request with seq_len < 0 or > max_ctx is
  * skipped (new_kv_len = -1), a move from or to a slot outside [0, num_slots)
  * is left out (SPEC_STAT_BAD_REQUEST each).  kv_pool 16-byte aligned,

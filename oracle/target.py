@@ -78,8 +78,8 @@ def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, n
     n >= num_nodes[b] are NaN.  A position whose slot is out of range is not
     attended; a request whose positions are out of range gives zeros.  With a
     window a node at position P sees, of this, the positions below sinks and
-    those above P - window (positions [B, N], seq_len + n without; taken into
-    [seq_len, seq_len + n])."""
+    those above P - window; P is seq_len + positions[b, n] - positions[b, 0]
+    (positions [B, N], seq_len + n without; taken into [seq_len, seq_len + n])."""
     q = np.asarray(q, np.float64)
     B, N, Hq, D = q.shape
     G = Hq // Hkv
@@ -99,7 +99,8 @@ def kv4_attention(q, rows, req_to_token, seq_lens, Hkv, scale, tree_mask=None, n
         if window is not None:
             at = np.arange(s + nn)
             if positions is not None:
-                at[s:] = np.clip(np.asarray(positions[b, :nn], np.int64), s, s + np.arange(nn))
+                depth = np.asarray(positions[b, :nn], np.int64)
+                at[s:] = s + np.clip(depth - depth[0], 0, np.arange(nn))
             see &= (at < sinks)[None] | (at[None] > at[s:, None] - window)
         see &= there
         for n in range(nn):

@@ -686,7 +686,8 @@ def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, 
                               tree_mask=None, scale=None, num_nodes=None, out=None, lse=None, ws=None, stats=None):
     """spec_kv4_attention with a sliding window: a node at position P sees, of
     what it would see there, the positions below ``sinks`` and those above P -
-    ``window``.  positions [B, N] int32: spec_build_tree's (None: a chain).
+    ``window``.  positions [B, N] int32: spec_build_tree's, of which the
+    distances to the root's count (None: a chain).
     Positions between the sinks and the window are not read."""
     return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
                       (positions, min(int(sinks), _INT_MAX), min(int(window), _INT_MAX)))  # beyond every position

@@ -101,11 +101,13 @@ struct Part {
   __device__ __forceinline__ bool complete() const { return t0 == 0 && t1 == tiles; }
 };
 
-// With a window: the depth of node n, its position less seq_len; a node has n
-// ancestors at most.
+// With a window: the depth of node n, its position less the root's (which is the
+// text's length, and may be further on than the cache's); a node has n ancestors
+// at most.
 __device__ __forceinline__ int attn_depth(const AttnArgs& a, const Part& p, int n) {
   if (a.positions == nullptr) return n;
-  const int64_t d = static_cast<int64_t>(__ldg(a.positions + static_cast<int64_t>(p.b) * a.N + n)) - (p.start + p.gap);
+  const int32_t* of = a.positions + static_cast<int64_t>(p.b) * a.N;
+  const int64_t d = static_cast<int64_t>(__ldg(of + n)) - __ldg(of);
   return d < 0 ? 0 : (d > n ? n : static_cast<int>(d));
 }
 // The place that every row's window has reached: from there on, and below cut,

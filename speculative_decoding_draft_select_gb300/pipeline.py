@@ -33,7 +33,9 @@ Behind compaction, a cache that has to stay bounded: run_weight_sums adds the
 attention weights that the accepted path's rows gave each position to its sum,
 and run_evict cuts the requests that have grown past a limit to the positions
 with the largest sums, the sinks and the latest ones (run_attention takes a
-window and sinks for layers that look no further).
+window and sinks for layers that look no further).  From then on a request has
+two lengths: run_draft gets the text's, which the caller keeps (buf.tree's
+positions are the target's), everything else the cache's.
 
 All buffers are allocated once in ``StepBuffers``; a step only enqueues
 kernels on the current stream, so a whole step can be captured once in a

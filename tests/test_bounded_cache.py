@@ -199,6 +199,24 @@ def test_two_captured_calls_do_not_share_a_workspace(gpu):
 
 
 @pytest.mark.gpu
+def test_text_longer_than_the_cache(gpu):
+    """After an eviction the drafts stand behind the text, the cache is shorter:
+    the windows are those of the cache."""
+    x = {k: v.cuda() for k, v in inputs(8, 16).items()}
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=16)
+    fill(x)
+    sd.spec_kv4_append(x["k"], x["v"], x["pool"], x["table"], x["lens"])
+    got, positions = [], []
+    for text in (x["lens"], x["lens"] + torch.tensor([0, 7, 4000, 2**30], dtype=torch.int32, device="cuda")):
+        pl.run_draft(buf, x["draft"], 1.0, x["root"], text)
+        positions.append(buf.tree["positions"] - text[:, None])
+        got += [pl.run_attention(buf, x["q"], x["lens"], x["table"], x["pool"], HKV, window=w, sinks=SINKS)
+                for w in (2, WINDOW)]
+    assert torch.equal(positions[0], positions[1]) and int(positions[0].max()) < N - 1
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
+@pytest.mark.gpu
 @pytest.mark.timeout(1200)
 def test_under_the_bounds_checking_build():
     """The new calls' tests against libspecdec_debug.so: no index that depends

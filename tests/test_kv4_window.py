@@ -266,3 +266,27 @@ def test_strided_queries_captured_on_another_stream(gpu):
         graph.replay()
     torch.cuda.synchronize()
     check(out, lse, expected(c, 4, 32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(1, 4), (5, 4), (12, 4), (34, 2), (70, 4)])
+@pytest.mark.parametrize("window", [1, 5, 40])
+def test_positions_count_from_the_root(gpu, N, G, window):
+    """Positions of the text, which an eviction has left behind the cache's: the
+    depths are the same, and so is every bit."""
+    c = make_case(N + window, 3, N, 2 * G, 2, 64, [300, 2, 45])
+    pos = c["lens"][:, None].astype(np.int64) + depths(c["mask"])
+    out, lse = run(c, 3, window, positions=pos)
+    check(out, lse, expected(c, 3, window, positions=pos))
+    moved = pos + np.array([[100000], [-7], [2**31 - 1 - 45 - N]])
+    again, again_lse = run(c, 3, window, positions=moved)
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+    check(again, again_lse, expected(c, 3, window, positions=moved))
+
+
+def test_reference_counts_positions_from_the_root():
+    c = make_case(1, 2, 9, 2, 1, 64, [20, 3])
+    pos = c["lens"][:, None].astype(np.int64) + depths(c["mask"])
+    want = expected(c, 1, 4, positions=pos)
+    moved = expected(c, 1, 4, positions=pos + np.array([[1000], [-3]]))
+    assert all(np.array_equal(want[n], moved[n]) for n in ("out", "lse", "count"))
