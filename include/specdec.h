@@ -691,7 +691,8 @@ int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, in
  *     (page id = slot / page_size, -1 of a negative slot), in the order of b and
  *     page.
  *   kept [B, budget] int32 out (-1 where the request is not cut); new_kv_len
- *     [B] = budget or seq_lens[b]; freed [freed_capacity], num_freed [1].
+ *     [B] = budget or seq_lens[b]; freed [freed_capacity], num_freed [1].  None
+ *     of the four may overlap seq_lens, which are read to the call's end.
  * From then on a request has two lengths: new_kv_len, which the calls on the
  * cache take, and the text's, which the caller keeps and gives to spec_build_tree,
  * since the rows that stay were made at their old positions.

@@ -792,7 +792,7 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
     [B, max_ctx] f32 among the others.  sums (or sums_out), and req_to_token with
     pages of one token, else kv_pool [slots, bytes] uint8, are updated.  Returns
     a dict of kept [B, budget] (-1 where nothing was cut), freed, num_freed and
-    new_kv_len."""
+    new_kv_len, which must be other tensors than seq_lens."""
     dev = _device(sums, "sums")
     if sums.dim() != 2 or req_to_token.shape != sums.shape:
         raise ValueError("sums and req_to_token must be [B, max_ctx]")

@@ -535,10 +535,18 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
   }
   if (B > 0 && (reinterpret_cast<uintptr_t>(ws) & 15) != 0) return SPEC_ERR_INVALID_ARG;
   if (B > 0 && ws_bytes < spec_evict_ws_size(B, page_size, budget)) return SPEC_ERR_WORKSPACE;
+  auto overlap = [](const void* x, uint64_t n, const void* y, uint64_t m) {  // of n and m 32-bit values
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+    return n > 0 && m > 0 && x0 < y0 + 4 * m && y0 < x0 + 4 * n;
+  };
+  // every CTA, and the payload's launch, reads the lengths while others write results
+  const uint64_t requests = static_cast<uint64_t>(B);
+  if (overlap(seq_lens, requests, new_kv_len, requests) || overlap(seq_lens, requests, kept, requests * budget) ||
+      overlap(seq_lens, requests, freed, static_cast<uint64_t>(freed_capacity)) ||
+      overlap(seq_lens, requests, num_freed, requests > 0 ? 1 : 0))
+    return SPEC_ERR_INVALID_ARG;
   // the sums are read while their new ones are written, unless they are the same
-  const uintptr_t s0 = reinterpret_cast<uintptr_t>(sums), o0 = reinterpret_cast<uintptr_t>(sums_out);
-  const uintptr_t wide = static_cast<uintptr_t>(B) * max_ctx * 4;
-  if (s0 != o0 && s0 < o0 + wide && o0 < s0 + wide) return SPEC_ERR_INVALID_ARG;
+  if (sums != sums_out && overlap(sums, requests * max_ctx, sums_out, requests * max_ctx)) return SPEC_ERR_INVALID_ARG;
   char* w = static_cast<char*>(ws);
   EvictArgs a{B, page_size, budget, limit, sinks, recent, seq_lens, sums, sums_out, req_to_token, max_ctx, kept, freed,
               freed_capacity, num_freed, new_kv_len,

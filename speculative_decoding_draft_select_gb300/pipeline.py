@@ -276,7 +276,8 @@ def run_evict(buf: StepBuffers, sums, seq_lens, req_to_token, page_size, budget,
     """Cuts requests longer than ``limit`` to ``budget`` positions
     (spec_evict_slots); seq_lens: run_compact's new_kv_len.  The results and the
     workspace of a size are allocated by its first call and kept as long as buf:
-    the next call of the same sizes writes the same tensors."""
+    the next call of the same sizes writes the same tensors, so its seq_lens are a
+    copy of the last call's new_kv_len, never that tensor itself."""
     B, ctx = sums.shape
     key = (B, ctx, int(page_size), int(budget))
     held = buf.evict_out.get(key)

@@ -217,6 +217,24 @@ def test_text_longer_than_the_cache(gpu):
 
 
 @pytest.mark.gpu
+def test_cut_again(gpu):
+    """The lengths of one cut go into the next as a copy; the held tensor itself,
+    which the next cut writes, is refused before anything is launched."""
+    x = {k: v.cuda() for k, v in inputs(9, 16).items()}
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=16)
+    cut = dict(sinks=SINKS, recent=RECENT, kv_pool=x["pool"])
+    first = pl.run_evict(buf, x["sums"], x["lens"], x["table"], 16, BUDGET, **cut)
+    assert first["new_kv_len"].tolist() == [0, BUDGET, BUDGET, BUDGET]
+    before = x["sums"].clone()
+    with pytest.raises(sd.SpecError):
+        pl.run_evict(buf, x["sums"], first["new_kv_len"], x["table"], 16, BUDGET, **cut)
+    assert torch.equal(before, x["sums"]) and first["new_kv_len"].tolist() == [0, BUDGET, BUDGET, BUDGET]
+    grown = first["new_kv_len"] + 1
+    again = pl.run_evict(buf, x["sums"], grown, x["table"], 16, BUDGET, **cut)
+    assert again is first and again["new_kv_len"].tolist() == [1, BUDGET, BUDGET, BUDGET]
+
+
+@pytest.mark.gpu
 @pytest.mark.timeout(1200)
 def test_under_the_bounds_checking_build():
     """The new calls' tests against libspecdec_debug.so: no index that depends

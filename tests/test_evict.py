@@ -101,6 +101,27 @@ def test_host_checks():
         assert call(**{**a, "out": ctypes.c_void_p(4100)}) == -1      # sums and their new ones overlap in part
 
 
+def test_lengths_apart_from_the_results():
+    """Lengths are read until the last launch ends: no result may lie over them."""
+    build()
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where nothing could run")
+    at = lambda a: ctypes.c_void_p(1 << 20 | a)  # noqa: E731
+
+    def call(B=4, page=16, lens=at(0), kept=at(0x1000), freed=at(0x2000), num=at(0x3000), new=at(0x4000), cap=64):
+        return sd.lib().spec_evict_slots(B, page, 4, 4, 1, 1, lens, at(0x10000), at(0x20000), at(0x30000), 8, kept, freed,
+                                         cap, num, new, at(0x40000), 8, 16, None, at(0x50000), 1 << 20, None)
+    refused = -1
+    for page in (1, 16):
+        assert call(page=page) != refused
+        assert call(page=page, new=at(0)) == refused                    # the lengths themselves
+    assert call(new=at(12)) == refused and call(lens=at(0x400c)) == refused
+    assert call(new=at(16)) != refused and call(lens=at(0x3ff0)) != refused  # neighbours
+    assert call(kept=at(0)) == refused and call(lens=at(0x103c)) == refused and call(lens=at(0x1040)) != refused
+    assert call(freed=at(8)) == refused and call(lens=at(0x20fc)) == refused and call(lens=at(0x2100)) != refused
+    assert call(num=at(12)) == refused and call(num=at(16)) != refused
+
+
 def test_binding_refuses_host_tensors():
     i = torch.zeros((1, 8), dtype=torch.int32)
     with pytest.raises(ValueError):
