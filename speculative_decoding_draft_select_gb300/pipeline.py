@@ -258,38 +258,45 @@ def run_compact(buf: StepBuffers, seq_lens, req_to_token, page_size, kv_pool=Non
                               kv_pool=kv_pool, out=buf.compact_out, stats=buf.stats)
 
 
-def run_weight_sums(buf: StepBuffers, q, lse, seq_lens, req_to_token, kv_pool, num_kv_heads, sums, scale=None):
+def run_weight_sums(buf: StepBuffers, q, lse, seq_lens, req_to_token, kv_pool, num_kv_heads, sums, scale=None, ws=None):
     """Adds the attention weights of the accepted path's rows of q [B, N, Hq, D]
     to sums [B, max_ctx]; behind run_compact, with the seq_lens and lse that
-    run_attention had.  The workspace is kept as run_attention's."""
+    run_attention had.  Without ``ws`` the workspace is kept as run_attention's;
+    calls of one buf that may run at the same time pass a ``ws`` each, of
+    spec_kv4_weight_sums_ws_size bytes (and sums of their own)."""
     v = buf.verify_out
-    need = spec_kv4_weight_sums_ws_size(*q.shape[:3], int(num_kv_heads), q.shape[3])
-    ws = buf.sums_ws.get(need)
-    if need and ws is None:
-        ws = buf.sums_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if ws is None:
+        need = spec_kv4_weight_sums_ws_size(*q.shape[:3], int(num_kv_heads), q.shape[3])
+        ws = buf.sums_ws.get(need)
+        if need and ws is None:
+            ws = buf.sums_ws[need] = torch.empty(need, dtype=torch.uint8, device=q.device)
     return spec_kv4_weight_sums(q, lse, kv_pool, req_to_token, seq_lens, num_kv_heads, accept_path=v["accept_path"],
                                 accept_length=v["accept_length"], prev=sums, scale=scale, ws=ws, stats=buf.stats)
 
 
 def run_evict(buf: StepBuffers, sums, seq_lens, req_to_token, page_size, budget, limit=None, sinks=0, recent=0,
-              kv_pool=None):
+              kv_pool=None, out=None, ws=None):
     """Cuts requests longer than ``limit`` to ``budget`` positions
-    (spec_evict_slots); seq_lens: run_compact's new_kv_len.  The results and the
-    workspace of a size are allocated by its first call and kept as long as buf:
-    the next call of the same sizes writes the same tensors, so its seq_lens are a
-    copy of the last call's new_kv_len, never that tensor itself."""
+    (spec_evict_slots); seq_lens: run_compact's new_kv_len.  Without ``out`` and
+    ``ws`` the results and the workspace of a size are allocated by its first call
+    and kept as long as buf: the next call of the same sizes writes the same
+    tensors, so its seq_lens are a copy of the last call's new_kv_len, never that
+    tensor itself.  Calls of one buf that may run at the same time pass an ``out``
+    (spec_evict_slots's results) and a ``ws`` of spec_evict_ws_size bytes each."""
     B, ctx = sums.shape
-    key = (B, ctx, int(page_size), int(budget))
-    held = buf.evict_out.get(key)
-    if held is None:
-        dev = sums.device
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
-        held = buf.evict_out[key] = (
-            {"kept": new(B, budget), "freed": new(max(1, spec_evict_freed_capacity(B, ctx, page_size, budget))),
-             "num_freed": new(1), "new_kv_len": new(B)},
-            torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=dev))
+    if out is None or ws is None:
+        key = (B, ctx, int(page_size), int(budget))
+        held = buf.evict_out.get(key)
+        if held is None:
+            dev = sums.device
+            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+            held = buf.evict_out[key] = (
+                {"kept": new(B, budget), "freed": new(max(1, spec_evict_freed_capacity(B, ctx, page_size, budget))),
+                 "num_freed": new(1), "new_kv_len": new(B)},
+                torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=dev))
+        out, ws = held[0] if out is None else out, held[1] if ws is None else ws
     return spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=limit, sinks=sinks, recent=recent,
-                            kv_pool=kv_pool, out=held[0], ws=held[1], stats=buf.stats)
+                            kv_pool=kv_pool, out=out, ws=ws, stats=buf.stats)
 
 
 def capture_step(fn, warm=True):

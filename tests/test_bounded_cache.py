@@ -234,6 +234,83 @@ def test_cut_again(gpu):
     assert again is first and again["new_kv_len"].tolist() == [1, BUDGET, BUDGET, BUDGET]
 
 
+def sums_case(buf, seed, heads):
+    """run_weight_sums's inputs of whole chains of nodes, and what it has to give."""
+    x = {k: v.cuda() for k, v in inputs(seed, 16).items()}
+    fill(x)
+    sd.spec_kv4_append(x["k"], x["v"], x["pool"], x["table"], x["lens"])
+    buf.verify_out["accept_length"].fill_(N - 1)
+    buf.verify_out["accept_path"].copy_(torch.arange(N, device="cuda").expand(B, N))
+    rng = np.random.default_rng(seed)
+    x["q"] = torch.from_numpy(rng.normal(0, 1, (B, N, heads, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    x["lse"] = torch.from_numpy(rng.normal(4, 1, (B, N, heads)).astype(np.float32)).cuda()
+    x["sums"] = torch.zeros((B, CTX), device="cuda")
+    r = ref.kv4_weight_sums(x["q"].float().cpu().numpy(), x["lse"].cpu().numpy(), x["pool"].cpu().numpy(),
+                            x["table"].cpu().numpy(), x["lens"].cpu().numpy(), HKV, D ** -0.5)
+    return x, r
+
+
+def check_case(x, r):
+    check_sums(torch.where(torch.from_numpy(r["touched"]).cuda(), x["sums"], 55.0), r, D)
+
+
+@pytest.mark.gpu
+def test_workspaces_of_two_sizes(gpu):
+    """Captured calls of 48 and of 144 rows a KV head: each keeps its own, and the
+    first's is still its own when the second has been captured."""
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=16)
+    cases = [sums_case(buf, 11, 4 * HKV), sums_case(buf, 12, 12 * HKV)]
+    graphs, held = [], []
+    for x, _ in cases:
+        graphs.append(pl.capture_step(lambda: pl.run_weight_sums(buf, x["q"], x["lse"], x["lens"], x["table"], x["pool"],
+                                                                 HKV, x["sums"])))
+        held.append({n: w.data_ptr() for n, w in buf.sums_ws.items()})
+    assert len(held[0]) == 1 and len(set(held[1].values())) == 2 and held[0].items() <= held[1].items()
+    for order in ((0, 1), (1, 0)):
+        for x, _ in cases:
+            x["sums"].zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for x, r in cases:
+            check_case(x, r)
+    assert {n: w.data_ptr() for n, w in buf.sums_ws.items()} == held[1]
+
+
+@pytest.mark.gpu
+def test_layers_side_by_side(gpu):
+    """Two layers' sums and cuts on two streams, each with tensors of its own."""
+    buf = pl.StepBuffers("tree", B, TOPK, STEPS, N, V, "cuda", want_q=False, page_size=16)
+    streams, layers = [torch.cuda.Stream() for _ in range(2)], []
+    for seed in (13, 14):
+        x, r = sums_case(buf, seed, 4 * HKV)
+        ws = torch.empty(sd.spec_kv4_weight_sums_ws_size(B, N, 4 * HKV, HKV, D), dtype=torch.uint8, device="cuda")
+        c = {k: v.cuda() for k, v in inputs(seed, 16).items()}
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+        out = {"kept": new(B, BUDGET), "freed": new(sd.spec_evict_freed_capacity(B, CTX, 16, BUDGET)), "num_freed": new(1),
+               "new_kv_len": new(B)}
+        cut_ws = torch.empty(sd.spec_evict_ws_size(B, 16, BUDGET), dtype=torch.uint8, device="cuda")
+        layers.append((x, r, ws, c, out, cut_ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, (x, r, ws, c, out, cut_ws) in zip(streams, layers):
+            with torch.cuda.stream(stream):
+                x["sums"].zero_()
+                pl.run_weight_sums(buf, x["q"], x["lse"], x["lens"], x["table"], x["pool"], HKV, x["sums"], ws=ws)
+                got = pl.run_evict(buf, c["sums"].clone(), c["lens"], c["table"], 16, BUDGET, sinks=SINKS, recent=RECENT,
+                                   out=out, ws=cut_ws)
+                assert got is out
+    torch.cuda.synchronize()
+    assert not buf.sums_ws and not buf.evict_out
+    for x, r, ws, c, out, cut_ws in layers:
+        check_case(x, r)
+        w = ref.evict(c["sums"].cpu().numpy(), c["lens"].cpu().numpy(), c["table"].cpu().numpy(), 16, BUDGET, BUDGET, SINKS,
+                      RECENT)
+        np.testing.assert_array_equal(out["kept"].cpu().numpy(), w["kept"])
+        assert out["freed"][:int(out["num_freed"])].tolist() == w["freed"]
+        np.testing.assert_array_equal(out["new_kv_len"].cpu().numpy(), w["new_kv_len"])
+
+
 @pytest.mark.gpu
 @pytest.mark.timeout(1200)
 def test_under_the_bounds_checking_build():
