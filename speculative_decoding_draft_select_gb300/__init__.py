@@ -507,6 +507,17 @@ def _arg(t, dtype, shape, dev, name):
     return t.data_ptr()
 
 
+def _i32(x, name, clamp=False):
+    """x as a 32-bit number, which ctypes would cut to without a word; clamp: one
+    beyond every position counts as the largest."""
+    x = int(x)
+    if clamp and x > _INT_MAX:
+        return _INT_MAX
+    if not -_INT_MAX <= x <= _INT_MAX:
+        raise ValueError(f"{name} must be a 32-bit number, got {x}")
+    return x
+
+
 def spec_adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, rep_penalty=None, freq_penalty=None,
                        pres_penalty=None, draft_token=None, tree_mask=None, bias_ids=None, bias_vals=None,
                        allowed=None, allowed_row=None, num_nodes=None, out=None, stats=None):
@@ -690,7 +701,7 @@ def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, 
     distances to the root's count (None: a chain).
     Positions between the sinks and the window are not read."""
     return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
-                      (positions, min(int(sinks), _INT_MAX), min(int(window), _INT_MAX)))  # beyond every position
+                      (positions, _i32(sinks, "sinks", clamp=True), _i32(window, "window", clamp=True)))
 
 
 def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats, window):
@@ -797,9 +808,9 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
     if sums.dim() != 2 or req_to_token.shape != sums.shape:
         raise ValueError("sums and req_to_token must be [B, max_ctx]")
     B, ctx = sums.shape
-    page_size, budget = int(page_size), int(budget)
-    if max(page_size, budget, int(sinks), int(recent)) > _INT_MAX:
-        raise ValueError("page_size, budget, sinks and recent must be 32-bit numbers")
+    page_size, budget = _i32(page_size, "page_size"), _i32(budget, "budget")
+    sinks, recent = _i32(sinks, "sinks"), _i32(recent, "recent")
+    limit = budget if limit is None else _i32(limit, "limit", clamp=True)
     i32, f32 = torch.int32, torch.float32
     src = _arg(sums, f32, (B, ctx), dev, "sums")
     dst = src if sums_out is None else _arg(sums_out, f32, (B, ctx), dev, "sums_out")
@@ -816,7 +827,7 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
     freed = out["freed"]
     if ws is None:
         ws = torch.empty(spec_evict_ws_size(B, page_size, budget), dtype=torch.uint8, device=sums.device)
-    rc = lib().spec_evict_slots(B, page_size, budget, budget if limit is None else min(int(limit), _INT_MAX), int(sinks), int(recent),
+    rc = lib().spec_evict_slots(B, page_size, budget, limit, sinks, recent,
                                 _arg(seq_lens, i32, (B,), dev, "seq_lens"), src, dst,
                                 _arg(req_to_token, i32, (B, ctx), dev, "req_to_token"), ctx,
                                 _arg(out["kept"], i32, (B, budget), dev, "kept"),

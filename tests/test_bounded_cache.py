@@ -23,6 +23,18 @@ B, TOPK, STEPS, N, V, HQ, HKV, D = 4, 3, 3, 12, 700, 8, 2, 64
 CTX, BUDGET, LIMIT, SINKS, RECENT, WINDOW = 192, 96, 120, 4, 16, 40
 
 
+def test_numbers_of_more_than_32_bits():
+    """ctypes cuts them to their lowest bits: -2^40 would be 0."""
+    assert sd._i32(-5, "sinks") == -5 and sd._i32(2**31 - 1, "sinks") == 2**31 - 1
+    assert sd._i32(2**40, "window", clamp=True) == 2**31 - 1 and sd._i32(7, "window", clamp=True) == 7
+    for x in (2**31, 2**40, -2**31 - 1, -2**40):
+        with pytest.raises(ValueError):
+            sd._i32(x, "sinks")
+        if x < 0:
+            with pytest.raises(ValueError):
+                sd._i32(x, "window", clamp=True)
+
+
 @pytest.fixture(scope="module")
 def gpu():
     if not torch.cuda.is_available():
@@ -309,6 +321,20 @@ def test_layers_side_by_side(gpu):
         np.testing.assert_array_equal(out["kept"].cpu().numpy(), w["kept"])
         assert out["freed"][:int(out["num_freed"])].tolist() == w["freed"]
         np.testing.assert_array_equal(out["new_kv_len"].cpu().numpy(), w["new_kv_len"])
+
+
+@pytest.mark.gpu
+def test_refusals_of_numbers_beyond_32_bits(gpu):
+    x = {k: v.cuda() for k, v in inputs(10, 16).items()}
+    start = {k: x[k].clone() for k in ("sums", "table")}
+    for sinks, window in ((-2**40, 5), (0, -2**40 + 5), (2, -2**32 + 1)):
+        with pytest.raises(ValueError):
+            sd.spec_kv4_attention_window(x["q"], x["pool"], x["table"], x["lens"], HKV, sinks, window)
+    for name in ("page_size", "budget", "limit", "sinks", "recent"):
+        a = {**dict(page_size=1, budget=BUDGET, limit=LIMIT, sinks=SINKS, recent=RECENT), name: -2**32 + 1}
+        with pytest.raises(ValueError):
+            sd.spec_evict_slots(x["sums"], x["lens"], x["table"], **a)
+    assert all(torch.equal(x[k], v) for k, v in start.items())
 
 
 @pytest.mark.gpu
