@@ -649,9 +649,10 @@ int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* 
  *   q [B, N, Hq, D] bf16, rows (b, n) q_stride elements apart; lse [B, N, Hq]
  *     fp32: a row whose lse is not finite adds nothing.
  *   prev_or_null, out [B, max_ctx] fp32 (NULL: zeros): the same, or apart.
- * Codes and q enter the products exactly (q's elements 2^-24 of its row's
- * largest may round), sums are fp32 in a fixed order; scale log2(e) times a
- * row's largest |q|, and the scores, have to stay in fp32's range.  A position
+ * Codes and q enter the products exactly (q's elements 2^-18 of its row's
+ * largest may round, by 2^-25 of that at most), sums are fp32 in a fixed order;
+ * scale log2(e) times a row's largest |q| has to stay below 2^118, the scores in
+ * fp32's range.  A position
  * whose slot is out of range receives nothing; a path entry out of range adds
  * nothing; a request whose accept_length is outside [0, N) or whose positions
  * do not fit max_ctx is skipped (SPEC_STAT_BAD_REQUEST each).  q and pool
@@ -696,6 +697,9 @@ int spec_kv4_weight_sums(int B, int N, int Hq, int Hkv, int D, const void* q, in
  * From then on a request has two lengths: new_kv_len, which the calls on the
  * cache take, and the text's, which the caller keeps and gives to spec_build_tree,
  * since the rows that stay were made at their old positions.
+ * Layers with a window that share the slots (spec_kv4_attention_window) count
+ * places of the cache: recent >= window - 1, and sinks no fewer than theirs, keep
+ * what they see.
  * The slots of a call are distinct.  A request with seq_len < 0 or > max_ctx is
  * skipped (new_kv_len = -1), a move from or to a slot outside [0, num_slots)
  * is left out (SPEC_STAT_BAD_REQUEST each).  kv_pool 16-byte aligned,

@@ -187,7 +187,7 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
   x.lo[lane] = make_uint2(t == 0 ? term[0][0] : t == 1 ? term[0][1] : t == 2 ? term[1][0] : term[1][1],
                           t == 0 ? term[2][0] : t == 1 ? term[2][1] : 0u);
   if (t == 0) {
-    // products come times 2^(14 - e - 24)
+    // products come times 2^(14 - e - 24): finite while scale log2(e) 2^e is below 2^118
     x.c[g] = in ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p10f : 0.0f;
     x.l[g] = in ? lse * kLog2e : __uint_as_float(0x7f800000u);
     x.row[g] = i;

@@ -320,6 +320,18 @@ def test_strided_captured_on_another_stream(gpu):
     assert torch.equal(sums[torch.from_numpy(~t).cuda()], x["prev"][torch.from_numpy(~t).cuda()])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,N", [(64, 2), (64, 12), (128, 2), (128, 12)])
+def test_rows_as_large_as_they_may_be(gpu, D, N):
+    """scale log2(e) |q| up to 2^118 over positions whose K is zero: equal weights."""
+    c = make_case(22, 2, N, 8, 2, D, [90, 0])
+    zero = np.zeros((c["rows"].shape[0], 2, D), np.float32)
+    c["rows"], c["scale"] = ref.kv4_rows(zero, zero), 2.0**-3
+    c["q"] = torch.where(c["q"].float() < 0, -1.0, 1.0).mul(1.375 * 2.0**120).to(torch.bfloat16)  # 2^117.99
+    add_rows(c)
+    check(run(c), expected(c), D)
+
+
 def wide_groups(rng, slots, Hkv, D, span):
     """K whose groups of 32 channels reach from one value to another `span`
     further on: the cache's whole range, spans on both sides of fp16's largest
