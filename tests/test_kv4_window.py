@@ -290,3 +290,17 @@ def test_reference_counts_positions_from_the_root():
     want = expected(c, 1, 4, positions=pos)
     moved = expected(c, 1, 4, positions=pos + np.array([[1000], [-3]]))
     assert all(np.array_equal(want[n], moved[n]) for n in ("out", "lse", "count"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,lens", [(1, 2048, 2, 1, 64, [300]), (2, 700, 4, 2, 128, [0, 2500]),
+                                               (1, 1025, 1, 1, 128, [77])])
+@pytest.mark.parametrize("sinks,window", [(4, 128), (0, 1024), (300, 1)])
+@pytest.mark.parametrize("tree", [True, False])
+def test_chunks_of_a_prompt(gpu, B, N, Hq, Hkv, D, lens, sinks, window, tree):
+    """Up to the most nodes a call may have, as a chain and as a tree."""
+    c = make_case(N + window, B, N, Hq, Hkv, D, lens, tree=tree)
+    stats = sd.new_stats()
+    out, lse = run(c, sinks, window, stats=stats)
+    check(out, lse, expected(c, sinks, window))
+    assert int(stats.sum()) == 0
