@@ -298,3 +298,34 @@ def test_captured_on_another_stream_and_again(gpu, page):
     np.testing.assert_array_equal(x["sums"].cpu().numpy(), r["sums"])
     if page > 1:
         np.testing.assert_array_equal(x["rows"].cpu().numpy(), r["pool"])
+
+
+@pytest.mark.gpu
+def test_payload_beyond_32_bits(gpu):
+    """Rows of 1 MB: the last slots lie more than 2^32 bytes behind the first."""
+    c = make(16, [90, 31, 70], 96, 16, width=48)
+    far, slots, width = 5000, c["rows"].shape[0], 1 << 20
+    table = on(c["table"] + (far - slots) // 16 * 16)
+    first = (far - slots) // 16 * 16
+    pool = torch.zeros((far, width), dtype=torch.uint8, device="cuda")
+    pool[first:first + slots, width - 48:] = on(c["rows"])
+    got = sd.spec_evict_slots(on(c["sums"]), on(c["lens"]), table, 16, 40, sinks=3, recent=9, kv_pool=pool)
+    r = ref.evict(c["sums"], c["lens"], c["table"], 16, 40, 40, 3, 9, rows=c["rows"])
+    np.testing.assert_array_equal(got["kept"].cpu().numpy(), r["kept"])
+    np.testing.assert_array_equal(pool[first:first + slots, width - 48:].cpu().numpy(), r["pool"])
+    assert int(pool[:, :width - 48].sum(dtype=torch.int64)) == 0 and int(pool[:first].sum(dtype=torch.int64)) == 0
+    assert got["freed"][:int(got["num_freed"])].tolist() == [p + first // 16 for p in r["freed"]]
+
+
+@pytest.mark.gpu
+def test_pages_larger_than_a_request(gpu):
+    run_and_check(make(17, [60, 33, 50], 60, 64, width=32), 64, 40, 45, 2, 5)
+
+
+@pytest.mark.gpu
+def test_most_requests(gpu):
+    """65535 requests, the most of a call: a few are cut."""
+    rng = np.random.default_rng(18)
+    lens = rng.integers(0, 9, 65535)
+    lens[::1000] = 12
+    run_and_check(make(18, lens, 12, 1), 1, 8, 9, 1, 2)

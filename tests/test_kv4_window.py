@@ -284,6 +284,31 @@ def test_positions_count_from_the_root(gpu, N, G, window):
     check(again, again_lse, expected(c, 3, window, positions=moved))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(9, 1), (9, 4), (40, 4)])
+@pytest.mark.parametrize("window", [3, 30])
+def test_a_mask_without_positions(gpu, N, G, window):
+    """Each node is then one further on, whatever its mask shows."""
+    c = make_case(N, 2, N, G, 1, 64, [100, 4])
+    out, lse = run(c, 2, window, positions=None)
+    check(out, lse, expected(c, 2, window, positions=None))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 4, 40])
+def test_slots_beyond_32_bits(gpu, N):
+    """Rows of 1 MB: the last slots lie more than 2^32 bytes behind the first."""
+    c = make_case(25, 2, N, 4, 1, 64, [130, 3])
+    slots, far = c["rows"].shape[0], 5000
+    wide = torch.zeros((far, 1 << 20), dtype=torch.uint8, device="cuda")
+    wide[far - slots:, :80] = torch.from_numpy(c["rows"]).cuda()
+    out = sd.spec_kv4_attention_window(
+        c["q"].cuda(), wide[:, :80], torch.from_numpy(c["table"] + far - slots).cuda(), torch.from_numpy(c["lens"]).cuda(), 1,
+        2, 50, positions=torch.from_numpy(c["lens"][:, None] + depths(c["mask"])).cuda(), scale=c["scale"],
+        tree_mask=torch.from_numpy(c["mask"]).cuda())
+    check(out, None, expected(c, 2, 50))
+
+
 def test_reference_counts_positions_from_the_root():
     c = make_case(1, 2, 9, 2, 1, 64, [20, 3])
     pos = c["lens"][:, None].astype(np.int64) + depths(c["mask"])

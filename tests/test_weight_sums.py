@@ -332,6 +332,47 @@ def test_rows_as_large_as_they_may_be(gpu, D, N):
     check(run(c), expected(c), D)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [2, 12, 40])
+@pytest.mark.parametrize("spread", [20.0, 400.0])
+def test_scores_far_from_zero(gpu, N, spread):
+    """Scores and lse of hundreds and thousands, whose difference counts."""
+    c = make_case(23, 2, N, 8, 2, 128, [300, 77], spread=spread)
+    add_rows(c)
+    check(run(c), expected(c), 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 1000, 1, 64), (1, 4096, 2, 64), (300, 8, 1, 64), (2, 512, 256, 64)])
+def test_many_heads(gpu, N, Hq, Hkv, D):
+    c = add_rows(make_case(N, 1, N, Hq, Hkv, D, [70]))
+    check(run(c), expected(c), D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [2, 20])
+def test_the_same_node_twice(gpu, N):
+    """A path may name a node again: another row, one position further on."""
+    c = make_case(24, 2, N, 4, 2, 64, [50, 9])
+    path = np.zeros((2, N), np.int32)
+    path[1] = N - 1
+    add_rows(c, 2, [N - 1, N - 1], path)
+    check(run(c), expected(c), 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 40])
+def test_slots_beyond_32_bits(gpu, N):
+    """Rows of 1 MB: the last slots lie more than 2^32 bytes behind the first."""
+    c = add_rows(make_case(25, 2, N, 4, 1, 64, [130, 3]))
+    slots, far = c["rows"].shape[0], 5000
+    wide = torch.zeros((far, 1 << 20), dtype=torch.uint8, device="cuda")
+    wide[far - slots:, :80] = on(c["rows"])
+    got = sd.spec_kv4_weight_sums(c["q"].cuda(), on(c["lse"]), wide[:, :80], on(c["table"] + far - slots), on(c["lens"]), 1,
+                                  prev=on(c["prev"]), out=torch.full(c["table"].shape, 55.0, device="cuda"), scale=c["scale"])
+    check(got, expected(c), 64)
+
+
 def wide_groups(rng, slots, Hkv, D, span):
     """K whose groups of 32 channels reach from one value to another `span`
     further on: the cache's whole range, spans on both sides of fp16's largest
