@@ -26,8 +26,8 @@ __all__ = [
     "tli_map_ids",
     "tli_check_config", "tli_pruned_head", "spec_filter_logits", "spec_wait_probe", "spec_debug_bounds",
     "new_stats", "new_pool", "spec_kv4_slot_bytes", "spec_kv4_append", "spec_kv4_gather",
-    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_kv4_weight_sums", "spec_kv4_weight_sums_ws_size",
-    "spec_evict_freed_capacity", "spec_evict_ws_size", "spec_evict_slots", "spec_adjust_logits",
+    "spec_kv4_attention_ws_size", "spec_kv4_attention", "spec_kv4_attention_window", "spec_kv4_weight_sums_ws_size",
+    "spec_kv4_weight_sums", "spec_evict_freed_capacity", "spec_evict_ws_size", "spec_evict_slots", "spec_adjust_logits",
 ]
 
 F32 = 0
@@ -94,15 +94,15 @@ _SIGS = {
     "spec_kv4_attention_ws_size": (_SZ, [_I, _I, _I, _I, _I]),
     "spec_kv4_attention": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _P, _F, _P, _P, _P, _P,
                                 _SZ, _P]),
-    "spec_kv4_attention_window": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32, _I32,
-                                       _F, _P, _P, _P, _P, _SZ, _P]),
-    "spec_kv4_weight_sums": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _P, _P,
-                                  _P, _SZ, _P]),
+    "spec_kv4_attention_window": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32,
+                                       _I32, _F, _P, _P, _P, _P, _SZ, _P]),
+    "spec_kv4_weight_sums": (_I, [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _P,
+                                  _P, _P, _SZ, _P]),
     "spec_kv4_weight_sums_ws_size": (_SZ, [_I, _I, _I, _I, _I]),
     "spec_evict_freed_capacity": (_I64, [_I, _I64, _I, _I]),
     "spec_evict_ws_size": (_SZ, [_I, _I, _I]),
-    "spec_evict_slots": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P,
-                              _SZ, _P]),
+    "spec_evict_slots": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P,
+                              _P, _SZ, _P]),
     "spec_adjust_logits": (_I, [_I, _I, _I64, _I, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P,
                                 _I64, _P, _P, _P]),
     "tli_pruned_head_ws_size": (_SZ, [_I64, _I64]),
@@ -689,8 +689,8 @@ def spec_kv4_attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_ma
     a uint8 workspace of spec_kv4_attention_ws_size bytes to reuse between
     calls that do not overlap.  stats: counts requests and slots out of range,
     and waits that ran out (results void).  Returns out [B, N, Hq, D] bf16."""
-    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
-                      None)
+    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws,
+                      stats, None)
 
 
 def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, sinks, window, positions=None,
@@ -700,11 +700,12 @@ def spec_kv4_attention_window(q, kv_pool, req_to_token, seq_lens, num_kv_heads, 
     ``window``.  positions [B, N] int32: spec_build_tree's, of which the
     distances to the root's count (None: a chain).
     Positions between the sinks and the window are not read."""
-    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
-                      (positions, _i32(sinks, "sinks", clamp=True), _i32(window, "window", clamp=True)))
+    return _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws,
+                      stats, (positions, _i32(sinks, "sinks", clamp=True), _i32(window, "window", clamp=True)))
 
 
-def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats, window):
+def _attention(q, kv_pool, req_to_token, seq_lens, num_kv_heads, tree_mask, scale, num_nodes, out, lse, ws, stats,
+               window):
     dev = _device(q, "q")
     qs = _rows(q, "q")
     if q.dtype is not torch.bfloat16:
@@ -834,8 +835,8 @@ def spec_evict_slots(sums, seq_lens, req_to_token, page_size, budget, limit=None
                                 _arg(freed, i32, (freed.numel(),), dev, "freed"), freed.numel(),
                                 _arg(out["num_freed"], i32, (1,), dev, "num_freed"),
                                 _arg(out["new_kv_len"], i32, (B,), dev, "new_kv_len"), pool or None, slots, width,
-                                _arg(stats, i32, (NUM_STATS,), dev, "stats"), _arg(ws, torch.uint8, ws.shape, dev, "ws"),
-                                ws.numel(), _stream())
+                                _arg(stats, i32, (NUM_STATS,), dev, "stats"),
+                                _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel(), _stream())
     if rc:
         raise SpecError("spec_evict_slots", rc)
     return out

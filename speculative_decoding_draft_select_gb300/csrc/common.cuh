@@ -248,9 +248,9 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
 
 // Thread-block clusters: this CTA's rank, a barrier over every thread of
 // every CTA of the cluster (release / acquire: shared-memory writes before
-// it, local or remote, are visible after it), and a store into the shared
-// memory of another CTA of the cluster at the address that corresponds to
-// a local one.
+// it, local or remote, are visible after it), and loads and stores of the
+// shared memory of another CTA of the cluster at the address that corresponds
+// to a local one.
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -258,6 +258,15 @@ __device__ __forceinline__ unsigned cluster_rank() {
 }
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <typename T>
+__device__ __forceinline__ T ld_cluster(const T* local, unsigned rank) {
+  static_assert(sizeof(T) == 4, "32-bit values");
+  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
+  unsigned r, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return *reinterpret_cast<T*>(&v);
 }
 __device__ __forceinline__ void st_cluster_f32(float* local, unsigned rank, float v) {
   const unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(local));

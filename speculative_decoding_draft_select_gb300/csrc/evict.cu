@@ -81,19 +81,11 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 // Whether position p of a request of length n stays in any case.
-__device__ __forceinline__ bool evict_stays(const EvictArgs& a, int p, int n) { return p < a.sinks || p >= n - a.recent; }
+__device__ __forceinline__ bool evict_stays(const EvictArgs& a, int p, int n) {
+  return p < a.sinks || p >= n - a.recent;
+}
 __device__ __forceinline__ uint32_t evict_key(const EvictArgs& a, const float* sums, int p, int n) {
   return evict_stays(a, p, n) ? ~0u : sum_key(__ldg(sums + p));
-}
-
-template <typename T>
-__device__ __forceinline__ T ld_cluster(const T* local, unsigned rank) {
-  static_assert(sizeof(T) == 4, "32-bit values");
-  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
-  unsigned r, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
-  return static_cast<T>(v);
 }
 
 __device__ __forceinline__ uint4 ld_cluster4(const unsigned* local, unsigned rank) {
@@ -178,7 +170,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       *a.num_freed = static_cast<int32_t>(all);
     }
   }
-  if (b >= a.B) return;  // no request at all: the launch has this one CTA
+  if (b >= a.B) return;  // no request at all: the launch has one cluster for num_freed
 
   const int n = evict_len(a, b);
   const bool cut = n > a.limit;
@@ -503,7 +495,8 @@ using namespace specdec;
 
 extern "C" int64_t spec_evict_freed_capacity(int B, int64_t max_ctx, int page_size, int budget) {
   if (B < 0 || max_ctx < 1 || max_ctx > INT_MAX || page_size < 1 || budget < 1) return -1;
-  const int64_t most = (max_ctx + page_size - 1) / page_size, stay = (static_cast<int64_t>(budget) + page_size - 1) / page_size;
+  const int64_t most = (max_ctx + page_size - 1) / page_size;
+  const int64_t stay = (static_cast<int64_t>(budget) + page_size - 1) / page_size;
   return most > stay ? B * (most - stay) : 0;
 }
 
@@ -570,7 +563,7 @@ extern "C" int spec_evict_slots(int B, int page_size, int budget, int limit, int
   int c = 1;
   while (c < kMaxCtas && B * slices * c < 2 * 152 && c * kRows < budget) c *= 2;
   if (!allow_wide_clusters<evict_payload_kernel>()) return SPEC_ERR_CUDA;
-  launch_kc(evict_payload_kernel, dim3(static_cast<unsigned>(slices * c), static_cast<unsigned>(B)), kMoveThreads, 0, s, c,
-            a, c);
+  const dim3 grid(static_cast<unsigned>(slices * c), static_cast<unsigned>(B));
+  launch_kc(evict_payload_kernel, grid, kMoveThreads, 0, s, c, a, c);
   return launch_status();
 }

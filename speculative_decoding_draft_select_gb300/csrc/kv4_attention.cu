@@ -59,14 +59,6 @@ constexpr int kAttThreads = 128;
 constexpr int kAttWarps = kAttThreads / 32;
 constexpr float kWeightExp = 15.0f;  // weights are held times 2^15
 
-// D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
-__device__ __forceinline__ void mma16816(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
 template <int BYTES>
 struct Vec;
 template <>
@@ -104,12 +96,14 @@ struct Stage {
   static constexpr int kV = D == 128 ? P * 80 : P * 32;         // V's first byte
   static constexpr int kBytes = P * kv4_head_bytes(D);
   // A lane's share of one position: K's codes and (step, lo), V's.
-  __device__ __forceinline__ static void k(const uint8_t* s, int pos, int t, typename Vec<D / 8>::type& c, uint32_t& m) {
+  __device__ __forceinline__ static void k(const uint8_t* s, int pos, int t, typename Vec<D / 8>::type& c,
+                                           uint32_t& m) {
     c = *reinterpret_cast<const typename Vec<D / 8>::type*>(s + pos * (D / 2) + t * (D / 8));
     m = *reinterpret_cast<const uint32_t*>(
         s + (D == 128 ? kKMeta + pos * 16 + t * 4 : kV + pos * kVRow + D / 2 + (t >> 1) * 4));
   }
-  __device__ __forceinline__ static void v(const uint8_t* s, int pos, int g, typename Vec<D / 16>::type& c, uint32_t& m) {
+  __device__ __forceinline__ static void v(const uint8_t* s, int pos, int g, typename Vec<D / 16>::type& c,
+                                           uint32_t& m) {
     const uint8_t* row = s + kV + pos * kVRow;
     c = *reinterpret_cast<const typename Vec<D / 16>::type*>(row + g * (D / 16));
     m = *reinterpret_cast<const uint32_t*>(row + (D == 128 ? 64 + (g >> 1) * 4 : 40 + (g >> 2) * 4));
@@ -140,7 +134,8 @@ struct Filler {
     head = a.pool + ap.h * kv4_head_bytes(D);
     row = a.table + static_cast<int64_t>(ap.b) * a.max_ctx + (threadIdx.x >> 5) * P + (threadIdx.x & (P - 1));
   }
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R, WIN>& walk, uint8_t* stages, unsigned* t) {
+  __device__ __forceinline__ void begin(const AttnArgs& a, const Walk<kTile, E, R, WIN>& walk, uint8_t* stages,
+                                        unsigned* t) {
     ahead = walk;
     more = ahead.next(a, ap);
     segment(a);
@@ -156,8 +151,8 @@ struct Filler {
   __device__ __forceinline__ void load_slot() {
     loaded = more;
     if (!more) return;
-    const int pos = next_tile * kTile + static_cast<int>(threadIdx.x >> 5) * P + static_cast<int>(threadIdx.x & (P - 1));
-    slot = pos < ap.end && spec_in(pos, ap.end, nullptr) 
+    const int pos = next_tile * kTile + static_cast<int>((threadIdx.x >> 5) * P + (threadIdx.x & (P - 1)));
+    slot = pos < ap.end && spec_in(pos, ap.end, nullptr)
                ? __ldg(row + next_tile * kTile + (WIN && pos >= ap.cut ? ap.gap : 0))
                : -2;
     ++next_tile;
@@ -179,7 +174,8 @@ struct Filler {
         const uint64_t src = __shfl_sync(0xffffffffu, mine, pos) + b * 16;
         // a position without a slot is zeroed: its weights are zero, its values must not be NaN
         const unsigned size = (have >> pos) & 1u ? 16u : 0u;
-        const unsigned k = ring + st * St::kBytes + pos * (D / 2) + b * 16, v = ring + st * St::kBytes + St::kV + pos * St::kVRow + b * 16;
+        const unsigned k = ring + st * St::kBytes + pos * (D / 2) + b * 16;
+        const unsigned v = ring + st * St::kBytes + St::kV + pos * St::kVRow + b * 16;
         constexpr int kk = D / 64;  // sectors of K's codes, and of V's
 #pragma unroll
         for (int i = 0; i < kk; ++i) {
@@ -764,7 +760,8 @@ __global__ void __launch_bounds__(kAttThreads, 3) kv4_attention8_kernel(const At
     }
     for (int i = threadIdx.x; i < rows * (D / 4); i += kAttThreads) {
       const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
-      const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][ch]), y = *reinterpret_cast<const float4*>(&sh.o[1][r][ch]);
+      const float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][ch]);
+      const float4 y = *reinterpret_cast<const float4*>(&sh.o[1][r][ch]);
       const float4 acc = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
       float top, sum;
       warps_sum(sh.m, sh.l, r, top, sum);
@@ -815,6 +812,7 @@ int rows_of(int64_t rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 0); }
 // tiles:
 //   D=128  552: 23.3/18.1   1081: 22.5/17.4   2073: 24.6/25.1   4416: 65/88
 //   D=64   811: 19.8/13.5   4264: 30.3/27.5   6490: 33.4/38.2
+// One limit for both, where D=128 turns: D=64 would gain a tenth up to some 5000.
 constexpr int64_t kFewTiles = 2000;
 bool few_tiles(int B, int N, int Hkv, int64_t rows, int64_t max_ctx, int sinks, int window) {
   const int64_t places = static_cast<int64_t>(sinks) + window + N;

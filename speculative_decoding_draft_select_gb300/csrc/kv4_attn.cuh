@@ -261,6 +261,14 @@ __device__ __forceinline__ void dequant4(uint32_t x, uint32_t step2, uint32_t lo
   }
 }
 
+// D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
+__device__ __forceinline__ void mma16816(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
 // Which halves of a (step, lo) pair of registers decode to finite values alone,
 // as a mask: every lo + c * step lies between lo and lo + 15 * step, and the sum
 // is an infinity or NaN where one of its terms is.  Appended rows pass.  A node
@@ -370,7 +378,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const AttnArgs
   if (mine >= rows) return;
   const float inv = attn_inv(l);
   const int64_t at = attn_row(a, b, h, rt * R + r);
-  if (!spec_in(at, static_cast<int64_t>(a.B) * a.N * a.Hq, a.stats) || !spec_in(blockIdx.x + pieces - 1, a.ctas, a.stats))
+  if (!spec_in(at, static_cast<int64_t>(a.B) * a.N * a.Hq, a.stats) ||
+      !spec_in(blockIdx.x + pieces - 1, a.ctas, a.stats))
     return;
   uint32_t v[per / 2];
 #pragma unroll

@@ -62,15 +62,7 @@ struct SumCfg {
   static constexpr int kCtas = RT == 1 ? 3 : 2;  // of an SM
 };
 
-// D += A B, 16 x 8 x 16, fp16 operands and fp32 sums.
-__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// D = A B.
+// mma16816 without sums before: D = A B.
 __device__ __forceinline__ void mma16816_zero(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -133,7 +125,8 @@ __device__ __forceinline__ void load_tile(const SumArgs& a, int b, int h, int r0
   for (int k = 0; k < D / 32; ++k) {
     v[k] = make_uint4(0, 0, 0, 0);
     if (in)
-      v[k] = __ldg(reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
+      v[k] = __ldg(
+          reinterpret_cast<const uint4*>(a.q + at * a.q_stride + static_cast<int64_t>(head) * D + k * 32 + t * 8));
   }
   in = in && isfinite(lse);
   // the largest magnitude: bf16 bits without the sign compare as integers
@@ -229,17 +222,19 @@ struct Ring {
     meta = mine + D;
     load(row, at + 1, end);
   }
-  __device__ __forceinline__ void copy(const SumArgs& a, const int32_t* row, int first, int end, int h0, int heads, int st,
-                                       unsigned* there, bool count) {
+  __device__ __forceinline__ void copy(const SumArgs& a, const int32_t* row, int first, int end, int h0, int heads,
+                                       int st, unsigned* there, bool count) {
     using P = Pos<D>;
     if (left > 0) {
       constexpr int per = D / 32;
       const int lane = threadIdx.x & 31;
-      const unsigned to = base + st * (kChunk * P::kBytes), off = static_cast<unsigned>(h0 + head) * kv4_head_bytes(D);
+      const unsigned to = base + st * (kChunk * P::kBytes);
+      const unsigned off = static_cast<unsigned>(h0 + head) * kv4_head_bytes(D);
       if (lane == 0) there[st] = have;
 #pragma unroll
       for (int u = 0; u < per; ++u)
-        put_async(to + (u * (32 / per) + lane / per) * P::kBytes + (lane % per) * 16, src[u] + off, ((size >> u) & 1u) * 16u);
+        put_async(to + (u * (32 / per) + lane / per) * P::kBytes + (lane % per) * 16, src[u] + off,
+                  ((size >> u) & 1u) * 16u);
       put_async(to + lane * P::kBytes + P::kCodes, meta + off, ((have >> lane) & 1u) * 16u);
       --left;
       if (++head == heads) {
@@ -281,7 +276,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // Rows [r0, r0 + 128) of KV head h as a block in the workspace: a CTA's work,
 // four rows a warp at a time.
 template <int D>
-__device__ __forceinline__ void write_block(const SumArgs& a, int b, int h, int r0, const SumReq& rq, RowsBlock<D>& out) {
+__device__ __forceinline__ void write_block(const SumArgs& a, int b, int h, int r0, const SumReq& rq,
+                                            RowsBlock<D>& out) {
   constexpr int kTurns = kRowsBlock / (4 * kWarps);
   __shared__ int s_top[kWarps], s_fold[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, c0 = warp * 4 + (lane >> 3);
@@ -561,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, SumCfg<RT>::kCtas) kv4_sums_kernel(c
                   for (int u = 0; u < 2; ++u) {
                     float p[4];
                     mma16816_zero(p, c[0][u], b0.x, b0.y);
-                    mma16816(p, c[1][u], b1.x, b1.y);
+                    mma16816(p, make_uint4(c[1][u][0], c[1][u][1], c[1][u][2], c[1][u][3]), b1.x, b1.y);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                       s[x][u][j] = k == 0 ? step[2 * u + (j >> 1)] * p[j]

@@ -36,16 +36,16 @@
 //
 // Measured at 32 heads over 8 of 128, 32 rows each, B=4, contexts 60001..131001
 // (100 GFLOP of scores, 391 M exponentials): 184 us with the launch that lays the
-// rows out (180 without the look for wide groups).  A step takes 1850 cycles, of
-// which the tensor pipe works 1090.  All products of a step go through one
-// accumulator, one after the other, and two steps' S and operands fill the tensor
-// memory.  The weights take 1350 cycles, the unpacking 2000 for two groups.  786
-// MB come from DRAM for 489 MB of rows, since the heads of a tile are some twenty
-// steps apart; shorter segments read less and take longer (8 tiles: 204 us).
-// Steps on the way here: K's operands in shared memory 319 us (the matrix
-// instructions then share its bandwidth), factor and lse read per column and rows
-// converted by every CTA 289, groups of weights on alternate steps 206, one lane
-// of a diverged warp issuing 204 instead of 182.
+// rows out (180 without the look for wide groups).  A step took 1830 cycles
+// without that look, of which the tensor pipe works 1090.  All products of a step
+// go through one accumulator, one after the other, and two steps' S and operands
+// fill the tensor memory.  The weights take 1350 cycles, the unpacking 2000 for
+// two groups.  786 MB come from DRAM for 489 MB of rows, since the heads of a
+// tile are some twenty steps apart; shorter segments read less and take longer (8
+// tiles: 204 us). Steps on the way here: K's operands in shared memory 319 us
+// (the matrix instructions then share its bandwidth), factor and lse read per
+// column and rows converted by every CTA 289, groups of weights on alternate
+// steps 206, one lane of a diverged warp issuing 204 instead of 182.
 #include "kv4_sums.cuh"
 #include "tcgen05.cuh"
 
@@ -150,14 +150,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __forceinline__ float ld_cluster(const float* local, unsigned rank) {
-  const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(local));
-  unsigned r;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
-  return v;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_sums_rows_kernel(const SumArgs a, int clusters, int ranks) {
@@ -601,6 +593,9 @@ int launch_rows(const SumArgs& a, int ranks, int sms, cudaStream_t s) {
   constexpr auto kernel = kv4_sums_rows_kernel<D>;
   constexpr size_t smem = sizeof(RowsShared<D>) + 1024;
   static_assert(smem + 1024 <= 227 * 1024, "a CTA's shared memory");
+  // a CTA holds all tensor memory of its SM while it waits for its cluster: two of
+  // two clusters on one SM could wait for each other
+  static_assert(2 * smem > 228 * 1024, "one CTA an SM");
   if (!allow_smem<kernel>(smem)) return SPEC_ERR_CUDA;
   const int clusters = sms / ranks;
   launch_kc(kernel, static_cast<unsigned>(clusters * ranks), kThreads, smem, s, ranks, a, clusters, ranks);

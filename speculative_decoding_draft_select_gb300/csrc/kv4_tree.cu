@@ -42,7 +42,11 @@
 //
 // With a sliding window and sinks (WIN, see kv4_attention.cu) only the bits of
 // what a row sees change.  64-node trees, B=128, contexts 16..8192, window 1024:
-// 253 us, as far from the products' floor as over whole contexts.
+// 253 us, as far from the products' floor as over whole contexts: by the number of
+// tiles 22 us each (3.3 a tile of a CTA's 6.7 segments, of which the tensor pipe
+// works a quarter) and 57 for all segments' beginnings, ends and the merge.  16-node
+// trees of 48 rows, D = 64, B=64, window 509: 33 us; where no segment is cut (B=76)
+// 2.8 us for each of five tiles and 13 for the launches, Q and the ends.
 #include "kv4_attn.cuh"
 #include "tcgen05.cuh"
 
@@ -291,7 +295,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int pos = at * kTT + p_of + i * kStep;
-        slot[i] = pos < ap.end ? __ldg(row + pos + (WIN && pos >= ap.cut ? ap.gap : 0)) : -2;  // -2: no position, -1 or out of range: a bad slot
+        // -2: no position, -1 or out of range: a bad slot
+        slot[i] = pos < ap.end ? __ldg(row + pos + (WIN && pos >= ap.cut ? ap.gap : 0)) : -2;
       }
       if (++next_tile == ap.t1) {
         more = ahead.next(a, ap);
@@ -448,7 +453,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
         if (j >= S) ok = wait_warp(&v_empty[st], static_cast<uint32_t>(j / S - 1) & 1u, &s_abort);
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) unpack_to(sm_v + st * C::kOperand, v[i], p_of + i * kStep, (tile + 1) * kTT > p.start);
+        for (int i = 0; i < kPer; ++i)
+          unpack_to(sm_v + st * C::kOperand, v[i], p_of + i * kStep, (tile + 1) * kTT > p.start);
         tc::fence_smem();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&v_full[j & 1]);
@@ -612,7 +618,8 @@ __global__ void __launch_bounds__(TreeCfg<D, MT>::kThreads, MT == 2 ? 1 : 2) kv4
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rr = r - lane + 8 * i + (lane >> 2);
-          to[i] = (p.complete() ? attn_row(a, p.b, p.h, r0 + rr) * (D * 2) : static_cast<int64_t>(rr) * (D * 4)) + 16 * (lane & 3);
+          to[i] = p.complete() ? attn_row(a, p.b, p.h, r0 + rr) * (D * 2) : static_cast<int64_t>(rr) * (D * 4);
+          to[i] += 16 * (lane & 3);
         }
 #pragma unroll 1
         for (int w = 0; w < D / cols; ++w) {
