@@ -401,3 +401,24 @@ def test_groups_wider_than_half_precision(gpu, D, N, G, span):
     got = run(c)
     check(got, expected(c), D)
     assert torch.equal(got, run(c))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,spread", [(4, 0), (12, 0), (33, 0), (33, 20)])
+def test_few_wide_groups(gpu, D, N, spread):
+    """Tiles with a wide group among tiles without, over several heads, segments and
+    requests; rows of one size and of many."""
+    c = make_case(19, 3, N, 8, 2, D, [9001, 0, 700])
+    rng = np.random.default_rng(D + N)
+    slots = c["rows"].shape[0]
+    k = rng.normal(0, 1, (slots, 2, D)).astype(np.float32)
+    at = rng.random(slots) < 0.003
+    k[at] = wide_groups(rng, int(at.sum()), 2, D, "all") * (rng.random((int(at.sum()), 2, D // 32)) < 0.5).repeat(32, 2)
+    c["rows"] = ref.kv4_rows(k, k)
+    size = 2.0 ** -rng.integers(0, spread + 1, (3, N, 8)) * 2.0**-15
+    c["q"] = (c["q"].float() * torch.from_numpy(size)[..., None].float()).to(torch.bfloat16)
+    add_rows(c)
+    got = run(c)
+    check(got, expected(c), D)
+    assert torch.equal(got, run(c))
