@@ -644,7 +644,8 @@ int spec_kv4_attention_window(int B, int N, int Hq, int Hkv, int D, const void* 
  * for p < seq_lens[b] + rows; other entries are left as they were.  Called
  * behind spec_compact_slots with the seq_lens, accept_path and accept_length
  * that it had, the accepted path's K lies in order; lse is what
- * spec_kv4_attention returned for the same nodes.  Layers that share the slots
+ * spec_kv4_attention returned for the same nodes (with a window's, positions that
+ * the window hides would be given weights too).  Layers that share the slots
  * add up by calls that follow one another.
  *   q [B, N, Hq, D] bf16, rows (b, n) q_stride elements apart; lse [B, N, Hq]
  *     fp32: a row whose lse is not finite adds nothing.

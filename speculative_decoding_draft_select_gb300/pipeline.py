@@ -261,7 +261,7 @@ def run_compact(buf: StepBuffers, seq_lens, req_to_token, page_size, kv_pool=Non
 def run_weight_sums(buf: StepBuffers, q, lse, seq_lens, req_to_token, kv_pool, num_kv_heads, sums, scale=None, ws=None):
     """Adds the attention weights of the accepted path's rows of q [B, N, Hq, D]
     to sums [B, max_ctx]; behind run_compact, with the seq_lens and lse that
-    run_attention had.  Without ``ws`` the workspace is kept as run_attention's;
+    run_attention had (without a window).  Without ``ws`` the workspace is kept as run_attention's;
     calls of one buf that may run at the same time pass a ``ws`` each, of
     spec_kv4_weight_sums_ws_size bytes (and sums of their own)."""
     v = buf.verify_out
